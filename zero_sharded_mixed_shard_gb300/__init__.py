@@ -32,7 +32,11 @@ MODE_FOLDED_STORAGE = 2
 MODE_SGD = 3
 MODE_MOMENTUM = 4
 
-# every symbol include/zero_step.h declares
+TYPE_FP16 = 0
+TYPE_BF16 = 1
+TYPE_FP32 = 2
+
+# every symbol the headers in include/ declare
 EXPORTED = ("zero_init_layout", "zero_free_layout", "zero_shard_range", "zero_memory_bytes",
             "zero_adam_step", "zero_adam_step_shard", "zero_plan_buckets", "zero_adam_step_range",
             "zero_adam_step_bucketed", "zero_set_step_max_sms", "zero_step_plan",
@@ -40,7 +44,8 @@ EXPORTED = ("zero_init_layout", "zero_free_layout", "zero_shard_range", "zero_me
             "zero_offload_step", "zero_mlp4_loss", "zero_mlp4_layer_grads",
             "zero_mlp4_zero3_step", "zero_mlp4_zero3_step_noalloc", "zero_device_timeouts",
             "zero_selftest_wait_timeout", "zero_selftest_mean_division", "zero_strerror",
-            "zero_last_cuda_error", "zero_last_cuda_error_string")
+            "zero_last_cuda_error", "zero_last_cuda_error_string",
+            "zero_adamw_plan", "zero_grad_norm", "zero_adamw_step")
 
 
 class ZeroError(RuntimeError):
@@ -74,6 +79,22 @@ class zero_layout_t(ctypes.Structure):
                 ("bytes_per_rank_mixed", ctypes.c_double),
                 ("floats_per_rank_p1", ctypes.c_double),
                 ("comm_elems_per_rank", ctypes.c_double)]
+
+
+class zero_adamw_tensor_t(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("rank_stride", ctypes.c_int64),
+                ("master", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("param", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("weight_decay", ctypes.c_float), ("lr_scale", ctypes.c_float)]
+
+
+class zero_adamw_plan_t(ctypes.Structure):
+    _fields_ = [("n_tensors", ctypes.c_int32), ("P", ctypes.c_int32),
+                ("grad_type", ctypes.c_int32), ("param_type", ctypes.c_int32),
+                ("state_bits", ctypes.c_int32), ("vector_tensors", ctypes.c_int32),
+                ("elements", ctypes.c_int64), ("chunks", ctypes.c_int64),
+                ("norm_chunks", ctypes.c_int64), ("table_bytes", ctypes.c_int64)]
 
 
 _lib = None
@@ -148,6 +169,14 @@ def lib() -> ctypes.CDLL:
     L.zero_selftest_mean_division.restype = ctypes.c_int
     L.zero_device_timeouts.argtypes = [ctypes.POINTER(ctypes.c_int64), i32]
     L.zero_device_timeouts.restype = ctypes.c_int
+    plan_p = ctypes.POINTER(zero_adamw_plan_t)
+    L.zero_adamw_plan.argtypes = [ctypes.POINTER(zero_adamw_tensor_t), i32, i32, i32, i32, i32,
+                                  plan_p, vp, i64]
+    L.zero_adamw_plan.restype = ctypes.c_int
+    L.zero_grad_norm.argtypes = [plan_p, vp, f32, f32, vp, vp]
+    L.zero_grad_norm.restype = ctypes.c_int
+    L.zero_adamw_step.argtypes = [plan_p, vp, vp, i64, f32, f32, f32, f32, ctypes.c_uint32, vp]
+    L.zero_adamw_step.restype = ctypes.c_int
     L.zero_strerror.argtypes = [ctypes.c_int]
     L.zero_strerror.restype = ctypes.c_char_p
     L.zero_last_cuda_error.argtypes = []
@@ -432,3 +461,66 @@ def zero_mlp4_zero3_step_noalloc(x, P: int, n: int, master, m, v, shard16, loss,
                                             mode, _stream(stream))
     if rc:
         raise ZeroError(rc, "zero_mlp4_zero3_step_noalloc")
+
+
+class AdamWPlan:
+    """A planned list of tensors: ``info`` (the host plan), ``table`` (its
+    device table, a uint8 tensor) and the tensors themselves, kept alive."""
+
+    def __init__(self, info: zero_adamw_plan_t, table, keep):
+        self.info, self.table, self.keep = info, table, keep
+
+
+def zero_adamw_plan(tensors, P: int, grad_type: int, param_type: int, state_bits: int,
+                    device=None) -> AdamWPlan:
+    """Plan an AdamW step over many tensors (see include/zero_train.h).
+
+    ``tensors``: a list of dicts with the keys of ``zero_adamw_tensor_t``:
+    ``n``, ``grad`` (rank 0's gradient) and, with ``P > 1``, ``rank_stride``;
+    ``master``, ``m``, ``v``, ``param`` and for 8-bit moments ``m_scale`` and
+    ``v_scale``; ``weight_decay`` (default 0) and ``lr_scale`` (default 1).
+    The device table is allocated and filled here, on the current stream."""
+    import torch
+    n = len(tensors)
+    arr = (zero_adamw_tensor_t * max(n, 1))()
+    for a, t in zip(arr, tensors):
+        for key in ("grad", "master", "m", "v", "m_scale", "v_scale", "param"):
+            setattr(a, key, _addr(t.get(key)))
+        a.n, a.rank_stride = t["n"], t.get("rank_stride", 0)
+        a.weight_decay, a.lr_scale = t.get("weight_decay", 0.0), t.get("lr_scale", 1.0)
+    info = zero_adamw_plan_t()
+    rc = lib().zero_adamw_plan(arr, n, P, grad_type, param_type, state_bits, ctypes.byref(info), None, 0)
+    if rc:
+        raise ZeroError(rc, "zero_adamw_plan")
+    host = torch.empty(info.table_bytes, dtype=torch.uint8)
+    rc = lib().zero_adamw_plan(arr, n, P, grad_type, param_type, state_bits, ctypes.byref(info),
+                               host.data_ptr(), info.table_bytes)
+    if rc:
+        raise ZeroError(rc, "zero_adamw_plan")
+    table = host.to("cuda" if device is None else device)
+    return AdamWPlan(info, table, [dict(t) for t in tensors])
+
+
+def zero_grad_plan(tensors, P: int, grad_type: int, device=None) -> AdamWPlan:
+    """A plan of gradients alone, for zero_grad_norm: ``n``, ``grad`` and
+    ``rank_stride`` of each tensor (zero_adamw_plan with state_bits 0)."""
+    return zero_adamw_plan(tensors, P, grad_type, TYPE_FP16, 0, device)
+
+
+def zero_grad_norm(plan: AdamWPlan, grad_scale: float, max_norm: float, stats, stream=None) -> None:
+    """Enqueue the global gradient norm and its clipping factor into
+    ``stats`` (fp32 [3]: norm, factor, finite; see include/zero_train.h)."""
+    rc = lib().zero_grad_norm(ctypes.byref(plan.info), _addr(plan.table), grad_scale, max_norm,
+                              _addr(stats), _stream(stream))
+    if rc:
+        raise ZeroError(rc, "zero_grad_norm")
+
+
+def zero_adamw_step(plan: AdamWPlan, stats, t: int, lr: float, beta1: float, beta2: float,
+                    eps: float, seed: int = 0, stream=None) -> None:
+    """Enqueue one AdamW step over the plan's tensors; ``stats`` of
+    zero_grad_norm or None (see include/zero_train.h)."""
+    rc = lib().zero_adamw_step(ctypes.byref(plan.info), _addr(plan.table), _addr(stats), t, lr, beta1,
+                               beta2, eps, seed, _stream(stream))
+    if rc:
+        raise ZeroError(rc, "zero_adamw_step")

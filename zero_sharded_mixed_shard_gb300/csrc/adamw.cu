@@ -1,0 +1,755 @@
+// AdamW over many separate tensors (moments in 32 or in 8 bits) and the
+// global gradient norm, each in one launch over a planned list of tensors.
+//
+// The plan cuts every tensor into chunks; a table in device memory holds one
+// record per tensor and the running count of chunks, so a CTA finds the
+// tensor of chunk c by bisection and a launch needs no per-tensor host work.
+// Both operators stream each byte once and are bound by HBM: with fp16
+// gradients and parameters a step moves 2P + 26 bytes per element with fp32
+// moments and 2P + 14 + 1/16 with 8-bit ones, the norm 2P.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <mutex>
+#include <new>
+#include <utility>
+#include <vector>
+
+#include "zero_train.h"
+
+// Defined in step.cu (not exported): keeps zero_last_cuda_error current.
+__attribute__((visibility("hidden"))) int zero_record_cuda_error(int err);
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBlock = 256;                    // elements of a warp's unit, and of an 8-bit scale
+constexpr int kChunk = kWarps * kBlock;        // elements of a CTA's unit of the step
+constexpr int kNormVecs = 4;                   // 8-element vectors a thread of the norm has in flight
+constexpr int kNormChunk = kThreads * 8 * kNormVecs;
+constexpr int kMaxPartials = 2048;             // CTAs of the norm at most
+constexpr float kMax8 = 448.0f;                // largest E4M3 value
+constexpr float kInvMax8 = 1.0f / 448.0f;
+constexpr float kTiny = 1.262177448353619e-29f; // 2^-96
+
+struct Tensor {
+    const void* g;
+    long long stride;
+    float* w;
+    void* m;
+    void* v;
+    float* ms;
+    float* vs;
+    void* p;
+    long long n;
+    float decay;     // weight_decay
+    float lr_scale;
+    int phase;       // elements between the preceding vector boundary and element 0, or -1: streams differ
+    int gphase;      // the same for the gradients alone
+};
+
+// The device table: this header, the running chunk counts of the step and of
+// the norm (n_tensors + 1 each), then the tensors' records.
+struct Header {
+    unsigned int ticket; // CTAs of the running norm that are done; 0 between calls
+    unsigned int pad[3];
+    double partial[kMaxPartials];
+};
+
+struct Args {
+    Header* head;
+    const long long* first;  // [n_tensors + 1] first chunk of each tensor
+    const Tensor* tensors;
+    int n_tensors;
+    int P;
+    int p_pow2;
+    float inv_p;
+    long long chunks;
+    const float* stats;
+    float lr, b1, b2, omb1, omb2, r1, c2, eps;
+    unsigned int seed;
+    float grad_scale, max_norm;
+    float* out;
+};
+
+// ---------------------------------------------------------------------------
+// Device helpers
+// ---------------------------------------------------------------------------
+
+// MurmurHash3's 32-bit finaliser (A. Appleby): every input bit reaches every
+// output bit, which is all that rounding needs.
+__host__ __device__ __forceinline__ unsigned int mix32(unsigned int h)
+{
+    h = (h ^ (h >> 16)) * 0x85ebca6bu;
+    h = (h ^ (h >> 13)) * 0xc2b2ae35u;
+    return h ^ (h >> 16);
+}
+
+template <int T> struct Elem;
+template <> struct Elem<ZERO_TYPE_FP16> { using type = __half; };
+template <> struct Elem<ZERO_TYPE_BF16> { using type = __nv_bfloat16; };
+template <> struct Elem<ZERO_TYPE_FP32> { using type = float; };
+
+__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_float(float x) { return x; }
+
+template <int T> __device__ __forceinline__ unsigned int pack2(float a, float b)
+{
+    if constexpr (T == ZERO_TYPE_FP16) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const unsigned int*>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const unsigned int*>(&h);
+    }
+}
+
+template <int T> __device__ __forceinline__ float2 unpack2(unsigned int u)
+{
+    if constexpr (T == ZERO_TYPE_FP16) return __half22float2(*reinterpret_cast<const __half2*>(&u));
+    else return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+
+// Eight consecutive gradients as loaded: one 16-byte access, two for fp32.
+template <int T> struct Raw8 {
+    uint4 a[T == ZERO_TYPE_FP32 ? 2 : 1];
+};
+
+template <int T> __device__ __forceinline__ Raw8<T> load8(const void* p)
+{
+    Raw8<T> r;
+    const uint4* q = static_cast<const uint4*>(p);
+    r.a[0] = __ldcs(q);
+    if constexpr (T == ZERO_TYPE_FP32) r.a[1] = __ldcs(q + 1);
+    return r;
+}
+
+template <int T> __device__ __forceinline__ void add8(float (&acc)[8], const Raw8<T>& r)
+{
+    const unsigned int u[4] = {r.a[0].x, r.a[0].y, r.a[0].z, r.a[0].w};
+    if constexpr (T == ZERO_TYPE_FP32) {
+        const unsigned int w[4] = {r.a[1].x, r.a[1].y, r.a[1].z, r.a[1].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            acc[j] = __fadd_rn(acc[j], __uint_as_float(u[j]));
+            acc[4 + j] = __fadd_rn(acc[4 + j], __uint_as_float(w[j]));
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = unpack2<T>(u[j]);
+            acc[2 * j] = __fadd_rn(acc[2 * j], f.x);
+            acc[2 * j + 1] = __fadd_rn(acc[2 * j + 1], f.y);
+        }
+    }
+}
+
+__device__ __forceinline__ float mean_of(float sum, const Args& a)
+{
+    if (a.P == 1) return sum;
+    return a.p_pow2 ? __fmul_rn(sum, a.inv_p) : __fdiv_rn(sum, static_cast<float>(a.P));
+}
+
+// The tensor that chunk c belongs to: the last one whose first chunk is <= c
+// (tensors without elements have no chunk and are never the last such one).
+__device__ __forceinline__ int find_tensor(const long long* first, int n, long long c)
+{
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(first + mid) <= c) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// ---------------------------------------------------------------------------
+// The step
+// ---------------------------------------------------------------------------
+
+// One warp per block of 256 elements.  Where a tensor's streams share one
+// 16-byte phase a lane owns 8 consecutive elements (whole-vector accesses;
+// the few lanes at the tensor's ends go element by element); otherwise lane l
+// owns elements l, l + 32, ... of the block, one access each.  The two differ
+// in which lane holds an element and in nothing else: results are the same.
+template <int GT, int PT, int BITS>
+__global__ void __launch_bounds__(kThreads, 4) zero_adamw_kernel(const __grid_constant__ Args a)
+{
+    using G = typename Elem<GT>::type;
+    using P16 = typename Elem<PT>::type;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float factor = 1.0f, go = 1.0f;
+    if (a.stats) {
+        factor = a.stats[1];
+        go = a.stats[2];
+    }
+    int ti = 0;
+    long long lo = 0, hi = 0;
+    Tensor x{};
+    unsigned int key = 0;
+    float lr = 0.0f, decay = 0.0f;
+    for (long long c = blockIdx.x; c < a.chunks; c += gridDim.x) {
+        if (c >= hi) {
+            ti = find_tensor(a.first, a.n_tensors, c);
+            lo = __ldg(a.first + ti);
+            hi = __ldg(a.first + ti + 1);
+            x = a.tensors[ti];
+            lr = __fmul_rn(a.lr, x.lr_scale);
+            decay = __fmul_rn(lr, x.decay);
+            if constexpr (BITS == 8) key = mix32(mix32(a.seed) + 0x9e3779b9u * static_cast<unsigned int>(ti + 1));
+        }
+        const bool vec = x.phase >= 0;
+        const long long b0 = (c - lo) * kChunk + warp * kBlock - (vec ? x.phase : 0); // the block's first element
+        const long long i0 = vec ? b0 + lane * 8 : b0 + lane;                         // the lane's first element
+        const int step = vec ? 1 : 32;
+        const bool whole = vec && i0 >= 0 && i0 + 8 <= x.n;
+        if (b0 >= x.n) continue;
+
+        float w[8], m[8], v[8], g[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] = 0.0f;
+        unsigned int mc[2] = {0u, 0u}, vc[2] = {0u, 0u}; // 8-bit codes as loaded
+        if (whole) {
+            const float4* wp = reinterpret_cast<const float4*>(x.w + i0);
+            *reinterpret_cast<float4*>(w) = __ldcs(wp);
+            *reinterpret_cast<float4*>(w + 4) = __ldcs(wp + 1);
+            if constexpr (BITS == 32) {
+                const float4* mp = reinterpret_cast<const float4*>(static_cast<float*>(x.m) + i0);
+                const float4* vp = reinterpret_cast<const float4*>(static_cast<float*>(x.v) + i0);
+                *reinterpret_cast<float4*>(m) = __ldcs(mp);
+                *reinterpret_cast<float4*>(m + 4) = __ldcs(mp + 1);
+                *reinterpret_cast<float4*>(v) = __ldcs(vp);
+                *reinterpret_cast<float4*>(v + 4) = __ldcs(vp + 1);
+            } else {
+                const uint2 mm = __ldcs(reinterpret_cast<const uint2*>(static_cast<unsigned char*>(x.m) + i0));
+                const uint2 vv = __ldcs(reinterpret_cast<const uint2*>(static_cast<unsigned char*>(x.v) + i0));
+                mc[0] = mm.x, mc[1] = mm.y, vc[0] = vv.x, vc[1] = vv.y;
+            }
+            const G* gp = static_cast<const G*>(x.g) + i0;
+            int r = 0;
+            for (; r + 4 <= a.P; r += 4) {
+                Raw8<GT> raw[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) raw[q] = load8<GT>(gp + (r + q) * x.stride);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) add8<GT>(g, raw[q]);
+            }
+            for (; r < a.P; ++r) add8<GT>(g, load8<GT>(gp + r * x.stride));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const long long i = i0 + j * step;
+                w[j] = m[j] = v[j] = 0.0f;
+                if (i < 0 || i >= x.n) continue;
+                w[j] = x.w[i];
+                if constexpr (BITS == 32) {
+                    m[j] = static_cast<const float*>(x.m)[i];
+                    v[j] = static_cast<const float*>(x.v)[i];
+                } else {
+                    mc[j >> 2] |= static_cast<unsigned int>(static_cast<const unsigned char*>(x.m)[i]) << (8 * (j & 3));
+                    vc[j >> 2] |= static_cast<unsigned int>(static_cast<const unsigned char*>(x.v)[i]) << (8 * (j & 3));
+                }
+                const G* gp = static_cast<const G*>(x.g) + i;
+                for (int r = 0; r < a.P; ++r) g[j] = __fadd_rn(g[j], to_float(gp[r * x.stride]));
+            }
+        }
+        if (go == 0.0f) return; // a gradient overflowed: nothing is written
+
+        const long long block = (b0 >= 0 ? b0 : 0) / kBlock;
+        if constexpr (BITS == 8) {
+            const float ms = x.ms[block], vs = x.vs[block];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const unsigned short cm = static_cast<unsigned short>(mc[q >> 1] >> (16 * (q & 1)));
+                const unsigned short cv = static_cast<unsigned short>(vc[q >> 1] >> (16 * (q & 1)));
+                const __half2_raw hm = __nv_cvt_fp8x2_to_halfraw2(cm, __NV_E4M3);
+                const __half2_raw hv = __nv_cvt_fp8x2_to_halfraw2(cv, __NV_E4M3);
+                const float2 fm = __half22float2(__half2(hm)), fv = __half22float2(__half2(hv));
+                m[2 * q] = __fmul_rn(fm.x, ms);
+                m[2 * q + 1] = __fmul_rn(fm.y, ms);
+                const float rx = __fmul_rn(fv.x, vs), ry = __fmul_rn(fv.y, vs);
+                v[2 * q] = __fmul_rn(rx, rx);
+                v[2 * q + 1] = __fmul_rn(ry, ry);
+            }
+        }
+
+        unsigned int high_m = 0, high_r = 0; // largest magnitudes, as bits: ordered like the values, NaN above infinity
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float gg = __fmul_rn(mean_of(g[j], a), factor);
+            m[j] = __fadd_rn(__fmul_rn(m[j], a.b1), __fmul_rn(gg, a.omb1));
+            v[j] = __fadd_rn(__fmul_rn(v[j], a.b2), __fmul_rn(__fmul_rn(gg, gg), a.omb2));
+            const float root = __fsqrt_rn(v[j]);
+            w[j] = __fsub_rn(w[j], __fmul_rn(decay, w[j]));
+            w[j] = __fsub_rn(w[j], __fmul_rn(lr, __fdividef(__fmul_rn(m[j], a.r1),
+                                                            __fadd_rn(__fmul_rn(root, a.c2), a.eps))));
+            if constexpr (BITS == 8) {
+                v[j] = root;
+                high_m = max(high_m, __float_as_uint(m[j]) & 0x7fffffffu);
+                high_r = max(high_r, __float_as_uint(root) & 0x7fffffffu);
+            }
+        }
+
+        unsigned int qm[2] = {0u, 0u}, qv[2] = {0u, 0u};
+        if constexpr (BITS == 8) {
+            high_m = __reduce_max_sync(0xffffffffu, high_m);
+            high_r = __reduce_max_sync(0xffffffffu, high_r);
+            const float am = __uint_as_float(high_m), ar = __uint_as_float(high_r);
+            const float im = am < kTiny ? 0.0f : __fdiv_rn(kMax8, am), ir = ar < kTiny ? 0.0f : __fdiv_rn(kMax8, ar);
+            if (lane == 0) {
+                const float nan = __int_as_float(0x7fffffff);
+                x.ms[block] = am < kTiny ? 0.0f : isfinite(am) ? __fmul_rn(am, kInvMax8) : nan;
+                x.vs[block] = ar < kTiny ? 0.0f : isfinite(ar) ? __fmul_rn(ar, kInvMax8) : nan;
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const __nv_fp8x2_storage_t two = __nv_cvt_float2_to_fp8x2(
+                    make_float2(__fmul_rn(m[2 * q], im), __fmul_rn(m[2 * q + 1], im)), __NV_SATFINITE, __NV_E4M3);
+                qm[q >> 1] |= static_cast<unsigned int>(two) << (16 * (q & 1));
+            }
+            unsigned int h = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                // Sixteen random bits per element, one hash for the two elements of a pair.
+                unsigned int bits16;
+                if (vec) {
+                    if ((j & 1) == 0) h = mix32(static_cast<unsigned int>((i0 + j) >> 1) + key);
+                    bits16 = (j & 1) ? h >> 16 : h & 0xffffu;
+                } else {
+                    const long long i = i0 + j * 32;
+                    h = mix32(static_cast<unsigned int>(i >> 1) + key);
+                    bits16 = (i & 1) ? h >> 16 : h & 0xffffu;
+                }
+                // Scaled by 2^-120 a value's E4M3 code is the top of its
+                // binary32 form (bits 30..20; E4M3's subnormals are fp32's),
+                // and adding random bits below bit 20 before cutting there
+                // rounds up with the probability of what is cut.
+                const float y = __fmul_rn(v[j], ir);
+                unsigned int code = (__float_as_uint(__fmul_rn(y, 7.52316384526264e-37f)) + (bits16 << 4)) >> 20;
+                code = y > 0.0f ? min(max(code, 1u), 0x7eu) : 0u;
+                qv[j >> 2] |= code << (8 * (j & 3));
+            }
+        }
+
+        if (whole) {
+            float4* wp = reinterpret_cast<float4*>(x.w + i0);
+            __stcs(wp, *reinterpret_cast<float4*>(w));
+            __stcs(wp + 1, *reinterpret_cast<float4*>(w + 4));
+            if constexpr (BITS == 32) {
+                float4* mp = reinterpret_cast<float4*>(static_cast<float*>(x.m) + i0);
+                float4* vp = reinterpret_cast<float4*>(static_cast<float*>(x.v) + i0);
+                __stcs(mp, *reinterpret_cast<float4*>(m));
+                __stcs(mp + 1, *reinterpret_cast<float4*>(m + 4));
+                __stcs(vp, *reinterpret_cast<float4*>(v));
+                __stcs(vp + 1, *reinterpret_cast<float4*>(v + 4));
+            } else {
+                __stcs(reinterpret_cast<uint2*>(static_cast<unsigned char*>(x.m) + i0), make_uint2(qm[0], qm[1]));
+                __stcs(reinterpret_cast<uint2*>(static_cast<unsigned char*>(x.v) + i0), make_uint2(qv[0], qv[1]));
+            }
+            __stcs(reinterpret_cast<uint4*>(static_cast<P16*>(x.p) + i0),
+                   make_uint4(pack2<PT>(w[0], w[1]), pack2<PT>(w[2], w[3]), pack2<PT>(w[4], w[5]), pack2<PT>(w[6], w[7])));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const long long i = i0 + j * step;
+                if (i < 0 || i >= x.n) continue;
+                x.w[i] = w[j];
+                if constexpr (BITS == 32) {
+                    static_cast<float*>(x.m)[i] = m[j];
+                    static_cast<float*>(x.v)[i] = v[j];
+                } else {
+                    static_cast<unsigned char*>(x.m)[i] = static_cast<unsigned char>(qm[j >> 2] >> (8 * (j & 3)));
+                    static_cast<unsigned char*>(x.v)[i] = static_cast<unsigned char>(qv[j >> 2] >> (8 * (j & 3)));
+                }
+                const unsigned short h = static_cast<unsigned short>(pack2<PT>(w[j], 0.0f));
+                reinterpret_cast<unsigned short*>(x.p)[i] = h;
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The norm
+// ---------------------------------------------------------------------------
+
+// Each thread squares eight means at a time and adds their sum to a
+// compensated fp32 sum (Kahan): the rounding error does not grow with the
+// number of elements.  The CTAs' sums are joined in fp64 by the last CTA to
+// finish, in CTA order, so the bits do not depend on which one that is.
+template <int GT>
+__global__ void __launch_bounds__(kThreads, 4) zero_grad_norm_kernel(const __grid_constant__ Args a)
+{
+    using G = typename Elem<GT>::type;
+    const int tid = threadIdx.x;
+    float sum = 0.0f, comp = 0.0f;
+    auto add = [&](float s) {
+        const float y = __fsub_rn(s, comp), t = __fadd_rn(sum, y);
+        comp = __fsub_rn(__fsub_rn(t, sum), y);
+        sum = t;
+    };
+    long long lo = 0, hi = 0;
+    Tensor x{};
+    for (long long c = blockIdx.x; c < a.chunks; c += gridDim.x) {
+        if (c >= hi) {
+            const int ti = find_tensor(a.first, a.n_tensors, c);
+            lo = __ldg(a.first + ti);
+            hi = __ldg(a.first + ti + 1);
+            x = a.tensors[ti];
+        }
+        const bool vec = x.gphase >= 0;
+        const long long c0 = (c - lo) * kNormChunk - (vec ? x.gphase : 0);
+        const G* gp = static_cast<const G*>(x.g);
+        if (vec && c0 >= 0 && c0 + kNormChunk <= x.n) {
+            float acc[kNormVecs][8];
+#pragma unroll
+            for (int k = 0; k < kNormVecs; ++k)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[k][j] = 0.0f;
+            for (int r = 0; r < a.P; ++r) {
+                Raw8<GT> raw[kNormVecs];
+#pragma unroll
+                for (int k = 0; k < kNormVecs; ++k)
+                    raw[k] = load8<GT>(gp + r * x.stride + c0 + (k * kThreads + tid) * 8);
+#pragma unroll
+                for (int k = 0; k < kNormVecs; ++k) add8<GT>(acc[k], raw[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < kNormVecs; ++k) {
+                float s = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float g = mean_of(acc[k][j], a);
+                    s = fmaf(g, g, s);
+                }
+                add(s);
+            }
+        } else {
+            for (int k = tid; k < kNormChunk; k += kThreads) {
+                const long long i = c0 + k;
+                if (i < 0 || i >= x.n) continue;
+                float g = 0.0f;
+                for (int r = 0; r < a.P; ++r) g = __fadd_rn(g, to_float(gp[r * x.stride + i]));
+                g = mean_of(g, a);
+                add(__fmul_rn(g, g));
+            }
+        }
+    }
+
+    __shared__ double part[kWarps];
+    __shared__ bool last;
+    auto block_sum = [&](double d) { // in thread 0
+        for (int o = 16; o; o >>= 1) d += __shfl_down_sync(0xffffffffu, d, o);
+        if ((tid & 31) == 0) part[tid >> 5] = d;
+        __syncthreads();
+        d = 0.0;
+        if (tid == 0)
+            for (int k = 0; k < kWarps; ++k) d += part[k];
+        return d;
+    };
+    // an infinite or NaN sum has no compensation: it stands for itself
+    const double mine = block_sum(isfinite(sum) ? static_cast<double>(sum) - static_cast<double>(comp)
+                                                : static_cast<double>(sum));
+    if (tid == 0) {
+        a.head->partial[blockIdx.x] = mine;
+        __threadfence();
+        last = atomicInc(&a.head->ticket, gridDim.x - 1) == gridDim.x - 1; // wraps to 0 for the next call
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    double d = 0.0;
+    for (int k = tid; k < static_cast<int>(gridDim.x); k += kThreads) d += __ldcg(&a.head->partial[k]);
+    __syncthreads(); // part is read above
+    d = block_sum(d);
+    if (tid == 0) {
+        const float norm = static_cast<float>(sqrt(d) * static_cast<double>(a.grad_scale));
+        const bool finite = isfinite(norm);
+        float clip = 1.0f;
+        if (a.max_norm > 0.0f) clip = fminf(1.0f, __fdiv_rn(a.max_norm, __fadd_rn(norm, 1e-6f)));
+        a.out[0] = norm;
+        a.out[1] = finite ? __fmul_rn(a.grad_scale, clip) : 0.0f;
+        a.out[2] = finite ? 1.0f : 0.0f;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+using Kernel = void (*)(Args);
+
+int record(cudaError_t e) { return zero_record_cuda_error(static_cast<int>(e)); }
+
+// CTAs of a kernel that fit the current device at once, asked for once.
+int resident_ctas(Kernel fn, int* out)
+{
+    static std::mutex mu;
+    static std::vector<std::pair<std::pair<int, Kernel>, int>> known;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return record(e);
+    std::lock_guard<std::mutex> lock(mu);
+    for (const auto& k : known)
+        if (k.first.first == dev && k.first.second == fn) {
+            *out = k.second;
+            return ZERO_OK;
+        }
+    int per_sm = 0, sms = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, kThreads, 0);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return record(e);
+    *out = std::max(1, per_sm * sms);
+    try {
+        known.push_back({{dev, fn}, *out});
+    } catch (const std::bad_alloc&) {
+    }
+    return ZERO_OK;
+}
+
+template <int GT, int PT> Kernel pick_bits(int bits)
+{
+    return bits == 32 ? zero_adamw_kernel<GT, PT, 32> : zero_adamw_kernel<GT, PT, 8>;
+}
+
+template <int GT> Kernel pick_param(int param, int bits)
+{
+    return param == ZERO_TYPE_FP16 ? pick_bits<GT, ZERO_TYPE_FP16>(bits) : pick_bits<GT, ZERO_TYPE_BF16>(bits);
+}
+
+Kernel pick_step(int grad, int param, int bits)
+{
+    switch (grad) {
+    case ZERO_TYPE_FP16: return pick_param<ZERO_TYPE_FP16>(param, bits);
+    case ZERO_TYPE_BF16: return pick_param<ZERO_TYPE_BF16>(param, bits);
+    default: return pick_param<ZERO_TYPE_FP32>(param, bits);
+    }
+}
+
+Kernel pick_norm(int grad)
+{
+    switch (grad) {
+    case ZERO_TYPE_FP16: return zero_grad_norm_kernel<ZERO_TYPE_FP16>;
+    case ZERO_TYPE_BF16: return zero_grad_norm_kernel<ZERO_TYPE_BF16>;
+    default: return zero_grad_norm_kernel<ZERO_TYPE_FP32>;
+    }
+}
+
+int64_t table_size(int64_t n)
+{
+    return static_cast<int64_t>(sizeof(Header)) + 2 * (n + 1) * 8 + n * static_cast<int64_t>(sizeof(Tensor));
+}
+
+static_assert(sizeof(Header) % 16 == 0 && sizeof(Tensor) % 8 == 0, "table layout");
+
+bool good_plan(const zero_adamw_plan_t* p, const void* table)
+{
+    return p && table && p->n_tensors >= 1 && p->P >= 1 && p->P <= ZERO_MAX_RANKS && p->grad_type >= 0 &&
+           p->grad_type <= 2 && p->elements >= 0 && p->chunks >= 0 && p->norm_chunks >= 0 &&
+           p->table_bytes == table_size(p->n_tensors);
+}
+
+Args base_args(const zero_adamw_plan_t* plan, void* table, bool norm)
+{
+    Args a{};
+    unsigned char* t = static_cast<unsigned char*>(table);
+    a.head = reinterpret_cast<Header*>(t);
+    const long long* first = reinterpret_cast<const long long*>(t + sizeof(Header));
+    a.first = norm ? first + plan->n_tensors + 1 : first;
+    a.tensors = reinterpret_cast<const Tensor*>(first + 2 * (static_cast<int64_t>(plan->n_tensors) + 1));
+    a.n_tensors = plan->n_tensors;
+    a.P = plan->P;
+    a.p_pow2 = (plan->P & (plan->P - 1)) == 0;
+    a.inv_p = 1.0f / static_cast<float>(plan->P);
+    a.chunks = norm ? plan->norm_chunks : plan->chunks;
+    return a;
+}
+
+int launch(Kernel fn, const Args& a, long long most, void* stream)
+{
+    int fit = 0;
+    const int rc = resident_ctas(fn, &fit);
+    if (rc) return rc;
+    const long long ctas = std::max(1ll, std::min(std::min<long long>(fit, most), static_cast<long long>(a.chunks)));
+    fn<<<static_cast<unsigned int>(ctas), kThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? ZERO_OK : record(e);
+}
+
+struct Span {
+    uintptr_t at, end;
+};
+
+uintptr_t addr(const void* p) { return reinterpret_cast<uintptr_t>(p); }
+
+// The vector phase of streams that are `size` bytes an element: elements past
+// a boundary of 8 elements; fp32 vectors are 4 elements long, so their phase
+// only has to agree modulo 4.
+bool phase_is(uintptr_t at, int size, int phase)
+{
+    const int q = size == 4 ? 4 : 8;
+    return static_cast<int>((at / size) % q) == phase % q;
+}
+
+int plan_tensors(const zero_adamw_tensor_t* tensors, int32_t n_tensors, int32_t P, int32_t grad_type, int32_t bits,
+                 zero_adamw_plan_t* plan, unsigned char* table)
+{
+    const int gs = grad_type == ZERO_TYPE_FP32 ? 4 : 2, ss = bits == 32 ? 4 : 1;
+    std::vector<Span> written, read;
+    long long* first = nullptr;
+    Tensor* rec = nullptr;
+    if (table) {
+        std::memset(table, 0, sizeof(Header));
+        first = reinterpret_cast<long long*>(table + sizeof(Header));
+        rec = reinterpret_cast<Tensor*>(first + 2 * (static_cast<int64_t>(n_tensors) + 1));
+    }
+    for (int32_t j = 0; j < n_tensors; ++j) {
+        const zero_adamw_tensor_t& t = tensors[j];
+        if (t.n < 0 || t.n > (INT64_MAX >> 5)) return ZERO_EINVAL;
+        Tensor x{};
+        long long chunks = 0, norm_chunks = 0;
+        if (bits && (!(t.weight_decay >= 0.0f) || !std::isfinite(t.weight_decay) || !(t.lr_scale >= 0.0f) ||
+                     !std::isfinite(t.lr_scale)))
+            return ZERO_EINVAL;
+        if (t.n > 0) {
+            if (!t.grad || (P > 1 && (t.rank_stride < t.n || t.rank_stride > (INT64_MAX >> 14)))) return ZERO_EINVAL;
+            const int64_t stride = P > 1 ? t.rank_stride : 0;
+            if (addr(t.grad) % gs) return ZERO_EALIGN;
+            for (int32_t r = 0; r < P; ++r) {
+                const uintptr_t at = addr(t.grad) + static_cast<uintptr_t>(r) * static_cast<uintptr_t>(stride) * gs;
+                read.push_back({at, at + static_cast<uintptr_t>(t.n) * gs});
+            }
+            x.g = t.grad;
+            x.stride = stride;
+            x.n = t.n;
+            x.gphase = static_cast<int>((addr(t.grad) / gs) % 8);
+            if ((stride * gs) % 16) x.gphase = -1;
+            x.phase = -1;
+            if (bits) {
+                if (!t.master || !t.m || !t.v || !t.param || (bits == 8 && (!t.m_scale || !t.v_scale)))
+                    return ZERO_EINVAL;
+                if (addr(t.master) % 4 || addr(t.m) % ss || addr(t.v) % ss || addr(t.param) % 2 ||
+                    (bits == 8 && (addr(t.m_scale) % 4 || addr(t.v_scale) % 4)))
+                    return ZERO_EALIGN;
+                const uintptr_t n = static_cast<uintptr_t>(t.n), blocks = (n + kBlock - 1) / kBlock;
+                written.push_back({addr(t.master), addr(t.master) + n * 4});
+                written.push_back({addr(t.m), addr(t.m) + n * ss});
+                written.push_back({addr(t.v), addr(t.v) + n * ss});
+                written.push_back({addr(t.param), addr(t.param) + n * 2});
+                if (bits == 8) {
+                    written.push_back({addr(t.m_scale), addr(t.m_scale) + blocks * 4});
+                    written.push_back({addr(t.v_scale), addr(t.v_scale) + blocks * 4});
+                }
+                x.w = t.master, x.m = t.m, x.v = t.v, x.ms = t.m_scale, x.vs = t.v_scale, x.p = t.param;
+                x.decay = t.weight_decay, x.lr_scale = t.lr_scale;
+                // a block of 8-bit scales starts with the tensor, so only phase 0 keeps vectors inside blocks
+                const int ph = static_cast<int>((addr(t.param) / 2) % 8);
+                if ((bits == 32 || ph == 0) && phase_is(addr(t.grad), gs, ph) && (stride * gs) % 16 == 0 &&
+                    phase_is(addr(t.master), 4, ph) && phase_is(addr(t.m), ss, ph) && phase_is(addr(t.v), ss, ph))
+                    x.phase = ph;
+                chunks = (t.n + std::max(x.phase, 0) + kChunk - 1) / kChunk;
+                plan->vector_tensors += x.phase >= 0;
+            }
+            norm_chunks = (t.n + std::max(x.gphase, 0) + kNormChunk - 1) / kNormChunk;
+        }
+        if (table) {
+            first[j] = plan->chunks;
+            first[n_tensors + 1 + j] = plan->norm_chunks;
+            std::memcpy(rec + j, &x, sizeof(x));
+        }
+        plan->chunks += chunks;
+        plan->norm_chunks += norm_chunks;
+        plan->elements += t.n;
+    }
+    if (table) {
+        first[n_tensors] = plan->chunks;
+        first[2 * n_tensors + 1] = plan->norm_chunks;
+    }
+    // no two written spans share a byte, and none shares one with a gradient
+    auto by_start = [](const Span& p, const Span& q) { return p.at < q.at; };
+    std::sort(written.begin(), written.end(), by_start);
+    for (size_t k = 1; k < written.size(); ++k)
+        if (written[k].at < written[k - 1].end) return ZERO_EOVERLAP;
+    for (const Span& s : read) { // the written spans are disjoint: only the first that ends past s.at can meet it first
+        auto it = std::lower_bound(written.begin(), written.end(), s.at,
+                                   [](const Span& p, uintptr_t at) { return p.end <= at; });
+        if (it != written.end() && it->at < s.end) return ZERO_EOVERLAP;
+    }
+    return ZERO_OK;
+}
+
+} // namespace
+
+extern "C" int zero_adamw_plan(const zero_adamw_tensor_t* tensors, int32_t n_tensors, int32_t P, int32_t grad_type,
+                               int32_t param_type, int32_t state_bits, zero_adamw_plan_t* plan, void* table_out,
+                               int64_t table_bytes)
+{
+    if (!tensors || !plan || n_tensors < 1 || P < 1 || P > ZERO_MAX_RANKS || grad_type < 0 || grad_type > 2 ||
+        (state_bits != 0 && state_bits != 8 && state_bits != 32) ||
+        (state_bits != 0 && param_type != ZERO_TYPE_FP16 && param_type != ZERO_TYPE_BF16))
+        return ZERO_EINVAL;
+    zero_adamw_plan_t p{};
+    p.n_tensors = n_tensors;
+    p.P = P;
+    p.grad_type = grad_type;
+    p.param_type = state_bits ? param_type : ZERO_TYPE_FP16;
+    p.state_bits = state_bits;
+    p.table_bytes = table_size(n_tensors);
+    if (table_out && table_bytes < p.table_bytes) return ZERO_EINVAL;
+    try {
+        // written to a copy first: a refused call leaves the caller's memory as it was
+        std::vector<unsigned char> table(table_out ? static_cast<size_t>(p.table_bytes) : 0);
+        const int rc = plan_tensors(tensors, n_tensors, P, grad_type, state_bits, &p, table_out ? table.data() : nullptr);
+        if (rc) return rc;
+        if (table_out) std::memcpy(table_out, table.data(), table.size());
+    } catch (const std::bad_alloc&) {
+        return ZERO_ENOMEM;
+    }
+    *plan = p;
+    return ZERO_OK;
+}
+
+extern "C" int zero_grad_norm(const zero_adamw_plan_t* plan, void* table, float grad_scale, float max_norm,
+                              float* stats, void* cuda_stream)
+{
+    if (!good_plan(plan, table) || !stats || !std::isfinite(grad_scale) || !(grad_scale > 0.0f) ||
+        std::isnan(max_norm))
+        return ZERO_EINVAL;
+    if (addr(table) % 16 || addr(stats) % 4) return ZERO_EALIGN;
+    Args a = base_args(plan, table, true);
+    a.grad_scale = grad_scale;
+    a.max_norm = max_norm;
+    a.out = stats;
+    return launch(pick_norm(plan->grad_type), a, kMaxPartials, cuda_stream);
+}
+
+extern "C" int zero_adamw_step(const zero_adamw_plan_t* plan, void* table, const float* stats, int64_t t, float lr,
+                               float beta1, float beta2, float eps, uint32_t seed, void* cuda_stream)
+{
+    if (!good_plan(plan, table) || (plan->state_bits != 8 && plan->state_bits != 32) || t < 1 ||
+        !std::isfinite(lr) || !(beta1 >= 0.0f && beta1 < 1.0f) || !(beta2 >= 0.0f && beta2 < 1.0f) ||
+        !std::isfinite(eps) || eps < 0.0f ||
+        (plan->param_type != ZERO_TYPE_FP16 && plan->param_type != ZERO_TYPE_BF16))
+        return ZERO_EINVAL;
+    if (addr(table) % 16 || addr(stats) % 4) return ZERO_EALIGN;
+    if (plan->chunks == 0) return ZERO_OK; // no elements
+    Args a = base_args(plan, table, false);
+    a.stats = stats;
+    a.lr = lr;
+    a.b1 = beta1;
+    a.b2 = beta2;
+    a.omb1 = 1.0f - beta1;
+    a.omb2 = 1.0f - beta2;
+    a.r1 = static_cast<float>(1.0 / (1.0 - std::pow(static_cast<double>(beta1), static_cast<double>(t))));
+    a.c2 = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(static_cast<double>(beta2), static_cast<double>(t))));
+    a.eps = eps;
+    a.seed = seed;
+    return launch(pick_step(plan->grad_type, plan->param_type, plan->state_bits), a, INT64_MAX, cuda_stream);
+}
