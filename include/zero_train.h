@@ -130,6 +130,66 @@ int zero_adamw_step(const zero_adamw_plan_t* plan, void* table, const float* sta
                     float lr, float beta1, float beta2, float eps, uint32_t seed,
                     void* cuda_stream);
 
+/* ------------------------------------------------------------------------ */
+/* The linear layer                                                         */
+/* ------------------------------------------------------------------------ */
+
+#define ZERO_ACT_NONE 0
+#define ZERO_ACT_RELU 1 /* derivative 0 at 0 */
+#define ZERO_ACT_GELU 2 /* tanh's form: z / (1 + exp(-2 sqrt(2/pi) (z + 0.044715 z^3))) */
+#define ZERO_ACT_SILU 3 /* z / (1 + exp(-z)) */
+
+/* Bytes of workspace that is enough for a call of zero_linear_forward
+ * (backward 0) or zero_linear_backward (backward 1) of these sizes.  aligned
+ * != 0 when x, w, dy and z start on 16 bytes and have row strides that are
+ * multiples of 8 elements; otherwise room for aligned copies is counted (rows
+ * laid out off that boundary are copied in every call: pad a weight's rows
+ * once to save it).  May be 0.  Host only.  Errors: ZERO_EINVAL. */
+int zero_linear_workspace(int64_t T, int64_t K, int64_t N, int32_t act, int32_t backward,
+                          int32_t aligned, int64_t* bytes);
+
+/* y = act(x w^T + bias) + residual for T tokens, K inputs, N features:
+ * x [T][ldx], w [N][ldw] (both K wide), bias [N] or NULL, residual [T][ldr]
+ * or NULL, y [T][ldy], all of `type` (ZERO_TYPE_FP16 or ZERO_TYPE_BF16).
+ * z [T][ldz] or NULL receives x w^T + bias, which the backward pass of a
+ * layer with an activation needs.  Products are summed in fp32; y and z are
+ * each rounded once, y from the unrounded z.  residual may be y itself (same
+ * pointer and stride).  T may be 0.
+ * workspace: device, 16-byte aligned, zero_linear_workspace bytes (may be
+ * NULL when that is 0); calls that share one must not overlap on the GPU.
+ * The same call gives the same bits.
+ * Errors: ZERO_EINVAL (sizes above 2^31 - 513, a null pointer, a row stride
+ * below its row, act or type unknown, workspace too small), ZERO_EALIGN
+ * (a pointer not on its element size, workspace not on 16 bytes),
+ * ZERO_EOVERLAP (y or z shares an element with an input or each other),
+ * ZERO_ECUDA. */
+int zero_linear_forward(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias,
+                        const void* residual, int64_t ldr, void* y, int64_t ldy, void* z,
+                        int64_t ldz, int64_t T, int64_t K, int64_t N, int32_t act, int32_t type,
+                        void* workspace, int64_t workspace_bytes, void* cuda_stream);
+
+/* The gradients of zero_linear_forward from dy [T][lddy], the gradient of y:
+ *   dz = dy * act'(z)   (z [T][ldz] of the forward call; unused with
+ *                        ZERO_ACT_NONE, may then be NULL)
+ *   dx = dz w  [T][lddx];  dw = dz^T x  [N][lddw];  db = sum over tokens of dz [N]
+ * The residual's gradient is dy itself.  dx, dw and db may each be NULL (not
+ * computed; w is unused without dx, x without dw).  dw and db may lie
+ * anywhere, for instance in a rank's gradients of the flat vector that
+ * zero_adam_step takes.  dz is rounded to `type` once, before the products;
+ * sums are in fp32.  With T = 0 dw and db become 0.
+ * workspace, errors: as zero_linear_forward (also ZERO_EINVAL when dx, dw and
+ * db are all NULL). */
+int zero_linear_backward(const void* dy, int64_t lddy, const void* z, int64_t ldz, const void* x,
+                         int64_t ldx, const void* w, int64_t ldw, void* dx, int64_t lddx, void* dw,
+                         int64_t lddw, void* db, int64_t T, int64_t K, int64_t N, int32_t act,
+                         int32_t type, void* workspace, int64_t workspace_bytes,
+                         void* cuda_stream);
+
+/* Bounded waits of the linear layer's kernels that gave up on the current
+ * device since the last reset; like zero_device_timeouts (0 in every correct
+ * run, reading it synchronises). */
+int zero_linear_timeouts(int64_t* count, int32_t reset);
+
 #ifdef __cplusplus
 }
 #endif

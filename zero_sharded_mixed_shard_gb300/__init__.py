@@ -36,6 +36,11 @@ TYPE_FP16 = 0
 TYPE_BF16 = 1
 TYPE_FP32 = 2
 
+ACT_NONE = 0
+ACT_RELU = 1
+ACT_GELU = 2
+ACT_SILU = 3
+
 # every symbol the headers in include/ declare
 EXPORTED = ("zero_init_layout", "zero_free_layout", "zero_shard_range", "zero_memory_bytes",
             "zero_adam_step", "zero_adam_step_shard", "zero_plan_buckets", "zero_adam_step_range",
@@ -45,7 +50,9 @@ EXPORTED = ("zero_init_layout", "zero_free_layout", "zero_shard_range", "zero_me
             "zero_mlp4_zero3_step", "zero_mlp4_zero3_step_noalloc", "zero_device_timeouts",
             "zero_selftest_wait_timeout", "zero_selftest_mean_division", "zero_strerror",
             "zero_last_cuda_error", "zero_last_cuda_error_string",
-            "zero_adamw_plan", "zero_grad_norm", "zero_adamw_step")
+            "zero_adamw_plan", "zero_grad_norm", "zero_adamw_step",
+            "zero_linear_workspace", "zero_linear_forward", "zero_linear_backward",
+            "zero_linear_timeouts")
 
 
 class ZeroError(RuntimeError):
@@ -177,6 +184,16 @@ def lib() -> ctypes.CDLL:
     L.zero_grad_norm.restype = ctypes.c_int
     L.zero_adamw_step.argtypes = [plan_p, vp, vp, i64, f32, f32, f32, f32, ctypes.c_uint32, vp]
     L.zero_adamw_step.restype = ctypes.c_int
+    L.zero_linear_workspace.argtypes = [i64, i64, i64, i32, i32, i32, ctypes.POINTER(ctypes.c_int64)]
+    L.zero_linear_workspace.restype = ctypes.c_int
+    L.zero_linear_forward.argtypes = [vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, i64, i64, i64, i64,
+                                      i32, i32, vp, i64, vp]
+    L.zero_linear_forward.restype = ctypes.c_int
+    L.zero_linear_backward.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp,
+                                       i64, i64, i64, i32, i32, vp, i64, vp]
+    L.zero_linear_backward.restype = ctypes.c_int
+    L.zero_linear_timeouts.argtypes = [ctypes.POINTER(ctypes.c_int64), i32]
+    L.zero_linear_timeouts.restype = ctypes.c_int
     L.zero_strerror.argtypes = [ctypes.c_int]
     L.zero_strerror.restype = ctypes.c_char_p
     L.zero_last_cuda_error.argtypes = []
@@ -524,3 +541,45 @@ def zero_adamw_step(plan: AdamWPlan, stats, t: int, lr: float, beta1: float, bet
                                beta2, eps, seed, _stream(stream))
     if rc:
         raise ZeroError(rc, "zero_adamw_step")
+
+
+def zero_linear_workspace(T: int, K: int, N: int, act: int, backward: bool, aligned: bool) -> int:
+    """Workspace bytes of a linear layer's call (see include/zero_train.h)."""
+    n = ctypes.c_int64()
+    rc = lib().zero_linear_workspace(T, K, N, act, 1 if backward else 0, 1 if aligned else 0,
+                                     ctypes.byref(n))
+    if rc:
+        raise ZeroError(rc, "zero_linear_workspace")
+    return n.value
+
+
+def zero_linear_forward(x, ldx: int, w, ldw: int, bias, residual, ldr: int, y, ldy: int, z, ldz: int,
+                        T: int, K: int, N: int, act: int, type: int, workspace=None,
+                        workspace_bytes: int = 0, stream=None) -> None:
+    """Enqueue y = act(x w^T + bias) + residual (see include/zero_train.h)."""
+    rc = lib().zero_linear_forward(_addr(x), ldx, _addr(w), ldw, _addr(bias), _addr(residual), ldr,
+                                   _addr(y), ldy, _addr(z), ldz, T, K, N, act, type,
+                                   _addr(workspace), workspace_bytes, _stream(stream))
+    if rc:
+        raise ZeroError(rc, "zero_linear_forward")
+
+
+def zero_linear_backward(dy, lddy: int, z, ldz: int, x, ldx: int, w, ldw: int, dx, lddx: int, dw,
+                         lddw: int, db, T: int, K: int, N: int, act: int, type: int,
+                         workspace=None, workspace_bytes: int = 0, stream=None) -> None:
+    """Enqueue the gradients of zero_linear_forward (see include/zero_train.h)."""
+    rc = lib().zero_linear_backward(_addr(dy), lddy, _addr(z), ldz, _addr(x), ldx, _addr(w), ldw,
+                                    _addr(dx), lddx, _addr(dw), lddw, _addr(db), T, K, N, act, type,
+                                    _addr(workspace), workspace_bytes, _stream(stream))
+    if rc:
+        raise ZeroError(rc, "zero_linear_backward")
+
+
+def zero_linear_timeouts(reset: bool = False) -> int:
+    """Bounded waits of the linear layer's kernels that gave up (0 in a
+    correct run); synchronises with the device."""
+    n = ctypes.c_int64()
+    rc = lib().zero_linear_timeouts(ctypes.byref(n), 1 if reset else 0)
+    if rc:
+        raise ZeroError(rc, "zero_linear_timeouts")
+    return n.value
