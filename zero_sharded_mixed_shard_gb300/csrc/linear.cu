@@ -10,14 +10,16 @@
 // in dW) is loaded as it lies and read by the tensor core in its "MN-major"
 // form: nothing is transposed in memory.
 //
-// Two kernels.  zero_gemm_kernel (many tiles): persistent CTAs, one TMA warp,
-// one MMA warp, four epilogue warps, accumulators doubled in tensor memory so
-// that a tile's epilogue runs under the next tile's products.
-// zero_gemm_split_kernel (few tiles): the contraction is cut over the CTAs of
-// a cluster, whose partial tiles are added through distributed shared memory
-// in a fixed order; with few tokens the operands change sides (m = feature),
-// so that a tile holds 128 rows of the weights and no more columns than
-// tokens.
+// Two kernels.  zero_gemm_pair_kernel (many tiles): persistent pairs of CTAs
+// that share one product of 256 rows (each holds half of the rows and half of
+// the columns' operand), one TMA warp, one MMA warp, four epilogue warps,
+// accumulators doubled in tensor memory so that a tile's epilogue runs under
+// the next tile's products.  zero_gemm_split_kernel (few tiles): the
+// contraction is cut over the CTAs of a cluster, whose partial tiles are added
+// through distributed shared memory in a fixed order; with few tokens the
+// operands change sides (m = feature), so that a tile holds 128 rows of the
+// weights and no more columns than tokens.  The backward pass gives both of
+// its products to one launch where they take the same kernel.
 //
 // Every wait is bounded: one that runs out counts itself
 // (zero_linear_timeouts), the CTA lets its copies and products in flight end,
@@ -55,12 +57,11 @@ struct Out {
     const void* bias;    // may be null
     const void* res;     // may be null
     long long ldy, ldz, ldr;
-    int rows, cols;      // of the output
     int act, bf16, swap;
-    int vec;             // 16-byte accesses allowed on y, z, res and bias rows
+    int vec;             // 16-byte accesses allowed on y, z, res and bias
 };
 
-struct GemmArgs {
+struct Problem {
     CUtensorMap a, b;
     Out o;
     int a_mn, b_mn;      // the operand's contiguous index is m (n), not k
@@ -68,6 +69,16 @@ struct GemmArgs {
     int tiles_m, tiles_n;
     int kblocks;
     unsigned int idesc;
+};
+
+// One launch: the tiles of one or two products, and the bias gradient's last
+// sum (columns of `sums` over its chunks), which a spare warp takes along.
+struct GemmArgs {
+    Problem p[2];
+    int tiles0, tiles;   // of the first product, of both
+    const float* sums;
+    void* db;
+    int chunks, n_db, bf16;
 };
 
 // ---------------------------------------------------------------------------
@@ -95,11 +106,6 @@ __device__ __forceinline__ void mbar_expect(uint64_t* bar, uint32_t bytes)
 {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes)
                  : "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar)
-{
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
 __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity)
@@ -165,6 +171,65 @@ __device__ __forceinline__ void tmem_free(uint32_t at, uint32_t columns)
 {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns));
 }
+
+// The forms for a pair of CTAs: the barrier may be the other CTA's, the
+// product reads both CTAs' operands, its end is told to both.
+__device__ __forceinline__ uint32_t peer_addr(uint32_t local, uint32_t rank)
+{
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(local), "r"(rank));
+    return at;
+}
+
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
+                 "l"(map), "r"(x), "r"(y), "r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+                 : "memory");
+}
+
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar)
+{
+    const uint16_t both = 3;
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                     smem_addr(bar)),
+                 "h"(both)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* out, uint32_t columns)
+{
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(out)),
+                 "r"(columns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+}
+
+__device__ __forceinline__ void tmem_free_pair(uint32_t at, uint32_t columns)
+{
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns));
+}
+
+// Programmatic launch: everything before the wait touches only this CTA's own
+// memory and runs under the preceding kernel's end; the wait returns when that
+// kernel is complete and its writes are visible.
+__device__ __forceinline__ void wait_for_predecessor() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_successor_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -234,12 +299,20 @@ __device__ __forceinline__ uint32_t cluster_size()
     return r;
 }
 
+__device__ __forceinline__ float4 peer_load4(uint32_t local, uint32_t rank)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(peer_addr(local, rank))
+                 : "memory");
+    return v;
+}
+
 __device__ __forceinline__ float peer_load(uint32_t local, uint32_t rank)
 {
-    uint32_t at;
     float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(local), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer_addr(local, rank)) : "memory");
     return v;
 }
 
@@ -316,7 +389,7 @@ __device__ __forceinline__ float slope(float z, int act)
 }
 
 // One output element from its accumulator.
-__device__ __forceinline__ void emit(const Out& o, int row, int col, float v)
+__device__ __forceinline__ void emit(const Out& o, long long row, int col, float v)
 {
     if (o.bias) v += load16(o.bias, col, o.bf16);
     if (o.z) store16(o.z, row * o.ldz + col, v, o.bf16);
@@ -325,100 +398,53 @@ __device__ __forceinline__ void emit(const Out& o, int row, int col, float v)
     store16(o.y, row * o.ldy + col, v, o.bf16);
 }
 
-// 32 consecutive elements of an output row, from column col on.
-__device__ __forceinline__ void emit32(const Out& o, long long row, int col, float (&v)[32])
+__device__ __forceinline__ void add8(float (&v)[8], const uint4& u, int bf16)
 {
-    if (!o.vec || col + 32 > o.cols) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (col + j < o.cols) emit(o, static_cast<int>(row), col + j, v[j]);
-        return;
+    for (int j = 0; j < 4; ++j) {
+        const float2 f = unpack16(w[j], bf16);
+        v[2 * j] += f.x;
+        v[2 * j + 1] += f.y;
     }
-    if (o.bias) {
-        const uint4* b = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(o.bias) + col);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const uint4 u = __ldg(b + q);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 f = unpack16(w[j], o.bf16);
-                v[q * 8 + 2 * j] += f.x;
-                v[q * 8 + 2 * j + 1] += f.y;
-            }
-        }
-    }
-    auto store = [&](void* base, long long ld) {
-        uint4* p = reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + row * ld + col);
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            p[q] = make_uint4(pack16(v[q * 8], v[q * 8 + 1], o.bf16), pack16(v[q * 8 + 2], v[q * 8 + 3], o.bf16),
-                              pack16(v[q * 8 + 4], v[q * 8 + 5], o.bf16), pack16(v[q * 8 + 6], v[q * 8 + 7], o.bf16));
-    };
-    if (o.z) store(o.z, o.ldz);
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&v)[8], int bf16)
+{
+    return make_uint4(pack16(v[0], v[1], bf16), pack16(v[2], v[3], bf16), pack16(v[4], v[5], bf16), pack16(v[6], v[7], bf16));
+}
+
+// The residual of 8 consecutive elements of an output row, asked for ahead.
+__device__ __forceinline__ uint4 load_res8(const Out& o, long long row, int col)
+{
+    return *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(o.res) + row * o.ldr + col);
+}
+
+// 8 consecutive elements of an output row (16-byte accesses allowed).
+__device__ __forceinline__ void emit8(const Out& o, long long row, int col, float (&v)[8], const uint4& res)
+{
+    if (o.bias) add8(v, __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(o.bias) + col)), o.bf16);
+    if (o.z) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(o.z) + row * o.ldz + col) = pack8(v, o.bf16);
     if (o.act != ZERO_ACT_NONE) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = activate(v[j], o.act);
+        for (int j = 0; j < 8; ++j) v[j] = activate(v[j], o.act);
     }
-    if (o.res) {
-        const uint4* r = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(o.res) + row * o.ldr + col);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const uint4 u = r[q];
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 f = unpack16(w[j], o.bf16);
-                v[q * 8 + 2 * j] += f.x;
-                v[q * 8 + 2 * j + 1] += f.y;
-            }
-        }
-    }
-    store(o.y, o.ldy);
+    if (o.res) add8(v, res, o.bf16);
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(o.y) + row * o.ldy + col) = pack8(v, o.bf16);
 }
 
 // ---------------------------------------------------------------------------
 // Pieces of both kernels
 // ---------------------------------------------------------------------------
 
-template <int BN> constexpr int kStageBytes = kATile + BN * kBK * 2;
-
-template <int BN>
-__device__ __forceinline__ void load_stage(const GemmArgs& g, unsigned char* stage, uint64_t* bar, int mt, int nt, int kb)
-{
-    mbar_expect(bar, kStageBytes<BN>);
-    unsigned char* sb = stage + kATile;
-    if (g.a_mn) {
-#pragma unroll
-        for (int i = 0; i < kBM / 64; ++i) tma_load(stage + i * 8192, &g.a, mt * kBM + i * 64, kb * kBK, bar);
-    } else {
-        tma_load(stage, &g.a, kb * kBK, mt * kBM, bar);
-    }
-    if (g.b_mn) {
-#pragma unroll
-        for (int i = 0; i < (BN + 63) / 64; ++i) tma_load(sb + i * 8192, &g.b, nt * BN + i * 64, kb * kBK, bar);
-    } else {
-        tma_load(sb, &g.b, kb * kBK, nt * BN, bar);
-    }
-}
-
-// The four products of a stage (16 contraction elements each).
-__device__ __forceinline__ void mma_stage(const GemmArgs& g, const unsigned char* stage, uint32_t d, bool first)
-{
-    const uint64_t a = tile_desc(stage, g.a_mn), b = tile_desc(stage + kATile, g.b_mn);
-    const uint64_t da = g.a_mn ? 2048 >> 4 : 32 >> 4, db = g.b_mn ? 2048 >> 4 : 32 >> 4;
-#pragma unroll
-    for (int k = 0; k < kBK / 16; ++k) mma(d, a + k * da, b + k * db, g.idesc, !(first && k == 0));
-}
-
 __device__ __forceinline__ unsigned char* aligned_smem(unsigned char* p)
 {
     return p + ((1024 - (smem_addr(p) & 1023)) & 1023);
 }
 
-// Tile t of the persistent order: columns of 16 m-tiles, so that the CTAs
-// that run together share both operands in L2.
-__device__ __forceinline__ void tile_at(const GemmArgs& g, int t, int* mt, int* nt)
+// Tile t of a product: columns of kGroup m-tiles, so that the CTAs that run
+// together share both operands in L2.
+__device__ __forceinline__ void tile_at(const Problem& g, int t, int* mt, int* nt)
 {
     constexpr int kGroup = 16;
     const int per = kGroup * g.tiles_n, group = t / per, in = t - group * per;
@@ -427,12 +453,30 @@ __device__ __forceinline__ void tile_at(const GemmArgs& g, int t, int* mt, int* 
     *mt = group * kGroup + in - *nt * rows;
 }
 
+// The bias gradient's last sum, by warp 3 of every CTA.
+__device__ __forceinline__ void bias_sum(const GemmArgs& args, int lane)
+{
+    for (int c = blockIdx.x * 32 + lane; c < args.n_db; c += gridDim.x * 32) {
+        float s = 0.0f;
+#pragma unroll 8
+        for (int k = 0; k < args.chunks; ++k) s += args.sums[static_cast<long long>(k) * args.n_db + c];
+        store16(args.db, c, s, args.bf16);
+    }
+}
+
 // ---------------------------------------------------------------------------
-// Many tiles: persistent CTAs
+// Many tiles: persistent pairs of CTAs
 // ---------------------------------------------------------------------------
 
+// A pair's tile is 256 x BN: CTA r of the pair loads rows [128 r, 128 r + 128)
+// of A and columns [BN/2 r, BN/2 r + BN/2) of B, and its tensor memory holds
+// its 128 rows of the result.  The even CTA issues the products for both.
+template <int BN> constexpr int kPairStage = kATile + BN / 2 * kBK * 2;
+constexpr int kStagePitch = 36; // floats of a staged row of 32: 16-byte accesses free of bank conflicts both ways
+constexpr int kEpilogueBytes = 4 * 32 * kStagePitch * 4;
+
 template <int BN, int STAGES>
-__global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_kernel(const __grid_constant__ GemmArgs g)
+__global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_pair_kernel(const __grid_constant__ GemmArgs args)
 {
     extern __shared__ unsigned char raw[];
     unsigned char* smem = aligned_smem(raw);
@@ -440,7 +484,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_kernel(const __grid
     __shared__ uint32_t tmem;
     __shared__ int abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int tiles = g.tiles_m * g.tiles_n;
+    const int rank = static_cast<int>(cluster_rank());
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], 1);
@@ -448,95 +493,164 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_kernel(const __grid
         }
         for (int k = 0; k < 2; ++k) {
             mbar_init(&acc_full[k], 1);
-            mbar_init(&acc_empty[k], 4);
+            mbar_init(&acc_empty[k], 8); // the epilogue warps of both CTAs
         }
         mbar_init(&drained, 1);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async;" ::: "memory");
     }
-    if (warp == 2) tmem_alloc(&tmem, 2 * BN);
+    if (warp == 2) tmem_alloc_pair(&tmem, 2 * BN);
     fence_before();
     __syncthreads();
+    cluster_sync(); // the barriers are set up in both CTAs
     fence_after();
     const uint32_t base = tmem;
     volatile int* abort = &abort_flag;
+    let_successor_start();
+    wait_for_predecessor();
 
     if (warp == 0 && lane == 0) {
         int it = 0;
         bool ok = true;
-        for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+        for (int t = pair; ok && t < args.tiles; t += pairs) {
+            const Problem& g = args.p[t >= args.tiles0];
             int mt, nt;
-            tile_at(g, t, &mt, &nt);
+            tile_at(g, t >= args.tiles0 ? t - args.tiles0 : t, &mt, &nt);
+            const int m0 = mt * 256 + rank * kBM, n0 = nt * BN + rank * (BN / 2);
             for (int kb = 0; kb < g.kblocks; ++kb, ++it) {
                 const int s = it % STAGES;
                 if (!wait(&empty[s], ((it / STAGES) & 1) ^ 1, abort)) {
                     ok = false;
                     break;
                 }
-                load_stage<BN>(g, smem + s * kStageBytes<BN>, &full[s], mt, nt, kb);
+                // both CTAs' copies count on the even CTA's barrier
+                const uint32_t bar = peer_addr(smem_addr(&full[s]), 0);
+                if (rank == 0) mbar_expect(&full[s], 2 * kPairStage<BN>);
+                unsigned char* sa = smem + s * kPairStage<BN>;
+                unsigned char* sb = sa + kATile;
+                if (g.a_mn) {
+                    tma_load_pair(sa, &g.a, m0, kb * kBK, bar);
+                    tma_load_pair(sa + 8192, &g.a, m0 + 64, kb * kBK, bar);
+                } else {
+                    tma_load_pair(sa, &g.a, kb * kBK, m0, bar);
+                }
+                if (g.b_mn) {
+#pragma unroll
+                    for (int i = 0; i < BN / 128; ++i) tma_load_pair(sb + i * 8192, &g.b, n0 + i * 64, kb * kBK, bar);
+                } else {
+                    tma_load_pair(sb, &g.b, kb * kBK, n0, bar);
+                }
             }
         }
-        // after a wait that ran out, the copies in flight land before the CTA ends
-        if (!ok) {
+        // after a wait that ran out, the copies in flight land before the CTAs end
+        if (!ok && rank == 0)
             for (int k = max(0, it - STAGES); k < it; ++k) wait_landed(&full[k % STAGES], (k / STAGES) & 1);
-        }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1 && lane == 0 && rank == 0) {
         int it = 0, n = 0;
         bool ok = true;
-        for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++n) {
-            const int acc = n & 1;
+        for (int t = pair; ok && t < args.tiles; t += pairs, ++n) {
+            const Problem& g = args.p[t >= args.tiles0];
+            const int acc = n & 1, kblocks = g.kblocks;
+            const uint64_t da = g.a_mn ? 2048 >> 4 : 32 >> 4, db = g.b_mn ? 2048 >> 4 : 32 >> 4;
+            const uint64_t a0 = tile_desc(smem, g.a_mn), b0 = tile_desc(smem + kATile, g.b_mn);
+            const uint32_t d = base + acc * BN, idesc = g.idesc;
             ok = wait(&acc_empty[acc], ((n >> 1) & 1) ^ 1, abort);
             fence_after();
-            for (int kb = 0; ok && kb < g.kblocks; ++kb, ++it) {
+            for (int kb = 0; ok && kb < kblocks; ++kb, ++it) {
                 const int s = it % STAGES;
                 if (!wait(&full[s], (it / STAGES) & 1, abort)) {
                     ok = false;
                     break;
                 }
                 fence_after();
-                mma_stage(g, smem + s * kStageBytes<BN>, base + acc * BN, kb == 0);
-                mma_commit(&empty[s]);
+                const uint64_t off = static_cast<uint64_t>(s) * (kPairStage<BN> >> 4);
+#pragma unroll
+                for (int k = 0; k < kBK / 16; ++k) mma_pair(d, a0 + off + k * da, b0 + off + k * db, idesc, (kb | k) != 0);
+                mma_commit_pair(&empty[s]);
             }
-            if (ok) mma_commit(&acc_full[acc]);
+            if (ok) mma_commit_pair(&acc_full[acc]);
         }
         if (!ok) { // products in flight end before the tensor memory goes
-            mma_commit(&drained);
+            mma_commit_pair(&drained);
             wait_landed(&drained, 0);
         }
+    } else if (warp == 3) {
+        bias_sum(args, lane);
     } else if (warp >= 4) {
         const int q = warp & 3;
+        float* stage = reinterpret_cast<float*>(smem + STAGES * kPairStage<BN>) + q * 32 * kStagePitch;
         int n = 0;
-        for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++n) {
+        for (int t = pair; t < args.tiles; t += pairs, ++n) {
+            const Problem& g = args.p[t >= args.tiles0];
             int mt, nt;
-            tile_at(g, t, &mt, &nt);
+            tile_at(g, t >= args.tiles0 ? t - args.tiles0 : t, &mt, &nt);
             const int acc = n & 1;
-            bool ok = wait(&acc_full[acc], (n >> 1) & 1, abort);
+            const bool ok = wait(&acc_full[acc], (n >> 1) & 1, abort);
             if (!__all_sync(0xffffffffu, ok)) break;
             fence_after();
-            const int row = mt * kBM + q * 32 + lane;
+            const int row0 = mt * 256 + rank * kBM + q * 32;
+            const Out& o = g.o;
+            const int rows = g.m - row0; // of this warp's 32 that exist; may be 0 or less
 #pragma unroll 1
             for (int c = 0; c < BN; c += 32) {
+                const int col0 = nt * BN + c;
                 float v[32];
                 tmem_load(base + acc * BN + c + (static_cast<uint32_t>(q * 32) << 16), v);
-                if (row < g.m && nt * BN + c < g.n) emit32(g.o, row, nt * BN + c, v);
+                if (c + 32 == BN) { // the accumulator is read: the next tile but one may have it
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_at(peer_addr(smem_addr(&acc_empty[acc]), 0));
+                }
+                if (rows <= 0 || col0 >= g.n) continue;
+                // through shared memory, so that lanes run along the output's rows
+                float* mine = stage + lane * kStagePitch;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    *reinterpret_cast<float4*>(mine + 4 * j) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                __syncwarp();
+                if (o.vec && col0 + 32 <= g.n) {
+                    const int r = lane >> 2, cc = (lane & 3) * 8;
+                    uint4 res[4] = {};
+                    if (o.res) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (k * 8 + r < rows) res[k] = load_res8(o, row0 + k * 8 + r, col0 + cc);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (k * 8 + r >= rows) continue;
+                        const float4* p = reinterpret_cast<const float4*>(stage + (k * 8 + r) * kStagePitch + cc);
+                        const float4 lo = p[0], hi = p[1];
+                        float w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                        emit8(o, row0 + k * 8 + r, col0 + cc, w, res[k]);
+                    }
+                } else {
+                    const int most = min(32, rows);
+                    if (col0 + lane < g.n) {
+#pragma unroll 4
+                        for (int r = 0; r < most; ++r) emit(o, row0 + r, col0 + lane, stage[r * kStagePitch + lane]);
+                    }
+                }
+                __syncwarp();
             }
-            fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[acc]);
         }
     }
     __syncthreads();
+    __syncwarp();
+    cluster_sync(); // neither CTA's memory is in use by the other any more
     fence_after();
-    if (warp == 2) tmem_free(base, 2 * BN);
+    if (warp == 2) tmem_free_pair(base, 2 * BN);
 }
 
 // ---------------------------------------------------------------------------
 // Few tiles: the contraction cut over a cluster
 // ---------------------------------------------------------------------------
 
+template <int BN> constexpr int kStageBytes = kATile + BN * kBK * 2;
+
 template <int BN, int STAGES>
-__global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_split_kernel(const __grid_constant__ GemmArgs g)
+__global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_split_kernel(const __grid_constant__ GemmArgs args)
 {
     extern __shared__ unsigned char raw[];
     unsigned char* smem = aligned_smem(raw);
@@ -544,14 +658,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_split_kernel(const 
     __shared__ uint32_t tmem;
     __shared__ int abort_flag;
     constexpr uint32_t kCols = BN < 32 ? 32 : BN;
-    constexpr int kPitch = kBM + 1; // odd: rows and columns of the partial tile are both free of bank conflicts
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_rank()), size = static_cast<int>(cluster_size());
     const int t = blockIdx.x / size;
+    const Problem& g = args.p[t >= args.tiles0];
     int mt, nt;
-    tile_at(g, t, &mt, &nt);
-    const int kb0 = static_cast<int>(static_cast<long long>(g.kblocks) * rank / size);
-    const int kb1 = static_cast<int>(static_cast<long long>(g.kblocks) * (rank + 1) / size);
+    tile_at(g, t >= args.tiles0 ? t - args.tiles0 : t, &mt, &nt);
+    const int parts = min(size, g.kblocks); // CTAs that have a part of the contraction
+    const int kb0 = static_cast<int>(static_cast<long long>(g.kblocks) * min(rank, parts) / parts);
+    const int kb1 = static_cast<int>(static_cast<long long>(g.kblocks) * min(rank + 1, parts) / parts);
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], 1);
@@ -569,6 +684,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_split_kernel(const 
     fence_after();
     const uint32_t base = tmem;
     volatile int* abort = &abort_flag;
+    let_successor_start();
+    wait_for_predecessor();
 
     if (warp == 0 && lane == 0) {
         int it = 0;
@@ -579,14 +696,29 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_split_kernel(const 
                 ok = false;
                 break;
             }
-            load_stage<BN>(g, smem + s * kStageBytes<BN>, &full[s], mt, nt, kb);
+            mbar_expect(&full[s], kStageBytes<BN>);
+            unsigned char* sa = smem + s * kStageBytes<BN>;
+            unsigned char* sb = sa + kATile;
+            if (g.a_mn) {
+                tma_load(sa, &g.a, mt * kBM, kb * kBK, &full[s]);
+                tma_load(sa + 8192, &g.a, mt * kBM + 64, kb * kBK, &full[s]);
+            } else {
+                tma_load(sa, &g.a, kb * kBK, mt * kBM, &full[s]);
+            }
+            if (BN >= 64 && g.b_mn) {
+#pragma unroll
+                for (int i = 0; i < BN / 64; ++i) tma_load(sb + i * 8192, &g.b, nt * BN + i * 64, kb * kBK, &full[s]);
+            } else {
+                tma_load(sb, &g.b, kb * kBK, nt * BN, &full[s]);
+            }
         }
-        if (!ok) {
+        if (!ok)
             for (int k = max(0, it - STAGES); k < it; ++k) wait_landed(&full[k % STAGES], (k / STAGES) & 1);
-        }
     } else if (warp == 1 && lane == 0) {
         int it = 0;
         bool ok = true;
+        const uint64_t da = g.a_mn ? 2048 >> 4 : 32 >> 4, db = g.b_mn ? 2048 >> 4 : 32 >> 4;
+        const uint64_t a0 = tile_desc(smem, g.a_mn), b0 = tile_desc(smem + kATile, g.b_mn);
         for (int kb = kb0; kb < kb1; ++kb, ++it) {
             const int s = it % STAGES;
             if (!wait(&full[s], (it / STAGES) & 1, abort)) {
@@ -594,39 +726,46 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_split_kernel(const 
                 break;
             }
             fence_after();
-            mma_stage(g, smem + s * kStageBytes<BN>, base, kb == kb0);
+            const uint64_t off = static_cast<uint64_t>(s) * (kStageBytes<BN> >> 4);
+#pragma unroll
+            for (int k = 0; k < kBK / 16; ++k) mma(base, a0 + off + k * da, b0 + off + k * db, g.idesc, kb > kb0 || k > 0);
             mma_commit(&empty[s]);
         }
         if (ok) {
-            mma_commit(&acc_full);
+            if (kb1 > kb0) mma_commit(&acc_full);
         } else {
             mma_commit(&drained);
             wait_landed(&drained, 0);
         }
+    } else if (warp == 3) {
+        bias_sum(args, lane);
     }
     __syncwarp();
     // The stages are free once the last product is done: the partial tile goes
-    // there, column by column.
+    // there with the output's contiguous index innermost.
+    const Out& o = g.o;
     float* part = reinterpret_cast<float*>(smem);
-    if (warp >= 4) {
+    const int pitch = (o.swap ? kBM : BN) + 4; // floats; 16-byte accesses free of bank conflicts
+    if (warp >= 4 && kb1 > kb0) {
         const int q = warp & 3;
         const bool ok = wait(&acc_full, 0, abort);
         if (__all_sync(0xffffffffu, ok)) {
             fence_after();
             const int row = q * 32 + lane;
             const uint32_t at = base + (static_cast<uint32_t>(q * 32) << 16);
-            if constexpr (BN == 16) {
-                float v[16];
-                tmem_load16(at, v);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) part[j * kPitch + row] = v[j];
-            } else {
+            constexpr int kStep = BN < 32 ? 16 : 32;
 #pragma unroll 1
-                for (int c = 0; c < BN; c += 32) {
-                    float v[32];
-                    tmem_load(at + c, v);
+            for (int c = 0; c < BN; c += kStep) {
+                float v[kStep];
+                if constexpr (kStep == 16) tmem_load16(at, v);
+                else tmem_load(at + c, v);
+                if (o.swap) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) part[(c + j) * kPitch + row] = v[j];
+                    for (int j = 0; j < kStep; ++j) part[(c + j) * pitch + row] = v[j];
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kStep; j += 4)
+                        *reinterpret_cast<float4*>(part + row * pitch + c + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
                 }
             }
             fence_before();
@@ -637,17 +776,65 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_split_kernel(const 
     // Each CTA finishes a share of the tile: the partial sums of the cluster
     // are added in rank order.
     const int rows = min(kBM, g.m - mt * kBM), cols = min(BN, g.n - nt * BN);
+    const int fast = o.swap ? rows : cols, slow = o.swap ? cols : rows; // extents along and across the output's rows
+    const long long row0 = o.swap ? nt * BN : mt * kBM;
+    const int col0 = o.swap ? mt * kBM : nt * BN;
     const uint32_t part_at = smem_addr(part);
-    const int fast = g.o.swap ? rows : cols, total = rows * cols; // the output's contiguous index runs over lanes
-    for (int e = rank * kGemmThreads + static_cast<int>(threadIdx.x); e < total; e += size * kGemmThreads) {
-        const int hi = e / fast, lo = e - hi * fast;
-        const int r = g.o.swap ? lo : hi, c = g.o.swap ? hi : lo;
-        const uint32_t at = part_at + static_cast<uint32_t>(c * kPitch + r) * 4;
-        float v = 0.0f;
-        for (int k = 0; k < size; ++k) v += peer_load(at, static_cast<uint32_t>(k));
-        const int gr = mt * kBM + r, gc = nt * BN + c;
-        if (g.o.swap) emit(g.o, gc, gr, v);
-        else emit(g.o, gr, gc, v);
+    const int self = rank * kGemmThreads + static_cast<int>(threadIdx.x), everyone = size * kGemmThreads;
+    const int vecs = o.vec ? fast / 8 : 0; // whole vectors of 8 of a row; the rest goes element by element
+    if (vecs) {
+        const int total = vecs * slow;
+        constexpr int kAhead = 2;
+        for (int e = self; e < total; e += everyone * kAhead) {
+            float v[kAhead][8];
+            int s_[kAhead], f_[kAhead];
+            uint4 res[kAhead] = {};
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int i = min(e + k * everyone, total - 1);
+                s_[k] = i / vecs;
+                f_[k] = (i - s_[k] * vecs) * 8;
+                if (o.res) res[k] = load_res8(o, row0 + s_[k], col0 + f_[k]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[k][j] = 0.0f;
+            }
+#pragma unroll 2
+            for (int p = 0; p < parts; ++p)
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const uint32_t at = part_at + static_cast<uint32_t>(s_[k] * pitch + f_[k]) * 4;
+                    const float4 lo = peer_load4(at, static_cast<uint32_t>(p)), hi = peer_load4(at + 16, static_cast<uint32_t>(p));
+                    v[k][0] += lo.x, v[k][1] += lo.y, v[k][2] += lo.z, v[k][3] += lo.w;
+                    v[k][4] += hi.x, v[k][5] += hi.y, v[k][6] += hi.z, v[k][7] += hi.w;
+                }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (e + k * everyone < total) emit8(o, row0 + s_[k], col0 + f_[k], v[k], res[k]);
+        }
+    }
+    const int left = fast - vecs * 8;
+    if (left) {
+        const int total = left * slow;
+        constexpr int kAhead = 4;
+        for (int e = self; e < total; e += everyone * kAhead) {
+            float v[kAhead];
+            int s_[kAhead], f_[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int i = min(e + k * everyone, total - 1);
+                s_[k] = i / left;
+                f_[k] = i - s_[k] * left + vecs * 8;
+                v[k] = 0.0f;
+            }
+#pragma unroll 2
+            for (int p = 0; p < parts; ++p)
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k)
+                    v[k] += peer_load(part_at + static_cast<uint32_t>(s_[k] * pitch + f_[k]) * 4, static_cast<uint32_t>(p));
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (e + k * everyone < total) emit(o, row0 + s_[k], col0 + f_[k], v[k]);
+        }
     }
     cluster_sync(); // peers have read this CTA's part
     fence_after();
@@ -660,58 +847,109 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_split_kernel(const 
 
 constexpr int kSumCols = 256; // columns of a CTA: 32 lanes of 8
 
-// Rows [chunk * rows_per, ...) of 256 columns: dz (where asked for) and the
-// fp32 sum of each column over these rows.
-__global__ void __launch_bounds__(256) zero_act_grad_kernel(const void* dy, long long lddy, const void* z, long long ldz,
-                                                            void* dz, long long lddz, float* sums, long long T, int N,
-                                                            int rows_per, int act, int bf16, int vec)
+// A matrix whose rows do not start on 16 bytes, laid out so that they do (a
+// tensor map needs it).
+struct Copy {
+    const uint16_t* src;
+    uint16_t* dst;
+    long long lds, ldd, rows;
+    int cols, ctas;
+};
+
+// What has to be done before the products: dz and its column sums over
+// chunks of rows (`stripes` x `chunks` CTAs), and up to three copies.
+struct PrepArgs {
+    const void* dy;
+    const void* z;
+    void* dz;            // null: dz is dy
+    float* sums;         // null: no bias gradient
+    long long lddy, ldz, lddz, T;
+    int N, rows_per, act, bf16, vec;
+    int stripes, chunks;
+    Copy copy[3];
+};
+
+__device__ __forceinline__ void copy_rows(const Copy& c, int cta)
 {
+    const int vecs = (c.cols + 7) / 8;
+    const long long total = c.rows * vecs;
+    for (long long i = cta * 256ll + threadIdx.x; i < total; i += c.ctas * 256ll) {
+        const long long r = i / vecs;
+        const int at = static_cast<int>(i - r * vecs) * 8;
+        const uint16_t* p = c.src + r * c.lds + at;
+        uint32_t h[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[j] = at + j < c.cols ? __ldg(p + j) : 0;
+        *reinterpret_cast<uint4*>(c.dst + r * c.ldd + at) =
+            make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+    }
+}
+
+__global__ void __launch_bounds__(256) zero_linear_prep_kernel(const __grid_constant__ PrepArgs a)
+{
+    let_successor_start();
+    wait_for_predecessor();
+    int cta = blockIdx.x - a.stripes * a.chunks;
+    if (cta >= 0) {
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            if (cta >= 0 && cta < a.copy[k].ctas) copy_rows(a.copy[k], cta);
+            cta -= a.copy[k].ctas;
+        }
+        return;
+    }
+    const int stripe = blockIdx.x % a.stripes, chunk = blockIdx.x / a.stripes;
     const int lane = threadIdx.x & 31, line = threadIdx.x >> 5;
-    const int col = blockIdx.x * kSumCols + lane * 8;
-    const long long r0 = static_cast<long long>(blockIdx.y) * rows_per, r1 = min(T, r0 + rows_per);
+    const int col = stripe * kSumCols + lane * 8;
+    const long long r0 = static_cast<long long>(chunk) * a.rows_per, r1 = min(a.T, r0 + a.rows_per);
+    const uint16_t* dy = static_cast<const uint16_t*>(a.dy);
+    const uint16_t* z = static_cast<const uint16_t*>(a.z);
+    uint16_t* dz = static_cast<uint16_t*>(a.dz);
+    const int act = a.act, bf16 = a.bf16;
     float sum[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
-    if (vec && col + 8 <= N) {
+    if (a.vec && col + 8 <= a.N) {
 #pragma unroll 4
         for (long long r = r0 + line; r < r1; r += 8) {
-            const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(dy) + r * lddy + col);
+            const uint4 u = *reinterpret_cast<const uint4*>(dy + r * a.lddy + col);
             uint32_t g[4] = {u.x, u.y, u.z, u.w};
+            uint32_t h[4] = {};
             if (act != ZERO_ACT_NONE) {
-                const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(z) + r * ldz + col);
-                const uint32_t h[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 d = unpack16(g[j], bf16), p = unpack16(h[j], bf16);
-                    const float a = d.x * slope(p.x, act), b = d.y * slope(p.y, act);
-                    sum[2 * j] += a;
-                    sum[2 * j + 1] += b;
-                    g[j] = pack16(a, b, bf16);
-                }
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(dz) + r * lddz + col) = make_uint4(g[0], g[1], g[2], g[3]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 d = unpack16(g[j], bf16);
-                    sum[2 * j] += d.x;
-                    sum[2 * j + 1] += d.y;
-                }
+                const uint4 w = *reinterpret_cast<const uint4*>(z + r * a.ldz + col);
+                h[0] = w.x, h[1] = w.y, h[2] = w.z, h[3] = w.w;
             }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float2 d = unpack16(g[j], bf16);
+                if (act != ZERO_ACT_NONE) {
+                    const float2 p = unpack16(h[j], bf16);
+                    d.x *= slope(p.x, act);
+                    d.y *= slope(p.y, act);
+                }
+                sum[2 * j] += d.x;
+                sum[2 * j + 1] += d.y;
+                g[j] = pack16(d.x, d.y, bf16);
+            }
+            if (dz) *reinterpret_cast<uint4*>(dz + r * a.lddz + col) = make_uint4(g[0], g[1], g[2], g[3]);
         }
     } else {
-        for (long long r = r0 + line; r < r1; r += 8)
+        for (long long r = r0 + line; r < r1; r += 8) {
+            float d[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                if (col + j >= N) continue;
-                float d = load16(dy, r * lddy + col + j, bf16);
-                if (act != ZERO_ACT_NONE) {
-                    d *= slope(load16(z, r * ldz + col + j, bf16), act);
-                    store16(dz, r * lddz + col + j, d, bf16);
+                d[j] = 0.0f;
+                if (col + j < a.N) {
+                    d[j] = load16(dy, r * a.lddy + col + j, bf16);
+                    if (act != ZERO_ACT_NONE) d[j] *= slope(load16(z, r * a.ldz + col + j, bf16), act);
                 }
-                sum[j] += d;
+                sum[j] += d[j];
             }
+            // rows of dz have room for whole vectors
+            if (dz && col < a.N) *reinterpret_cast<uint4*>(dz + r * a.lddz + col) = pack8(d, bf16);
+        }
     }
-    if (!sums) return;
+    if (!a.sums) return;
     __shared__ float part[8][kSumCols];
 #pragma unroll
     for (int j = 0; j < 8; ++j) part[line][lane * 8 + j] = sum[j];
@@ -719,26 +957,15 @@ __global__ void __launch_bounds__(256) zero_act_grad_kernel(const void* dy, long
     float s = 0.0f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) s += part[k][threadIdx.x];
-    const int c = blockIdx.x * kSumCols + threadIdx.x;
-    if (c < N) sums[static_cast<long long>(blockIdx.y) * N + c] = s;
+    const int c = stripe * kSumCols + threadIdx.x;
+    if (c < a.N) a.sums[static_cast<long long>(chunk) * a.N + c] = s;
 }
 
-__global__ void __launch_bounds__(256) zero_bias_grad_kernel(const float* sums, int chunks, int N, void* db, int bf16)
+// The bias gradient's last sum where no product follows to take it along.
+__global__ void __launch_bounds__(32) zero_bias_grad_kernel(const __grid_constant__ GemmArgs args)
 {
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= N) return;
-    float s = 0.0f;
-    for (int k = 0; k < chunks; ++k) s += sums[static_cast<long long>(k) * N + c];
-    store16(db, c, s, bf16);
-}
-
-// Rows that do not start on 16 bytes, laid out so that they do (a tensor map
-// needs it).
-__global__ void __launch_bounds__(256) zero_align_rows_kernel(const uint16_t* src, long long lds, uint16_t* dst,
-                                                              long long ldd, long long rows, int cols)
-{
-    for (long long r = blockIdx.y; r < rows; r += gridDim.y)
-        for (int c = blockIdx.x * 256 + threadIdx.x; c < cols; c += gridDim.x * 256) dst[r * ldd + c] = src[r * lds + c];
+    wait_for_predecessor();
+    bias_sum(args, threadIdx.x);
 }
 
 // ---------------------------------------------------------------------------
@@ -800,7 +1027,7 @@ int sm_count(int* out)
 using GemmKernel = void (*)(GemmArgs);
 
 // Dynamic shared memory above 48 KB is allowed once per kernel and device.
-int allow_smem(GemmKernel fn, int bytes, int cluster)
+int allow_smem(GemmKernel fn, int bytes)
 {
     static std::mutex mu;
     static struct { int dev; GemmKernel fn; } known[64];
@@ -812,95 +1039,155 @@ int allow_smem(GemmKernel fn, int bytes, int cluster)
     for (int k = 0; k < n_known; ++k)
         if (known[k].dev == dev && known[k].fn == fn) return ZERO_OK;
     e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess && cluster) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return record(e);
     if (n_known < 64) known[n_known++] = {dev, fn};
     return ZERO_OK;
 }
 
-template <int BN> constexpr int kSplitStages = BN >= 256 ? 4 : BN >= 128 ? 6 : 8;
+template <int BN> constexpr int kSplitStages = BN >= 128 ? 6 : 8;
 template <int BN> constexpr int kSplitSmem = kSplitStages<BN> * kStageBytes<BN> + 1024;
+template <int BN> constexpr int kPairStages = BN >= 256 ? 6 : 8;
+template <int BN> constexpr int kPairSmem = kPairStages<BN> * kPairStage<BN> + kEpilogueBytes + 1024;
 
-struct Choice {
-    GemmKernel fn;
-    int bn, smem;
+// A product to be launched: D[m, n] = sum_k A[m, k] B[n, k].
+struct Product {
+    Matrix a, b;
+    int a_mn, b_mn;
+    int64_t m, n, k;
+    Out o;
 };
 
-Choice pick_split(int bn)
+Product product(const Matrix& a, int a_mn, const Matrix& b, int b_mn, const Out& o)
 {
-    switch (bn) {
-    case 16: return {zero_gemm_split_kernel<16, kSplitStages<16>>, 16, kSplitSmem<16>};
-    case 32: return {zero_gemm_split_kernel<32, kSplitStages<32>>, 32, kSplitSmem<32>};
-    case 64: return {zero_gemm_split_kernel<64, kSplitStages<64>>, 64, kSplitSmem<64>};
-    default: return {zero_gemm_split_kernel<128, kSplitStages<128>>, 128, kSplitSmem<128>};
-    }
+    return {a, b, a_mn, b_mn, a_mn ? a.cols : a.rows, b_mn ? b.cols : b.rows, a_mn ? a.rows : a.cols, o};
 }
 
-// D[m, n] = sum_k A B with A = a (or its transpose, a_mn) and B likewise.
-// Extents are below 2^31 - 256 (checked by the callers).
-int gemm(const Matrix& a, int a_mn, const Matrix& b, int b_mn, int64_t k, Out o, int type, cudaStream_t stream)
+// Which kernel takes a launch, with what tile.
+struct Variant {
+    bool pair;
+    int bn, parts; // columns of a tile; CTAs that share a contraction
+};
+
+struct BiasSum {
+    const float* sums;
+    void* db;
+    int chunks, n;
+};
+
+template <class Kernel, class Args>
+int launch_after(Kernel fn, const Args& args, int64_t ctas, int threads, int smem, int cluster, cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned int>(ctas));
+    cfg.blockDim = dim3(static_cast<unsigned int>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[2] = {};
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = static_cast<unsigned int>(cluster);
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return record(cudaLaunchKernelEx(&cfg, fn, args));
+}
+
+int64_t tiles_of(const Product& p, const Variant& v)
+{
+    const int64_t bm = v.pair ? 256 : kBM;
+    return ((p.m + bm - 1) / bm) * ((p.n + v.bn - 1) / v.bn);
+}
+
+int64_t kblocks_of(const Product& p) { return (p.k + kBK - 1) / kBK; }
+
+Variant choose(const Product* p, int count, int sms)
+{
+    if (count == 1 && p[0].o.swap) { // few tokens: no more columns than that
+        Variant v{false, 128, 1};
+        while (v.bn > 16 && p[0].n <= v.bn / 2) v.bn /= 2;
+        const int64_t tiles = tiles_of(p[0], v);
+        while (v.parts < 8 && tiles * v.parts * 2 <= sms && kblocks_of(p[0]) >= v.parts * 4) v.parts *= 2;
+        return v;
+    }
+    double best = 1e30;
+    Variant out{true, 256, 1};
+    auto consider = [&](Variant v, double per_block, double per_tile) {
+        int64_t ctas = 0;
+        double work = 0.0, longest = 0.0;
+        for (int k = 0; k < count; ++k) {
+            const double one = per_block * std::ceil(static_cast<double>(kblocks_of(p[k])) / v.parts) + per_tile;
+            const int64_t t = tiles_of(p[k], v);
+            ctas += t;
+            work += one * static_cast<double>(t);
+            longest = std::max(longest, one);
+        }
+        const double slots = v.pair ? sms / 2 : static_cast<double>(sms) / v.parts;
+        const double rounds = std::ceil(static_cast<double>(ctas) / std::floor(slots));
+        const double time = std::max(work / static_cast<double>(ctas) * rounds, longest);
+        if (time < best) best = time, out = v;
+    };
+    consider({true, 256, 1}, 0.36, 2.0);
+    for (int bn : {128, 64})
+        for (int parts = 1; parts <= 8; parts *= 2)
+            consider({false, bn, parts}, bn == 128 ? 0.24 : 0.18, 3.0 + (parts > 1 ? 1.0 : 0.0));
+    return out;
+}
+
+// One or two products in one launch, and the bias gradient's last sum.
+int gemm(const Product* p, int count, int type, const BiasSum* bias, cudaStream_t stream)
 {
     int sms = 0;
     int rc = sm_count(&sms);
     if (rc) return rc;
-    GemmArgs g{};
-    const int64_t m = a_mn ? a.cols : a.rows, n = b_mn ? b.cols : b.rows;
-    g.m = static_cast<int>(m);
-    g.n = static_cast<int>(n);
-    g.kblocks = static_cast<int>((k + kBK - 1) / kBK);
-    g.a_mn = a_mn;
-    g.b_mn = b_mn;
-    o.bf16 = type == ZERO_TYPE_BF16;
-    g.o = o;
-    g.tiles_m = static_cast<int>((m + kBM - 1) / kBM);
-
-    // Few tiles leave SMs without work: below one big tile per SM the tiles
-    // get smaller and the contraction is cut over a cluster.
-    const int64_t big = g.tiles_m * ((n + 255) / 256);
-    const bool split = big < sms;
-    int bn = 256, parts = 1;
-    if (split) {
-        bn = 128;
-        if (!b_mn)
-            while (bn > 16 && n <= bn / 2) bn /= 2;
-        else if (n <= 64) bn = 64;
-        const int64_t tiles = g.tiles_m * ((n + bn - 1) / bn);
-        while (parts < 8 && tiles * parts * 2 <= 2 * sms && g.kblocks >= parts * 4) parts *= 2;
-    }
-    g.tiles_n = static_cast<int>((n + bn - 1) / bn);
-    const int64_t tiles = static_cast<int64_t>(g.tiles_m) * g.tiles_n;
-    if (tiles * parts > INT32_MAX) return ZERO_EINVAL;
+    const Variant v = choose(p, count, sms);
+    GemmArgs args{};
+    int64_t tiles = 0;
     const unsigned int t = type == ZERO_TYPE_BF16 ? 1 : 0;
-    g.idesc = (1u << 4) | (t << 7) | (t << 10) | (static_cast<unsigned int>(a_mn) << 15) |
-              (static_cast<unsigned int>(b_mn) << 16) | (static_cast<unsigned int>(bn >> 3) << 17) | ((kBM >> 4) << 24);
-    rc = make_map(&g.a, a, a_mn ? 64 : kBM);
-    if (rc) return rc;
-    rc = make_map(&g.b, b, b_mn ? 64 : bn);
-    if (rc) return rc;
-
-    if (!split) {
-        constexpr int kStages = 4, kSmem = kStages * kStageBytes<256> + 1024;
-        GemmKernel fn = zero_gemm_kernel<256, kStages>;
-        rc = allow_smem(fn, kSmem, 0);
-        if (rc) return rc;
-        fn<<<static_cast<unsigned int>(std::min<int64_t>(tiles, sms)), kGemmThreads, kSmem, stream>>>(g);
-        return record(cudaGetLastError());
+    for (int k = 0; k < count; ++k) {
+        Problem& g = args.p[k];
+        const int bm = v.pair ? 256 : kBM, b_box = v.pair ? v.bn / 2 : v.bn;
+        g.o = p[k].o;
+        g.o.bf16 = type == ZERO_TYPE_BF16;
+        g.a_mn = p[k].a_mn;
+        g.b_mn = p[k].b_mn;
+        g.m = static_cast<int>(p[k].m);
+        g.n = static_cast<int>(p[k].n);
+        g.tiles_m = static_cast<int>((p[k].m + bm - 1) / bm);
+        g.tiles_n = static_cast<int>((p[k].n + v.bn - 1) / v.bn);
+        g.kblocks = static_cast<int>(kblocks_of(p[k]));
+        g.idesc = (1u << 4) | (t << 7) | (t << 10) | (static_cast<unsigned int>(g.a_mn) << 15) |
+                  (static_cast<unsigned int>(g.b_mn) << 16) | (static_cast<unsigned int>(v.bn >> 3) << 17) |
+                  (static_cast<unsigned int>(bm >> 4) << 24);
+        if ((rc = make_map(&g.a, p[k].a, g.a_mn ? 64 : kBM))) return rc;
+        if ((rc = make_map(&g.b, p[k].b, g.b_mn ? 64 : b_box))) return rc;
+        tiles += tiles_of(p[k], v);
+        if (tiles * v.parts > INT32_MAX) return ZERO_EINVAL;
+        if (k == 0) args.tiles0 = static_cast<int>(tiles);
     }
-    const Choice c = pick_split(bn);
-    rc = allow_smem(c.fn, c.smem, 1);
-    if (rc) return rc;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned int>(tiles * parts));
-    cfg.blockDim = dim3(kGemmThreads);
-    cfg.dynamicSmemBytes = static_cast<size_t>(c.smem);
-    cfg.stream = stream;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = static_cast<unsigned int>(parts);
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return record(cudaLaunchKernelEx(&cfg, c.fn, g));
+    args.tiles = static_cast<int>(tiles);
+    if (bias) {
+        args.sums = bias->sums;
+        args.db = bias->db;
+        args.chunks = bias->chunks;
+        args.n_db = bias->n;
+        args.bf16 = type == ZERO_TYPE_BF16;
+    }
+    if (v.pair) {
+        GemmKernel fn = zero_gemm_pair_kernel<256, kPairStages<256>>;
+        if ((rc = allow_smem(fn, kPairSmem<256>))) return rc;
+        return launch_after(fn, args, 2 * std::min<int64_t>(tiles, sms / 2), kGemmThreads, kPairSmem<256>, 2, stream);
+    }
+    GemmKernel fn;
+    int smem;
+    switch (v.bn) {
+    case 16: fn = zero_gemm_split_kernel<16, kSplitStages<16>>, smem = kSplitSmem<16>; break;
+    case 32: fn = zero_gemm_split_kernel<32, kSplitStages<32>>, smem = kSplitSmem<32>; break;
+    case 64: fn = zero_gemm_split_kernel<64, kSplitStages<64>>, smem = kSplitSmem<64>; break;
+    default: fn = zero_gemm_split_kernel<128, kSplitStages<128>>, smem = kSplitSmem<128>; break;
+    }
+    if ((rc = allow_smem(fn, smem))) return rc;
+    return launch_after(fn, args, tiles * v.parts, kGemmThreads, smem, v.parts, stream);
 }
 
 bool aligned16(const void* p, int64_t ld) { return addr(p) % 16 == 0 && ld % 8 == 0; }
@@ -919,6 +1206,9 @@ bool share(const void* p, int64_t ldp, int64_t rp, int64_t cp, const void* q, in
     const uintptr_t d = addr(q) >= addr(p) ? (addr(q) - addr(p)) % pitch : (pitch - (addr(p) - addr(q)) % pitch) % pitch;
     return !(d >= static_cast<uintptr_t>(cp) * 2 && pitch - d >= static_cast<uintptr_t>(cq) * 2);
 }
+
+// Up to this many tokens a tile's rows are features (y) or inputs (dx), its columns tokens.
+constexpr int64_t kFewTokens = 128;
 
 constexpr int64_t kMostExtent = INT32_MAX - 512;
 constexpr int64_t kMostElements = int64_t{1} << 48; // of one matrix: far above any memory, so that no size overflows
@@ -962,16 +1252,21 @@ struct Carver {
 
 int64_t matrix_bytes(int64_t rows, int64_t cols) { return rows * up(cols, 8) * 2; }
 
-int align_rows(Matrix* x, void* to, cudaStream_t stream)
+// Adds the copy of x to rows on 16 bytes to a launch of the preparing kernel.
+void add_copy(PrepArgs* a, int* ctas, int slot, Matrix* x, void* to)
 {
-    const int64_t ld = up(x->cols, 8);
-    const dim3 grid(static_cast<unsigned int>(std::min<int64_t>(8, (x->cols + 255) / 256)),
-                    static_cast<unsigned int>(std::min<int64_t>(x->rows, 16384)));
-    zero_align_rows_kernel<<<grid, 256, 0, stream>>>(static_cast<const uint16_t*>(x->p), x->ld, static_cast<uint16_t*>(to), ld,
-                                                     x->rows, static_cast<int>(x->cols));
+    const int64_t ld = up(x->cols, 8), vecs = x->rows * (ld / 8);
+    Copy& c = a->copy[slot];
+    c.src = static_cast<const uint16_t*>(x->p);
+    c.dst = static_cast<uint16_t*>(to);
+    c.lds = x->ld;
+    c.ldd = ld;
+    c.rows = x->rows;
+    c.cols = static_cast<int>(x->cols);
+    c.ctas = static_cast<int>(std::min<int64_t>(1216, (vecs + 255) / 256));
+    *ctas += c.ctas;
     x->p = to;
     x->ld = ld;
-    return record(cudaGetLastError());
 }
 
 } // namespace
@@ -1025,18 +1320,17 @@ extern "C" int zero_linear_forward(const void* x, int64_t ldx, const void* w, in
         if (addr(workspace) % 16) return ZERO_EALIGN;
     }
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-    int rc = ZERO_OK;
-    if (fix_x && (rc = align_rows(&mx, tx, st))) return rc;
-    if (fix_w && (rc = align_rows(&mw, tw, st))) return rc;
+    int rc = ZERO_OK, ctas = 0;
+    PrepArgs prep{};
+    if (fix_x) add_copy(&prep, &ctas, 0, &mx, tx);
+    if (fix_w) add_copy(&prep, &ctas, 1, &mw, tw);
+    if (ctas && (rc = launch_after(zero_linear_prep_kernel, prep, ctas, 256, 0, 1, st))) return rc;
     Out o{};
-    o.y = y, o.ldy = ldy, o.z = z, o.ldz = ldz, o.bias = bias, o.res = residual, o.ldr = ldr;
-    o.rows = static_cast<int>(T), o.cols = static_cast<int>(N), o.act = act;
+    o.y = y, o.ldy = ldy, o.z = z, o.ldz = ldz, o.bias = bias, o.res = residual, o.ldr = ldr, o.act = act;
     o.vec = aligned16(y, ldy) && (!z || aligned16(z, ldz)) && (!residual || aligned16(residual, ldr)) && addr(bias) % 16 == 0;
-    if (T <= 128) {
-        o.swap = 1;
-        return gemm(mw, 0, mx, 0, K, o, type, st);
-    }
-    return gemm(mx, 0, mw, 0, K, o, type, st);
+    o.swap = T <= kFewTokens;
+    const Product p = o.swap ? product(mw, 0, mx, 0, o) : product(mx, 0, mw, 0, o);
+    return gemm(&p, 1, type, nullptr, st);
 }
 
 extern "C" int zero_linear_backward(const void* dy, int64_t lddy, const void* z, int64_t ldz, const void* x, int64_t ldx,
@@ -1076,11 +1370,11 @@ extern "C" int zero_linear_backward(const void* dy, int64_t lddy, const void* z,
 
     const bool has_act = act != ZERO_ACT_NONE, products = dx || dw;
     const bool fix_x = dw && !aligned16(x, ldx), fix_w = dx && !aligned16(w, ldw);
-    const bool fix_dy = products && !has_act && !aligned16(dy, lddy);
+    const bool make_dz = products && (has_act || !aligned16(dy, lddy));
     Carver c{static_cast<unsigned char*>(workspace)};
     void* tx = fix_x ? c.take(matrix_bytes(T, K)) : nullptr;
     void* tw = fix_w ? c.take(matrix_bytes(N, K)) : nullptr;
-    void* tz = has_act || fix_dy ? c.take(matrix_bytes(T, N)) : nullptr;
+    void* tz = make_dz ? c.take(matrix_bytes(T, N)) : nullptr;
     const int64_t chunks = sum_chunks(T, N);
     float* sums = db ? static_cast<float*>(c.take(chunks * N * 4)) : nullptr;
     if (c.used > 0) {
@@ -1088,42 +1382,50 @@ extern "C" int zero_linear_backward(const void* dy, int64_t lddy, const void* z,
         if (addr(workspace) % 16) return ZERO_EALIGN;
     }
     Matrix mx{x, ldx, T, K}, mw{w, ldw, N, K}, mz{dy, lddy, T, N};
-    int rc = ZERO_OK;
-    const int bf16 = type == ZERO_TYPE_BF16;
-    if (has_act || db) {
-        const int vec = aligned16(dy, lddy) && (!has_act || aligned16(z, ldz));
-        const int64_t ldt = up(N, 8);
-        const dim3 grid(static_cast<unsigned int>((N + kSumCols - 1) / kSumCols), static_cast<unsigned int>(chunks));
-        zero_act_grad_kernel<<<grid, 256, 0, st>>>(dy, lddy, z, ldz, has_act ? tz : nullptr, ldt, sums, T, static_cast<int>(N),
-                                                   sum_rows(T, N), act, bf16, vec);
-        if ((rc = record(cudaGetLastError()))) return rc;
-        if (has_act) mz = {tz, ldt, T, N};
-        if (db) {
-            zero_bias_grad_kernel<<<static_cast<unsigned int>((N + 255) / 256), 256, 0, st>>>(sums, static_cast<int>(chunks),
-                                                                                              static_cast<int>(N), db, bf16);
-            if ((rc = record(cudaGetLastError()))) return rc;
-        }
+    int rc = ZERO_OK, ctas = 0;
+    PrepArgs prep{};
+    if (make_dz || db) {
+        prep.dy = dy, prep.lddy = lddy, prep.z = z, prep.ldz = ldz, prep.dz = tz, prep.lddz = up(N, 8), prep.sums = sums;
+        prep.T = T, prep.N = static_cast<int>(N), prep.rows_per = sum_rows(T, N);
+        prep.act = act, prep.bf16 = type == ZERO_TYPE_BF16;
+        prep.vec = aligned16(dy, lddy) && (!has_act || aligned16(z, ldz));
+        prep.stripes = static_cast<int>((N + kSumCols - 1) / kSumCols);
+        prep.chunks = static_cast<int>(chunks);
+        if (chunks * prep.stripes > INT32_MAX - 4096) return ZERO_EINVAL;
+        ctas = prep.stripes * prep.chunks;
+        if (make_dz) mz = {tz, up(N, 8), T, N};
     }
-    if (fix_dy && (rc = align_rows(&mz, tz, st))) return rc;
-    if (fix_x && (rc = align_rows(&mx, tx, st))) return rc;
-    if (fix_w && (rc = align_rows(&mw, tw, st))) return rc;
+    if (fix_x) add_copy(&prep, &ctas, 0, &mx, tx);
+    if (fix_w) add_copy(&prep, &ctas, 1, &mw, tw);
+    if (ctas && (rc = launch_after(zero_linear_prep_kernel, prep, ctas, 256, 0, 1, st))) return rc;
+
+    const BiasSum bias{sums, db, static_cast<int>(chunks), static_cast<int>(N)};
+    if (!products) {
+        GemmArgs args{};
+        args.sums = sums, args.db = db, args.chunks = bias.chunks, args.n_db = bias.n, args.bf16 = type == ZERO_TYPE_BF16;
+        return launch_after(zero_bias_grad_kernel, args, (N + 31) / 32, 32, 0, 1, st);
+    }
+    Product p[2];
+    int count = 0;
+    bool few = false;
     if (dx) {
         Out o{};
-        o.y = dx, o.ldy = lddx, o.rows = static_cast<int>(T), o.cols = static_cast<int>(K), o.vec = aligned16(dx, lddx);
-        if (T <= 128) {
-            o.swap = 1;
-            rc = gemm(mw, 1, mz, 0, N, o, type, st);
-        } else {
-            rc = gemm(mz, 0, mw, 1, N, o, type, st);
-        }
-        if (rc) return rc;
+        o.y = dx, o.ldy = lddx, o.vec = aligned16(dx, lddx), o.swap = T <= kFewTokens;
+        few = o.swap;
+        p[count++] = o.swap ? product(mw, 1, mz, 0, o) : product(mz, 0, mw, 1, o);
     }
     if (dw) {
         Out o{};
-        o.y = dw, o.ldy = lddw, o.rows = static_cast<int>(N), o.cols = static_cast<int>(K), o.vec = aligned16(dw, lddw);
-        rc = gemm(mz, 1, mx, 1, T, o, type, st);
+        o.y = dw, o.ldy = lddw, o.vec = aligned16(dw, lddw);
+        p[count++] = product(mz, 1, mx, 1, o);
     }
-    return rc;
+    const BiasSum* with = db ? &bias : nullptr;
+    if (few && count == 2) { // the operands of dx change sides: another tile than dw's
+        if ((rc = gemm(p, 1, type, with, st))) return rc;
+        return gemm(p + 1, 1, type, nullptr, st);
+    }
+    if (count == 2 && kblocks_of(p[1]) > kblocks_of(p[0])) std::swap(p[0], p[1]); // the longer tiles first
+    return gemm(p, count, type, with, st);
 }
 
 extern "C" int zero_linear_timeouts(int64_t* count, int32_t reset)
