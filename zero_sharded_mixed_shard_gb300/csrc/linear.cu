@@ -33,6 +33,8 @@
 #include <cmath>
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
+#include <utility>
 
 #include "zero_train.h"
 
@@ -229,6 +231,20 @@ __device__ __forceinline__ void tmem_free_pair(uint32_t at, uint32_t columns)
 // memory and runs under the preceding kernel's end; the wait returns when that
 // kernel is complete and its writes are visible.
 __device__ __forceinline__ void wait_for_predecessor() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// One lane of a converged warp.  The copy and product instructions take
+// uniform registers: issued under this predicate the compiler knows that one
+// thread runs them, under `lane == 0` it does not and each of them costs
+// several hundred cycles (x [16384, 8192] W^T [2048]: 386 against 314 us).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\t"
+                 "elect.sync _|q, 0xffffffff;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(p));
+    return p != 0;
+}
+
 __device__ __forceinline__ void let_successor_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -446,7 +462,7 @@ __device__ __forceinline__ unsigned char* aligned_smem(unsigned char* p)
 // together share both operands in L2.
 __device__ __forceinline__ void tile_at(const Problem& g, int t, int* mt, int* nt)
 {
-    constexpr int kGroup = 16;
+    constexpr int kGroup = 8;
     const int per = kGroup * g.tiles_n, group = t / per, in = t - group * per;
     const int rows = min(kGroup, g.tiles_m - group * kGroup);
     *nt = in / rows;
@@ -475,7 +491,7 @@ template <int BN> constexpr int kPairStage = kATile + BN / 2 * kBK * 2;
 constexpr int kStagePitch = 36; // floats of a staged row of 32: 16-byte accesses free of bank conflicts both ways
 constexpr int kEpilogueBytes = 4 * 32 * kStagePitch * 4;
 
-template <int BN, int STAGES>
+template <int BN, int STAGES, int COUNT>
 __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_pair_kernel(const __grid_constant__ GemmArgs args)
 {
     extern __shared__ unsigned char raw[];
@@ -483,7 +499,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_pair_kernel(const _
     __shared__ uint64_t full[STAGES], empty[STAGES], acc_full[2], acc_empty[2], drained;
     __shared__ uint32_t tmem;
     __shared__ int abort_flag;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31; // warp: uniform
     const int rank = static_cast<int>(cluster_rank());
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     if (threadIdx.x == 0) {
@@ -510,13 +526,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_pair_kernel(const _
     let_successor_start();
     wait_for_predecessor();
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0 && elect_one()) {
         int it = 0;
         bool ok = true;
         for (int t = pair; ok && t < args.tiles; t += pairs) {
-            const Problem& g = args.p[t >= args.tiles0];
+            const Problem& g = args.p[COUNT == 1 ? 0 : t >= args.tiles0];
             int mt, nt;
-            tile_at(g, t >= args.tiles0 ? t - args.tiles0 : t, &mt, &nt);
+            tile_at(g, COUNT == 2 && t >= args.tiles0 ? t - args.tiles0 : t, &mt, &nt);
             const int m0 = mt * 256 + rank * kBM, n0 = nt * BN + rank * (BN / 2);
             for (int kb = 0; kb < g.kblocks; ++kb, ++it) {
                 const int s = it % STAGES;
@@ -546,11 +562,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_pair_kernel(const _
         // after a wait that ran out, the copies in flight land before the CTAs end
         if (!ok && rank == 0)
             for (int k = max(0, it - STAGES); k < it; ++k) wait_landed(&full[k % STAGES], (k / STAGES) & 1);
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0 && elect_one()) {
         int it = 0, n = 0;
         bool ok = true;
         for (int t = pair; ok && t < args.tiles; t += pairs, ++n) {
-            const Problem& g = args.p[t >= args.tiles0];
+            const Problem& g = args.p[COUNT == 1 ? 0 : t >= args.tiles0];
             const int acc = n & 1, kblocks = g.kblocks;
             const uint64_t da = g.a_mn ? 2048 >> 4 : 32 >> 4, db = g.b_mn ? 2048 >> 4 : 32 >> 4;
             const uint64_t a0 = tile_desc(smem, g.a_mn), b0 = tile_desc(smem + kATile, g.b_mn);
@@ -582,9 +598,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_pair_kernel(const _
         float* stage = reinterpret_cast<float*>(smem + STAGES * kPairStage<BN>) + q * 32 * kStagePitch;
         int n = 0;
         for (int t = pair; t < args.tiles; t += pairs, ++n) {
-            const Problem& g = args.p[t >= args.tiles0];
+            const Problem& g = args.p[COUNT == 1 ? 0 : t >= args.tiles0];
             int mt, nt;
-            tile_at(g, t >= args.tiles0 ? t - args.tiles0 : t, &mt, &nt);
+            tile_at(g, COUNT == 2 && t >= args.tiles0 ? t - args.tiles0 : t, &mt, &nt);
             const int acc = n & 1;
             const bool ok = wait(&acc_full[acc], (n >> 1) & 1, abort);
             if (!__all_sync(0xffffffffu, ok)) break;
@@ -649,7 +665,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_pair_kernel(const _
 
 template <int BN> constexpr int kStageBytes = kATile + BN * kBK * 2;
 
-template <int BN, int STAGES>
+template <int BN, int STAGES, int COUNT>
 __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_split_kernel(const __grid_constant__ GemmArgs args)
 {
     extern __shared__ unsigned char raw[];
@@ -658,12 +674,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_split_kernel(const 
     __shared__ uint32_t tmem;
     __shared__ int abort_flag;
     constexpr uint32_t kCols = BN < 32 ? 32 : BN;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31; // warp: uniform
     const int rank = static_cast<int>(cluster_rank()), size = static_cast<int>(cluster_size());
     const int t = blockIdx.x / size;
-    const Problem& g = args.p[t >= args.tiles0];
+    const Problem& g = args.p[COUNT == 1 ? 0 : t >= args.tiles0];
     int mt, nt;
-    tile_at(g, t >= args.tiles0 ? t - args.tiles0 : t, &mt, &nt);
+    tile_at(g, COUNT == 2 && t >= args.tiles0 ? t - args.tiles0 : t, &mt, &nt);
     const int parts = min(size, g.kblocks); // CTAs that have a part of the contraction
     const int kb0 = static_cast<int>(static_cast<long long>(g.kblocks) * min(rank, parts) / parts);
     const int kb1 = static_cast<int>(static_cast<long long>(g.kblocks) * min(rank + 1, parts) / parts);
@@ -687,7 +703,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_split_kernel(const 
     let_successor_start();
     wait_for_predecessor();
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0 && elect_one()) {
         int it = 0;
         bool ok = true;
         for (int kb = kb0; kb < kb1; ++kb, ++it) {
@@ -714,7 +730,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_split_kernel(const 
         }
         if (!ok)
             for (int k = max(0, it - STAGES); k < it; ++k) wait_landed(&full[k % STAGES], (k / STAGES) & 1);
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1 && elect_one()) {
         int it = 0;
         bool ok = true;
         const uint64_t da = g.a_mn ? 2048 >> 4 : 32 >> 4, db = g.b_mn ? 2048 >> 4 : 32 >> 4;
@@ -1174,17 +1190,22 @@ int gemm(const Product* p, int count, int type, const BiasSum* bias, cudaStream_
         args.bf16 = type == ZERO_TYPE_BF16;
     }
     if (v.pair) {
-        GemmKernel fn = zero_gemm_pair_kernel<256, kPairStages<256>>;
+        GemmKernel fn = count == 1 ? zero_gemm_pair_kernel<256, kPairStages<256>, 1> : zero_gemm_pair_kernel<256, kPairStages<256>, 2>;
         if ((rc = allow_smem(fn, kPairSmem<256>))) return rc;
         return launch_after(fn, args, 2 * std::min<int64_t>(tiles, sms / 2), kGemmThreads, kPairSmem<256>, 2, stream);
     }
-    GemmKernel fn;
-    int smem;
+    GemmKernel fn = nullptr;
+    int smem = 0;
+    auto pick = [&](auto tag) {
+        constexpr int BN = decltype(tag)::value;
+        fn = count == 1 ? zero_gemm_split_kernel<BN, kSplitStages<BN>, 1> : zero_gemm_split_kernel<BN, kSplitStages<BN>, 2>;
+        smem = kSplitSmem<BN>;
+    };
     switch (v.bn) {
-    case 16: fn = zero_gemm_split_kernel<16, kSplitStages<16>>, smem = kSplitSmem<16>; break;
-    case 32: fn = zero_gemm_split_kernel<32, kSplitStages<32>>, smem = kSplitSmem<32>; break;
-    case 64: fn = zero_gemm_split_kernel<64, kSplitStages<64>>, smem = kSplitSmem<64>; break;
-    default: fn = zero_gemm_split_kernel<128, kSplitStages<128>>, smem = kSplitSmem<128>; break;
+    case 16: pick(std::integral_constant<int, 16>{}); break;
+    case 32: pick(std::integral_constant<int, 32>{}); break;
+    case 64: pick(std::integral_constant<int, 64>{}); break;
+    default: pick(std::integral_constant<int, 128>{}); break;
     }
     if ((rc = allow_smem(fn, smem))) return rc;
     return launch_after(fn, args, tiles * v.parts, kGemmThreads, smem, v.parts, stream);
