@@ -43,7 +43,8 @@ __attribute__((visibility("hidden"))) int zero_record_cuda_error(int err);
 
 namespace {
 
-constexpr int kGemmThreads = 256; // warp 0 TMA, warp 1 MMA, warp 2 tensor memory, warps 4..7 epilogue
+constexpr int kGemmThreads = 384; // warp 0 TMA, warp 1 MMA, warp 2 tensor memory, warp 3 bias sums, warps 4..11 epilogue
+constexpr int kEpilogueWarps = 8;
 constexpr int kBM = 128;          // rows of a tile: the lanes of tensor memory
 constexpr int kBK = 64;           // contraction per stage: 128 bytes, one swizzle row
 constexpr int kATile = kBM * kBK * 2;
@@ -404,17 +405,7 @@ __device__ __forceinline__ float slope(float z, int act)
     return 1.0f;
 }
 
-// One output element from its accumulator.
-__device__ __forceinline__ void emit(const Out& o, long long row, int col, float v)
-{
-    if (o.bias) v += load16(o.bias, col, o.bf16);
-    if (o.z) store16(o.z, row * o.ldz + col, v, o.bf16);
-    v = activate(v, o.act);
-    if (o.res) v += load16(o.res, row * o.ldr + col, o.bf16);
-    store16(o.y, row * o.ldy + col, v, o.bf16);
-}
-
-__device__ __forceinline__ void add8(float (&v)[8], const uint4& u, int bf16)
+__device__ __forceinline__ void add8(float* v, const uint4& u, int bf16)
 {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -425,28 +416,132 @@ __device__ __forceinline__ void add8(float (&v)[8], const uint4& u, int bf16)
     }
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&v)[8], int bf16)
+__device__ __forceinline__ uint4 pack8(const float* v, int bf16)
 {
     return make_uint4(pack16(v[0], v[1], bf16), pack16(v[2], v[3], bf16), pack16(v[4], v[5], bf16), pack16(v[6], v[7], bf16));
 }
 
-// The residual of 8 consecutive elements of an output row, asked for ahead.
-__device__ __forceinline__ uint4 load_res8(const Out& o, long long row, int col)
+__device__ __forceinline__ uint16_t* at16(const void* p, long long ld, long long row, int col)
 {
-    return *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(o.res) + row * o.ldr + col);
+    return static_cast<uint16_t*>(const_cast<void*>(p)) + row * ld + col;
 }
 
-// 8 consecutive elements of an output row (16-byte accesses allowed).
+// The result in v (one or eight consecutive elements of an output row; res:
+// their residual, loaded ahead).
+__device__ __forceinline__ void emit(const Out& o, long long row, int col, float v, uint16_t res)
+{
+    if (o.bias) v += load16(o.bias, col, o.bf16);
+    if (o.z) store16(o.z, row * o.ldz + col, v, o.bf16);
+    v = activate(v, o.act);
+    if (o.res) v += load16(&res, 0, o.bf16);
+    store16(o.y, row * o.ldy + col, v, o.bf16);
+}
+
 __device__ __forceinline__ void emit8(const Out& o, long long row, int col, float (&v)[8], const uint4& res)
 {
-    if (o.bias) add8(v, __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(o.bias) + col)), o.bf16);
-    if (o.z) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(o.z) + row * o.ldz + col) = pack8(v, o.bf16);
+    if (o.bias) add8(v, __ldg(reinterpret_cast<const uint4*>(at16(o.bias, 0, 0, col))), o.bf16);
+    if (o.z) *reinterpret_cast<uint4*>(at16(o.z, o.ldz, row, col)) = pack8(v, o.bf16);
     if (o.act != ZERO_ACT_NONE) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = activate(v[j], o.act);
     }
     if (o.res) add8(v, res, o.bf16);
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(o.y) + row * o.ldy + col) = pack8(v, o.bf16);
+    *reinterpret_cast<uint4*>(at16(o.y, o.ldy, row, col)) = pack8(v, o.bf16);
+}
+
+// A warp's 32 x 32 piece of an output, 16 bits each, in 2 KB of shared
+// memory: row r's 16-byte quarter q at 4 r + (q ^ (r / 2 & 3)), so that lanes
+// that hold a row each and lanes that run along rows are both free of bank
+// conflicts.
+__device__ __forceinline__ int piece_at(int r, int q) { return 4 * r + (q ^ ((r >> 1) & 3)); }
+
+// `rows` x `cols` of the piece to or from memory, lanes along the rows.
+__device__ __forceinline__ void piece_out(const uint4* piece, uint16_t* to, long long ld, int rows, int cols, bool vec, int lane)
+{
+    if (vec && cols == 32) {
+        const int r0 = lane >> 2, q = lane & 3;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (r0 + 8 * k < rows) *reinterpret_cast<uint4*>(to + (r0 + 8 * k) * ld + q * 8) = piece[piece_at(r0 + 8 * k, q)];
+    } else if (lane < cols) {
+        const uint16_t* p = reinterpret_cast<const uint16_t*>(piece);
+#pragma unroll 8
+        for (int r = 0; r < rows; ++r) to[r * ld + lane] = p[piece_at(r, lane >> 3) * 8 + (lane & 7)];
+    }
+}
+
+__device__ __forceinline__ void piece_in(uint4* piece, const uint16_t* from, long long ld, int rows, int cols, int lane)
+{
+    if (lane >= cols) return;
+    uint16_t* p = reinterpret_cast<uint16_t*>(piece);
+#pragma unroll 8
+    for (int r = 0; r < rows; ++r) p[piece_at(r, lane >> 3) * 8 + (lane & 7)] = from[r * ld + lane];
+}
+
+// Row `lane` of the piece from this lane's 32 values.
+__device__ __forceinline__ void piece_row(uint4* piece, const float (&v)[32], int bf16, int lane)
+{
+#pragma unroll
+    for (int q = 0; q < 4; ++q) piece[piece_at(lane, q)] = pack8(v + 8 * q, bf16);
+}
+
+// The 32 x 32 results of a warp, lane l holding row row0 + l: bias,
+// pre-activation, activation, residual, and the stores.  rows, cols: how many
+// exist.
+__device__ __forceinline__ void emit_piece(const Out& o, long long row0, int rows, int col0, int cols, float (&v)[32],
+                                           uint4* piece, int lane)
+{
+    const bool vec = o.vec && cols == 32;
+    uint4 res[4] = {};
+    if (o.res && vec) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if ((lane >> 2) + 8 * k < rows)
+                res[k] = *reinterpret_cast<const uint4*>(at16(o.res, o.ldr, row0 + (lane >> 2) + 8 * k, col0 + (lane & 3) * 8));
+    }
+    if (o.bias) {
+        if (vec) {
+            const uint4* b = reinterpret_cast<const uint4*>(at16(o.bias, 0, 0, col0));
+#pragma unroll
+            for (int q = 0; q < 4; ++q) add8(v + 8 * q, __ldg(b + q), o.bf16);
+        } else {
+            const float mine = lane < cols ? load16(o.bias, col0 + lane, o.bf16) : 0.0f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] += __shfl_sync(0xffffffffu, mine, j);
+        }
+    }
+    if (o.z) {
+        piece_row(piece, v, o.bf16, lane);
+        __syncwarp();
+        piece_out(piece, at16(o.z, o.ldz, row0, col0), o.ldz, rows, cols, o.vec, lane);
+        __syncwarp();
+    }
+    if (o.act == ZERO_ACT_RELU) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = activate(v[j], ZERO_ACT_RELU);
+    } else if (o.act == ZERO_ACT_GELU) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = activate(v[j], ZERO_ACT_GELU);
+    } else if (o.act == ZERO_ACT_SILU) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = activate(v[j], ZERO_ACT_SILU);
+    }
+    if (o.res) {
+        if (vec) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) piece[piece_at((lane >> 2) + 8 * k, lane & 3)] = res[k];
+        } else {
+            piece_in(piece, at16(o.res, o.ldr, row0, col0), o.ldr, rows, cols, lane);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) add8(v + 8 * q, piece[piece_at(lane, q)], o.bf16);
+        __syncwarp();
+    }
+    piece_row(piece, v, o.bf16, lane);
+    __syncwarp();
+    piece_out(piece, at16(o.y, o.ldy, row0, col0), o.ldy, rows, cols, o.vec, lane);
+    __syncwarp();
 }
 
 // ---------------------------------------------------------------------------
@@ -488,8 +583,8 @@ __device__ __forceinline__ void bias_sum(const GemmArgs& args, int lane)
 // of A and columns [BN/2 r, BN/2 r + BN/2) of B, and its tensor memory holds
 // its 128 rows of the result.  The even CTA issues the products for both.
 template <int BN> constexpr int kPairStage = kATile + BN / 2 * kBK * 2;
-constexpr int kStagePitch = 36; // floats of a staged row of 32: 16-byte accesses free of bank conflicts both ways
-constexpr int kEpilogueBytes = 4 * 32 * kStagePitch * 4;
+constexpr int kPieceBytes = 32 * 32 * 2;
+constexpr int kEpilogueBytes = kEpilogueWarps * kPieceBytes;
 
 template <int BN, int STAGES, int COUNT>
 __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_pair_kernel(const __grid_constant__ GemmArgs args)
@@ -509,7 +604,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_pair_kernel(const _
         }
         for (int k = 0; k < 2; ++k) {
             mbar_init(&acc_full[k], 1);
-            mbar_init(&acc_empty[k], 8); // the epilogue warps of both CTAs
+            mbar_init(&acc_empty[k], 2 * kEpilogueWarps); // the epilogue warps of both CTAs
         }
         mbar_init(&drained, 1);
         abort_flag = 0;
@@ -594,8 +689,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_pair_kernel(const _
     } else if (warp == 3) {
         bias_sum(args, lane);
     } else if (warp >= 4) {
-        const int q = warp & 3;
-        float* stage = reinterpret_cast<float*>(smem + STAGES * kPairStage<BN>) + q * 32 * kStagePitch;
+        // two warps for each 32 rows, each with half of the columns
+        const int q = warp & 3, c0 = ((warp - 4) >> 2) * (BN / 2);
+        uint4* piece = reinterpret_cast<uint4*>(smem + STAGES * kPairStage<BN> + (warp - 4) * kPieceBytes);
         int n = 0;
         for (int t = pair; t < args.tiles; t += pairs, ++n) {
             const Problem& g = args.p[COUNT == 1 ? 0 : t >= args.tiles0];
@@ -606,49 +702,18 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_pair_kernel(const _
             if (!__all_sync(0xffffffffu, ok)) break;
             fence_after();
             const int row0 = mt * 256 + rank * kBM + q * 32;
-            const Out& o = g.o;
-            const int rows = g.m - row0; // of this warp's 32 that exist; may be 0 or less
+            const int rows = min(32, g.m - row0); // that exist; may be 0 or less
 #pragma unroll 1
-            for (int c = 0; c < BN; c += 32) {
-                const int col0 = nt * BN + c;
+            for (int c = c0; c < c0 + BN / 2; c += 32) {
                 float v[32];
                 tmem_load(base + acc * BN + c + (static_cast<uint32_t>(q * 32) << 16), v);
-                if (c + 32 == BN) { // the accumulator is read: the next tile but one may have it
+                if (c + 32 == c0 + BN / 2) { // this warp's part is read: the next tile but one may have it
                     fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_at(peer_addr(smem_addr(&acc_empty[acc]), 0));
                 }
-                if (rows <= 0 || col0 >= g.n) continue;
-                // through shared memory, so that lanes run along the output's rows
-                float* mine = stage + lane * kStagePitch;
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    *reinterpret_cast<float4*>(mine + 4 * j) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-                __syncwarp();
-                if (o.vec && col0 + 32 <= g.n) {
-                    const int r = lane >> 2, cc = (lane & 3) * 8;
-                    uint4 res[4] = {};
-                    if (o.res) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (k * 8 + r < rows) res[k] = load_res8(o, row0 + k * 8 + r, col0 + cc);
-                    }
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if (k * 8 + r >= rows) continue;
-                        const float4* p = reinterpret_cast<const float4*>(stage + (k * 8 + r) * kStagePitch + cc);
-                        const float4 lo = p[0], hi = p[1];
-                        float w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-                        emit8(o, row0 + k * 8 + r, col0 + cc, w, res[k]);
-                    }
-                } else {
-                    const int most = min(32, rows);
-                    if (col0 + lane < g.n) {
-#pragma unroll 4
-                        for (int r = 0; r < most; ++r) emit(o, row0 + r, col0 + lane, stage[r * kStagePitch + lane]);
-                    }
-                }
-                __syncwarp();
+                const int cols = min(32, g.n - (nt * BN + c));
+                if (rows > 0 && cols > 0) emit_piece(g.o, row0, rows, nt * BN + c, cols, v, piece, lane);
             }
         }
     }
@@ -664,6 +729,89 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_pair_kernel(const _
 // ---------------------------------------------------------------------------
 
 template <int BN> constexpr int kStageBytes = kATile + BN * kBK * 2;
+
+// A CTA's share of joining a tile.
+struct Join {
+    uint32_t part;       // shared-memory address of the partial tile, the same in every CTA
+    int pitch, fast, slow;
+    long long row0;
+    int col0, self, everyone;
+};
+
+// Sum over the cluster's partial tiles in rank order, all of a thread's reads
+// in flight together (PARTS 0: the number is read at run time).
+template <int PARTS> __device__ __forceinline__ void join(const Out& o, const Join& j, int parts)
+{
+    const int vecs = o.vec ? j.fast / 8 : 0; // whole vectors of 8 of a row; the rest goes element by element
+    if (vecs) {
+        const int total = vecs * j.slow;
+        constexpr int kAhead = PARTS == 1 ? 4 : PARTS == 2 ? 2 : 1;
+        for (int e = j.self; e < total; e += j.everyone * kAhead) {
+            float v[kAhead][8];
+            int s[kAhead], f[kAhead];
+            uint4 res[kAhead] = {};
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int i = min(e + k * j.everyone, total - 1);
+                s[k] = i / vecs;
+                f[k] = (i - s[k] * vecs) * 8;
+                if (o.res) res[k] = *reinterpret_cast<const uint4*>(at16(o.res, o.ldr, j.row0 + s[k], j.col0 + f[k]));
+#pragma unroll
+                for (int h = 0; h < 8; ++h) v[k][h] = 0.0f;
+            }
+            auto add = [&](int p) {
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const uint32_t at = j.part + static_cast<uint32_t>(s[k] * j.pitch + f[k]) * 4;
+                    const float4 lo = peer_load4(at, static_cast<uint32_t>(p)), hi = peer_load4(at + 16, static_cast<uint32_t>(p));
+                    v[k][0] += lo.x, v[k][1] += lo.y, v[k][2] += lo.z, v[k][3] += lo.w;
+                    v[k][4] += hi.x, v[k][5] += hi.y, v[k][6] += hi.z, v[k][7] += hi.w;
+                }
+            };
+            if constexpr (PARTS > 0) {
+#pragma unroll
+                for (int p = 0; p < PARTS; ++p) add(p);
+            } else {
+                for (int p = 0; p < parts; ++p) add(p);
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (e + k * j.everyone < total) emit8(o, j.row0 + s[k], j.col0 + f[k], v[k], res[k]);
+        }
+    }
+    const int left = j.fast - vecs * 8;
+    if (left) {
+        const int total = left * j.slow;
+        constexpr int kAhead = PARTS == 8 ? 4 : 8;
+        for (int e = j.self; e < total; e += j.everyone * kAhead) {
+            float v[kAhead];
+            int s[kAhead], f[kAhead];
+            uint16_t res[kAhead] = {};
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int i = min(e + k * j.everyone, total - 1);
+                s[k] = i / left;
+                f[k] = i - s[k] * left + vecs * 8;
+                if (o.res) res[k] = *at16(o.res, o.ldr, j.row0 + s[k], j.col0 + f[k]);
+                v[k] = 0.0f;
+            }
+            auto add = [&](int p) {
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k)
+                    v[k] += peer_load(j.part + static_cast<uint32_t>(s[k] * j.pitch + f[k]) * 4, static_cast<uint32_t>(p));
+            };
+            if constexpr (PARTS > 0) {
+#pragma unroll
+                for (int p = 0; p < PARTS; ++p) add(p);
+            } else {
+                for (int p = 0; p < parts; ++p) add(p);
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (e + k * j.everyone < total) emit(o, j.row0 + s[k], j.col0 + f[k], v[k], res[k]);
+        }
+    }
+}
 
 template <int BN, int STAGES, int COUNT>
 __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_split_kernel(const __grid_constant__ GemmArgs args)
@@ -757,12 +905,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_split_kernel(const 
         bias_sum(args, lane);
     }
     __syncwarp();
-    // The stages are free once the last product is done: the partial tile goes
-    // there with the output's contiguous index innermost.
+    // The stages are free once the last product is done.
     const Out& o = g.o;
+    const int rows = min(kBM, g.m - mt * kBM), cols = min(BN, g.n - nt * BN);
     float* part = reinterpret_cast<float*>(smem);
     const int pitch = (o.swap ? kBM : BN) + 4; // floats; 16-byte accesses free of bank conflicts
-    if (warp >= 4 && kb1 > kb0) {
+    const bool direct = BN >= 64 && parts == 1 && !o.swap; // nothing to join: straight from tensor memory
+    constexpr int kHalf = BN < 64 ? BN : BN / 2; // the columns of one of the two warps that share 32 rows
+    const int c0 = ((warp - 4) >> 2) * kHalf;
+    if (warp >= 4 && kb1 > kb0 && c0 < BN) {
         const int q = warp & 3;
         const bool ok = wait(&acc_full, 0, abort);
         if (__all_sync(0xffffffffu, ok)) {
@@ -771,10 +922,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_split_kernel(const 
             const uint32_t at = base + (static_cast<uint32_t>(q * 32) << 16);
             constexpr int kStep = BN < 32 ? 16 : 32;
 #pragma unroll 1
-            for (int c = 0; c < BN; c += kStep) {
+            for (int c = c0; c < c0 + kHalf; c += kStep) {
                 float v[kStep];
                 if constexpr (kStep == 16) tmem_load16(at, v);
                 else tmem_load(at + c, v);
+                if constexpr (BN >= 64) {
+                    if (direct) {
+                        if (q * 32 < rows && c < cols)
+                            emit_piece(o, mt * kBM + q * 32, min(32, rows - q * 32), nt * BN + c, min(32, cols - c), v,
+                                       reinterpret_cast<uint4*>(smem + (warp - 4) * kPieceBytes), lane);
+                        continue;
+                    }
+                }
+                // the partial tile, with the output's contiguous index innermost
                 if (o.swap) {
 #pragma unroll
                     for (int j = 0; j < kStep; ++j) part[(c + j) * pitch + row] = v[j];
@@ -789,67 +949,24 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_split_kernel(const 
     }
     __syncwarp();
     cluster_sync();
-    // Each CTA finishes a share of the tile: the partial sums of the cluster
-    // are added in rank order.
-    const int rows = min(kBM, g.m - mt * kBM), cols = min(BN, g.n - nt * BN);
-    const int fast = o.swap ? rows : cols, slow = o.swap ? cols : rows; // extents along and across the output's rows
-    const long long row0 = o.swap ? nt * BN : mt * kBM;
-    const int col0 = o.swap ? mt * kBM : nt * BN;
-    const uint32_t part_at = smem_addr(part);
-    const int self = rank * kGemmThreads + static_cast<int>(threadIdx.x), everyone = size * kGemmThreads;
-    const int vecs = o.vec ? fast / 8 : 0; // whole vectors of 8 of a row; the rest goes element by element
-    if (vecs) {
-        const int total = vecs * slow;
-        constexpr int kAhead = 2;
-        for (int e = self; e < total; e += everyone * kAhead) {
-            float v[kAhead][8];
-            int s_[kAhead], f_[kAhead];
-            uint4 res[kAhead] = {};
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const int i = min(e + k * everyone, total - 1);
-                s_[k] = i / vecs;
-                f_[k] = (i - s_[k] * vecs) * 8;
-                if (o.res) res[k] = load_res8(o, row0 + s_[k], col0 + f_[k]);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[k][j] = 0.0f;
-            }
-#pragma unroll 2
-            for (int p = 0; p < parts; ++p)
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k) {
-                    const uint32_t at = part_at + static_cast<uint32_t>(s_[k] * pitch + f_[k]) * 4;
-                    const float4 lo = peer_load4(at, static_cast<uint32_t>(p)), hi = peer_load4(at + 16, static_cast<uint32_t>(p));
-                    v[k][0] += lo.x, v[k][1] += lo.y, v[k][2] += lo.z, v[k][3] += lo.w;
-                    v[k][4] += hi.x, v[k][5] += hi.y, v[k][6] += hi.z, v[k][7] += hi.w;
-                }
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k)
-                if (e + k * everyone < total) emit8(o, row0 + s_[k], col0 + f_[k], v[k], res[k]);
-        }
-    }
-    const int left = fast - vecs * 8;
-    if (left) {
-        const int total = left * slow;
-        constexpr int kAhead = 4;
-        for (int e = self; e < total; e += everyone * kAhead) {
-            float v[kAhead];
-            int s_[kAhead], f_[kAhead];
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const int i = min(e + k * everyone, total - 1);
-                s_[k] = i / left;
-                f_[k] = i - s_[k] * left + vecs * 8;
-                v[k] = 0.0f;
-            }
-#pragma unroll 2
-            for (int p = 0; p < parts; ++p)
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k)
-                    v[k] += peer_load(part_at + static_cast<uint32_t>(s_[k] * pitch + f_[k]) * 4, static_cast<uint32_t>(p));
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k)
-                if (e + k * everyone < total) emit(o, row0 + s_[k], col0 + f_[k], v[k]);
+    if (!direct) {
+        // Each CTA finishes a share of the tile: the partial sums of the
+        // cluster are added in rank order.
+        Join j;
+        j.part = smem_addr(part);
+        j.pitch = pitch;
+        j.fast = o.swap ? rows : cols; // extents along and across the output's rows
+        j.slow = o.swap ? cols : rows;
+        j.row0 = o.swap ? nt * BN : mt * kBM;
+        j.col0 = o.swap ? mt * kBM : nt * BN;
+        j.self = rank * kGemmThreads + static_cast<int>(threadIdx.x);
+        j.everyone = size * kGemmThreads;
+        switch (parts) {
+        case 1: join<1>(o, j, parts); break;
+        case 2: join<2>(o, j, parts); break;
+        case 4: join<4>(o, j, parts); break;
+        case 8: join<8>(o, j, parts); break;
+        default: join<0>(o, j, parts); break;
         }
     }
     cluster_sync(); // peers have read this CTA's part
