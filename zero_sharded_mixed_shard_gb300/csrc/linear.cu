@@ -45,6 +45,7 @@ namespace {
 
 constexpr int kGemmThreads = 384; // warp 0 TMA, warp 1 MMA, warp 2 tensor memory, warp 3 bias sums, warps 4..11 epilogue
 constexpr int kEpilogueWarps = 8;
+constexpr int kSplitThreads = 256; // the same roles, warps 4..7 epilogue: two CTAs fit an SM
 constexpr int kBM = 128;          // rows of a tile: the lanes of tensor memory
 constexpr int kBK = 64;           // contraction per stage: 128 bytes, one swizzle row
 constexpr int kATile = kBM * kBK * 2;
@@ -67,10 +68,11 @@ struct Out {
 struct Problem {
     CUtensorMap a, b;
     Out o;
-    int a_mn, b_mn;      // the operand's contiguous index is m (n), not k
+    int a_mn, b_mn;      // 0: the operand's contiguous index is k; 1: it is m (n); 2: that, in whole blocks of 64
     int m, n;            // extents on the A and the B side
     int tiles_m, tiles_n;
     int kblocks;
+    int cut;             // split kernel: a cluster shares each tile's contraction, else every CTA has a tile of its own
     unsigned int idesc;
 };
 
@@ -78,7 +80,7 @@ struct Problem {
 // sum (columns of `sums` over its chunks), which a spare warp takes along.
 struct GemmArgs {
     Problem p[2];
-    int tiles0, tiles;   // of the first product, of both
+    int tiles0, tiles;   // of the first product, of both (split kernel: its clusters)
     const float* sums;
     void* db;
     int chunks, n_db, bf16;
@@ -189,6 +191,24 @@ __device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map,
     asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
                  " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
                  "l"(map), "r"(x), "r"(y), "r"(bar)
+                 : "memory");
+}
+
+// The same from a map of three dimensions: 64 contiguous elements, the
+// contraction index, blocks of 64 (an MN-major operand in one instruction).
+__device__ __forceinline__ void tma_load_pair3(void* dst, const CUtensorMap* map, int k, int block, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
+                 "l"(map), "r"(0), "r"(k), "r"(block), "r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tma_load3(void* dst, const CUtensorMap* map, int k, int block, uint64_t* bar)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
+                 "l"(map), "r"(0), "r"(k), "r"(block), "r"(smem_addr(bar))
                  : "memory");
 }
 
@@ -378,31 +398,64 @@ __device__ __forceinline__ float2 unpack16(uint32_t u, int bf16)
     return __half22float2(*reinterpret_cast<const __half2*>(&u));
 }
 
-// 2 sqrt(2 / pi): tanh's form of GELU is z / (1 + exp(-kGelu (z + 0.044715 z^3))).
-constexpr float kGelu = 1.5957691216057308f;
-constexpr float kCube = 0.044715f;
-
-__device__ __forceinline__ float activate(float z, int act)
+// 2^x and 1 / x by the hardware's approximations (2 and 1 ulp).
+__device__ __forceinline__ float fast_exp2(float x)
 {
-    if (act == ZERO_ACT_RELU) return z > 0.0f ? z : 0.0f;
-    if (act == ZERO_ACT_GELU) return __fdividef(z, 1.0f + __expf(-kGelu * (z + kCube * z * z * z)));
-    if (act == ZERO_ACT_SILU) return __fdividef(z, 1.0f + __expf(-z));
-    return z;
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-// The activation's derivative at z.
-__device__ __forceinline__ float slope(float z, int act)
+__device__ __forceinline__ float fast_rcp(float x)
 {
-    if (act == ZERO_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
-    if (act == ZERO_ACT_GELU) {
-        const float p = __fdividef(1.0f, 1.0f + __expf(-kGelu * (z + kCube * z * z * z)));
-        return p + z * p * (1.0f - p) * kGelu * (1.0f + 3.0f * kCube * z * z);
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// GELU in tanh's form is z s(u), u = 2 sqrt(2 / pi) (z + 0.044715 z^3), and
+// SiLU z s(z), with s the logistic function 1 / (1 + 2^(-x log2 e)).
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kGelu = 1.5957691216057308f;
+constexpr float kGelu3 = kGelu * 0.044715f;
+
+template <int ACT> __device__ __forceinline__ float logistic(float z)
+{
+    const float x = ACT == ZERO_ACT_GELU ? z * fmaf(z * z, -kLog2e * kGelu3, -kLog2e * kGelu) : z * -kLog2e;
+    return fast_rcp(1.0f + fast_exp2(x));
+}
+
+template <int ACT> __device__ __forceinline__ float activate(float z)
+{
+    if constexpr (ACT == ZERO_ACT_RELU) return z > 0.0f ? z : 0.0f;
+    else if constexpr (ACT == ZERO_ACT_NONE) return z;
+    else return z * logistic<ACT>(z);
+}
+
+// The activation's derivative at z: s + z s (1 - s) u'(z).
+template <int ACT> __device__ __forceinline__ float slope(float z)
+{
+    if constexpr (ACT == ZERO_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
+    else if constexpr (ACT == ZERO_ACT_NONE) return 1.0f;
+    else {
+        const float p = logistic<ACT>(z), q = fmaf(-p, p, p);
+        return fmaf(q, ACT == ZERO_ACT_GELU ? z * fmaf(z * z, 3.0f * kGelu3, kGelu) : z, p);
     }
-    if (act == ZERO_ACT_SILU) {
-        const float p = __fdividef(1.0f, 1.0f + __expf(-z));
-        return p + z * p * (1.0f - p);
+}
+
+// N values at once: the choice of the activation stands outside the loop.
+template <int N> __device__ __forceinline__ void activate_all(float (&v)[N], int act)
+{
+    if (act == ZERO_ACT_RELU) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = activate<ZERO_ACT_RELU>(v[j]);
+    } else if (act == ZERO_ACT_GELU) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = activate<ZERO_ACT_GELU>(v[j]);
+    } else if (act == ZERO_ACT_SILU) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = activate<ZERO_ACT_SILU>(v[j]);
     }
-    return 1.0f;
 }
 
 __device__ __forceinline__ void add8(float* v, const uint4& u, int bf16)
@@ -432,19 +485,17 @@ __device__ __forceinline__ void emit(const Out& o, long long row, int col, float
 {
     if (o.bias) v += load16(o.bias, col, o.bf16);
     if (o.z) store16(o.z, row * o.ldz + col, v, o.bf16);
-    v = activate(v, o.act);
-    if (o.res) v += load16(&res, 0, o.bf16);
-    store16(o.y, row * o.ldy + col, v, o.bf16);
+    float w[1] = {v};
+    activate_all(w, o.act);
+    if (o.res) w[0] += load16(&res, 0, o.bf16);
+    store16(o.y, row * o.ldy + col, w[0], o.bf16);
 }
 
 __device__ __forceinline__ void emit8(const Out& o, long long row, int col, float (&v)[8], const uint4& res)
 {
     if (o.bias) add8(v, __ldg(reinterpret_cast<const uint4*>(at16(o.bias, 0, 0, col))), o.bf16);
     if (o.z) *reinterpret_cast<uint4*>(at16(o.z, o.ldz, row, col)) = pack8(v, o.bf16);
-    if (o.act != ZERO_ACT_NONE) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = activate(v[j], o.act);
-    }
+    activate_all(v, o.act);
     if (o.res) add8(v, res, o.bf16);
     *reinterpret_cast<uint4*>(at16(o.y, o.ldy, row, col)) = pack8(v, o.bf16);
 }
@@ -488,7 +539,8 @@ __device__ __forceinline__ void piece_row(uint4* piece, const float (&v)[32], in
 // The 32 x 32 results of a warp, lane l holding row row0 + l: bias,
 // pre-activation, activation, residual, and the stores.  rows, cols: how many
 // exist.
-__device__ __forceinline__ void emit_piece(const Out& o, long long row0, int rows, int col0, int cols, float (&v)[32],
+template <int BF16>
+__device__ __forceinline__ void emit_piece_as(const Out& o, long long row0, int rows, int col0, int cols, float (&v)[32],
                                            uint4* piece, int lane)
 {
     const bool vec = o.vec && cols == 32;
@@ -503,29 +555,20 @@ __device__ __forceinline__ void emit_piece(const Out& o, long long row0, int row
         if (vec) {
             const uint4* b = reinterpret_cast<const uint4*>(at16(o.bias, 0, 0, col0));
 #pragma unroll
-            for (int q = 0; q < 4; ++q) add8(v + 8 * q, __ldg(b + q), o.bf16);
+            for (int q = 0; q < 4; ++q) add8(v + 8 * q, __ldg(b + q), BF16);
         } else {
-            const float mine = lane < cols ? load16(o.bias, col0 + lane, o.bf16) : 0.0f;
+            const float mine = lane < cols ? load16(o.bias, col0 + lane, BF16) : 0.0f;
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] += __shfl_sync(0xffffffffu, mine, j);
         }
     }
     if (o.z) {
-        piece_row(piece, v, o.bf16, lane);
+        piece_row(piece, v, BF16, lane);
         __syncwarp();
         piece_out(piece, at16(o.z, o.ldz, row0, col0), o.ldz, rows, cols, o.vec, lane);
         __syncwarp();
     }
-    if (o.act == ZERO_ACT_RELU) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = activate(v[j], ZERO_ACT_RELU);
-    } else if (o.act == ZERO_ACT_GELU) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = activate(v[j], ZERO_ACT_GELU);
-    } else if (o.act == ZERO_ACT_SILU) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = activate(v[j], ZERO_ACT_SILU);
-    }
+    activate_all(v, o.act);
     if (o.res) {
         if (vec) {
 #pragma unroll
@@ -535,13 +578,20 @@ __device__ __forceinline__ void emit_piece(const Out& o, long long row0, int row
         }
         __syncwarp();
 #pragma unroll
-        for (int q = 0; q < 4; ++q) add8(v + 8 * q, piece[piece_at(lane, q)], o.bf16);
+        for (int q = 0; q < 4; ++q) add8(v + 8 * q, piece[piece_at(lane, q)], BF16);
         __syncwarp();
     }
-    piece_row(piece, v, o.bf16, lane);
+    piece_row(piece, v, BF16, lane);
     __syncwarp();
     piece_out(piece, at16(o.y, o.ldy, row0, col0), o.ldy, rows, cols, o.vec, lane);
     __syncwarp();
+}
+
+__device__ __forceinline__ void emit_piece(const Out& o, long long row0, int rows, int col0, int cols, float (&v)[32],
+                                           uint4* piece, int lane)
+{
+    if (o.bf16) emit_piece_as<1>(o, row0, rows, col0, cols, v, piece, lane);
+    else emit_piece_as<0>(o, row0, rows, col0, cols, v, piece, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -640,13 +690,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_pair_kernel(const _
                 if (rank == 0) mbar_expect(&full[s], 2 * kPairStage<BN>);
                 unsigned char* sa = smem + s * kPairStage<BN>;
                 unsigned char* sb = sa + kATile;
-                if (g.a_mn) {
+                if (g.a_mn == 2) {
+                    tma_load_pair3(sa, &g.a, kb * kBK, m0 / 64, bar);
+                } else if (g.a_mn) {
                     tma_load_pair(sa, &g.a, m0, kb * kBK, bar);
                     tma_load_pair(sa + 8192, &g.a, m0 + 64, kb * kBK, bar);
                 } else {
                     tma_load_pair(sa, &g.a, kb * kBK, m0, bar);
                 }
-                if (g.b_mn) {
+                if (g.b_mn == 2) {
+                    tma_load_pair3(sb, &g.b, kb * kBK, n0 / 64, bar);
+                } else if (g.b_mn) {
 #pragma unroll
                     for (int i = 0; i < BN / 128; ++i) tma_load_pair(sb + i * 8192, &g.b, n0 + i * 64, kb * kBK, bar);
                 } else {
@@ -736,11 +790,12 @@ struct Join {
     int pitch, fast, slow;
     long long row0;
     int col0, self, everyone;
+    uint32_t first;      // the rank of the first partial tile
 };
 
 // Sum over the cluster's partial tiles in rank order, all of a thread's reads
-// in flight together (PARTS 0: the number is read at run time).
-template <int PARTS> __device__ __forceinline__ void join(const Out& o, const Join& j, int parts)
+// in flight together.
+template <int PARTS> __device__ __forceinline__ void join(const Out& o, const Join& j)
 {
     const int vecs = o.vec ? j.fast / 8 : 0; // whole vectors of 8 of a row; the rest goes element by element
     if (vecs) {
@@ -763,17 +818,13 @@ template <int PARTS> __device__ __forceinline__ void join(const Out& o, const Jo
 #pragma unroll
                 for (int k = 0; k < kAhead; ++k) {
                     const uint32_t at = j.part + static_cast<uint32_t>(s[k] * j.pitch + f[k]) * 4;
-                    const float4 lo = peer_load4(at, static_cast<uint32_t>(p)), hi = peer_load4(at + 16, static_cast<uint32_t>(p));
+                    const float4 lo = peer_load4(at, j.first + p), hi = peer_load4(at + 16, j.first + p);
                     v[k][0] += lo.x, v[k][1] += lo.y, v[k][2] += lo.z, v[k][3] += lo.w;
                     v[k][4] += hi.x, v[k][5] += hi.y, v[k][6] += hi.z, v[k][7] += hi.w;
                 }
             };
-            if constexpr (PARTS > 0) {
 #pragma unroll
-                for (int p = 0; p < PARTS; ++p) add(p);
-            } else {
-                for (int p = 0; p < parts; ++p) add(p);
-            }
+            for (int p = 0; p < PARTS; ++p) add(p);
 #pragma unroll
             for (int k = 0; k < kAhead; ++k)
                 if (e + k * j.everyone < total) emit8(o, j.row0 + s[k], j.col0 + f[k], v[k], res[k]);
@@ -798,14 +849,10 @@ template <int PARTS> __device__ __forceinline__ void join(const Out& o, const Jo
             auto add = [&](int p) {
 #pragma unroll
                 for (int k = 0; k < kAhead; ++k)
-                    v[k] += peer_load(j.part + static_cast<uint32_t>(s[k] * j.pitch + f[k]) * 4, static_cast<uint32_t>(p));
+                    v[k] += peer_load(j.part + static_cast<uint32_t>(s[k] * j.pitch + f[k]) * 4, j.first + p);
             };
-            if constexpr (PARTS > 0) {
 #pragma unroll
-                for (int p = 0; p < PARTS; ++p) add(p);
-            } else {
-                for (int p = 0; p < parts; ++p) add(p);
-            }
+            for (int p = 0; p < PARTS; ++p) add(p);
 #pragma unroll
             for (int k = 0; k < kAhead; ++k)
                 if (e + k * j.everyone < total) emit(o, j.row0 + s[k], j.col0 + f[k], v[k], res[k]);
@@ -814,7 +861,7 @@ template <int PARTS> __device__ __forceinline__ void join(const Out& o, const Jo
 }
 
 template <int BN, int STAGES, int COUNT>
-__global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_split_kernel(const __grid_constant__ GemmArgs args)
+__global__ void __launch_bounds__(kSplitThreads, 2) zero_gemm_split_kernel(const __grid_constant__ GemmArgs args)
 {
     extern __shared__ unsigned char raw[];
     unsigned char* smem = aligned_smem(raw);
@@ -824,13 +871,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_split_kernel(const 
     constexpr uint32_t kCols = BN < 32 ? 32 : BN;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31; // warp: uniform
     const int rank = static_cast<int>(cluster_rank()), size = static_cast<int>(cluster_size());
-    const int t = blockIdx.x / size;
-    const Problem& g = args.p[COUNT == 1 ? 0 : t >= args.tiles0];
+    const int cluster = blockIdx.x / size;
+    const bool second = COUNT == 2 && cluster >= args.tiles0;
+    const Problem& g = args.p[COUNT == 1 ? 0 : second];
+    const int at = cluster - (second ? args.tiles0 : 0), t = g.cut ? at : at * size + rank;
+    const bool idle = t >= g.tiles_m * g.tiles_n; // the last cluster may have CTAs without a tile
     int mt, nt;
-    tile_at(g, COUNT == 2 && t >= args.tiles0 ? t - args.tiles0 : t, &mt, &nt);
-    const int parts = min(size, g.kblocks); // CTAs that have a part of the contraction
-    const int kb0 = static_cast<int>(static_cast<long long>(g.kblocks) * min(rank, parts) / parts);
-    const int kb1 = static_cast<int>(static_cast<long long>(g.kblocks) * min(rank + 1, parts) / parts);
+    tile_at(g, idle ? 0 : t, &mt, &nt);
+    const int parts = g.cut ? size : 1; // CTAs that share the contraction
+    const int kb0 = g.cut ? static_cast<int>(static_cast<long long>(g.kblocks) * rank / parts) : 0;
+    const int kb1 = g.cut ? static_cast<int>(static_cast<long long>(g.kblocks) * (rank + 1) / parts) : idle ? 0 : g.kblocks;
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], 1);
@@ -863,13 +913,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_split_kernel(const 
             mbar_expect(&full[s], kStageBytes<BN>);
             unsigned char* sa = smem + s * kStageBytes<BN>;
             unsigned char* sb = sa + kATile;
-            if (g.a_mn) {
+            if (g.a_mn == 2) {
+                tma_load3(sa, &g.a, kb * kBK, mt * (kBM / 64), &full[s]);
+            } else if (g.a_mn) {
                 tma_load(sa, &g.a, mt * kBM, kb * kBK, &full[s]);
                 tma_load(sa + 8192, &g.a, mt * kBM + 64, kb * kBK, &full[s]);
             } else {
                 tma_load(sa, &g.a, kb * kBK, mt * kBM, &full[s]);
             }
-            if (BN >= 64 && g.b_mn) {
+            if (BN >= 64 && g.b_mn == 2) {
+                tma_load3(sb, &g.b, kb * kBK, nt * (BN / 64), &full[s]);
+            } else if (BN >= 64 && g.b_mn) {
 #pragma unroll
                 for (int i = 0; i < BN / 64; ++i) tma_load(sb + i * 8192, &g.b, nt * BN + i * 64, kb * kBK, &full[s]);
             } else {
@@ -907,25 +961,23 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_split_kernel(const 
     __syncwarp();
     // The stages are free once the last product is done.
     const Out& o = g.o;
-    const int rows = min(kBM, g.m - mt * kBM), cols = min(BN, g.n - nt * BN);
+    const int rows = idle ? 0 : min(kBM, g.m - mt * kBM), cols = min(BN, g.n - nt * BN);
     float* part = reinterpret_cast<float*>(smem);
     const int pitch = (o.swap ? kBM : BN) + 4; // floats; 16-byte accesses free of bank conflicts
     const bool direct = BN >= 64 && parts == 1 && !o.swap; // nothing to join: straight from tensor memory
-    constexpr int kHalf = BN < 64 ? BN : BN / 2; // the columns of one of the two warps that share 32 rows
-    const int c0 = ((warp - 4) >> 2) * kHalf;
-    if (warp >= 4 && kb1 > kb0 && c0 < BN) {
+    if (warp >= 4 && kb1 > kb0) {
         const int q = warp & 3;
         const bool ok = wait(&acc_full, 0, abort);
         if (__all_sync(0xffffffffu, ok)) {
             fence_after();
             const int row = q * 32 + lane;
-            const uint32_t at = base + (static_cast<uint32_t>(q * 32) << 16);
+            const uint32_t acc = base + (static_cast<uint32_t>(q * 32) << 16);
             constexpr int kStep = BN < 32 ? 16 : 32;
 #pragma unroll 1
-            for (int c = c0; c < c0 + kHalf; c += kStep) {
+            for (int c = 0; c < BN; c += kStep) {
                 float v[kStep];
-                if constexpr (kStep == 16) tmem_load16(at, v);
-                else tmem_load(at + c, v);
+                if constexpr (kStep == 16) tmem_load16(acc, v);
+                else tmem_load(acc + c, v);
                 if constexpr (BN >= 64) {
                     if (direct) {
                         if (q * 32 < rows && c < cols)
@@ -959,14 +1011,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_split_kernel(const 
         j.slow = o.swap ? cols : rows;
         j.row0 = o.swap ? nt * BN : mt * kBM;
         j.col0 = o.swap ? mt * kBM : nt * BN;
-        j.self = rank * kGemmThreads + static_cast<int>(threadIdx.x);
-        j.everyone = size * kGemmThreads;
+        j.first = g.cut ? 0 : static_cast<uint32_t>(rank);
+        j.self = (g.cut ? rank * kSplitThreads : 0) + static_cast<int>(threadIdx.x);
+        j.everyone = (g.cut ? size : 1) * kSplitThreads;
         switch (parts) {
-        case 1: join<1>(o, j, parts); break;
-        case 2: join<2>(o, j, parts); break;
-        case 4: join<4>(o, j, parts); break;
-        case 8: join<8>(o, j, parts); break;
-        default: join<0>(o, j, parts); break;
+        case 1: join<1>(o, j); break;
+        case 2: join<2>(o, j); break;
+        case 4: join<4>(o, j); break;
+        default: join<8>(o, j); break;
         }
     }
     cluster_sync(); // peers have read this CTA's part
@@ -997,7 +1049,7 @@ struct PrepArgs {
     void* dz;            // null: dz is dy
     float* sums;         // null: no bias gradient
     long long lddy, ldz, lddz, T;
-    int N, rows_per, act, bf16, vec;
+    int N, rows_per, vec;
     int stripes, chunks;
     Copy copy[3];
 };
@@ -1018,6 +1070,7 @@ __device__ __forceinline__ void copy_rows(const Copy& c, int cta)
     }
 }
 
+template <int ACT, int BF16>
 __global__ void __launch_bounds__(256) zero_linear_prep_kernel(const __grid_constant__ PrepArgs a)
 {
     let_successor_start();
@@ -1038,7 +1091,6 @@ __global__ void __launch_bounds__(256) zero_linear_prep_kernel(const __grid_cons
     const uint16_t* dy = static_cast<const uint16_t*>(a.dy);
     const uint16_t* z = static_cast<const uint16_t*>(a.z);
     uint16_t* dz = static_cast<uint16_t*>(a.dz);
-    const int act = a.act, bf16 = a.bf16;
     float sum[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
@@ -1048,21 +1100,21 @@ __global__ void __launch_bounds__(256) zero_linear_prep_kernel(const __grid_cons
             const uint4 u = *reinterpret_cast<const uint4*>(dy + r * a.lddy + col);
             uint32_t g[4] = {u.x, u.y, u.z, u.w};
             uint32_t h[4] = {};
-            if (act != ZERO_ACT_NONE) {
+            if (ACT != ZERO_ACT_NONE) {
                 const uint4 w = *reinterpret_cast<const uint4*>(z + r * a.ldz + col);
                 h[0] = w.x, h[1] = w.y, h[2] = w.z, h[3] = w.w;
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                float2 d = unpack16(g[j], bf16);
-                if (act != ZERO_ACT_NONE) {
-                    const float2 p = unpack16(h[j], bf16);
-                    d.x *= slope(p.x, act);
-                    d.y *= slope(p.y, act);
+                float2 d = unpack16(g[j], BF16);
+                if (ACT != ZERO_ACT_NONE) {
+                    const float2 p = unpack16(h[j], BF16);
+                    d.x *= slope<ACT>(p.x);
+                    d.y *= slope<ACT>(p.y);
                 }
                 sum[2 * j] += d.x;
                 sum[2 * j + 1] += d.y;
-                g[j] = pack16(d.x, d.y, bf16);
+                g[j] = pack16(d.x, d.y, BF16);
             }
             if (dz) *reinterpret_cast<uint4*>(dz + r * a.lddz + col) = make_uint4(g[0], g[1], g[2], g[3]);
         }
@@ -1073,13 +1125,13 @@ __global__ void __launch_bounds__(256) zero_linear_prep_kernel(const __grid_cons
             for (int j = 0; j < 8; ++j) {
                 d[j] = 0.0f;
                 if (col + j < a.N) {
-                    d[j] = load16(dy, r * a.lddy + col + j, bf16);
-                    if (act != ZERO_ACT_NONE) d[j] *= slope(load16(z, r * a.ldz + col + j, bf16), act);
+                    d[j] = load16(dy, r * a.lddy + col + j, BF16);
+                    if (ACT != ZERO_ACT_NONE) d[j] *= slope<ACT>(load16(z, r * a.ldz + col + j, BF16));
                 }
                 sum[j] += d[j];
             }
             // rows of dz have room for whole vectors
-            if (dz && col < a.N) *reinterpret_cast<uint4*>(dz + r * a.lddz + col) = pack8(d, bf16);
+            if (dz && col < a.N) *reinterpret_cast<uint4*>(dz + r * a.lddz + col) = pack8(d, BF16);
         }
     }
     if (!a.sums) return;
@@ -1136,15 +1188,19 @@ struct Matrix {
     int64_t ld, rows, cols;
 };
 
-int make_map(CUtensorMap* map, const Matrix& x, int box_rows)
+// mn 0, 1: boxes of 64 elements of `extent` rows.  mn 2: boxes of `extent`
+// blocks of 64 elements of 64 rows (cols is a multiple of 64).
+int make_map(CUtensorMap* map, const Matrix& x, int mn, int extent)
 {
     EncodeFn encode = tensor_map_encoder();
     if (!encode) return zero_record_cuda_error(static_cast<int>(cudaErrorNotSupported));
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(x.cols), static_cast<cuuint64_t>(x.rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(x.ld) * 2};
-    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)}, step[2] = {1, 1};
-    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(x.p), dims, strides, box, step,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    const cuuint64_t cols = static_cast<cuuint64_t>(x.cols), rows = static_cast<cuuint64_t>(x.rows);
+    const cuuint64_t dims[3] = {mn == 2 ? 64 : cols, rows, cols / 64};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(x.ld) * 2, 128};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(mn == 2 ? 64 : extent), static_cast<cuuint32_t>(extent)};
+    const cuuint32_t step[3] = {1, 1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, mn == 2 ? 3 : 2, const_cast<void*>(x.p), dims, strides, box,
+                              step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? ZERO_OK : zero_record_cuda_error(static_cast<int>(cudaErrorInvalidValue));
 }
@@ -1158,6 +1214,18 @@ int sm_count(int* out)
 }
 
 using GemmKernel = void (*)(GemmArgs);
+using PrepKernel = void (*)(PrepArgs);
+
+PrepKernel pick_prep(int act, int type)
+{
+    const bool b = type == ZERO_TYPE_BF16;
+    switch (act) {
+    case ZERO_ACT_RELU: return b ? zero_linear_prep_kernel<ZERO_ACT_RELU, 1> : zero_linear_prep_kernel<ZERO_ACT_RELU, 0>;
+    case ZERO_ACT_GELU: return b ? zero_linear_prep_kernel<ZERO_ACT_GELU, 1> : zero_linear_prep_kernel<ZERO_ACT_GELU, 0>;
+    case ZERO_ACT_SILU: return b ? zero_linear_prep_kernel<ZERO_ACT_SILU, 1> : zero_linear_prep_kernel<ZERO_ACT_SILU, 0>;
+    default: return b ? zero_linear_prep_kernel<ZERO_ACT_NONE, 1> : zero_linear_prep_kernel<ZERO_ACT_NONE, 0>;
+    }
+}
 
 // Dynamic shared memory above 48 KB is allowed once per kernel and device.
 int allow_smem(GemmKernel fn, int bytes)
@@ -1177,7 +1245,8 @@ int allow_smem(GemmKernel fn, int bytes)
     return ZERO_OK;
 }
 
-template <int BN> constexpr int kSplitStages = BN >= 128 ? 6 : 8;
+// as many stages as leave room for two CTAs on an SM
+template <int BN> constexpr int kSplitStages = BN >= 128 ? 3 : BN >= 64 ? 4 : BN >= 32 ? 5 : 6;
 template <int BN> constexpr int kSplitSmem = kSplitStages<BN> * kStageBytes<BN> + 1024;
 template <int BN> constexpr int kPairStages = BN >= 256 ? 6 : 8;
 template <int BN> constexpr int kPairSmem = kPairStages<BN> * kPairStage<BN> + kEpilogueBytes + 1024;
@@ -1234,36 +1303,51 @@ int64_t tiles_of(const Product& p, const Variant& v)
 
 int64_t kblocks_of(const Product& p) { return (p.k + kBK - 1) / kBK; }
 
+// Whether a cluster of v.parts CTAs shares a tile's contraction; one with
+// fewer than two blocks a CTA is left whole.
+bool is_cut(const Product& p, const Variant& v) { return v.parts > 1 && kblocks_of(p) >= 2 * v.parts; }
+
+int64_t clusters_of(const Product& p, const Variant& v)
+{
+    const int64_t t = tiles_of(p, v);
+    return v.pair || is_cut(p, v) ? t : (t + v.parts - 1) / v.parts;
+}
+
 Variant choose(const Product* p, int count, int sms)
 {
-    if (count == 1 && p[0].o.swap) { // few tokens: no more columns than that
-        Variant v{false, 128, 1};
-        while (v.bn > 16 && p[0].n <= v.bn / 2) v.bn /= 2;
-        const int64_t tiles = tiles_of(p[0], v);
-        while (v.parts < 8 && tiles * v.parts * 2 <= sms && kblocks_of(p[0]) >= v.parts * 4) v.parts *= 2;
-        return v;
+    // a tile has no more columns than the narrowest operand needs; an MN-major one comes in blocks of 64
+    int widest = 16;
+    for (int k = 0; k < count; ++k) {
+        int bn = p[k].b_mn ? 64 : 16;
+        while (bn < 128 && bn < p[k].n) bn *= 2;
+        widest = std::max(widest, bn);
     }
     double best = 1e30;
     Variant out{true, 256, 1};
     auto consider = [&](Variant v, double per_block, double per_tile) {
-        int64_t ctas = 0;
-        double work = 0.0, longest = 0.0;
+        double work = 0.0, longest = 0.0, ctas = 0.0;
         for (int k = 0; k < count; ++k) {
-            const double one = per_block * std::ceil(static_cast<double>(kblocks_of(p[k])) / v.parts) + per_tile;
-            const int64_t t = tiles_of(p[k], v);
-            ctas += t;
-            work += one * static_cast<double>(t);
+            const int64_t blocks = kblocks_of(p[k]);
+            const double one = per_block * static_cast<double>(is_cut(p[k], v) ? (blocks + v.parts - 1) / v.parts : blocks) +
+                               per_tile;
+            const double c = static_cast<double>(clusters_of(p[k], v)) * v.parts;
+            ctas += c;
+            work += one * c;
             longest = std::max(longest, one);
         }
-        const double slots = v.pair ? sms / 2 : static_cast<double>(sms) / v.parts;
-        const double rounds = std::ceil(static_cast<double>(ctas) / std::floor(slots));
-        const double time = std::max(work / static_cast<double>(ctas) * rounds, longest);
+        const double slots = v.pair ? sms / 2 : 2.0 * sms;
+        const double rounds = std::ceil(ctas / slots);
+        // two CTAs of an SM share its copy and tensor rates
+        const double share = v.pair ? 1.0 : ctas > sms ? std::min(2.0, ctas / sms / rounds) : 1.0;
+        const double time = std::max(work / ctas * rounds * share, longest);
         if (time < best) best = time, out = v;
     };
-    consider({true, 256, 1}, 0.36, 2.0);
-    for (int bn : {128, 64})
+    bool swapped = false;
+    for (int k = 0; k < count; ++k) swapped = swapped || p[k].o.swap;
+    if (!swapped) consider({true, 256, 1}, 0.30, 1.5);
+    for (int bn = widest; bn >= std::min(widest, 64); bn /= 2)
         for (int parts = 1; parts <= 8; parts *= 2)
-            consider({false, bn, parts}, bn == 128 ? 0.24 : 0.18, 3.0 + (parts > 1 ? 1.0 : 0.0));
+            consider({false, bn, parts}, bn == 128 ? 0.20 : bn == 64 ? 0.16 : 0.14, 2.0 + 0.5 * std::log2(parts));
     return out;
 }
 
@@ -1279,22 +1363,24 @@ int gemm(const Product* p, int count, int type, const BiasSum* bias, cudaStream_
     const unsigned int t = type == ZERO_TYPE_BF16 ? 1 : 0;
     for (int k = 0; k < count; ++k) {
         Problem& g = args.p[k];
-        const int bm = v.pair ? 256 : kBM, b_box = v.pair ? v.bn / 2 : v.bn;
+        const int bm = v.pair ? 256 : kBM, b_rows = v.pair ? v.bn / 2 : v.bn;
         g.o = p[k].o;
         g.o.bf16 = type == ZERO_TYPE_BF16;
-        g.a_mn = p[k].a_mn;
-        g.b_mn = p[k].b_mn;
+        g.a_mn = p[k].a_mn ? (p[k].a.cols % 64 == 0 ? 2 : 1) : 0;
+        g.b_mn = p[k].b_mn ? (p[k].b.cols % 64 == 0 ? 2 : 1) : 0;
         g.m = static_cast<int>(p[k].m);
         g.n = static_cast<int>(p[k].n);
         g.tiles_m = static_cast<int>((p[k].m + bm - 1) / bm);
         g.tiles_n = static_cast<int>((p[k].n + v.bn - 1) / v.bn);
         g.kblocks = static_cast<int>(kblocks_of(p[k]));
-        g.idesc = (1u << 4) | (t << 7) | (t << 10) | (static_cast<unsigned int>(g.a_mn) << 15) |
-                  (static_cast<unsigned int>(g.b_mn) << 16) | (static_cast<unsigned int>(v.bn >> 3) << 17) |
+        g.cut = is_cut(p[k], v);
+        g.idesc = (1u << 4) | (t << 7) | (t << 10) | (static_cast<unsigned int>(g.a_mn != 0) << 15) |
+                  (static_cast<unsigned int>(g.b_mn != 0) << 16) | (static_cast<unsigned int>(v.bn >> 3) << 17) |
                   (static_cast<unsigned int>(bm >> 4) << 24);
-        if ((rc = make_map(&g.a, p[k].a, g.a_mn ? 64 : kBM))) return rc;
-        if ((rc = make_map(&g.b, p[k].b, g.b_mn ? 64 : b_box))) return rc;
-        tiles += tiles_of(p[k], v);
+        if ((rc = make_map(&g.a, p[k].a, g.a_mn, g.a_mn == 2 ? kBM / 64 : g.a_mn ? 64 : kBM))) return rc;
+        if ((rc = make_map(&g.b, p[k].b, g.b_mn, g.b_mn == 2 ? b_rows / 64 : g.b_mn ? 64 : b_rows))) return rc;
+        if (tiles_of(p[k], v) > INT32_MAX - 64) return ZERO_EINVAL;
+        tiles += clusters_of(p[k], v);
         if (tiles * v.parts > INT32_MAX) return ZERO_EINVAL;
         if (k == 0) args.tiles0 = static_cast<int>(tiles);
     }
@@ -1325,7 +1411,7 @@ int gemm(const Product* p, int count, int type, const BiasSum* bias, cudaStream_
     default: pick(std::integral_constant<int, 128>{}); break;
     }
     if ((rc = allow_smem(fn, smem))) return rc;
-    return launch_after(fn, args, tiles * v.parts, kGemmThreads, smem, v.parts, stream);
+    return launch_after(fn, args, tiles * v.parts, kSplitThreads, smem, v.parts, stream);
 }
 
 bool aligned16(const void* p, int64_t ld) { return addr(p) % 16 == 0 && ld % 8 == 0; }
@@ -1462,7 +1548,7 @@ extern "C" int zero_linear_forward(const void* x, int64_t ldx, const void* w, in
     PrepArgs prep{};
     if (fix_x) add_copy(&prep, &ctas, 0, &mx, tx);
     if (fix_w) add_copy(&prep, &ctas, 1, &mw, tw);
-    if (ctas && (rc = launch_after(zero_linear_prep_kernel, prep, ctas, 256, 0, 1, st))) return rc;
+    if (ctas && (rc = launch_after(pick_prep(ZERO_ACT_NONE, type), prep, ctas, 256, 0, 1, st))) return rc;
     Out o{};
     o.y = y, o.ldy = ldy, o.z = z, o.ldz = ldz, o.bias = bias, o.res = residual, o.ldr = ldr, o.act = act;
     o.vec = aligned16(y, ldy) && (!z || aligned16(z, ldz)) && (!residual || aligned16(residual, ldr)) && addr(bias) % 16 == 0;
@@ -1525,7 +1611,6 @@ extern "C" int zero_linear_backward(const void* dy, int64_t lddy, const void* z,
     if (make_dz || db) {
         prep.dy = dy, prep.lddy = lddy, prep.z = z, prep.ldz = ldz, prep.dz = tz, prep.lddz = up(N, 8), prep.sums = sums;
         prep.T = T, prep.N = static_cast<int>(N), prep.rows_per = sum_rows(T, N);
-        prep.act = act, prep.bf16 = type == ZERO_TYPE_BF16;
         prep.vec = aligned16(dy, lddy) && (!has_act || aligned16(z, ldz));
         prep.stripes = static_cast<int>((N + kSumCols - 1) / kSumCols);
         prep.chunks = static_cast<int>(chunks);
@@ -1535,7 +1620,7 @@ extern "C" int zero_linear_backward(const void* dy, int64_t lddy, const void* z,
     }
     if (fix_x) add_copy(&prep, &ctas, 0, &mx, tx);
     if (fix_w) add_copy(&prep, &ctas, 1, &mw, tw);
-    if (ctas && (rc = launch_after(zero_linear_prep_kernel, prep, ctas, 256, 0, 1, st))) return rc;
+    if (ctas && (rc = launch_after(pick_prep(act, type), prep, ctas, 256, 0, 1, st))) return rc;
 
     const BiasSum bias{sums, db, static_cast<int>(chunks), static_cast<int>(N)};
     if (!products) {
@@ -1545,11 +1630,9 @@ extern "C" int zero_linear_backward(const void* dy, int64_t lddy, const void* z,
     }
     Product p[2];
     int count = 0;
-    bool few = false;
     if (dx) {
         Out o{};
         o.y = dx, o.ldy = lddx, o.vec = aligned16(dx, lddx), o.swap = T <= kFewTokens;
-        few = o.swap;
         p[count++] = o.swap ? product(mw, 1, mz, 0, o) : product(mz, 0, mw, 1, o);
     }
     if (dw) {
@@ -1558,10 +1641,6 @@ extern "C" int zero_linear_backward(const void* dy, int64_t lddy, const void* z,
         p[count++] = product(mz, 1, mx, 1, o);
     }
     const BiasSum* with = db ? &bias : nullptr;
-    if (few && count == 2) { // the operands of dx change sides: another tile than dw's
-        if ((rc = gemm(p, 1, type, with, st))) return rc;
-        return gemm(p + 1, 1, type, nullptr, st);
-    }
     if (count == 2 && kblocks_of(p[1]) > kblocks_of(p[0])) std::swap(p[0], p[1]); // the longer tiles first
     return gemm(p, count, type, with, st);
 }
