@@ -45,7 +45,6 @@ namespace {
 
 constexpr int kGemmThreads = 384; // warp 0 TMA, warp 1 MMA, warp 2 tensor memory, warp 3 bias sums, warps 4..11 epilogue
 constexpr int kEpilogueWarps = 8;
-constexpr int kSplitThreads = 256; // the same roles, warps 4..7 epilogue: two CTAs fit an SM
 constexpr int kBM = 128;          // rows of a tile: the lanes of tensor memory
 constexpr int kBK = 64;           // contraction per stage: 128 bytes, one swizzle row
 constexpr int kATile = kBM * kBK * 2;
@@ -860,9 +859,17 @@ template <int PARTS> __device__ __forceinline__ void join(const Out& o, const Jo
     }
 }
 
-template <int BN, int STAGES, int COUNT>
-__global__ void __launch_bounds__(kSplitThreads, 2) zero_gemm_split_kernel(const __grid_constant__ GemmArgs args)
+// PER_SM 1: one CTA on an SM, stages as deep as they go, eight epilogue warps.
+// PER_SM 2: half of all that, so that one CTA's start and end run under the
+// other's products and a cluster of eight needs only four SMs.
+template <int BN, int PER_SM> constexpr int kSplitThreads = PER_SM == 2 ? 256 : 384;
+template <int BN, int PER_SM> constexpr int kSplitStages = PER_SM == 1 ? (BN >= 128 ? 6 : 8) : BN >= 64 ? 4 : BN >= 32 ? 5 : 6;
+template <int BN, int PER_SM> constexpr int kSplitSmem = kSplitStages<BN, PER_SM> * kStageBytes<BN> + 1024;
+
+template <int BN, int PER_SM, int COUNT>
+__global__ void __launch_bounds__((kSplitThreads<BN, PER_SM>), PER_SM) zero_gemm_split_kernel(const __grid_constant__ GemmArgs args)
 {
+    constexpr int STAGES = kSplitStages<BN, PER_SM>, kThreads = kSplitThreads<BN, PER_SM>;
     extern __shared__ unsigned char raw[];
     unsigned char* smem = aligned_smem(raw);
     __shared__ uint64_t full[STAGES], empty[STAGES], acc_full, drained;
@@ -965,7 +972,10 @@ __global__ void __launch_bounds__(kSplitThreads, 2) zero_gemm_split_kernel(const
     float* part = reinterpret_cast<float*>(smem);
     const int pitch = (o.swap ? kBM : BN) + 4; // floats; 16-byte accesses free of bank conflicts
     const bool direct = BN >= 64 && parts == 1 && !o.swap; // nothing to join: straight from tensor memory
-    if (warp >= 4 && kb1 > kb0) {
+    // with eight epilogue warps two share 32 rows, each with half of the columns
+    constexpr int kSpan = kThreads == 384 && BN >= 64 ? BN / 2 : BN;
+    const int c0 = ((warp - 4) >> 2) * kSpan;
+    if (warp >= 4 && kb1 > kb0 && c0 < BN) {
         const int q = warp & 3;
         const bool ok = wait(&acc_full, 0, abort);
         if (__all_sync(0xffffffffu, ok)) {
@@ -974,7 +984,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) zero_gemm_split_kernel(const
             const uint32_t acc = base + (static_cast<uint32_t>(q * 32) << 16);
             constexpr int kStep = BN < 32 ? 16 : 32;
 #pragma unroll 1
-            for (int c = 0; c < BN; c += kStep) {
+            for (int c = c0; c < c0 + kSpan; c += kStep) {
                 float v[kStep];
                 if constexpr (kStep == 16) tmem_load16(acc, v);
                 else tmem_load(acc + c, v);
@@ -1012,8 +1022,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) zero_gemm_split_kernel(const
         j.row0 = o.swap ? nt * BN : mt * kBM;
         j.col0 = o.swap ? mt * kBM : nt * BN;
         j.first = g.cut ? 0 : static_cast<uint32_t>(rank);
-        j.self = (g.cut ? rank * kSplitThreads : 0) + static_cast<int>(threadIdx.x);
-        j.everyone = (g.cut ? size : 1) * kSplitThreads;
+        j.self = (g.cut ? rank * kThreads : 0) + static_cast<int>(threadIdx.x);
+        j.everyone = (g.cut ? size : 1) * kThreads;
         switch (parts) {
         case 1: join<1>(o, j); break;
         case 2: join<2>(o, j); break;
@@ -1245,9 +1255,6 @@ int allow_smem(GemmKernel fn, int bytes)
     return ZERO_OK;
 }
 
-// as many stages as leave room for two CTAs on an SM
-template <int BN> constexpr int kSplitStages = BN >= 128 ? 3 : BN >= 64 ? 4 : BN >= 32 ? 5 : 6;
-template <int BN> constexpr int kSplitSmem = kSplitStages<BN> * kStageBytes<BN> + 1024;
 template <int BN> constexpr int kPairStages = BN >= 256 ? 6 : 8;
 template <int BN> constexpr int kPairSmem = kPairStages<BN> * kPairStage<BN> + kEpilogueBytes + 1024;
 
@@ -1268,6 +1275,7 @@ Product product(const Matrix& a, int a_mn, const Matrix& b, int b_mn, const Out&
 struct Variant {
     bool pair;
     int bn, parts; // columns of a tile; CTAs that share a contraction
+    int per_sm;    // CTAs on an SM
 };
 
 struct BiasSum {
@@ -1313,41 +1321,59 @@ int64_t clusters_of(const Product& p, const Variant& v)
     return v.pair || is_cut(p, v) ? t : (t + v.parts - 1) / v.parts;
 }
 
-Variant choose(const Product* p, int count, int sms)
+// The variant with the least estimated time.  The estimates (us) are
+// base + rounds of CTAs x (tail + block x blocks of 64 of the contraction),
+// read off measured times, among them (tokens x inputs -> features):
+//   16 columns, 2 a SM   4 x 2048 -> 8192: contraction cut in 1, 2, 4: 11.5, 8.7, 8.2
+//                        4 x 8192 -> 2048: in 1, 2, 4, 8: 31.3, 18.7, 12.3, 9.3
+//   64 columns, 1 a SM   1024 x 1024 -> 1024: 7.6 (2 a SM 8.7, 128 columns 8.8, pairs 12.2)
+//   64 columns, 2 a SM   2048 x 1024 -> 1024: 9.2 (1 a SM 15.1: its 256 CTAs take two rounds)
+//   128 columns          256 x 4096 -> 4096 cut in 1, 2, 4: 21.2, 16.4, 26.1 (pairs 26.2)
+//   pairs                2048 x 2048 -> 2048: 18.6 (128 columns 25.7); 8192 x 2048 -> 8192: 156
+// A second CTA on the SM (CTAs above the number of SMs) costs the first no
+// time with 64 columns, and about half of its speed with fewer.
+Variant choose(const Product* p, int count, int sms, double* estimate)
 {
-    // a tile has no more columns than the narrowest operand needs; an MN-major one comes in blocks of 64
+    // a tile has no more columns than the widest product needs; an MN-major operand comes in blocks of 64
     int widest = 16;
+    bool swapped = false;
     for (int k = 0; k < count; ++k) {
         int bn = p[k].b_mn ? 64 : 16;
         while (bn < 128 && bn < p[k].n) bn *= 2;
         widest = std::max(widest, bn);
+        swapped = swapped || p[k].o.swap;
     }
     double best = 1e30;
-    Variant out{true, 256, 1};
-    auto consider = [&](Variant v, double per_block, double per_tile) {
+    Variant out{true, 256, 1, 1};
+    auto consider = [&](const Variant& v, double base, double tail, double block) {
         double work = 0.0, longest = 0.0, ctas = 0.0;
         for (int k = 0; k < count; ++k) {
             const int64_t blocks = kblocks_of(p[k]);
-            const double one = per_block * static_cast<double>(is_cut(p[k], v) ? (blocks + v.parts - 1) / v.parts : blocks) +
-                               per_tile;
+            const double one =
+                block * static_cast<double>(is_cut(p[k], v) ? (blocks + v.parts - 1) / v.parts : blocks) + tail;
             const double c = static_cast<double>(clusters_of(p[k], v)) * v.parts;
             ctas += c;
             work += one * c;
             longest = std::max(longest, one);
         }
-        const double slots = v.pair ? sms / 2 : 2.0 * sms;
-        const double rounds = std::ceil(ctas / slots);
-        // two CTAs of an SM share its copy and tensor rates
-        const double share = v.pair ? 1.0 : ctas > sms ? std::min(2.0, ctas / sms / rounds) : 1.0;
-        const double time = std::max(work / ctas * rounds * share, longest);
+        const double rounds = std::ceil(ctas / (v.pair ? sms / 2 : v.per_sm * sms));
+        const double time = base + std::max(work / ctas * rounds, longest);
         if (time < best) best = time, out = v;
     };
-    bool swapped = false;
-    for (int k = 0; k < count; ++k) swapped = swapped || p[k].o.swap;
-    if (!swapped) consider({true, 256, 1}, 0.30, 1.5);
-    for (int bn = widest; bn >= std::min(widest, 64); bn /= 2)
-        for (int parts = 1; parts <= 8; parts *= 2)
-            consider({false, bn, parts}, bn == 128 ? 0.20 : bn == 64 ? 0.16 : 0.14, 2.0 + 0.5 * std::log2(parts));
+    if (!swapped) consider({true, 256, 1, 1}, 6.3, 1.5, 0.30);
+    for (int parts = 1; parts <= 8; parts *= 2) {
+        const double join = std::log2(parts);
+        if (widest == 128) consider({false, 128, parts, 1}, 2.2, 2.0 + 2.2 * join, 0.29);
+        if (widest >= 64) {
+            consider({false, 64, parts, 1}, 2.0, 1.7 + 1.5 * join, 0.25);
+            consider({false, 64, parts, 2}, 2.0, 1.7 + 2.4 * join, 0.34);
+        }
+        if (widest <= 32) {
+            const bool crowded = tiles_of(p[0], {false, widest, parts, 2}) * parts > sms;
+            consider({false, widest, parts, 2}, 3.5, 2.0 + 0.3 * join, !crowded ? 0.20 : widest == 16 ? 0.35 : 0.45);
+        }
+    }
+    *estimate = best;
     return out;
 }
 
@@ -1357,7 +1383,8 @@ int gemm(const Product* p, int count, int type, const BiasSum* bias, cudaStream_
     int sms = 0;
     int rc = sm_count(&sms);
     if (rc) return rc;
-    const Variant v = choose(p, count, sms);
+    double estimate;
+    const Variant v = choose(p, count, sms, &estimate);
     GemmArgs args{};
     int64_t tiles = 0;
     const unsigned int t = type == ZERO_TYPE_BF16 ? 1 : 0;
@@ -1399,19 +1426,21 @@ int gemm(const Product* p, int count, int type, const BiasSum* bias, cudaStream_
     }
     GemmKernel fn = nullptr;
     int smem = 0;
-    auto pick = [&](auto tag) {
-        constexpr int BN = decltype(tag)::value;
-        fn = count == 1 ? zero_gemm_split_kernel<BN, kSplitStages<BN>, 1> : zero_gemm_split_kernel<BN, kSplitStages<BN>, 2>;
-        smem = kSplitSmem<BN>;
+    int threads = 0;
+    auto pick = [&](auto columns, auto per_sm) {
+        constexpr int BN = decltype(columns)::value, PER = decltype(per_sm)::value;
+        fn = count == 1 ? zero_gemm_split_kernel<BN, PER, 1> : zero_gemm_split_kernel<BN, PER, 2>;
+        smem = kSplitSmem<BN, PER>;
+        threads = kSplitThreads<BN, PER>;
     };
-    switch (v.bn) {
-    case 16: pick(std::integral_constant<int, 16>{}); break;
-    case 32: pick(std::integral_constant<int, 32>{}); break;
-    case 64: pick(std::integral_constant<int, 64>{}); break;
-    default: pick(std::integral_constant<int, 128>{}); break;
-    }
+    using std::integral_constant;
+    if (v.bn == 16) pick(integral_constant<int, 16>{}, integral_constant<int, 2>{});
+    else if (v.bn == 32) pick(integral_constant<int, 32>{}, integral_constant<int, 2>{});
+    else if (v.bn == 64 && v.per_sm == 2) pick(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+    else if (v.bn == 64) pick(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+    else pick(integral_constant<int, 128>{}, integral_constant<int, 1>{});
     if ((rc = allow_smem(fn, smem))) return rc;
-    return launch_after(fn, args, tiles * v.parts, kSplitThreads, smem, v.parts, stream);
+    return launch_after(fn, args, tiles * v.parts, threads, smem, v.parts, stream);
 }
 
 bool aligned16(const void* p, int64_t ld) { return addr(p) % 16 == 0 && ld % 8 == 0; }
@@ -1641,6 +1670,20 @@ extern "C" int zero_linear_backward(const void* dy, int64_t lddy, const void* z,
         p[count++] = product(mz, 1, mx, 1, o);
     }
     const BiasSum* with = db ? &bias : nullptr;
+    if (count == 2 && p[0].o.swap) {
+        // few tokens: the products want tiles of different shapes, so one launch is not always the quicker form
+        // (64 tokens, 2048 -> 2048: 10 us in one, 24 in two; 4 tokens, 2048 -> 8192: 30 in one, 27 in two)
+        int sms = 0;
+        if ((rc = sm_count(&sms))) return rc;
+        double one, first, second;
+        choose(p, 2, sms, &one);
+        choose(p, 1, sms, &first);
+        choose(p + 1, 1, sms, &second);
+        if (first + second < one) {
+            if ((rc = gemm(p, 1, type, with, st))) return rc;
+            return gemm(p + 1, 1, type, nullptr, st);
+        }
+    }
     if (count == 2 && kblocks_of(p[1]) > kblocks_of(p[0])) std::swap(p[0], p[1]); // the longer tiles first
     return gemm(p, count, type, with, st);
 }
