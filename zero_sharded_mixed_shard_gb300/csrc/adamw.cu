@@ -132,6 +132,23 @@ template <int T> __device__ __forceinline__ Raw8<T> load8(const void* p)
     return r;
 }
 
+template <int T> __device__ __forceinline__ void set8(float (&v)[8], const Raw8<T>& r)
+{
+    const unsigned int u[4] = {r.a[0].x, r.a[0].y, r.a[0].z, r.a[0].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (T == ZERO_TYPE_FP32) {
+            const unsigned int w[4] = {r.a[1].x, r.a[1].y, r.a[1].z, r.a[1].w};
+            v[j] = __uint_as_float(u[j]);
+            v[4 + j] = __uint_as_float(w[j]);
+        } else {
+            const float2 f = unpack2<T>(u[j]);
+            v[2 * j] = f.x;
+            v[2 * j + 1] = f.y;
+        }
+    }
+}
+
 template <int T> __device__ __forceinline__ void add8(float (&acc)[8], const Raw8<T>& r)
 {
     const unsigned int u[4] = {r.a[0].x, r.a[0].y, r.a[0].z, r.a[0].w};
@@ -152,10 +169,23 @@ template <int T> __device__ __forceinline__ void add8(float (&acc)[8], const Raw
     }
 }
 
+// x / d from r close to 1 / d: the quotient x r and one correction step by its
+// exact remainder (P. Markstein, IBM J. Res. Dev. 34(1), 1990).  For x a sum of
+// gradients and d a number of ranks the result is the correctly rounded one
+// (zero_selftest_mean_division) unless it is below fp32's normal range.  It
+// has no rare path, unlike CUDA's division, whose call costs the step's loop
+// its registers.
+__device__ __forceinline__ float divide(float x, float d, float r)
+{
+    const float q = __fmul_rn(x, r);
+    const float c = __fmaf_rn(__fmaf_rn(-q, d, x), r, q);
+    return fabsf(q) < __int_as_float(0x7f800000) ? c : q; // an infinite quotient has no remainder
+}
+
 __device__ __forceinline__ float mean_of(float sum, const Args& a)
 {
     if (a.P == 1) return sum;
-    return a.p_pow2 ? __fmul_rn(sum, a.inv_p) : __fdiv_rn(sum, static_cast<float>(a.P));
+    return a.p_pow2 ? __fmul_rn(sum, a.inv_p) : divide(sum, static_cast<float>(a.P), a.inv_p);
 }
 
 // The tensor that chunk c belongs to: the last one whose first chunk is <= c
@@ -171,208 +201,262 @@ __device__ __forceinline__ int find_tensor(const long long* first, int n, long l
     return lo;
 }
 
+// Programmatic launch: the wait returns when the preceding kernel is complete
+// and its writes are visible; nothing is read before it.
+__device__ __forceinline__ void wait_for_predecessor() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_successor_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+__device__ __forceinline__ float fast_sqrt(float x)
+{
+    float y;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x)); // relative error at most 2^-23
+    return y;
+}
+
+__device__ __forceinline__ float fast_rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x)); // 1 ulp
+    return y;
+}
+
 // ---------------------------------------------------------------------------
 // The step
 // ---------------------------------------------------------------------------
 
-// One warp per block of 256 elements.  Where a tensor's streams share one
-// 16-byte phase a lane owns 8 consecutive elements (whole-vector accesses;
-// the few lanes at the tensor's ends go element by element); otherwise lane l
-// owns elements l, l + 32, ... of the block, one access each.  The two differ
-// in which lane holds an element and in nothing else: results are the same.
+// What a warp knows of its block of 256 elements besides the tensor.
+struct Block {
+    float lr, decay, factor;
+    unsigned int key;    // of the tensor and the seed
+    long long scale;     // index of the block's scales
+};
+
+// The update of a lane's eight elements in registers.  g: sums over the
+// ranks.  With 8-bit moments mc, vc hold the codes and receive the new ones;
+// the whole warp calls it, and `pair(j)` is element j's place in its tensor's
+// pairs, `odd(j)` its place in the pair.
+template <int BITS, bool ONE, class Pair, class Odd>
+__device__ __forceinline__ void update(const Args& a, const Tensor* x, const Block& k, float (&w)[8], float (&m)[8],
+                                       float (&v)[8], const float (&g)[8], unsigned int (&mc)[2], unsigned int (&vc)[2],
+                                       Pair pair, Odd odd)
+{
+    if constexpr (BITS == 8) {
+        const float ms = x->ms[k.scale], vs = x->vs[k.scale];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const unsigned short cm = static_cast<unsigned short>(mc[q >> 1] >> (16 * (q & 1)));
+            const unsigned short cv = static_cast<unsigned short>(vc[q >> 1] >> (16 * (q & 1)));
+            const float2 fm = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(cm, __NV_E4M3)));
+            const float2 fv = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(cv, __NV_E4M3)));
+            m[2 * q] = __fmul_rn(fm.x, ms);
+            m[2 * q + 1] = __fmul_rn(fm.y, ms);
+            const float rx = __fmul_rn(fv.x, vs), ry = __fmul_rn(fv.y, vs);
+            v[2 * q] = __fmul_rn(rx, rx);
+            v[2 * q + 1] = __fmul_rn(ry, ry);
+        }
+    }
+    unsigned int high_m = 0, high_r = 0; // largest magnitudes, as bits: ordered like the values, NaN above infinity
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float gg = __fmul_rn(ONE ? g[j] : mean_of(g[j], a), k.factor);
+        m[j] = __fadd_rn(__fmul_rn(m[j], a.b1), __fmul_rn(gg, a.omb1));
+        v[j] = __fadd_rn(__fmul_rn(v[j], a.b2), __fmul_rn(__fmul_rn(gg, gg), a.omb2));
+        const float root = fast_sqrt(v[j]);
+        const float inv = fast_rcp(__fadd_rn(__fmul_rn(root, a.c2), a.eps));
+        w[j] = __fsub_rn(w[j], __fmul_rn(k.decay, w[j]));
+        w[j] = __fsub_rn(w[j], __fmul_rn(k.lr, __fmul_rn(__fmul_rn(m[j], a.r1), inv)));
+        if constexpr (BITS == 8) {
+            v[j] = root;
+            high_m = max(high_m, __float_as_uint(m[j]) & 0x7fffffffu);
+            high_r = max(high_r, __float_as_uint(root));
+        }
+    }
+    if constexpr (BITS == 8) {
+        high_m = __reduce_max_sync(0xffffffffu, high_m);
+        high_r = __reduce_max_sync(0xffffffffu, high_r);
+        const float am = __uint_as_float(high_m), ar = __uint_as_float(high_r);
+        const float im = am < kTiny ? 0.0f : divide(kMax8, am, fast_rcp(am)), ir = ar < kTiny ? 0.0f : divide(kMax8, ar, fast_rcp(ar));
+        if ((threadIdx.x & 31) == 0) {
+            const float nan = __int_as_float(0x7fffffff);
+            x->ms[k.scale] = am < kTiny ? 0.0f : isfinite(am) ? __fmul_rn(am, kInvMax8) : nan;
+            x->vs[k.scale] = ar < kTiny ? 0.0f : isfinite(ar) ? __fmul_rn(ar, kInvMax8) : nan;
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const unsigned int lo = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(m[4 * q], im), __fmul_rn(m[4 * q + 1], im)),
+                                                             __NV_SATFINITE, __NV_E4M3);
+            const unsigned int hi = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(m[4 * q + 2], im), __fmul_rn(m[4 * q + 3], im)),
+                                                             __NV_SATFINITE, __NV_E4M3);
+            mc[q] = lo + (hi << 16);
+        }
+        unsigned int h = 0, code[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            // Sixteen random bits for each element, one hash for a pair.
+            if (j == 0 || pair(j) != pair(j - 1)) h = mix32(pair(j) + k.key);
+            const unsigned int random = odd(j) ? h >> 16 : h & 0xffffu;
+            // Scaled by 2^-120 a value's E4M3 code is the top of its binary32
+            // form (bits 30..20; E4M3's subnormals are fp32's), and adding
+            // random bits below bit 20 before cutting there rounds up with
+            // the probability of what is cut.  A zero stays 0, a root above
+            // zero is at least 1.
+            const float y = __fmul_rn(v[j], ir);
+            const unsigned int cut = (__float_as_uint(__fmul_rn(y, 7.52316384526264e-37f)) + (random << 4)) >> 20;
+            code[j] = min(max(cut, min(__float_as_uint(y), 1u)), 0x7eu);
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            vc[q] = (code[4 * q] + (code[4 * q + 1] << 8)) + ((code[4 * q + 2] << 16) + (code[4 * q + 3] << 24));
+    }
+}
+
+// A block at a tensor's end, or of a tensor whose streams do not share one
+// phase: lane l has elements l, l + 32, ..., one access each.  Kept out of the
+// main path's registers.
 template <int GT, int PT, int BITS>
+__device__ __noinline__ void step_by_elements(const Args& a, const Tensor* x, float lr, float decay, float factor,
+                                               unsigned int key, long long b0, float go)
+{
+    const Block k{lr, decay, factor, key, b0 / kBlock};
+    using G = typename Elem<GT>::type;
+    const long long n = x->n, stride = x->stride, first = b0 + (threadIdx.x & 31);
+    float w[8], m[8], v[8], g[8];
+    unsigned int mc[2] = {0u, 0u}, vc[2] = {0u, 0u};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const long long i = first + j * 32;
+        w[j] = m[j] = v[j] = g[j] = 0.0f;
+        if (i < 0 || i >= n) continue;
+        w[j] = x->w[i];
+        if constexpr (BITS == 32) {
+            m[j] = static_cast<const float*>(x->m)[i];
+            v[j] = static_cast<const float*>(x->v)[i];
+        } else {
+            mc[j >> 2] |= static_cast<unsigned int>(static_cast<const unsigned char*>(x->m)[i]) << (8 * (j & 3));
+            vc[j >> 2] |= static_cast<unsigned int>(static_cast<const unsigned char*>(x->v)[i]) << (8 * (j & 3));
+        }
+        g[j] = to_float(static_cast<const G*>(x->g)[i]);
+    }
+    for (int r = 1; r < a.P; ++r)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const long long i = first + j * 32;
+            if (i >= 0 && i < n) g[j] = __fadd_rn(g[j], to_float(static_cast<const G*>(x->g)[r * stride + i]));
+        }
+    if (go == 0.0f) return;
+    update<BITS, false>(a, x, k, w, m, v, g, mc, vc, [&](int j) { return static_cast<unsigned int>((first + j * 32) >> 1); },
+                        [&](int) { return (first & 1) != 0; });
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const long long i = first + j * 32;
+        if (i < 0 || i >= n) continue;
+        x->w[i] = w[j];
+        if constexpr (BITS == 32) {
+            static_cast<float*>(x->m)[i] = m[j];
+            static_cast<float*>(x->v)[i] = v[j];
+        } else {
+            static_cast<unsigned char*>(x->m)[i] = static_cast<unsigned char>(mc[j >> 2] >> (8 * (j & 3)));
+            static_cast<unsigned char*>(x->v)[i] = static_cast<unsigned char>(vc[j >> 2] >> (8 * (j & 3)));
+        }
+        static_cast<unsigned short*>(x->p)[i] = static_cast<unsigned short>(pack2<PT>(w[j], 0.0f));
+    }
+}
+
+// One warp per block of 256 elements.  Where a tensor's streams share one
+// 16-byte phase a lane owns 8 consecutive elements (whole-vector accesses);
+// the blocks at its ends, and every block of other tensors, go element by
+// element.  The two differ in which lane holds an element and in nothing
+// else: results are the same.
+template <int GT, int PT, int BITS, bool ONE>
 __global__ void __launch_bounds__(kThreads, 4) zero_adamw_kernel(const __grid_constant__ Args a)
 {
     using G = typename Elem<GT>::type;
-    using P16 = typename Elem<PT>::type;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float factor = 1.0f, go = 1.0f;
+    let_successor_start();
+    wait_for_predecessor();
+    Block k;
+    float go = 1.0f;
+    k.factor = 1.0f;
     if (a.stats) {
-        factor = a.stats[1];
+        k.factor = a.stats[1];
         go = a.stats[2];
     }
-    int ti = 0;
-    long long lo = 0, hi = 0;
-    Tensor x{};
-    unsigned int key = 0;
-    float lr = 0.0f, decay = 0.0f;
+    long long lo = 0, hi = 0, n = 0;
+    int phase = 0;
+    const Tensor* x = nullptr;
     for (long long c = blockIdx.x; c < a.chunks; c += gridDim.x) {
         if (c >= hi) {
-            ti = find_tensor(a.first, a.n_tensors, c);
+            const int ti = find_tensor(a.first, a.n_tensors, c);
             lo = __ldg(a.first + ti);
             hi = __ldg(a.first + ti + 1);
-            x = a.tensors[ti];
-            lr = __fmul_rn(a.lr, x.lr_scale);
-            decay = __fmul_rn(lr, x.decay);
-            if constexpr (BITS == 8) key = mix32(mix32(a.seed) + 0x9e3779b9u * static_cast<unsigned int>(ti + 1));
+            x = a.tensors + ti;
+            n = x->n;
+            phase = x->phase;
+            k.lr = __fmul_rn(a.lr, x->lr_scale);
+            k.decay = __fmul_rn(k.lr, x->decay);
+            k.key = BITS == 8 ? mix32(mix32(a.seed) + 0x9e3779b9u * static_cast<unsigned int>(ti + 1)) : 0u;
         }
-        const bool vec = x.phase >= 0;
-        const long long b0 = (c - lo) * kChunk + warp * kBlock - (vec ? x.phase : 0); // the block's first element
-        const long long i0 = vec ? b0 + lane * 8 : b0 + lane;                         // the lane's first element
-        const int step = vec ? 1 : 32;
-        const bool whole = vec && i0 >= 0 && i0 + 8 <= x.n;
-        if (b0 >= x.n) continue;
-
+        const long long b0 = (c - lo) * kChunk + warp * kBlock - max(phase, 0); // the block's first element
+        if (b0 >= n) continue;
+        k.scale = b0 / kBlock; // used with 8-bit moments only: blocks then start on multiples of 256
+        if (phase < 0 || b0 < 0 || b0 + kBlock > n) {
+            step_by_elements<GT, PT, BITS>(a, x, k.lr, k.decay, k.factor, k.key, b0, go);
+            if (go == 0.0f) return;
+            continue;
+        }
+        const long long i0 = b0 + lane * 8;
         float w[8], m[8], v[8], g[8];
+        unsigned int mc[2] = {0u, 0u}, vc[2] = {0u, 0u}; // 8-bit codes
+        float4* wp = reinterpret_cast<float4*>(x->w + i0);
+        *reinterpret_cast<float4*>(w) = __ldcs(wp);
+        *reinterpret_cast<float4*>(w + 4) = __ldcs(wp + 1);
+        if constexpr (BITS == 32) {
+            const float4* mp = reinterpret_cast<const float4*>(static_cast<float*>(x->m) + i0);
+            const float4* vp = reinterpret_cast<const float4*>(static_cast<float*>(x->v) + i0);
+            *reinterpret_cast<float4*>(m) = __ldcs(mp);
+            *reinterpret_cast<float4*>(m + 4) = __ldcs(mp + 1);
+            *reinterpret_cast<float4*>(v) = __ldcs(vp);
+            *reinterpret_cast<float4*>(v + 4) = __ldcs(vp + 1);
+        } else {
+            const uint2 mm = __ldcs(reinterpret_cast<const uint2*>(static_cast<unsigned char*>(x->m) + i0));
+            const uint2 vv = __ldcs(reinterpret_cast<const uint2*>(static_cast<unsigned char*>(x->v) + i0));
+            mc[0] = mm.x, mc[1] = mm.y, vc[0] = vv.x, vc[1] = vv.y;
+        }
+        const G* gp = static_cast<const G*>(x->g) + i0;
+        if constexpr (ONE) {
+            set8<GT>(g, load8<GT>(gp));
+        } else {
+            const long long stride = x->stride;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] = 0.0f;
-        unsigned int mc[2] = {0u, 0u}, vc[2] = {0u, 0u}; // 8-bit codes as loaded
-        if (whole) {
-            const float4* wp = reinterpret_cast<const float4*>(x.w + i0);
-            *reinterpret_cast<float4*>(w) = __ldcs(wp);
-            *reinterpret_cast<float4*>(w + 4) = __ldcs(wp + 1);
-            if constexpr (BITS == 32) {
-                const float4* mp = reinterpret_cast<const float4*>(static_cast<float*>(x.m) + i0);
-                const float4* vp = reinterpret_cast<const float4*>(static_cast<float*>(x.v) + i0);
-                *reinterpret_cast<float4*>(m) = __ldcs(mp);
-                *reinterpret_cast<float4*>(m + 4) = __ldcs(mp + 1);
-                *reinterpret_cast<float4*>(v) = __ldcs(vp);
-                *reinterpret_cast<float4*>(v + 4) = __ldcs(vp + 1);
-            } else {
-                const uint2 mm = __ldcs(reinterpret_cast<const uint2*>(static_cast<unsigned char*>(x.m) + i0));
-                const uint2 vv = __ldcs(reinterpret_cast<const uint2*>(static_cast<unsigned char*>(x.v) + i0));
-                mc[0] = mm.x, mc[1] = mm.y, vc[0] = vv.x, vc[1] = vv.y;
-            }
-            const G* gp = static_cast<const G*>(x.g) + i0;
+            for (int j = 0; j < 8; ++j) g[j] = 0.0f;
             int r = 0;
             for (; r + 4 <= a.P; r += 4) {
                 Raw8<GT> raw[4];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) raw[q] = load8<GT>(gp + (r + q) * x.stride);
+                for (int q = 0; q < 4; ++q) raw[q] = load8<GT>(gp + (r + q) * stride);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) add8<GT>(g, raw[q]);
             }
-            for (; r < a.P; ++r) add8<GT>(g, load8<GT>(gp + r * x.stride));
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const long long i = i0 + j * step;
-                w[j] = m[j] = v[j] = 0.0f;
-                if (i < 0 || i >= x.n) continue;
-                w[j] = x.w[i];
-                if constexpr (BITS == 32) {
-                    m[j] = static_cast<const float*>(x.m)[i];
-                    v[j] = static_cast<const float*>(x.v)[i];
-                } else {
-                    mc[j >> 2] |= static_cast<unsigned int>(static_cast<const unsigned char*>(x.m)[i]) << (8 * (j & 3));
-                    vc[j >> 2] |= static_cast<unsigned int>(static_cast<const unsigned char*>(x.v)[i]) << (8 * (j & 3));
-                }
-                const G* gp = static_cast<const G*>(x.g) + i;
-                for (int r = 0; r < a.P; ++r) g[j] = __fadd_rn(g[j], to_float(gp[r * x.stride]));
-            }
+            for (; r < a.P; ++r) add8<GT>(g, load8<GT>(gp + r * stride));
         }
         if (go == 0.0f) return; // a gradient overflowed: nothing is written
-
-        const long long block = (b0 >= 0 ? b0 : 0) / kBlock;
-        if constexpr (BITS == 8) {
-            const float ms = x.ms[block], vs = x.vs[block];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const unsigned short cm = static_cast<unsigned short>(mc[q >> 1] >> (16 * (q & 1)));
-                const unsigned short cv = static_cast<unsigned short>(vc[q >> 1] >> (16 * (q & 1)));
-                const __half2_raw hm = __nv_cvt_fp8x2_to_halfraw2(cm, __NV_E4M3);
-                const __half2_raw hv = __nv_cvt_fp8x2_to_halfraw2(cv, __NV_E4M3);
-                const float2 fm = __half22float2(__half2(hm)), fv = __half22float2(__half2(hv));
-                m[2 * q] = __fmul_rn(fm.x, ms);
-                m[2 * q + 1] = __fmul_rn(fm.y, ms);
-                const float rx = __fmul_rn(fv.x, vs), ry = __fmul_rn(fv.y, vs);
-                v[2 * q] = __fmul_rn(rx, rx);
-                v[2 * q + 1] = __fmul_rn(ry, ry);
-            }
-        }
-
-        unsigned int high_m = 0, high_r = 0; // largest magnitudes, as bits: ordered like the values, NaN above infinity
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float gg = __fmul_rn(mean_of(g[j], a), factor);
-            m[j] = __fadd_rn(__fmul_rn(m[j], a.b1), __fmul_rn(gg, a.omb1));
-            v[j] = __fadd_rn(__fmul_rn(v[j], a.b2), __fmul_rn(__fmul_rn(gg, gg), a.omb2));
-            const float root = __fsqrt_rn(v[j]);
-            w[j] = __fsub_rn(w[j], __fmul_rn(decay, w[j]));
-            w[j] = __fsub_rn(w[j], __fmul_rn(lr, __fdividef(__fmul_rn(m[j], a.r1),
-                                                            __fadd_rn(__fmul_rn(root, a.c2), a.eps))));
-            if constexpr (BITS == 8) {
-                v[j] = root;
-                high_m = max(high_m, __float_as_uint(m[j]) & 0x7fffffffu);
-                high_r = max(high_r, __float_as_uint(root) & 0x7fffffffu);
-            }
-        }
-
-        unsigned int qm[2] = {0u, 0u}, qv[2] = {0u, 0u};
-        if constexpr (BITS == 8) {
-            high_m = __reduce_max_sync(0xffffffffu, high_m);
-            high_r = __reduce_max_sync(0xffffffffu, high_r);
-            const float am = __uint_as_float(high_m), ar = __uint_as_float(high_r);
-            const float im = am < kTiny ? 0.0f : __fdiv_rn(kMax8, am), ir = ar < kTiny ? 0.0f : __fdiv_rn(kMax8, ar);
-            if (lane == 0) {
-                const float nan = __int_as_float(0x7fffffff);
-                x.ms[block] = am < kTiny ? 0.0f : isfinite(am) ? __fmul_rn(am, kInvMax8) : nan;
-                x.vs[block] = ar < kTiny ? 0.0f : isfinite(ar) ? __fmul_rn(ar, kInvMax8) : nan;
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const __nv_fp8x2_storage_t two = __nv_cvt_float2_to_fp8x2(
-                    make_float2(__fmul_rn(m[2 * q], im), __fmul_rn(m[2 * q + 1], im)), __NV_SATFINITE, __NV_E4M3);
-                qm[q >> 1] |= static_cast<unsigned int>(two) << (16 * (q & 1));
-            }
-            unsigned int h = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                // Sixteen random bits per element, one hash for the two elements of a pair.
-                unsigned int bits16;
-                if (vec) {
-                    if ((j & 1) == 0) h = mix32(static_cast<unsigned int>((i0 + j) >> 1) + key);
-                    bits16 = (j & 1) ? h >> 16 : h & 0xffffu;
-                } else {
-                    const long long i = i0 + j * 32;
-                    h = mix32(static_cast<unsigned int>(i >> 1) + key);
-                    bits16 = (i & 1) ? h >> 16 : h & 0xffffu;
-                }
-                // Scaled by 2^-120 a value's E4M3 code is the top of its
-                // binary32 form (bits 30..20; E4M3's subnormals are fp32's),
-                // and adding random bits below bit 20 before cutting there
-                // rounds up with the probability of what is cut.
-                const float y = __fmul_rn(v[j], ir);
-                unsigned int code = (__float_as_uint(__fmul_rn(y, 7.52316384526264e-37f)) + (bits16 << 4)) >> 20;
-                code = y > 0.0f ? min(max(code, 1u), 0x7eu) : 0u;
-                qv[j >> 2] |= code << (8 * (j & 3));
-            }
-        }
-
-        if (whole) {
-            float4* wp = reinterpret_cast<float4*>(x.w + i0);
-            __stcs(wp, *reinterpret_cast<float4*>(w));
-            __stcs(wp + 1, *reinterpret_cast<float4*>(w + 4));
-            if constexpr (BITS == 32) {
-                float4* mp = reinterpret_cast<float4*>(static_cast<float*>(x.m) + i0);
-                float4* vp = reinterpret_cast<float4*>(static_cast<float*>(x.v) + i0);
-                __stcs(mp, *reinterpret_cast<float4*>(m));
-                __stcs(mp + 1, *reinterpret_cast<float4*>(m + 4));
-                __stcs(vp, *reinterpret_cast<float4*>(v));
-                __stcs(vp + 1, *reinterpret_cast<float4*>(v + 4));
-            } else {
-                __stcs(reinterpret_cast<uint2*>(static_cast<unsigned char*>(x.m) + i0), make_uint2(qm[0], qm[1]));
-                __stcs(reinterpret_cast<uint2*>(static_cast<unsigned char*>(x.v) + i0), make_uint2(qv[0], qv[1]));
-            }
-            __stcs(reinterpret_cast<uint4*>(static_cast<P16*>(x.p) + i0),
-                   make_uint4(pack2<PT>(w[0], w[1]), pack2<PT>(w[2], w[3]), pack2<PT>(w[4], w[5]), pack2<PT>(w[6], w[7])));
+        update<BITS, ONE>(a, x, k, w, m, v, g, mc, vc, [&](int j) { return static_cast<unsigned int>(i0 >> 1) + (j >> 1); },
+                          [](int j) { return (j & 1) != 0; });
+        __stcs(wp, *reinterpret_cast<float4*>(w));
+        __stcs(wp + 1, *reinterpret_cast<float4*>(w + 4));
+        if constexpr (BITS == 32) {
+            float4* mp = reinterpret_cast<float4*>(static_cast<float*>(x->m) + i0);
+            float4* vp = reinterpret_cast<float4*>(static_cast<float*>(x->v) + i0);
+            __stcs(mp, *reinterpret_cast<float4*>(m));
+            __stcs(mp + 1, *reinterpret_cast<float4*>(m + 4));
+            __stcs(vp, *reinterpret_cast<float4*>(v));
+            __stcs(vp + 1, *reinterpret_cast<float4*>(v + 4));
         } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const long long i = i0 + j * step;
-                if (i < 0 || i >= x.n) continue;
-                x.w[i] = w[j];
-                if constexpr (BITS == 32) {
-                    static_cast<float*>(x.m)[i] = m[j];
-                    static_cast<float*>(x.v)[i] = v[j];
-                } else {
-                    static_cast<unsigned char*>(x.m)[i] = static_cast<unsigned char>(qm[j >> 2] >> (8 * (j & 3)));
-                    static_cast<unsigned char*>(x.v)[i] = static_cast<unsigned char>(qv[j >> 2] >> (8 * (j & 3)));
-                }
-                const unsigned short h = static_cast<unsigned short>(pack2<PT>(w[j], 0.0f));
-                reinterpret_cast<unsigned short*>(x.p)[i] = h;
-            }
+            __stcs(reinterpret_cast<uint2*>(static_cast<unsigned char*>(x->m) + i0), make_uint2(mc[0], mc[1]));
+            __stcs(reinterpret_cast<uint2*>(static_cast<unsigned char*>(x->v) + i0), make_uint2(vc[0], vc[1]));
         }
+        __stcs(reinterpret_cast<uint4*>(static_cast<unsigned short*>(x->p) + i0),
+               make_uint4(pack2<PT>(w[0], w[1]), pack2<PT>(w[2], w[3]), pack2<PT>(w[4], w[5]), pack2<PT>(w[6], w[7])));
     }
 }
 
@@ -389,57 +473,67 @@ __global__ void __launch_bounds__(kThreads, 4) zero_grad_norm_kernel(const __gri
 {
     using G = typename Elem<GT>::type;
     const int tid = threadIdx.x;
+    let_successor_start();
+    wait_for_predecessor();
     float sum = 0.0f, comp = 0.0f;
     auto add = [&](float s) {
         const float y = __fsub_rn(s, comp), t = __fadd_rn(sum, y);
         comp = __fsub_rn(__fsub_rn(t, sum), y);
         sum = t;
     };
-    long long lo = 0, hi = 0;
-    Tensor x{};
+    long long lo = 0, hi = 0, n = 0, stride = 0;
+    int phase = 0;
+    const G* gp = nullptr;
     for (long long c = blockIdx.x; c < a.chunks; c += gridDim.x) {
         if (c >= hi) {
             const int ti = find_tensor(a.first, a.n_tensors, c);
             lo = __ldg(a.first + ti);
             hi = __ldg(a.first + ti + 1);
-            x = a.tensors[ti];
+            const Tensor* x = a.tensors + ti;
+            n = x->n;
+            stride = x->stride;
+            phase = x->gphase;
+            gp = static_cast<const G*>(x->g);
         }
-        const bool vec = x.gphase >= 0;
-        const long long c0 = (c - lo) * kNormChunk - (vec ? x.gphase : 0);
-        const G* gp = static_cast<const G*>(x.g);
-        if (vec && c0 >= 0 && c0 + kNormChunk <= x.n) {
-            float acc[kNormVecs][8];
+        const long long c0 = (c - lo) * kNormChunk - max(phase, 0);
+        float acc[kNormVecs][8];
 #pragma unroll
-            for (int k = 0; k < kNormVecs; ++k)
+        for (int k = 0; k < kNormVecs; ++k)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) acc[k][j] = 0.0f;
+            for (int j = 0; j < 8; ++j) acc[k][j] = 0.0f;
+        if (phase >= 0 && c0 >= 0 && c0 + kNormChunk <= n) {
             for (int r = 0; r < a.P; ++r) {
                 Raw8<GT> raw[kNormVecs];
 #pragma unroll
-                for (int k = 0; k < kNormVecs; ++k)
-                    raw[k] = load8<GT>(gp + r * x.stride + c0 + (k * kThreads + tid) * 8);
+                for (int k = 0; k < kNormVecs; ++k) raw[k] = load8<GT>(gp + r * stride + c0 + (k * kThreads + tid) * 8);
 #pragma unroll
                 for (int k = 0; k < kNormVecs; ++k) add8<GT>(acc[k], raw[k]);
             }
+        } else { // a tensor's end, or rows off 16 bytes: one element an access, lanes side by side, the loads of a rank together
+            for (int r = 0; r < a.P; ++r) {
+                const G* row = gp + r * stride + c0 + tid;
 #pragma unroll
-            for (int k = 0; k < kNormVecs; ++k) {
-                float s = 0.0f;
+                for (int k = 0; k < kNormVecs; ++k) {
+                    float e[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float g = mean_of(acc[k][j], a);
-                    s = fmaf(g, g, s);
+                    for (int j = 0; j < 8; ++j) {
+                        const long long at = c0 + tid + (k * 8 + j) * kThreads;
+                        e[j] = at >= 0 && at < n ? to_float(row[(k * 8 + j) * kThreads]) : 0.0f;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) acc[k][j] = __fadd_rn(acc[k][j], e[j]);
                 }
-                add(s);
             }
-        } else {
-            for (int k = tid; k < kNormChunk; k += kThreads) {
-                const long long i = c0 + k;
-                if (i < 0 || i >= x.n) continue;
-                float g = 0.0f;
-                for (int r = 0; r < a.P; ++r) g = __fadd_rn(g, to_float(gp[r * x.stride + i]));
-                g = mean_of(g, a);
-                add(__fmul_rn(g, g));
+        }
+#pragma unroll
+        for (int k = 0; k < kNormVecs; ++k) {
+            float s = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float g = mean_of(acc[k][j], a);
+                s = fmaf(g, g, s);
             }
+            add(s);
         }
     }
 
@@ -514,22 +608,23 @@ int resident_ctas(Kernel fn, int* out)
     return ZERO_OK;
 }
 
-template <int GT, int PT> Kernel pick_bits(int bits)
+template <int GT, int PT> Kernel pick_bits(int bits, bool one)
 {
-    return bits == 32 ? zero_adamw_kernel<GT, PT, 32> : zero_adamw_kernel<GT, PT, 8>;
+    if (bits == 32) return one ? zero_adamw_kernel<GT, PT, 32, true> : zero_adamw_kernel<GT, PT, 32, false>;
+    return one ? zero_adamw_kernel<GT, PT, 8, true> : zero_adamw_kernel<GT, PT, 8, false>;
 }
 
-template <int GT> Kernel pick_param(int param, int bits)
+template <int GT> Kernel pick_param(int param, int bits, bool one)
 {
-    return param == ZERO_TYPE_FP16 ? pick_bits<GT, ZERO_TYPE_FP16>(bits) : pick_bits<GT, ZERO_TYPE_BF16>(bits);
+    return param == ZERO_TYPE_FP16 ? pick_bits<GT, ZERO_TYPE_FP16>(bits, one) : pick_bits<GT, ZERO_TYPE_BF16>(bits, one);
 }
 
-Kernel pick_step(int grad, int param, int bits)
+Kernel pick_step(int grad, int param, int bits, int P)
 {
     switch (grad) {
-    case ZERO_TYPE_FP16: return pick_param<ZERO_TYPE_FP16>(param, bits);
-    case ZERO_TYPE_BF16: return pick_param<ZERO_TYPE_BF16>(param, bits);
-    default: return pick_param<ZERO_TYPE_FP32>(param, bits);
+    case ZERO_TYPE_FP16: return pick_param<ZERO_TYPE_FP16>(param, bits, P == 1);
+    case ZERO_TYPE_BF16: return pick_param<ZERO_TYPE_BF16>(param, bits, P == 1);
+    default: return pick_param<ZERO_TYPE_FP32>(param, bits, P == 1);
     }
 }
 
@@ -578,8 +673,17 @@ int launch(Kernel fn, const Args& a, long long most, void* stream)
     const int rc = resident_ctas(fn, &fit);
     if (rc) return rc;
     const long long ctas = std::max(1ll, std::min(std::min<long long>(fit, most), static_cast<long long>(a.chunks)));
-    fn<<<static_cast<unsigned int>(ctas), kThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    // the kernel may be set up while its predecessor ends (it waits for it before it reads anything)
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned int>(ctas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, a);
     return e == cudaSuccess ? ZERO_OK : record(e);
 }
 
@@ -751,5 +855,5 @@ extern "C" int zero_adamw_step(const zero_adamw_plan_t* plan, void* table, const
     a.c2 = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(static_cast<double>(beta2), static_cast<double>(t))));
     a.eps = eps;
     a.seed = seed;
-    return launch(pick_step(plan->grad_type, plan->param_type, plan->state_bits), a, INT64_MAX, cuda_stream);
+    return launch(pick_step(plan->grad_type, plan->param_type, plan->state_bits, plan->P), a, INT64_MAX, cuda_stream);
 }
