@@ -57,6 +57,8 @@ typedef struct {
     int32_t param_type;
     int32_t state_bits; /* 32, 8, or 0: gradients only (zero_grad_norm) */
     int32_t vector_tensors; /* tensors whose streams share one 16-byte phase: whole-vector accesses */
+    int32_t pipeline;       /* 1: all of them do (8-bit codes on 16 bytes), a large step may copy in bulk */
+    int32_t reserved;
     int64_t elements;   /* of all tensors */
     int64_t chunks;     /* units of work of a step */
     int64_t norm_chunks;
@@ -186,10 +188,10 @@ int zero_linear_backward(const void* dy, int64_t lddy, const void* z, int64_t ld
                          int32_t type, void* workspace, int64_t workspace_bytes,
                          void* cuda_stream);
 
-/* Bounded waits of the linear layer's kernels that gave up on the current
+/* Bounded waits of the kernels of this header that gave up on the current
  * device since the last reset; like zero_device_timeouts (0 in every correct
  * run, reading it synchronises). */
-int zero_linear_timeouts(int64_t* count, int32_t reset);
+int zero_train_timeouts(int64_t* count, int32_t reset);
 
 #ifdef __cplusplus
 }

@@ -162,6 +162,38 @@ def test_step(z, bits, P, gt, pt, shift, pad, congruent):
         c.check(before, t)
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("P,gt,pt,shift", [(1, 0, 0, 0), (1, 2, 1, 0), (2, 1, 0, 0), (3, 0, 1, 0), (8, 0, 0, 0), (4, 1, 1, 5), (40, 0, 0, 0)])
+def test_many_chunks(z, bits, P, gt, pt, shift):
+    """Enough chunks for the pipeline of bulk copies (P = 40 has too few stages for it), with ragged ends, tiny tensors
+    between, and a skipped step; 32-bit moments also against the vector kernel, tensor by tensor, bit for bit."""
+    sizes = [1500000, 257, 0, 1300001, 64, 5000, 255]
+    c = Case(z, sizes, P, gt, pt, bits, shift, seed=P)
+    assert c.plan.info.chunks >= 1216 and c.plan.info.pipeline == (1 if bits == 32 or shift == 0 else 0)
+    for t in (1, 20):
+        before = c.state()
+        z.zero_adamw_step(c.plan, None, t, LR, B1, B2, EPS, t)
+        torch.cuda.synchronize()
+        c.check(before, t)
+    after = c.state()
+    if bits == 32:
+        for x, y in zip((c.master, c.m, c.v, c.param), before):
+            x.copy_(y)
+        for k, n in enumerate(sizes):
+            o = c.offs[k]
+            if n:
+                one = z.zero_adamw_plan([dict(grad=c.g[0, o:], rank_stride=c.stride, master=c.master[o:], m=c.m[o:], v=c.v[o:],
+                                              param=c.param[o:], n=n, weight_decay=c.wd[k], lr_scale=c.ls[k])], P, gt, pt, bits)
+                assert one.info.chunks < 1216
+                z.zero_adamw_step(one, None, 20, LR, B1, B2, EPS, 20)
+        for x, y in zip(c.state(), after):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    z.zero_adamw_step(c.plan, torch.zeros(3, device="cuda"), 21, LR, B1, B2, EPS, 21)
+    for x, y in zip(c.state(), after):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    assert z.zero_train_timeouts() == 0
+
+
 def test_paths_agree(z):
     """The same tensors on whole vectors and element by element: the same bits."""
     for bits in (32, 8):

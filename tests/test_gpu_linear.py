@@ -23,7 +23,7 @@ def z(zlib):
     if not torch.cuda.is_available():
         pytest.fail("the GPU tests need a CUDA device")
     yield zlib
-    assert zlib.zero_linear_timeouts() == 0
+    assert zlib.zero_train_timeouts() == 0
 
 
 def act64(a, z):

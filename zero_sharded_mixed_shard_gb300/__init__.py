@@ -52,7 +52,7 @@ EXPORTED = ("zero_init_layout", "zero_free_layout", "zero_shard_range", "zero_me
             "zero_last_cuda_error", "zero_last_cuda_error_string",
             "zero_adamw_plan", "zero_grad_norm", "zero_adamw_step",
             "zero_linear_workspace", "zero_linear_forward", "zero_linear_backward",
-            "zero_linear_timeouts")
+            "zero_train_timeouts")
 
 
 class ZeroError(RuntimeError):
@@ -100,6 +100,7 @@ class zero_adamw_plan_t(ctypes.Structure):
     _fields_ = [("n_tensors", ctypes.c_int32), ("P", ctypes.c_int32),
                 ("grad_type", ctypes.c_int32), ("param_type", ctypes.c_int32),
                 ("state_bits", ctypes.c_int32), ("vector_tensors", ctypes.c_int32),
+                ("pipeline", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("elements", ctypes.c_int64), ("chunks", ctypes.c_int64),
                 ("norm_chunks", ctypes.c_int64), ("table_bytes", ctypes.c_int64)]
 
@@ -192,8 +193,8 @@ def lib() -> ctypes.CDLL:
     L.zero_linear_backward.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp,
                                        i64, i64, i64, i32, i32, vp, i64, vp]
     L.zero_linear_backward.restype = ctypes.c_int
-    L.zero_linear_timeouts.argtypes = [ctypes.POINTER(ctypes.c_int64), i32]
-    L.zero_linear_timeouts.restype = ctypes.c_int
+    L.zero_train_timeouts.argtypes = [ctypes.POINTER(ctypes.c_int64), i32]
+    L.zero_train_timeouts.restype = ctypes.c_int
     L.zero_strerror.argtypes = [ctypes.c_int]
     L.zero_strerror.restype = ctypes.c_char_p
     L.zero_last_cuda_error.argtypes = []
@@ -575,11 +576,11 @@ def zero_linear_backward(dy, lddy: int, z, ldz: int, x, ldx: int, w, ldw: int, d
         raise ZeroError(rc, "zero_linear_backward")
 
 
-def zero_linear_timeouts(reset: bool = False) -> int:
-    """Bounded waits of the linear layer's kernels that gave up (0 in a
+def zero_train_timeouts(reset: bool = False) -> int:
+    """Bounded waits of the training operators' kernels that gave up (0 in a
     correct run); synchronises with the device."""
     n = ctypes.c_int64()
-    rc = lib().zero_linear_timeouts(ctypes.byref(n), 1 if reset else 0)
+    rc = lib().zero_train_timeouts(ctypes.byref(n), 1 if reset else 0)
     if rc:
-        raise ZeroError(rc, "zero_linear_timeouts")
+        raise ZeroError(rc, "zero_train_timeouts")
     return n.value

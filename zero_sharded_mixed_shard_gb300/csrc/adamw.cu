@@ -75,6 +75,7 @@ struct Args {
     const float* stats;
     float lr, b1, b2, omb1, omb2, r1, c2, eps;
     unsigned int seed;
+    int stages, stage_bytes; // pipeline kernel
     float grad_scale, max_norm;
     float* out;
 };
@@ -461,6 +462,239 @@ __global__ void __launch_bounds__(kThreads, 4) zero_adamw_kernel(const __grid_co
 }
 
 // ---------------------------------------------------------------------------
+// The step as a pipeline of bulk copies
+// ---------------------------------------------------------------------------
+
+// One CTA per SM.  A warp copies whole chunks (2048 elements of master, m, v
+// and every rank's gradients) into a ring of shared-memory stages; groups of
+// eight warps take the chunks in turn, a warp a block of 256, hand the stage
+// back as soon as they have read it, and store their results directly.  The
+// copies in flight do not depend on the warps' registers, which bounds the
+// vector kernel: 1.3e9 parameters ...
+constexpr int kGroups = 3;
+constexpr int kPipeThreads = 32 + kGroups * kThreads;
+// A multiple of the groups: a stage always goes to the same group, which so
+// waits for each of its fills in turn (a wait tells a fill from the next one
+// only by parity).
+constexpr int kMaxStages = 15;
+constexpr int kPipeSmem = 225 * 1024;
+constexpr int kMinStages = kGroups;
+static_assert(kMaxStages % kGroups == 0, "stages by groups");
+constexpr int kPipeChunks = 1216; // chunks from which the pipeline pays
+constexpr unsigned long long kWaitLimitNs = 2000000000ull;
+
+__device__ unsigned int g_adamw_timeouts;
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+
+__device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done)
+                 : "r"(smem_addr(bar)), "r"(parity)
+                 : "memory");
+    return done != 0;
+}
+
+// Waits for the phase of the given parity; false when two seconds have passed
+// or another warp has given up.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort)
+{
+    unsigned long long t0, t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+    for (int round = 0; round < (1 << 22); ++round) {
+        for (int k = 0; k < 64; ++k)
+            if (mbar_try(bar, parity)) return true;
+        if (abort && *abort) return false;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+        if (t - t0 > kWaitLimitNs) break;
+    }
+    if (abort && atomicExch(const_cast<int*>(abort), 1) == 0) atomicAdd(&g_adamw_timeouts, 1u);
+    return false;
+}
+
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort)
+{
+    return mbar_try(bar, parity) || wait_slow(bar, parity, abort);
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_addr(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_addr(bar))
+                 : "memory");
+}
+
+// What the copying warp says about a stage's chunk.
+struct Chunk {
+    const Tensor* x;
+    long long b0;        // first element of its first block (may be negative)
+    int from, to;        // blocks that are in the stage; the others go element by element
+    float lr, decay;
+    unsigned int key;
+};
+
+template <int GT, int PT, int BITS, bool ONE>
+__global__ void __launch_bounds__(kPipeThreads, 1) zero_adamw_pipeline_kernel(const __grid_constant__ Args a)
+{
+    using G = typename Elem<GT>::type;
+    constexpr int kGrad = kChunk * static_cast<int>(sizeof(G)); // bytes of a rank's row, of a moment's
+    constexpr int kMoment = kChunk * BITS / 8;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages];
+    __shared__ Chunk meta[kMaxStages];
+    __shared__ int abort_flag;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    volatile int* abort = &abort_flag;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < a.stages; ++s) {
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(&full[s])), "r"(1) : "memory");
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(&empty[s])), "r"(kWarps) : "memory");
+        }
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async;" ::: "memory");
+    }
+    __syncthreads();
+    let_successor_start();
+    wait_for_predecessor();
+    float factor = 1.0f;
+    if (a.stats) {
+        factor = a.stats[1];
+        if (a.stats[2] == 0.0f) return; // a gradient overflowed: nothing is written
+    }
+    if (warp == 0) {
+        long long lo = 0, hi = 0, n = 0, stride = 0;
+        Tensor x{};
+        Chunk k{};
+        int it = 0;
+        bool ok = true;
+        for (long long c = blockIdx.x; ok && c < a.chunks; c += gridDim.x, ++it) {
+            if (c >= hi) {
+                const int ti = find_tensor(a.first, a.n_tensors, c);
+                lo = __ldg(a.first + ti);
+                hi = __ldg(a.first + ti + 1);
+                k.x = a.tensors + ti;
+                x = *k.x;
+                n = x.n;
+                stride = x.stride;
+                k.lr = __fmul_rn(a.lr, x.lr_scale);
+                k.decay = __fmul_rn(k.lr, x.decay);
+                k.key = BITS == 8 ? mix32(mix32(a.seed) + 0x9e3779b9u * static_cast<unsigned int>(ti + 1)) : 0u;
+            }
+            const int s = it % a.stages;
+            ok = wait(&empty[s], ((it / a.stages) & 1) ^ 1, abort);
+            if (!ok) break;
+            k.b0 = (c - lo) * kChunk - max(x.phase, 0);
+            k.from = k.b0 < 0 ? 1 : 0;
+            k.to = static_cast<int>(max(0ll, min(static_cast<long long>(kWarps), (n - k.b0) / kBlock)));
+            if (x.phase < 0 || k.to <= k.from) k.from = k.to = 0;
+            const long long e0 = k.b0 + k.from * kBlock;
+            const uint32_t count = static_cast<uint32_t>(k.to - k.from) * kBlock;
+            if (lane == 0) {
+                meta[s] = k;
+                const uint32_t bytes = count * (4 + BITS / 4 + static_cast<uint32_t>(sizeof(G)) * a.P);
+                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(&full[s])), "r"(bytes)
+                             : "memory");
+            }
+            __syncwarp();
+            if (count > 0) { // one row a lane
+                unsigned char* st = smem + s * a.stage_bytes;
+                const int at = k.from * kBlock;
+                for (int row = lane; row < 3 + a.P; row += 32) {
+                    if (row == 0) bulk_load(st + at * 4, x.w + e0, count * 4, &full[s]);
+                    else if (row == 1) bulk_load(st + kChunk * 4 + at * BITS / 8, static_cast<unsigned char*>(x.m) + e0 * (BITS / 8), count * (BITS / 8), &full[s]);
+                    else if (row == 2) bulk_load(st + kChunk * 4 + kMoment + at * BITS / 8, static_cast<unsigned char*>(x.v) + e0 * (BITS / 8), count * (BITS / 8), &full[s]);
+                    else bulk_load(st + kChunk * 4 + 2 * kMoment + (row - 3) * kGrad + at * sizeof(G), static_cast<const G*>(x.g) + (row - 3) * stride + e0, count * static_cast<uint32_t>(sizeof(G)), &full[s]);
+                }
+            }
+        }
+        if (!ok) // the copies in flight land before the CTA ends
+            for (int k2 = max(0, it - a.stages); k2 < it; ++k2) wait_slow(&full[k2 % a.stages], (k2 / a.stages) & 1, nullptr);
+        return;
+    }
+    const int group = (warp - 1) / kWarps, mine = (warp - 1) % kWarps;
+    int it = 0;
+    for (long long c = blockIdx.x; c < a.chunks; c += gridDim.x, ++it) {
+        if (it % kGroups != group) continue;
+        const int s = it % a.stages;
+        const bool ok = wait(&full[s], (it / a.stages) & 1, abort);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        const Chunk& ch = meta[s];
+        const Tensor* x = ch.x;
+        const long long b0 = ch.b0 + mine * kBlock;
+        Block k{ch.lr, ch.decay, factor, ch.key, b0 / kBlock};
+        const bool staged = mine >= ch.from && mine < ch.to;
+        if (!staged) {
+            __syncwarp();
+            if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&empty[s])) : "memory");
+            if (b0 < x->n) step_by_elements<GT, PT, BITS>(a, x, k.lr, k.decay, factor, k.key, b0, 1.0f);
+            continue;
+        }
+        // lane l has elements 4 l .. 4 l + 3 of each half of the block: accesses of 16 bytes (fp32) side by side
+        const unsigned char* st = smem + s * a.stage_bytes;
+        const int at = mine * kBlock + lane * 4;
+        float w[8], m[8], v[8], g[8];
+        unsigned int mc[2] = {0u, 0u}, vc[2] = {0u, 0u};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int e = at + h * 128;
+            *reinterpret_cast<float4*>(w + 4 * h) = *reinterpret_cast<const float4*>(st + e * 4);
+            if constexpr (BITS == 32) {
+                *reinterpret_cast<float4*>(m + 4 * h) = *reinterpret_cast<const float4*>(st + (kChunk + e) * 4);
+                *reinterpret_cast<float4*>(v + 4 * h) = *reinterpret_cast<const float4*>(st + (2 * kChunk + e) * 4);
+            } else {
+                mc[h] = *reinterpret_cast<const unsigned int*>(st + kChunk * 4 + e);
+                vc[h] = *reinterpret_cast<const unsigned int*>(st + kChunk * 4 + kMoment + e);
+            }
+        }
+        const unsigned char* gr = st + kChunk * 4 + 2 * kMoment + at * sizeof(G);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] = 0.0f;
+#pragma unroll 4
+        for (int r = 0; r < (ONE ? 1 : a.P); ++r)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float f[4];
+                const unsigned char* q = gr + r * kGrad + h * 128 * sizeof(G);
+                if constexpr (GT == ZERO_TYPE_FP32) {
+                    *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(q);
+                } else {
+                    const uint2 u = *reinterpret_cast<const uint2*>(q);
+                    const float2 f0 = unpack2<GT>(u.x), f1 = unpack2<GT>(u.y);
+                    f[0] = f0.x, f[1] = f0.y, f[2] = f1.x, f[3] = f1.y;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) g[4 * h + j] = ONE ? f[j] : __fadd_rn(g[4 * h + j], f[j]);
+            }
+        __syncwarp();
+        if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&empty[s])) : "memory");
+        const long long i0 = b0 + lane * 4;
+        update<BITS, ONE>(a, x, k, w, m, v, g, mc, vc,
+                          [&](int j) { return static_cast<unsigned int>(i0 >> 1) + (j >> 1) + (j >= 4 ? 62u : 0u); },
+                          [](int j) { return (j & 1) != 0; });
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const long long i = i0 + h * 128;
+            __stcs(reinterpret_cast<float4*>(x->w + i), *reinterpret_cast<float4*>(w + 4 * h));
+            if constexpr (BITS == 32) {
+                __stcs(reinterpret_cast<float4*>(static_cast<float*>(x->m) + i), *reinterpret_cast<float4*>(m + 4 * h));
+                __stcs(reinterpret_cast<float4*>(static_cast<float*>(x->v) + i), *reinterpret_cast<float4*>(v + 4 * h));
+            } else {
+                __stcs(reinterpret_cast<unsigned int*>(static_cast<unsigned char*>(x->m) + i), mc[h]);
+                __stcs(reinterpret_cast<unsigned int*>(static_cast<unsigned char*>(x->v) + i), vc[h]);
+            }
+            __stcs(reinterpret_cast<uint2*>(static_cast<unsigned short*>(x->p) + i),
+                   make_uint2(pack2<PT>(w[4 * h], w[4 * h + 1]), pack2<PT>(w[4 * h + 2], w[4 * h + 3])));
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
 // The norm
 // ---------------------------------------------------------------------------
 
@@ -582,8 +816,9 @@ using Kernel = void (*)(Args);
 
 int record(cudaError_t e) { return zero_record_cuda_error(static_cast<int>(e)); }
 
-// CTAs of a kernel that fit the current device at once, asked for once.
-int resident_ctas(Kernel fn, int* out)
+// CTAs of a kernel that fit the current device at once, asked for once (and
+// its shared memory allowed).
+int resident_ctas(Kernel fn, int threads, int smem, int* out)
 {
     static std::mutex mu;
     static std::vector<std::pair<std::pair<int, Kernel>, int>> known;
@@ -597,7 +832,8 @@ int resident_ctas(Kernel fn, int* out)
             return ZERO_OK;
         }
     int per_sm = 0, sms = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, kThreads, 0);
+    if (smem) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, threads, static_cast<size_t>(smem));
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return record(e);
     *out = std::max(1, per_sm * sms);
@@ -608,18 +844,25 @@ int resident_ctas(Kernel fn, int* out)
     return ZERO_OK;
 }
 
-template <int GT, int PT> Kernel pick_bits(int bits, bool one)
+struct StepKernels {
+    Kernel vector, pipeline;
+};
+
+template <int GT, int PT> StepKernels pick_bits(int bits, bool one)
 {
-    if (bits == 32) return one ? zero_adamw_kernel<GT, PT, 32, true> : zero_adamw_kernel<GT, PT, 32, false>;
-    return one ? zero_adamw_kernel<GT, PT, 8, true> : zero_adamw_kernel<GT, PT, 8, false>;
+    if (bits == 32)
+        return one ? StepKernels{zero_adamw_kernel<GT, PT, 32, true>, zero_adamw_pipeline_kernel<GT, PT, 32, true>}
+                   : StepKernels{zero_adamw_kernel<GT, PT, 32, false>, zero_adamw_pipeline_kernel<GT, PT, 32, false>};
+    return one ? StepKernels{zero_adamw_kernel<GT, PT, 8, true>, zero_adamw_pipeline_kernel<GT, PT, 8, true>}
+               : StepKernels{zero_adamw_kernel<GT, PT, 8, false>, zero_adamw_pipeline_kernel<GT, PT, 8, false>};
 }
 
-template <int GT> Kernel pick_param(int param, int bits, bool one)
+template <int GT> StepKernels pick_param(int param, int bits, bool one)
 {
     return param == ZERO_TYPE_FP16 ? pick_bits<GT, ZERO_TYPE_FP16>(bits, one) : pick_bits<GT, ZERO_TYPE_BF16>(bits, one);
 }
 
-Kernel pick_step(int grad, int param, int bits, int P)
+StepKernels pick_step(int grad, int param, int bits, int P)
 {
     switch (grad) {
     case ZERO_TYPE_FP16: return pick_param<ZERO_TYPE_FP16>(param, bits, P == 1);
@@ -667,16 +910,17 @@ Args base_args(const zero_adamw_plan_t* plan, void* table, bool norm)
     return a;
 }
 
-int launch(Kernel fn, const Args& a, long long most, void* stream)
+int launch(Kernel fn, const Args& a, long long most, int threads, int smem, void* stream)
 {
     int fit = 0;
-    const int rc = resident_ctas(fn, &fit);
+    const int rc = resident_ctas(fn, threads, smem, &fit);
     if (rc) return rc;
     const long long ctas = std::max(1ll, std::min(std::min<long long>(fit, most), static_cast<long long>(a.chunks)));
     // the kernel may be set up while its predecessor ends (it waits for it before it reads anything)
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned int>(ctas));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(static_cast<unsigned int>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -758,6 +1002,8 @@ int plan_tensors(const zero_adamw_tensor_t* tensors, int32_t n_tensors, int32_t 
                 if ((bits == 32 || ph == 0) && phase_is(addr(t.grad), gs, ph) && (stride * gs) % 16 == 0 &&
                     phase_is(addr(t.master), 4, ph) && phase_is(addr(t.m), ss, ph) && phase_is(addr(t.v), ss, ph))
                     x.phase = ph;
+                // bulk copies start on 16 bytes, which the phase grants all streams but the 8-bit codes
+                if (x.phase < 0 || (bits == 8 && (addr(t.m) % 16 || addr(t.v) % 16))) plan->pipeline = 0;
                 chunks = (t.n + std::max(x.phase, 0) + kChunk - 1) / kChunk;
                 plan->vector_tensors += x.phase >= 0;
             }
@@ -805,6 +1051,7 @@ extern "C" int zero_adamw_plan(const zero_adamw_tensor_t* tensors, int32_t n_ten
     p.grad_type = grad_type;
     p.param_type = state_bits ? param_type : ZERO_TYPE_FP16;
     p.state_bits = state_bits;
+    p.pipeline = state_bits != 0;
     p.table_bytes = table_size(n_tensors);
     if (table_out && table_bytes < p.table_bytes) return ZERO_EINVAL;
     try {
@@ -831,7 +1078,7 @@ extern "C" int zero_grad_norm(const zero_adamw_plan_t* plan, void* table, float 
     a.grad_scale = grad_scale;
     a.max_norm = max_norm;
     a.out = stats;
-    return launch(pick_norm(plan->grad_type), a, kMaxPartials, cuda_stream);
+    return launch(pick_norm(plan->grad_type), a, kMaxPartials, kThreads, 0, cuda_stream);
 }
 
 extern "C" int zero_adamw_step(const zero_adamw_plan_t* plan, void* table, const float* stats, int64_t t, float lr,
@@ -855,5 +1102,22 @@ extern "C" int zero_adamw_step(const zero_adamw_plan_t* plan, void* table, const
     a.c2 = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(static_cast<double>(beta2), static_cast<double>(t))));
     a.eps = eps;
     a.seed = seed;
-    return launch(pick_step(plan->grad_type, plan->param_type, plan->state_bits, plan->P), a, INT64_MAX, cuda_stream);
+    const StepKernels fn = pick_step(plan->grad_type, plan->param_type, plan->state_bits, plan->P);
+    const int64_t stage = kChunk * (4 + plan->state_bits / 4 + (plan->grad_type == ZERO_TYPE_FP32 ? 4 : 2) * int64_t{plan->P});
+    a.stages = static_cast<int>(std::min<int64_t>(kMaxStages, kPipeSmem / stage) / kGroups * kGroups);
+    a.stage_bytes = static_cast<int>(std::min<int64_t>(stage, kPipeSmem));
+    if (plan->pipeline && a.stages >= kMinStages && plan->chunks >= kPipeChunks)
+        return launch(fn.pipeline, a, INT64_MAX, kPipeThreads, kPipeSmem, cuda_stream);
+    return launch(fn.vector, a, INT64_MAX, kThreads, 0, cuda_stream);
+}
+
+// Bounded waits of the pipeline that gave up (zero_train_timeouts adds them).
+__attribute__((visibility("hidden"))) int zero_adamw_wait_timeouts(unsigned int* count, int reset)
+{
+    cudaError_t e = cudaMemcpyFromSymbol(count, g_adamw_timeouts, sizeof(*count));
+    if (e == cudaSuccess && reset) {
+        const unsigned int zero = 0;
+        e = cudaMemcpyToSymbol(g_adamw_timeouts, &zero, sizeof(zero));
+    }
+    return e == cudaSuccess ? ZERO_OK : record(e);
 }

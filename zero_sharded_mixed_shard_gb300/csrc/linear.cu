@@ -22,7 +22,7 @@
 // its products to one launch where they take the same kernel.
 //
 // Every wait is bounded: one that runs out counts itself
-// (zero_linear_timeouts), the CTA lets its copies and products in flight end,
+// (zero_train_timeouts), the CTA lets its copies and products in flight end,
 // frees its tensor memory and returns.
 #include <cuda.h> // driver types only: the tensor-map encoder is found through the runtime
 #include <cuda_bf16.h>
@@ -40,6 +40,8 @@
 
 // Defined in step.cu (not exported): keeps zero_last_cuda_error current.
 __attribute__((visibility("hidden"))) int zero_record_cuda_error(int err);
+// Defined in adamw.cu (not exported): the step's part of zero_train_timeouts.
+__attribute__((visibility("hidden"))) int zero_adamw_wait_timeouts(unsigned int* count, int reset);
 
 namespace {
 
@@ -1688,7 +1690,7 @@ extern "C" int zero_linear_backward(const void* dy, int64_t lddy, const void* z,
     return gemm(p, count, type, with, st);
 }
 
-extern "C" int zero_linear_timeouts(int64_t* count, int32_t reset)
+extern "C" int zero_train_timeouts(int64_t* count, int32_t reset)
 {
     if (!count) return ZERO_EINVAL;
     unsigned int n = 0;
@@ -1698,6 +1700,9 @@ extern "C" int zero_linear_timeouts(int64_t* count, int32_t reset)
         e = cudaMemcpyToSymbol(g_linear_timeouts, &zero, sizeof(zero));
     }
     if (e != cudaSuccess) return record(e);
-    *count = n;
+    unsigned int steps = 0;
+    const int rc = zero_adamw_wait_timeouts(&steps, reset);
+    if (rc) return rc;
+    *count = static_cast<int64_t>(n) + steps;
     return ZERO_OK;
 }
