@@ -225,11 +225,13 @@ __device__ __forceinline__ float fast_rcp(float x)
 // The step
 // ---------------------------------------------------------------------------
 
-// What a warp knows of its block of 256 elements besides the tensor.
+// What a warp knows of its block of 256 elements besides the elements.
 struct Block {
     float lr, decay, factor;
     unsigned int key;    // of the tensor and the seed
-    long long scale;     // index of the block's scales
+    float ms, vs;        // 8-bit moments: the block's scales, and where the new ones go
+    float* ms_out;
+    float* vs_out;
 };
 
 // The update of a lane's eight elements in registers.  g: sums over the
@@ -237,12 +239,12 @@ struct Block {
 // the whole warp calls it, and `pair(j)` is element j's place in its tensor's
 // pairs, `odd(j)` its place in the pair.
 template <int BITS, bool ONE, class Pair, class Odd>
-__device__ __forceinline__ void update(const Args& a, const Tensor* x, const Block& k, float (&w)[8], float (&m)[8],
+__device__ __forceinline__ void update(const Args& a, const Block& k, float (&w)[8], float (&m)[8],
                                        float (&v)[8], const float (&g)[8], unsigned int (&mc)[2], unsigned int (&vc)[2],
                                        Pair pair, Odd odd)
 {
     if constexpr (BITS == 8) {
-        const float ms = x->ms[k.scale], vs = x->vs[k.scale];
+        const float ms = k.ms, vs = k.vs;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const unsigned short cm = static_cast<unsigned short>(mc[q >> 1] >> (16 * (q & 1)));
@@ -279,8 +281,8 @@ __device__ __forceinline__ void update(const Args& a, const Tensor* x, const Blo
         const float im = am < kTiny ? 0.0f : divide(kMax8, am, fast_rcp(am)), ir = ar < kTiny ? 0.0f : divide(kMax8, ar, fast_rcp(ar));
         if ((threadIdx.x & 31) == 0) {
             const float nan = __int_as_float(0x7fffffff);
-            x->ms[k.scale] = am < kTiny ? 0.0f : isfinite(am) ? __fmul_rn(am, kInvMax8) : nan;
-            x->vs[k.scale] = ar < kTiny ? 0.0f : isfinite(ar) ? __fmul_rn(ar, kInvMax8) : nan;
+            *k.ms_out = am < kTiny ? 0.0f : isfinite(am) ? __fmul_rn(am, kInvMax8) : nan;
+            *k.vs_out = ar < kTiny ? 0.0f : isfinite(ar) ? __fmul_rn(ar, kInvMax8) : nan;
         }
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -318,9 +320,15 @@ template <int GT, int PT, int BITS>
 __device__ __noinline__ void step_by_elements(const Args& a, const Tensor* x, float lr, float decay, float factor,
                                                unsigned int key, long long b0, float go)
 {
-    const Block k{lr, decay, factor, key, b0 / kBlock};
     using G = typename Elem<GT>::type;
     const long long n = x->n, stride = x->stride, first = b0 + (threadIdx.x & 31);
+    Block k{lr, decay, factor, key, 0.0f, 0.0f, nullptr, nullptr};
+    if constexpr (BITS == 8) {
+        k.ms_out = x->ms + b0 / kBlock;
+        k.vs_out = x->vs + b0 / kBlock;
+        k.ms = *k.ms_out;
+        k.vs = *k.vs_out;
+    }
     float w[8], m[8], v[8], g[8];
     unsigned int mc[2] = {0u, 0u}, vc[2] = {0u, 0u};
 #pragma unroll
@@ -345,7 +353,7 @@ __device__ __noinline__ void step_by_elements(const Args& a, const Tensor* x, fl
             if (i >= 0 && i < n) g[j] = __fadd_rn(g[j], to_float(static_cast<const G*>(x->g)[r * stride + i]));
         }
     if (go == 0.0f) return;
-    update<BITS, false>(a, x, k, w, m, v, g, mc, vc, [&](int j) { return static_cast<unsigned int>((first + j * 32) >> 1); },
+    update<BITS, false>(a, k, w, m, v, g, mc, vc, [&](int j) { return static_cast<unsigned int>((first + j * 32) >> 1); },
                         [&](int) { return (first & 1) != 0; });
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -369,7 +377,7 @@ __device__ __noinline__ void step_by_elements(const Args& a, const Tensor* x, fl
 // element.  The two differ in which lane holds an element and in nothing
 // else: results are the same.
 template <int GT, int PT, int BITS, bool ONE>
-__global__ void __launch_bounds__(kThreads, 4) zero_adamw_kernel(const __grid_constant__ Args a)
+__global__ void __launch_bounds__(kThreads, 3) zero_adamw_kernel(const __grid_constant__ Args a)
 {
     using G = typename Elem<GT>::type;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -399,7 +407,6 @@ __global__ void __launch_bounds__(kThreads, 4) zero_adamw_kernel(const __grid_co
         }
         const long long b0 = (c - lo) * kChunk + warp * kBlock - max(phase, 0); // the block's first element
         if (b0 >= n) continue;
-        k.scale = b0 / kBlock; // used with 8-bit moments only: blocks then start on multiples of 256
         if (phase < 0 || b0 < 0 || b0 + kBlock > n) {
             step_by_elements<GT, PT, BITS>(a, x, k.lr, k.decay, k.factor, k.key, b0, go);
             if (go == 0.0f) return;
@@ -422,6 +429,10 @@ __global__ void __launch_bounds__(kThreads, 4) zero_adamw_kernel(const __grid_co
             const uint2 mm = __ldcs(reinterpret_cast<const uint2*>(static_cast<unsigned char*>(x->m) + i0));
             const uint2 vv = __ldcs(reinterpret_cast<const uint2*>(static_cast<unsigned char*>(x->v) + i0));
             mc[0] = mm.x, mc[1] = mm.y, vc[0] = vv.x, vc[1] = vv.y;
+            k.ms_out = x->ms + b0 / kBlock; // blocks start on multiples of 256 here
+            k.vs_out = x->vs + b0 / kBlock;
+            k.ms = *k.ms_out;
+            k.vs = *k.vs_out;
         }
         const G* gp = static_cast<const G*>(x->g) + i0;
         if constexpr (ONE) {
@@ -441,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 4) zero_adamw_kernel(const __grid_co
             for (; r < a.P; ++r) add8<GT>(g, load8<GT>(gp + r * stride));
         }
         if (go == 0.0f) return; // a gradient overflowed: nothing is written
-        update<BITS, ONE>(a, x, k, w, m, v, g, mc, vc, [&](int j) { return static_cast<unsigned int>(i0 >> 1) + (j >> 1); },
+        update<BITS, ONE>(a, k, w, m, v, g, mc, vc, [&](int j) { return static_cast<unsigned int>(i0 >> 1) + (j >> 1); },
                           [](int j) { return (j & 1) != 0; });
         __stcs(wp, *reinterpret_cast<float4*>(w));
         __stcs(wp + 1, *reinterpret_cast<float4*>(w + 4));
@@ -469,18 +480,19 @@ __global__ void __launch_bounds__(kThreads, 4) zero_adamw_kernel(const __grid_co
 // and every rank's gradients) into a ring of shared-memory stages; groups of
 // eight warps take the chunks in turn, a warp a block of 256, hand the stage
 // back as soon as they have read it, and store their results directly.  The
-// copies in flight do not depend on the warps' registers, which bounds the
-// vector kernel: 1.3e9 parameters ...
+// copies in flight do not depend on the warps' registers or on how far their
+// arithmetic has come, which is what bounds the vector kernel.
 constexpr int kGroups = 3;
 constexpr int kPipeThreads = 32 + kGroups * kThreads;
 // A multiple of the groups: a stage always goes to the same group, which so
 // waits for each of its fills in turn (a wait tells a fill from the next one
 // only by parity).
 constexpr int kMaxStages = 15;
-constexpr int kPipeSmem = 225 * 1024;
-constexpr int kMinStages = kGroups;
+constexpr int kPipeSmem = 224 * 1024;
+// More copies in flight than this cost the stores: 32-bit moments, P = 1,
+// 3 stages of 28 KB 6620 GB/s, 6 stages 6410 GB/s.
+constexpr int kPipeTarget = 112 * 1024;
 static_assert(kMaxStages % kGroups == 0, "stages by groups");
-constexpr int kPipeChunks = 1216; // chunks from which the pipeline pays
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;
 
 __device__ unsigned int g_adamw_timeouts;
@@ -529,9 +541,26 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                  : "memory");
 }
 
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\t"
+                 "elect.sync _|q, 0xffffffff;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(p));
+    return p != 0;
+}
+
 // What the copying warp says about a stage's chunk.
 struct Chunk {
     const Tensor* x;
+    float* w;
+    void* m;
+    void* v;
+    void* p;
+    float* ms;
+    float* vs;
+    long long n;
     long long b0;        // first element of its first block (may be negative)
     int from, to;        // blocks that are in the stage; the others go element by element
     float lr, decay;
@@ -582,6 +611,7 @@ __global__ void __launch_bounds__(kPipeThreads, 1) zero_adamw_pipeline_kernel(co
                 x = *k.x;
                 n = x.n;
                 stride = x.stride;
+                k.w = x.w, k.m = x.m, k.v = x.v, k.p = x.p, k.ms = x.ms, k.vs = x.vs, k.n = n;
                 k.lr = __fmul_rn(a.lr, x.lr_scale);
                 k.decay = __fmul_rn(k.lr, x.decay);
                 k.key = BITS == 8 ? mix32(mix32(a.seed) + 0x9e3779b9u * static_cast<unsigned int>(ti + 1)) : 0u;
@@ -602,16 +632,22 @@ __global__ void __launch_bounds__(kPipeThreads, 1) zero_adamw_pipeline_kernel(co
                              : "memory");
             }
             __syncwarp();
-            if (count > 0) { // one row a lane
+            // One elected lane issues the rows: the copy instruction takes uniform registers, and under a condition on the
+            // lane each would cost several hundred cycles.
+            if (count > 0 && elect_one()) {
                 unsigned char* st = smem + s * a.stage_bytes;
                 const int at = k.from * kBlock;
-                for (int row = lane; row < 3 + a.P; row += 32) {
-                    if (row == 0) bulk_load(st + at * 4, x.w + e0, count * 4, &full[s]);
-                    else if (row == 1) bulk_load(st + kChunk * 4 + at * BITS / 8, static_cast<unsigned char*>(x.m) + e0 * (BITS / 8), count * (BITS / 8), &full[s]);
-                    else if (row == 2) bulk_load(st + kChunk * 4 + kMoment + at * BITS / 8, static_cast<unsigned char*>(x.v) + e0 * (BITS / 8), count * (BITS / 8), &full[s]);
-                    else bulk_load(st + kChunk * 4 + 2 * kMoment + (row - 3) * kGrad + at * sizeof(G), static_cast<const G*>(x.g) + (row - 3) * stride + e0, count * static_cast<uint32_t>(sizeof(G)), &full[s]);
-                }
+                bulk_load(st + at * 4, x.w + e0, count * 4, &full[s]);
+                st += kChunk * 4;
+                bulk_load(st + at * BITS / 8, static_cast<unsigned char*>(x.m) + e0 * (BITS / 8), count * (BITS / 8), &full[s]);
+                st += kMoment;
+                bulk_load(st + at * BITS / 8, static_cast<unsigned char*>(x.v) + e0 * (BITS / 8), count * (BITS / 8), &full[s]);
+                st += kMoment + at * sizeof(G);
+                const G* g = static_cast<const G*>(x.g) + e0;
+                for (int r = 0; r < (ONE ? 1 : a.P); ++r, st += kGrad, g += stride)
+                    bulk_load(st, g, count * static_cast<uint32_t>(sizeof(G)), &full[s]);
             }
+            __syncwarp();
         }
         if (!ok) // the copies in flight land before the CTA ends
             for (int k2 = max(0, it - a.stages); k2 < it; ++k2) wait_slow(&full[k2 % a.stages], (k2 / a.stages) & 1, nullptr);
@@ -624,16 +660,20 @@ __global__ void __launch_bounds__(kPipeThreads, 1) zero_adamw_pipeline_kernel(co
         const int s = it % a.stages;
         const bool ok = wait(&full[s], (it / a.stages) & 1, abort);
         if (!__all_sync(0xffffffffu, ok)) break;
-        const Chunk& ch = meta[s];
-        const Tensor* x = ch.x;
+        const Chunk ch = meta[s];
         const long long b0 = ch.b0 + mine * kBlock;
-        Block k{ch.lr, ch.decay, factor, ch.key, b0 / kBlock};
-        const bool staged = mine >= ch.from && mine < ch.to;
-        if (!staged) {
+        if (mine < ch.from || mine >= ch.to) {
             __syncwarp();
             if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&empty[s])) : "memory");
-            if (b0 < x->n) step_by_elements<GT, PT, BITS>(a, x, k.lr, k.decay, factor, k.key, b0, 1.0f);
+            if (b0 < ch.n) step_by_elements<GT, PT, BITS>(a, ch.x, ch.lr, ch.decay, factor, ch.key, b0, 1.0f);
             continue;
+        }
+        Block k{ch.lr, ch.decay, factor, ch.key, 0.0f, 0.0f, nullptr, nullptr};
+        if constexpr (BITS == 8) {
+            k.ms_out = ch.ms + b0 / kBlock;
+            k.vs_out = ch.vs + b0 / kBlock;
+            k.ms = *k.ms_out;
+            k.vs = *k.vs_out;
         }
         // lane l has elements 4 l .. 4 l + 3 of each half of the block: accesses of 16 bytes (fp32) side by side
         const unsigned char* st = smem + s * a.stage_bytes;
@@ -674,21 +714,21 @@ __global__ void __launch_bounds__(kPipeThreads, 1) zero_adamw_pipeline_kernel(co
         __syncwarp();
         if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&empty[s])) : "memory");
         const long long i0 = b0 + lane * 4;
-        update<BITS, ONE>(a, x, k, w, m, v, g, mc, vc,
+        update<BITS, ONE>(a, k, w, m, v, g, mc, vc,
                           [&](int j) { return static_cast<unsigned int>(i0 >> 1) + (j >> 1) + (j >= 4 ? 62u : 0u); },
                           [](int j) { return (j & 1) != 0; });
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const long long i = i0 + h * 128;
-            __stcs(reinterpret_cast<float4*>(x->w + i), *reinterpret_cast<float4*>(w + 4 * h));
+            __stcs(reinterpret_cast<float4*>(ch.w + i), *reinterpret_cast<float4*>(w + 4 * h));
             if constexpr (BITS == 32) {
-                __stcs(reinterpret_cast<float4*>(static_cast<float*>(x->m) + i), *reinterpret_cast<float4*>(m + 4 * h));
-                __stcs(reinterpret_cast<float4*>(static_cast<float*>(x->v) + i), *reinterpret_cast<float4*>(v + 4 * h));
+                __stcs(reinterpret_cast<float4*>(static_cast<float*>(ch.m) + i), *reinterpret_cast<float4*>(m + 4 * h));
+                __stcs(reinterpret_cast<float4*>(static_cast<float*>(ch.v) + i), *reinterpret_cast<float4*>(v + 4 * h));
             } else {
-                __stcs(reinterpret_cast<unsigned int*>(static_cast<unsigned char*>(x->m) + i), mc[h]);
-                __stcs(reinterpret_cast<unsigned int*>(static_cast<unsigned char*>(x->v) + i), vc[h]);
+                __stcs(reinterpret_cast<unsigned int*>(static_cast<unsigned char*>(ch.m) + i), mc[h]);
+                __stcs(reinterpret_cast<unsigned int*>(static_cast<unsigned char*>(ch.v) + i), vc[h]);
             }
-            __stcs(reinterpret_cast<uint2*>(static_cast<unsigned short*>(x->p) + i),
+            __stcs(reinterpret_cast<uint2*>(static_cast<unsigned short*>(ch.p) + i),
                    make_uint2(pack2<PT>(w[4 * h], w[4 * h + 1]), pack2<PT>(w[4 * h + 2], w[4 * h + 3])));
         }
     }
@@ -879,6 +919,22 @@ Kernel pick_norm(int grad)
     default: return zero_grad_norm_kernel<ZERO_TYPE_FP32>;
     }
 }
+
+// Stages of the pipeline: about 112 KB, and three at least where they fit.
+int pipeline_stages(int64_t stage)
+{
+    const int64_t n = std::min<int64_t>(kMaxStages, kPipeTarget / stage) / kGroups * kGroups;
+    return static_cast<int>(std::max<int64_t>(n, kGroups * stage <= kPipeSmem ? kGroups : 0));
+}
+
+// Where the pipeline beats the vector kernel.  Measured (GB/s, vector against
+// pipeline): 32-bit moments, P = 1, 3.0e8 elements 6070 / 6640, 1.2e7 5560 /
+// 5690, 3.9e6 4920 / 4350; P = 2 6740 / 6660, P = 4 6730 / 6740, P = 8 6640 /
+// 6470 (more ranks read more than they write and leave the vector kernel
+// enough copies in flight).  8-bit moments, P = 1, 3.0e8 elements 5860 / 6070,
+// 9.4e6 4170 / 4080, 3.9e6 3160 / 2730; P = 4 9.4e6 4550 / 5000; P = 8 5.0e7
+// 5580 / 6990.
+bool takes_pipeline(int64_t chunks, int bits, int P) { return chunks >= 4096 && (bits == 8 || P == 1); }
 
 int64_t table_size(int64_t n)
 {
@@ -1104,9 +1160,9 @@ extern "C" int zero_adamw_step(const zero_adamw_plan_t* plan, void* table, const
     a.seed = seed;
     const StepKernels fn = pick_step(plan->grad_type, plan->param_type, plan->state_bits, plan->P);
     const int64_t stage = kChunk * (4 + plan->state_bits / 4 + (plan->grad_type == ZERO_TYPE_FP32 ? 4 : 2) * int64_t{plan->P});
-    a.stages = static_cast<int>(std::min<int64_t>(kMaxStages, kPipeSmem / stage) / kGroups * kGroups);
+    a.stages = pipeline_stages(stage);
     a.stage_bytes = static_cast<int>(std::min<int64_t>(stage, kPipeSmem));
-    if (plan->pipeline && a.stages >= kMinStages && plan->chunks >= kPipeChunks)
+    if (plan->pipeline && a.stages > 0 && takes_pipeline(plan->chunks, plan->state_bits, plan->P))
         return launch(fn.pipeline, a, INT64_MAX, kPipeThreads, kPipeSmem, cuda_stream);
     return launch(fn.vector, a, INT64_MAX, kThreads, 0, cuda_stream);
 }
