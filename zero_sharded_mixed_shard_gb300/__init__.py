@@ -215,17 +215,22 @@ def zero_strerror(code: int) -> str:
 
 def _addr(x) -> int | None:
     """Address of a torch tensor or numpy array (or pass an int / None through)."""
-    if x is None or isinstance(x, int):
+    if x is None or x.__class__ is int:
         return x
-    if hasattr(x, "data_ptr"):
+    try:
         return x.data_ptr()
-    return x.__array_interface__["data"][0]
+    except AttributeError:
+        return int(x) if isinstance(x, int) else x.__array_interface__["data"][0]
 
 
 def _stream(stream) -> int | None:
+    """The stream's handle; None: torch's current stream (looked up without
+    building a Stream object, which takes longer than a small kernel's launch)."""
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        if not torch.cuda.is_initialized():
+            return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
