@@ -191,13 +191,18 @@ __device__ __forceinline__ float mean_of(float sum, const Args& a)
 
 // The tensor that chunk c belongs to: the last one whose first chunk is <= c
 // (tensors without elements have no chunk and are never the last such one).
+// A warp looks at 32 places at once: two dependent reads find one of a
+// thousand tensors.
 __device__ __forceinline__ int find_tensor(const long long* first, int n, long long c)
 {
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(first + mid) <= c) lo = mid;
-        else hi = mid;
+    const int lane = threadIdx.x & 31;
+    int lo = 0;
+    while (n > 1) {
+        const int step = (n + 31) / 32, at = lane * step;
+        const unsigned int before = __ballot_sync(0xffffffffu, at < n && __ldg(first + lo + at) <= c);
+        const int skip = (__popc(before) - 1) * step; // lane 0's place is always before
+        lo += skip;
+        n = min(step, n - skip);
     }
     return lo;
 }

@@ -64,6 +64,7 @@ struct Out {
     long long ldy, ldz, ldr;
     int act, bf16, swap;
     int vec;             // 16-byte accesses allowed on y, z, res and bias
+    int wide_y, wide_z, wide_r; // elements of the widest access on each: 8, 2 or 1
 };
 
 struct Problem {
@@ -507,10 +508,21 @@ __device__ __forceinline__ void emit8(const Out& o, long long row, int col, floa
 // conflicts.
 __device__ __forceinline__ int piece_at(int r, int q) { return 4 * r + (q ^ ((r >> 1) & 3)); }
 
-// `rows` x `cols` of the piece to or from memory, lanes along the rows.
-__device__ __forceinline__ void piece_out(const uint4* piece, uint16_t* to, long long ld, int rows, int cols, bool vec, int lane)
+// `rows` x `cols` of the piece to or from memory, lanes along the rows; wide:
+// elements of an access.  Rows off 16 bytes are the slow case (1009 x 1001 ->
+// 1543 with residual and z: two bytes at a time 16.0 us, four 15 us; on 16
+// bytes, without copies of the operands, 9 us).
+__device__ __forceinline__ void piece_out(const uint4* piece, uint16_t* to, long long ld, int rows, int cols, int wide, int lane)
 {
-    if (vec && cols == 32) {
+    if (cols == 32 && wide == 2) {
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(piece);
+        const int r0 = lane >> 4, e = lane & 15;
+#pragma unroll 8
+        for (int r = r0; r < rows; r += 2)
+            *reinterpret_cast<uint32_t*>(to + r * ld + 2 * e) = p[piece_at(r, e >> 2) * 4 + (e & 3)];
+        return;
+    }
+    if (cols == 32 && wide == 8) {
         const int r0 = lane >> 2, q = lane & 3;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -522,8 +534,16 @@ __device__ __forceinline__ void piece_out(const uint4* piece, uint16_t* to, long
     }
 }
 
-__device__ __forceinline__ void piece_in(uint4* piece, const uint16_t* from, long long ld, int rows, int cols, int lane)
+__device__ __forceinline__ void piece_in(uint4* piece, const uint16_t* from, long long ld, int rows, int cols, int wide, int lane)
 {
+    if (cols == 32 && wide > 1) {
+        uint32_t* p = reinterpret_cast<uint32_t*>(piece);
+        const int r0 = lane >> 4, e = lane & 15;
+#pragma unroll 8
+        for (int r = r0; r < rows; r += 2)
+            p[piece_at(r, e >> 2) * 4 + (e & 3)] = *reinterpret_cast<const uint32_t*>(from + r * ld + 2 * e);
+        return;
+    }
     if (lane >= cols) return;
     uint16_t* p = reinterpret_cast<uint16_t*>(piece);
 #pragma unroll 8
@@ -544,9 +564,9 @@ template <int BF16>
 __device__ __forceinline__ void emit_piece_as(const Out& o, long long row0, int rows, int col0, int cols, float (&v)[32],
                                            uint4* piece, int lane)
 {
-    const bool vec = o.vec && cols == 32;
+    const bool vec = o.vec && cols == 32, vec_res = o.wide_r == 8 && cols == 32;
     uint4 res[4] = {};
-    if (o.res && vec) {
+    if (o.res && vec_res) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             if ((lane >> 2) + 8 * k < rows)
@@ -566,16 +586,16 @@ __device__ __forceinline__ void emit_piece_as(const Out& o, long long row0, int 
     if (o.z) {
         piece_row(piece, v, BF16, lane);
         __syncwarp();
-        piece_out(piece, at16(o.z, o.ldz, row0, col0), o.ldz, rows, cols, o.vec, lane);
+        piece_out(piece, at16(o.z, o.ldz, row0, col0), o.ldz, rows, cols, o.wide_z, lane);
         __syncwarp();
     }
     activate_all(v, o.act);
     if (o.res) {
-        if (vec) {
+        if (vec_res) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) piece[piece_at((lane >> 2) + 8 * k, lane & 3)] = res[k];
         } else {
-            piece_in(piece, at16(o.res, o.ldr, row0, col0), o.ldr, rows, cols, lane);
+            piece_in(piece, at16(o.res, o.ldr, row0, col0), o.ldr, rows, cols, o.wide_r, lane);
         }
         __syncwarp();
 #pragma unroll
@@ -584,7 +604,7 @@ __device__ __forceinline__ void emit_piece_as(const Out& o, long long row0, int 
     }
     piece_row(piece, v, BF16, lane);
     __syncwarp();
-    piece_out(piece, at16(o.y, o.ldy, row0, col0), o.ldy, rows, cols, o.vec, lane);
+    piece_out(piece, at16(o.y, o.ldy, row0, col0), o.ldy, rows, cols, o.wide_y, lane);
     __syncwarp();
 }
 
@@ -1273,6 +1293,11 @@ Product product(const Matrix& a, int a_mn, const Matrix& b, int b_mn, const Out&
     return {a, b, a_mn, b_mn, a_mn ? a.cols : a.rows, b_mn ? b.cols : b.rows, a_mn ? a.rows : a.cols, o};
 }
 
+bool aligned16(const void* p, int64_t ld) { return addr(p) % 16 == 0 && ld % 8 == 0; }
+
+// Elements of the widest access that every row start allows.
+int widest_access(const void* p, int64_t ld) { return aligned16(p, ld) ? 8 : addr(p) % 4 == 0 && ld % 2 == 0 ? 2 : 1; }
+
 // Which kernel takes a launch, with what tile.
 struct Variant {
     bool pair;
@@ -1394,6 +1419,9 @@ int gemm(const Product* p, int count, int type, const BiasSum* bias, cudaStream_
         Problem& g = args.p[k];
         const int bm = v.pair ? 256 : kBM, b_rows = v.pair ? v.bn / 2 : v.bn;
         g.o = p[k].o;
+        g.o.wide_y = widest_access(g.o.y, g.o.ldy);
+        g.o.wide_z = widest_access(g.o.z, g.o.ldz);
+        g.o.wide_r = widest_access(g.o.res, g.o.ldr);
         g.o.bf16 = type == ZERO_TYPE_BF16;
         g.a_mn = p[k].a_mn ? (p[k].a.cols % 64 == 0 ? 2 : 1) : 0;
         g.b_mn = p[k].b_mn ? (p[k].b.cols % 64 == 0 ? 2 : 1) : 0;
@@ -1444,8 +1472,6 @@ int gemm(const Product* p, int count, int type, const BiasSum* bias, cudaStream_
     if ((rc = allow_smem(fn, smem))) return rc;
     return launch_after(fn, args, tiles * v.parts, threads, smem, v.parts, stream);
 }
-
-bool aligned16(const void* p, int64_t ld) { return addr(p) % 16 == 0 && ld % 8 == 0; }
 
 // Whether two strided matrices share an element.  Matrices of one row pitch
 // may lie beside each other in the same rows.
