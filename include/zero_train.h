@@ -188,6 +188,16 @@ int zero_linear_backward(const void* dy, int64_t lddy, const void* z, int64_t ld
                          int32_t type, void* workspace, int64_t workspace_bytes,
                          void* cuda_stream);
 
+/* Which kernel the products of a linear layer would take (a diagnostic like
+ * zero_step_plan: nothing is launched).  products: 0 the forward product, 1 dx,
+ * 2 dw, 3 both.  *launches: how many the products take; of the first one, the
+ * *rows x *columns of a tile, the CTAs of a *cluster (256 rows: a pair that
+ * shares a tile; 128 rows: they share a contraction) and the CTAs *per_sm.
+ * Depends on the current device's SM count.
+ * Errors: ZERO_EINVAL (also T < 1), ZERO_ECUDA. */
+int zero_linear_plan(int64_t T, int64_t K, int64_t N, int32_t products, int32_t* launches,
+                     int32_t* rows, int32_t* columns, int32_t* cluster, int32_t* per_sm);
+
 /* Bounded waits of the kernels of this header that gave up on the current
  * device since the last reset; like zero_device_timeouts (0 in every correct
  * run, reading it synchronises). */

@@ -149,10 +149,38 @@ def test_forward(z, T, K, N, act, ty, pad, shift):
     check_forward(z, T, K, N, act, ty, pad, shift, seed=T + N)
 
 
-@pytest.mark.parametrize("T,K,N,pad", [(5000, 200, 1000, 0), (4993, 1000, 1100, 8), (6000, 72, 1027, 0), (2500, 520, 2600, 3), (20000, 64, 256, 0)])
+MANY = [(5000, 200, 1000, 0), (4993, 1000, 1100, 8), (6000, 72, 1027, 0), (2500, 520, 2600, 3), (20000, 64, 256, 0), (4096, 2048, 2050, 0)]
+# few tokens against wide layers: contractions cut over a cluster
+WIDE = [(5, 2048, 4096), (30, 2048, 2048), (60, 2048, 2000), (128, 2048, 4096), (250, 2048, 2048), (200, 200, 9000), (400, 320, 4096), (2048, 1024, 1024), (512, 2048, 2048)]
+
+
+@pytest.mark.parametrize("T,K,N,pad", MANY)
 @pytest.mark.parametrize("act,ty", [(0, 1), (2, 0), (3, 1)])
 def test_forward_many_tiles(z, T, K, N, pad, act, ty):
     check_forward(z, T, K, N, act, ty, pad, seed=K)
+
+
+def test_every_kernel_is_covered(z):
+    """The shapes of the tests above and below reach every kernel: each tile width, whole and cut contractions, pairs,
+    one product and two in a launch, two launches."""
+    seen, both = set(), set()
+    for T, K, N in FORWARD + [s[:3] for s in MANY] + WIDE:
+        p = z.zero_linear_plan(T, K, N, 0)
+        seen.add((p["rows"], p["columns"], p["per_sm"], p["cluster"] > 1))
+    for T, K, N in BACKWARD + [s[:3] for s in MANY_BACK]:
+        p = z.zero_linear_plan(T, K, N, 3)
+        both.add((p["rows"], p["columns"], p["per_sm"], p["launches"]))
+    for want in [(128, 16, 2, False), (128, 16, 2, True), (128, 32, 2, True), (128, 64, 1, True), (128, 64, 2, False),
+                 (128, 128, 1, False), (128, 128, 1, True), (256, 256, 1, True)]:
+        assert want in seen, (want, sorted(seen))
+    assert {(r, c) for r, c, _, n in both if n == 1} >= {(128, 64), (128, 128), (256, 256)}, sorted(both)
+    assert any(n == 2 for *_, n in both), sorted(both)
+
+
+@pytest.mark.parametrize("T,K,N", WIDE)
+def test_forward_wide(z, T, K, N):
+    check_forward(z, T, K, N, 2, 1, 0, 0, seed=T)
+    check_forward(z, T, K, N, 0, 0, 2, 0, seed=T)              # rows on 4 bytes
 
 
 @pytest.mark.parametrize("bias,res,keep,inplace", [(False, False, False, False), (True, False, False, False), (False, True, False, False),
@@ -172,7 +200,10 @@ def test_backward(z, T, K, N, act, ty, pad, shift, dwpad):
     check_backward(z, T, K, N, act, ty, pad, shift, seed=T + K, dwpad=dwpad)
 
 
-@pytest.mark.parametrize("T,K,N,pad", [(5000, 1000, 200, 0), (300, 1000, 5000, 0), (5100, 1030, 5000, 0), (2600, 2500, 523, 3)])
+MANY_BACK = [(5000, 1000, 200, 0), (300, 1000, 5000, 0), (5100, 1030, 5000, 0), (2600, 2500, 523, 3), (4, 2048, 8192, 0), (60, 2048, 2048, 0), (512, 784, 1192, 0)]
+
+
+@pytest.mark.parametrize("T,K,N,pad", MANY_BACK)
 @pytest.mark.parametrize("act,ty", [(0, 1), (2, 0)])
 def test_backward_many_tiles(z, T, K, N, pad, act, ty):
     check_backward(z, T, K, N, act, ty, pad, seed=K)

@@ -51,7 +51,7 @@ EXPORTED = ("zero_init_layout", "zero_free_layout", "zero_shard_range", "zero_me
             "zero_selftest_wait_timeout", "zero_selftest_mean_division", "zero_strerror",
             "zero_last_cuda_error", "zero_last_cuda_error_string",
             "zero_adamw_plan", "zero_grad_norm", "zero_adamw_step",
-            "zero_linear_workspace", "zero_linear_forward", "zero_linear_backward",
+            "zero_linear_plan", "zero_linear_workspace", "zero_linear_forward", "zero_linear_backward",
             "zero_train_timeouts")
 
 
@@ -185,6 +185,9 @@ def lib() -> ctypes.CDLL:
     L.zero_grad_norm.restype = ctypes.c_int
     L.zero_adamw_step.argtypes = [plan_p, vp, vp, i64, f32, f32, f32, f32, ctypes.c_uint32, vp]
     L.zero_adamw_step.restype = ctypes.c_int
+    i32p = ctypes.POINTER(ctypes.c_int32)
+    L.zero_linear_plan.argtypes = [i64, i64, i64, i32, i32p, i32p, i32p, i32p, i32p]
+    L.zero_linear_plan.restype = ctypes.c_int
     L.zero_linear_workspace.argtypes = [i64, i64, i64, i32, i32, i32, ctypes.POINTER(ctypes.c_int64)]
     L.zero_linear_workspace.restype = ctypes.c_int
     L.zero_linear_forward.argtypes = [vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, i64, i64, i64, i64,
@@ -547,6 +550,17 @@ def zero_adamw_step(plan: AdamWPlan, stats, t: int, lr: float, beta1: float, bet
                                beta2, eps, seed, _stream(stream))
     if rc:
         raise ZeroError(rc, "zero_adamw_step")
+
+
+def zero_linear_plan(T: int, K: int, N: int, products: int) -> dict:
+    """The kernel a linear layer's products would take (0 forward, 1 dx, 2 dw,
+    3 both): {"launches", "rows", "columns", "cluster", "per_sm"} (see
+    include/zero_train.h); nothing is launched."""
+    v = [ctypes.c_int32() for _ in range(5)]
+    rc = lib().zero_linear_plan(T, K, N, products, *map(ctypes.byref, v))
+    if rc:
+        raise ZeroError(rc, "zero_linear_plan")
+    return dict(zip(("launches", "rows", "columns", "cluster", "per_sm"), (x.value for x in v)))
 
 
 def zero_linear_workspace(T: int, K: int, N: int, act: int, backward: bool, aligned: bool) -> int:

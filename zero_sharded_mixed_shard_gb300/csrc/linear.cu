@@ -1404,6 +1404,20 @@ Variant choose(const Product* p, int count, int sms, double* estimate)
     return out;
 }
 
+// Whether the gradients' two products go into launches of their own.  With few
+// tokens they want tiles of different shapes, and one launch is not always the
+// quicker form (64 tokens, 2048 -> 2048: 10 us in one, 24 in two; 4 tokens,
+// 2048 -> 8192: 30 in one, 27 in two).
+bool apart(const Product* p, int sms)
+{
+    if (!p[0].o.swap) return false;
+    double one, first, second;
+    choose(p, 2, sms, &one);
+    choose(p, 1, sms, &first);
+    choose(p + 1, 1, sms, &second);
+    return first + second < one;
+}
+
 // One or two products in one launch, and the bias gradient's last sum.
 int gemm(const Product* p, int count, int type, const BiasSum* bias, cudaStream_t stream)
 {
@@ -1552,6 +1566,34 @@ void add_copy(PrepArgs* a, int* ctas, int slot, Matrix* x, void* to)
 
 } // namespace
 
+extern "C" int zero_linear_plan(int64_t T, int64_t K, int64_t N, int32_t products, int32_t* launches, int32_t* rows,
+                                int32_t* columns, int32_t* cluster, int32_t* per_sm)
+{
+    if (!launches || !rows || !columns || !cluster || !per_sm || products < 0 || products > 3 || T < 1 ||
+        bad_sizes(T, K, N, ZERO_ACT_NONE, ZERO_TYPE_FP16))
+        return ZERO_EINVAL;
+    int sms = 0;
+    int rc = sm_count(&sms);
+    if (rc) return rc;
+    const Matrix x{nullptr, K, T, K}, w{nullptr, K, N, K}, dz{nullptr, N, T, N};
+    Out o{};
+    o.swap = T <= kFewTokens;
+    Product p[2];
+    int count = 0;
+    if (products == 0) p[count++] = o.swap ? product(w, 0, x, 0, o) : product(x, 0, w, 0, o);
+    if (products & 1) p[count++] = o.swap ? product(w, 1, dz, 0, o) : product(dz, 0, w, 1, o);
+    o.swap = 0;
+    if (products & 2) p[count++] = product(dz, 1, x, 1, o);
+    *launches = count == 2 && apart(p, sms) ? 2 : 1;
+    double estimate;
+    const Variant v = choose(p, *launches == 2 ? 1 : count, sms, &estimate);
+    *rows = v.pair ? 256 : kBM;
+    *columns = v.bn;
+    *cluster = v.pair ? 2 : v.parts;
+    *per_sm = v.per_sm;
+    return ZERO_OK;
+}
+
 extern "C" int zero_linear_workspace(int64_t T, int64_t K, int64_t N, int32_t act, int32_t backward, int32_t aligned,
                                      int64_t* bytes)
 {
@@ -1698,19 +1740,11 @@ extern "C" int zero_linear_backward(const void* dy, int64_t lddy, const void* z,
         p[count++] = product(mz, 1, mx, 1, o);
     }
     const BiasSum* with = db ? &bias : nullptr;
-    if (count == 2 && p[0].o.swap) {
-        // few tokens: the products want tiles of different shapes, so one launch is not always the quicker form
-        // (64 tokens, 2048 -> 2048: 10 us in one, 24 in two; 4 tokens, 2048 -> 8192: 30 in one, 27 in two)
-        int sms = 0;
-        if ((rc = sm_count(&sms))) return rc;
-        double one, first, second;
-        choose(p, 2, sms, &one);
-        choose(p, 1, sms, &first);
-        choose(p + 1, 1, sms, &second);
-        if (first + second < one) {
-            if ((rc = gemm(p, 1, type, with, st))) return rc;
-            return gemm(p + 1, 1, type, nullptr, st);
-        }
+    int sms = 0;
+    if ((rc = sm_count(&sms))) return rc;
+    if (count == 2 && apart(p, sms)) {
+        if ((rc = gemm(p, 1, type, with, st))) return rc;
+        return gemm(p + 1, 1, type, nullptr, st);
     }
     if (count == 2 && kblocks_of(p[1]) > kblocks_of(p[0])) std::swap(p[0], p[1]); // the longer tiles first
     return gemm(p, count, type, with, st);
