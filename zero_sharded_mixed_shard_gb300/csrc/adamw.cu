@@ -395,26 +395,34 @@ __global__ void __launch_bounds__(kThreads, 3) zero_adamw_kernel(const __grid_co
         k.factor = a.stats[1];
         go = a.stats[2];
     }
-    long long lo = 0, hi = 0, n = 0;
+    // The place of the CTA's next chunk, looked up while the current one's loads are in flight.
+    long long c = blockIdx.x, lo = 0, hi = 0, n = 0;
     int phase = 0;
     const Tensor* x = nullptr;
-    for (long long c = blockIdx.x; c < a.chunks; c += gridDim.x) {
-        if (c >= hi) {
-            const int ti = find_tensor(a.first, a.n_tensors, c);
-            lo = __ldg(a.first + ti);
-            hi = __ldg(a.first + ti + 1);
-            x = a.tensors + ti;
-            n = x->n;
-            phase = x->phase;
-            k.lr = __fmul_rn(a.lr, x->lr_scale);
-            k.decay = __fmul_rn(k.lr, x->decay);
-            k.key = BITS == 8 ? mix32(mix32(a.seed) + 0x9e3779b9u * static_cast<unsigned int>(ti + 1)) : 0u;
-        }
+    auto look_up = [&] {
+        if (c >= a.chunks || c < hi) return;
+        const int ti = find_tensor(a.first, a.n_tensors, c);
+        lo = __ldg(a.first + ti);
+        hi = __ldg(a.first + ti + 1);
+        x = a.tensors + ti;
+        n = x->n;
+        phase = x->phase;
+        k.lr = __fmul_rn(a.lr, x->lr_scale);
+        k.decay = __fmul_rn(k.lr, x->decay);
+        k.key = BITS == 8 ? mix32(mix32(a.seed) + 0x9e3779b9u * static_cast<unsigned int>(ti + 1)) : 0u;
+    };
+    look_up();
+    while (c < a.chunks) {
         const long long b0 = (c - lo) * kChunk + warp * kBlock - max(phase, 0); // the block's first element
-        if (b0 >= n) continue;
+        c += gridDim.x;
+        if (b0 >= n) {
+            look_up();
+            continue;
+        }
         if (phase < 0 || b0 < 0 || b0 + kBlock > n) {
             step_by_elements<GT, PT, BITS>(a, x, k.lr, k.decay, k.factor, k.key, b0, go);
             if (go == 0.0f) return;
+            look_up();
             continue;
         }
         const long long i0 = b0 + lane * 8;
@@ -457,22 +465,27 @@ __global__ void __launch_bounds__(kThreads, 3) zero_adamw_kernel(const __grid_co
             for (; r < a.P; ++r) add8<GT>(g, load8<GT>(gp + r * stride));
         }
         if (go == 0.0f) return; // a gradient overflowed: nothing is written
-        update<BITS, ONE>(a, k, w, m, v, g, mc, vc, [&](int j) { return static_cast<unsigned int>(i0 >> 1) + (j >> 1); },
+        const Block now = k;
+        float* mp_out = static_cast<float*>(x->m);
+        float* vp_out = static_cast<float*>(x->v);
+        unsigned short* p_out = static_cast<unsigned short*>(x->p) + i0;
+        look_up();
+        update<BITS, ONE>(a, now, w, m, v, g, mc, vc, [&](int j) { return static_cast<unsigned int>(i0 >> 1) + (j >> 1); },
                           [](int j) { return (j & 1) != 0; });
         __stcs(wp, *reinterpret_cast<float4*>(w));
         __stcs(wp + 1, *reinterpret_cast<float4*>(w + 4));
         if constexpr (BITS == 32) {
-            float4* mp = reinterpret_cast<float4*>(static_cast<float*>(x->m) + i0);
-            float4* vp = reinterpret_cast<float4*>(static_cast<float*>(x->v) + i0);
+            float4* mp = reinterpret_cast<float4*>(mp_out + i0);
+            float4* vp = reinterpret_cast<float4*>(vp_out + i0);
             __stcs(mp, *reinterpret_cast<float4*>(m));
             __stcs(mp + 1, *reinterpret_cast<float4*>(m + 4));
             __stcs(vp, *reinterpret_cast<float4*>(v));
             __stcs(vp + 1, *reinterpret_cast<float4*>(v + 4));
         } else {
-            __stcs(reinterpret_cast<uint2*>(static_cast<unsigned char*>(x->m) + i0), make_uint2(mc[0], mc[1]));
-            __stcs(reinterpret_cast<uint2*>(static_cast<unsigned char*>(x->v) + i0), make_uint2(vc[0], vc[1]));
+            __stcs(reinterpret_cast<uint2*>(reinterpret_cast<unsigned char*>(mp_out) + i0), make_uint2(mc[0], mc[1]));
+            __stcs(reinterpret_cast<uint2*>(reinterpret_cast<unsigned char*>(vp_out) + i0), make_uint2(vc[0], vc[1]));
         }
-        __stcs(reinterpret_cast<uint4*>(static_cast<unsigned short*>(x->p) + i0),
+        __stcs(reinterpret_cast<uint4*>(p_out),
                make_uint4(pack2<PT>(w[0], w[1]), pack2<PT>(w[2], w[3]), pack2<PT>(w[4], w[5]), pack2<PT>(w[6], w[7])));
     }
 }

@@ -1127,7 +1127,9 @@ __global__ void __launch_bounds__(256) zero_linear_prep_kernel(const __grid_cons
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
     if (a.vec && col + 8 <= a.N) {
-#pragma unroll 4
+        // rows in flight: 8192 x 8192 with GELU, 2 rows 51 us, 4 rows 60 us; without activation 4 rows 24 us
+        constexpr int kRows = ACT == ZERO_ACT_NONE ? 4 : 2;
+#pragma unroll kRows
         for (long long r = r0 + line; r < r1; r += 8) {
             const uint4 u = *reinterpret_cast<const uint4*>(dy + r * a.lddy + col);
             uint32_t g[4] = {u.x, u.y, u.z, u.w};
