@@ -640,7 +640,7 @@ __device__ __forceinline__ void bias_sum(const GemmArgs& args, int lane)
 {
     for (int c = blockIdx.x * 32 + lane; c < args.n_db; c += gridDim.x * 32) {
         float s = 0.0f;
-#pragma unroll 8
+#pragma unroll 16
         for (int k = 0; k < args.chunks; ++k) s += args.sums[static_cast<long long>(k) * args.n_db + c];
         store16(args.db, c, s, args.bf16);
     }
@@ -1127,8 +1127,9 @@ __global__ void __launch_bounds__(256) zero_linear_prep_kernel(const __grid_cons
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
     if (a.vec && col + 8 <= a.N) {
-        // rows in flight: 8192 x 8192 with GELU, 2 rows 51 us, 4 rows 60 us; without activation 4 rows 24 us
-        constexpr int kRows = ACT == ZERO_ACT_NONE ? 4 : 2;
+        // rows a thread has in flight: 8192 x 8192, sums alone: GELU 1 row (six CTAs an SM) 50 us, 2 rows 55 us, 4 rows
+        // 77 us; no activation 4 rows (four CTAs an SM) 24 us, 1 row 45 us
+        constexpr int kRows = ACT == ZERO_ACT_NONE ? 4 : 1;
 #pragma unroll kRows
         for (long long r = r0 + line; r < r1; r += 8) {
             const uint4 u = *reinterpret_cast<const uint4*>(dy + r * a.lddy + col);
@@ -1153,6 +1154,7 @@ __global__ void __launch_bounds__(256) zero_linear_prep_kernel(const __grid_cons
             if (dz) *reinterpret_cast<uint4*>(dz + r * a.lddz + col) = make_uint4(g[0], g[1], g[2], g[3]);
         }
     } else {
+#pragma unroll 2
         for (long long r = r0 + line; r < r1; r += 8) {
             float d[8];
 #pragma unroll
@@ -1521,17 +1523,18 @@ constexpr int64_t kMostLd = int64_t{1} << 38;
 
 bool bad_ld(int64_t ld, int64_t cols) { return ld < cols || ld > kMostLd; }
 
-// Rows of a chunk of the column sums: about four CTAs per SM, at least 32 rows.
-int sum_rows(int64_t T, int64_t N)
+// Rows of a chunk of the column sums: four CTAs per SM, six where an
+// activation's arithmetic wants the warps, and at least 8 rows.
+int sum_rows(int64_t T, int64_t N, int act)
 {
     const int64_t stripes = (N + kSumCols - 1) / kSumCols;
-    const int64_t want = std::max<int64_t>(1, 608 / stripes);
-    return static_cast<int>(std::max<int64_t>(32, up((T + want - 1) / want, 8)));
+    const int64_t want = std::max<int64_t>(1, (act == ZERO_ACT_NONE ? 608 : 912) / stripes);
+    return static_cast<int>(std::max<int64_t>(8, up((T + want - 1) / want, 8)));
 }
 
-int64_t sum_chunks(int64_t T, int64_t N)
+int64_t sum_chunks(int64_t T, int64_t N, int act)
 {
-    const int64_t r = sum_rows(T, N);
+    const int64_t r = sum_rows(T, N, act);
     return std::max<int64_t>(1, (T + r - 1) / r);
 }
 
@@ -1607,7 +1610,7 @@ extern "C" int zero_linear_workspace(int64_t T, int64_t K, int64_t N, int32_t ac
     }
     if (backward) {
         if (act != ZERO_ACT_NONE || !aligned) c.take(matrix_bytes(T, N));
-        c.take(sum_chunks(T, N) * N * 4);
+        c.take(sum_chunks(T, N, act) * N * 4);
     }
     *bytes = c.used;
     return ZERO_OK;
@@ -1700,7 +1703,7 @@ extern "C" int zero_linear_backward(const void* dy, int64_t lddy, const void* z,
     void* tx = fix_x ? c.take(matrix_bytes(T, K)) : nullptr;
     void* tw = fix_w ? c.take(matrix_bytes(N, K)) : nullptr;
     void* tz = make_dz ? c.take(matrix_bytes(T, N)) : nullptr;
-    const int64_t chunks = sum_chunks(T, N);
+    const int64_t chunks = sum_chunks(T, N, act);
     float* sums = db ? static_cast<float*>(c.take(chunks * N * 4)) : nullptr;
     if (c.used > 0) {
         if (!workspace || workspace_bytes < c.used) return ZERO_EINVAL;
@@ -1711,7 +1714,7 @@ extern "C" int zero_linear_backward(const void* dy, int64_t lddy, const void* z,
     PrepArgs prep{};
     if (make_dz || db) {
         prep.dy = dy, prep.lddy = lddy, prep.z = z, prep.ldz = ldz, prep.dz = tz, prep.lddz = up(N, 8), prep.sums = sums;
-        prep.T = T, prep.N = static_cast<int>(N), prep.rows_per = sum_rows(T, N);
+        prep.T = T, prep.N = static_cast<int>(N), prep.rows_per = sum_rows(T, N, act);
         prep.vec = aligned16(dy, lddy) && (!has_act || aligned16(z, ldz));
         prep.stripes = static_cast<int>((N + kSumCols - 1) / kSumCols);
         prep.chunks = static_cast<int>(chunks);
