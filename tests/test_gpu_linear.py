@@ -28,7 +28,7 @@ def z(zlib):
 
 def act64(a, z):
     if a == 1:
-        return torch.where(z > 0, z, torch.zeros_like(z))
+        return torch.where(z < 0, torch.zeros_like(z), z)     # NaN stays NaN
     if a == 2:
         return torch.nn.functional.gelu(z, approximate="tanh")
     if a == 3:
@@ -270,6 +270,55 @@ def test_non_finite_values_stay_in_their_rows(z):
         ok = torch.ones(T, dtype=torch.bool, device="cuda")
         ok[1] = ok[5] = False
         assert torch.equal(y0[ok], y1[ok]) and bool(torch.isnan(y1[1]).all()) and not bool(torch.isfinite(y1[5]).any())
+
+
+def test_activations_at_extreme_values(z):
+    """Pre-activations as far out as bf16 goes, through a layer of one input (z = x): the activation and its slope take
+    their limits, NaN stays NaN."""
+    vals = [0.0, -0.0, 1e-38, -1e-38, 30.0, -30.0, 1e4, -1e4, 1e19, -1e19, 3e38, -3e38, math.inf, NAN]
+    T = len(vals)
+    x = torch.tensor(vals, device="cuda").bfloat16()[:, None]
+    one = torch.ones((1, 1), dtype=torch.bfloat16, device="cuda")
+    ws, n = workspace(z, T, 1, 1, 2, True, False)
+    for act in (1, 2, 3):
+        y, zz, dx = (torch.empty((T, 1), dtype=torch.bfloat16, device="cuda") for _ in range(3))
+        z.zero_linear_forward(x, 1, one, 1, None, None, 0, y, 1, zz, 1, T, 1, 1, act, 1, ws, n)
+        z.zero_linear_backward(one.expand(T, 1).contiguous(), 1, zz, 1, x, 1, one, 1, dx, 1, None, 0, None, T, 1, 1, act, 1, ws, n)
+        xd = x.double()
+        want = torch.where(xd > 40, xd, torch.where(xd < -40, torch.zeros_like(xd), act64(act, xd)))
+        slope = torch.where(xd > 40, 1.0, torch.where(xd < -40, 0.0, slope64(act, xd)))
+        if act == 1:
+            slope[-1] = 0                                     # the slope of ReLU is a comparison
+        for got, ref in ((y, want), (dx, slope)):
+            got, ref = got.double(), ref.double()
+            assert torch.equal(torch.isnan(got), torch.isnan(ref)), (act, got, ref)
+            ok = ~torch.isnan(ref) & ~torch.isinf(ref)
+            assert bool((got[ok] - ref[ok]).abs().le(2.0 ** -7 * ref[ok].abs() + 1e-30).all()), (act, got, ref)
+            assert torch.equal(got[torch.isinf(ref)], ref[torch.isinf(ref)])
+
+
+def test_large_offsets(z):
+    """An output of more than 2^31 elements, few inputs: its first and last rows."""
+    T, K, N = 270000, 64, 8192
+    x, w = torch.randn((T, K), device="cuda").bfloat16(), (torch.randn((N, K), device="cuda") / 8).bfloat16()
+    b = torch.randn(N, device="cuda").bfloat16()
+    y = torch.empty((T, N), dtype=torch.bfloat16, device="cuda")
+    z.zero_linear_forward(x, K, w, K, b, None, 0, y, N, None, 0, T, K, N, 1, 1)
+    rowsel = torch.cat([torch.arange(300), torch.arange(262140, 262150), torch.arange(T - 300, T)]).cuda()
+    ref = (x[rowsel].double() @ w.double().T + b.double()).clamp(min=0)
+    mag = x[rowsel].double().abs() @ w.double().abs().T + b.double().abs()
+    assert bool(((y[rowsel].double() - ref).abs() <= (K + 8) * 2.0 ** -23 * mag + 2.0 ** -8 * ref.abs() + 1e-30).all())
+    dw, db = torch.empty_like(w), torch.empty_like(b)
+    ws, n = workspace(z, T, K, N, 1, True, True)
+    dy = y                                                     # any values will do: y as its own gradient, ReLU by y's sign
+    z.zero_linear_backward(dy, N, y, N, x, K, None, 0, None, 0, dw, K, db, T, K, N, 1, 1, ws, n)
+    part = [(dy[r:r + 30000].float(), x[r:r + 30000].float()) for r in range(0, T, 30000)]
+    ref = sum((d.double().sum(0) for d, _ in part))
+    assert bool(((db.double() - ref).abs() <= (T + 8) * 2.0 ** -23 * ref + 2.0 ** -8 * ref).all())
+    cols = torch.arange(0, N, 1000, device="cuda")
+    ref = sum(d[:, cols].double().T @ v.double() for d, v in part)
+    mag = sum(d[:, cols].double().T @ v.double().abs() for d, v in part)
+    assert bool(((dw[cols].double() - ref).abs() <= (T + 8) * 2.0 ** -23 * mag + 2.0 ** -8 * ref.abs()).all())
 
 
 def test_column_slices_of_one_buffer_and_streams(z):

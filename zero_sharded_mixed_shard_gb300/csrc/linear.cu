@@ -429,7 +429,7 @@ template <int ACT> __device__ __forceinline__ float logistic(float z)
 
 template <int ACT> __device__ __forceinline__ float activate(float z)
 {
-    if constexpr (ACT == ZERO_ACT_RELU) return z > 0.0f ? z : 0.0f;
+    if constexpr (ACT == ZERO_ACT_RELU) return z < 0.0f ? 0.0f : z; // NaN stays NaN
     else if constexpr (ACT == ZERO_ACT_NONE) return z;
     else return z * logistic<ACT>(z);
 }
@@ -441,7 +441,8 @@ template <int ACT> __device__ __forceinline__ float slope(float z)
     else if constexpr (ACT == ZERO_ACT_NONE) return 1.0f;
     else {
         const float p = logistic<ACT>(z), q = fmaf(-p, p, p);
-        return fmaf(q, ACT == ZERO_ACT_GELU ? z * fmaf(z * z, 3.0f * kGelu3, kGelu) : z, p);
+        const float d = fmaf(q, ACT == ZERO_ACT_GELU ? z * fmaf(z * z, 3.0f * kGelu3, kGelu) : z, p);
+        return q == 0.0f ? p : d; // far out, where z's powers may be infinite
     }
 }
 
