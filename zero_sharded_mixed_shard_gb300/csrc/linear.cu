@@ -1099,6 +1099,8 @@ struct PrepArgs {
     Copy copy[3];
 };
 
+// 8 elements a thread, two bytes at a time (four-byte reads where rows allow
+// them were no faster: the copies' time is latency).
 __device__ __forceinline__ void copy_rows(const Copy& c, int cta)
 {
     const int vecs = (c.cols + 7) / 8;
@@ -1143,7 +1145,7 @@ __global__ void __launch_bounds__(256) zero_linear_prep_kernel(const __grid_cons
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
     if (a.vec && col + 8 <= a.N) {
-        // rows a thread has in flight: 8192 x 8192, sums alone: GELU 1 row (six CTAs an SM) 50 us, 2 rows 55 us, 4 rows
+        // rows a thread has in flight: 8192 x 8192, sums alone: GELU 1 row (five CTAs an SM) 53 us, 2 rows 63 us, 4 rows
         // 77 us; no activation 4 rows (four CTAs an SM) 24 us, 1 row 45 us
         constexpr int kRows = ACT == ZERO_ACT_NONE ? 4 : 1;
 #pragma unroll kRows
@@ -1539,12 +1541,12 @@ constexpr int64_t kMostLd = int64_t{1} << 38;
 
 bool bad_ld(int64_t ld, int64_t cols) { return ld < cols || ld > kMostLd; }
 
-// Rows of a chunk of the column sums: four CTAs per SM, six where an
-// activation's arithmetic wants the warps, and at least 8 rows.
+// Rows of a chunk of the column sums: four CTAs per SM, five (all that fit)
+// where an activation's arithmetic wants the warps, and at least 8 rows.
 int sum_rows(int64_t T, int64_t N, int act)
 {
     const int64_t stripes = (N + kSumCols - 1) / kSumCols;
-    const int64_t want = std::max<int64_t>(1, (act == ZERO_ACT_NONE ? 608 : 912) / stripes);
+    const int64_t want = std::max<int64_t>(1, (act == ZERO_ACT_NONE ? 608 : 760) / stripes);
     return static_cast<int>(std::max<int64_t>(8, up((T + want - 1) / want, 8)));
 }
 
