@@ -164,8 +164,8 @@ int zero_linear_workspace(int64_t T, int64_t K, int64_t N, int32_t act, int32_t 
  * Errors: ZERO_EINVAL (sizes above 2^31 - 513, a null pointer, a row stride
  * below its row, act or type unknown, workspace too small), ZERO_EALIGN
  * (a pointer not on its element size, workspace not on 16 bytes),
- * ZERO_EOVERLAP (y or z shares an element with an input or each other),
- * ZERO_ECUDA. */
+ * ZERO_EOVERLAP (y or z shares an element with an input or each other, or the
+ * used workspace a byte with any of them), ZERO_ECUDA. */
 int zero_linear_forward(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias,
                         const void* residual, int64_t ldr, void* y, int64_t ldy, void* z,
                         int64_t ldz, int64_t T, int64_t K, int64_t N, int32_t act, int32_t type,

@@ -126,7 +126,7 @@ X, W, B, Y, ZZ, DX, DW, DB, DY, WS = (BASE * (16 + 16 * k) for k in range(10))
 @pytest.mark.parametrize("kw,code", [
     (dict(x=None), -1), (dict(w=None), -1), (dict(y=None), -1), (dict(T=-1), -1), (dict(K=0), -1), (dict(N=1 << 31), -1), (dict(ldx=63), -1),
     (dict(ldw=63), -1), (dict(ldy=127), -1), (dict(z=ZZ, ldz=100), -1), (dict(r=ZZ, ldr=100), -1), (dict(act=5), -1), (dict(ty=2), -1),
-    (dict(x=X + 2), -1), (dict(ldw=65), -1), (dict(x=X + 2, ws=WS, n=100), -1), (dict(x=X + 2, ws=WS + 8, n=1 << 20), -2),
+    (dict(x=X + 2), -1), (dict(ldw=65), -1), (dict(x=X + 2, ws=WS, n=100), -1), (dict(x=X + 2, ws=WS + 8, n=1 << 20), -2), (dict(x=X + 2, ws=Y - 256, n=1 << 20), -3),
     (dict(x=X + 1), -2), (dict(b=B + 1), -2), (dict(y=Y + 1), -2),
     (dict(y=X), -3), (dict(y=W + 64), -3), (dict(y=B), -3), (dict(z=Y + 2, ldz=128), -3), (dict(r=Y + 2, ldr=128), -3), (dict(z=B, ldz=128), -3)])
 def test_linear_forward_refuses(zlib, kw, code):
@@ -140,7 +140,7 @@ def test_linear_forward_refuses(zlib, kw, code):
     (dict(dy=None), -1), (dict(x=None), -1), (dict(w=None), -1), (dict(z=None), -1), (dict(dx=None, dw=None, db=None), -1), (dict(lddy=100), -1),
     (dict(ldz=100), -1), (dict(lddx=60), -1), (dict(lddw=60), -1), (dict(act=9), -1), (dict(ty=2), -1), (dict(ws=None, n=0), -1), (dict(n=100), -1),
     (dict(dy=DY + 1), -2), (dict(dw=DW + 1), -2), (dict(db=DB + 1), -2), (dict(ws=WS + 4), -2),
-    (dict(dx=DY), -3), (dict(dw=X), -3), (dict(db=DW + 64), -3), (dict(dw=DX + 64), -3), (dict(dx=W), -3), (dict(db=ZZ), -3)])
+    (dict(dx=DY), -3), (dict(dw=X), -3), (dict(db=DW + 64), -3), (dict(dw=DX + 64), -3), (dict(dx=W), -3), (dict(db=ZZ), -3), (dict(ws=DX), -3), (dict(ws=ZZ + 256), -3)])
 def test_linear_backward_refuses(zlib, kw, code):
     a = dict(dy=DY, lddy=128, z=ZZ, ldz=128, x=X, ldx=64, w=W, ldw=64, dx=DX, lddx=64, dw=DW, lddw=64, db=DB, T=10, K=64, N=128, act=2, ty=0,
              ws=WS, n=1 << 20)

@@ -1087,7 +1087,7 @@ struct Copy {
 };
 
 // What has to be done before the products: dz and its column sums over
-// chunks of rows (`stripes` x `chunks` CTAs), and up to three copies.
+// chunks of rows (`stripes` x `chunks` CTAs), and up to two copies.
 struct PrepArgs {
     const void* dy;
     const void* z;
@@ -1096,7 +1096,7 @@ struct PrepArgs {
     long long lddy, ldz, lddz, T;
     int N, rows_per, vec;
     int stripes, chunks;
-    Copy copy[3];
+    Copy copy[2];        // x, w
 };
 
 // 8 elements a thread, two bytes at a time (four-byte reads where rows allow
@@ -1128,7 +1128,7 @@ __global__ void __launch_bounds__(256) zero_linear_prep_kernel(const __grid_cons
     int cta = blockIdx.x - a.stripes * a.chunks;
     if (cta >= 0) {
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
+        for (int k = 0; k < 2; ++k) {
             if (cta >= 0 && cta < a.copy[k].ctas) copy_rows(a.copy[k], cta);
             cta -= a.copy[k].ctas;
         }
@@ -1537,6 +1537,14 @@ bool bad_sizes(int64_t T, int64_t K, int64_t N, int32_t act, int32_t type)
            (type != ZERO_TYPE_FP16 && type != ZERO_TYPE_BF16);
 }
 
+// Whether a matrix has a byte in the used part of the workspace.
+bool in_workspace(const void* ws, int64_t used, const void* p, int64_t ld, int64_t rows, int64_t cols)
+{
+    if (!p || rows < 1) return false;
+    const uintptr_t end = addr(p) + (static_cast<uintptr_t>(rows - 1) * ld + cols) * 2;
+    return addr(p) < addr(ws) + static_cast<uintptr_t>(used) && addr(ws) < end;
+}
+
 constexpr int64_t kMostLd = int64_t{1} << 38;
 
 bool bad_ld(int64_t ld, int64_t cols) { return ld < cols || ld > kMostLd; }
@@ -1664,6 +1672,9 @@ extern "C" int zero_linear_forward(const void* x, int64_t ldx, const void* w, in
     if (c.used > 0) {
         if (!workspace || workspace_bytes < c.used) return ZERO_EINVAL;
         if (addr(workspace) % 16) return ZERO_EALIGN;
+        const Matrix all[] = {{x, ldx, T, K}, {w, ldw, N, K}, {bias, N, 1, N}, {residual, ldr, T, N}, {y, ldy, T, N}, {z, ldz, T, N}};
+        for (const Matrix& q : all)
+            if (in_workspace(workspace, c.used, q.p, q.ld, q.rows, q.cols)) return ZERO_EOVERLAP;
     }
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
     int rc = ZERO_OK, ctas = 0;
@@ -1726,6 +1737,10 @@ extern "C" int zero_linear_backward(const void* dy, int64_t lddy, const void* z,
     if (c.used > 0) {
         if (!workspace || workspace_bytes < c.used) return ZERO_EINVAL;
         if (addr(workspace) % 16) return ZERO_EALIGN;
+        for (const auto& q : in)
+            if (in_workspace(workspace, c.used, q.p, q.ld, q.rows, q.cols)) return ZERO_EOVERLAP;
+        for (const auto& q : out)
+            if (in_workspace(workspace, c.used, q.p, q.ld, q.rows, q.cols)) return ZERO_EOVERLAP;
     }
     Matrix mx{x, ldx, T, K}, mw{w, ldw, N, K}, mz{dy, lddy, T, N};
     int rc = ZERO_OK, ctas = 0;
