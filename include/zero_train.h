@@ -109,8 +109,9 @@ int zero_grad_norm(const zero_adamw_plan_t* plan, void* table, float grad_scale,
  *   param = round(w)  (nearest even)
  * with lr_j = lr * lr_scale_j, 1-b in fp32, r1 = fp32(1 / (1 - b1^t)) and
  * c2 = fp32(1 / sqrt(1 - b2^t)) (from the fp32 betas, in double).  The
- * square root and the quotient are within 2 ulp (they enter the update, which
- * is small against the weight); every other operation is correctly rounded.
+ * quotient, and with 32-bit moments the square root, are within 2 ulp (they
+ * enter the update, which is small against the weight); every other operation
+ * is correctly rounded (the root for v >= 2^-126).
  * stats NULL: no factor.  stats (of zero_grad_norm, on the same stream):
  * g is multiplied by stats[1], and when stats[2] is 0 the step leaves
  * everything as it was (a gradient overflowed).

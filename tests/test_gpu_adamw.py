@@ -217,6 +217,47 @@ def test_paths_agree(z):
             assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
 
 
+def mix(h):
+    h = ((h ^ (h >> 16)) * 0x85EBCA6B) & 0xFFFFFFFF
+    h = ((h ^ (h >> 13)) * 0xC2B2AE35) & 0xFFFFFFFF
+    return h ^ (h >> 16)
+
+
+@pytest.mark.parametrize("n,P,gt", [(12000000, 1, 1), (300000, 3, 0), (12000000, 2, 2)])
+def test_8_bit_states_bit_for_bit(z, n, P, gt):
+    """Codes and scales of two steps against the formulas in separately rounded fp32 torch operations: equal bits, on the
+    pipeline and on the vector kernel.  (A code that differed would move the next step's weight by up to a tenth of an
+    update.)"""
+    c = Case(z, [n], P, gt, 0, 8, seed=n + P)
+    o, nb, so, top = c.offs[0], -(-n // 256), c.so[0], torch.tensor(448.0)
+    pad = lambda t: torch.nn.functional.pad(t, (0, nb * 256 - n)).view(nb, 256)  # noqa: E731
+    one, b1, b2 = np.float32(1), np.float32(B1), np.float32(B2)
+    for t in (7, 8):
+        m8, v8, ms, vs = c.m[o:o + n].clone(), c.v[o:o + n].clone(), c.ms[so:so + nb].clone(), c.vs[so:so + nb].clone()
+        z.zero_adamw_step(c.plan, None, t, LR, B1, B2, EPS, t)
+        g = c.g[0, o:o + n].float()
+        for r in range(1, P):
+            g = g + c.g[r, o:o + n].float()
+        if P > 1:
+            g = g / torch.full((), P, dtype=torch.float32, device="cuda")
+        g = pad(g)
+        m = pad(m8.view(torch.float8_e4m3fn).float()) * ms[:, None]
+        r = pad(v8.view(torch.float8_e4m3fn).float()) * vs[:, None]
+        m = m * float(b1) + g * float(one - b1)
+        r = ((r * r) * float(b2) + (g * g) * float(one - b2)).sqrt()
+        hm, hr = m.abs().amax(1, keepdim=True), r.amax(1, keepdim=True)
+        assert torch.equal(c.ms[so:so + nb], (hm * f32(1 / 448)).view(-1)) and torch.equal(c.vs[so:so + nb], (hr * f32(1 / 448)).view(-1))
+        code = (m * (top / hm)).to(torch.float8_e4m3fn).view(torch.uint8).view(-1)[:n]
+        assert torch.equal(c.m[o:o + n], code)
+        key = mix((mix(t) + 0x9E3779B9) & 0xFFFFFFFF)
+        h = mix((torch.arange(nb * 128, device="cuda") + key) & 0xFFFFFFFF)
+        bits = torch.stack((h & 0xFFFF, h >> 16), 1).view(nb, 256).int()
+        y = r * (top / hr)
+        cut = ((y * 2.0 ** -120).view(torch.int32) + (bits << 4)) >> 20
+        code = torch.where(y > 0, cut.clamp(1, 0x7E), 0).to(torch.uint8).view(-1)[:n]
+        assert torch.equal(c.v[o:o + n], code)
+
+
 def test_zero_state_and_zero_gradients(z):
     """The first step from zero moments; elements without a gradient keep their weight (no decay) and zero moments."""
     for bits in (32, 8):

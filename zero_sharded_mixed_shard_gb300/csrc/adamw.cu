@@ -227,11 +227,32 @@ __device__ __forceinline__ float fast_sqrt(float x)
     return y;
 }
 
+// The root correctly rounded from the approximate one, s = x y: s plus half of
+// y times the exact remainder x - s^2 (P. Markstein, as above).  A stored code
+// follows from the root's bits, so that a step on equal states gives equal
+// codes wherever the same fp32 operations are done.  x >= 0; below 2^-126 the
+// result is only between 0 and 2^-63.
+__device__ __forceinline__ float exact_sqrt(float x)
+{
+    float y;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaxf(x, 1.17549435e-38f)));
+    const float s = __fmul_rn(x, y);
+    return __fmaf_rn(__fmaf_rn(-s, s, x), __fmul_rn(0.5f, y), s);
+}
+
 __device__ __forceinline__ float fast_rcp(float x)
 {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x)); // 1 ulp
     return y;
+}
+
+// 448 / a correctly rounded: the reciprocal refined to the nearest one, then
+// the quotient.
+__device__ __forceinline__ float scale_inverse(float a)
+{
+    const float r = fast_rcp(a);
+    return divide(kMax8, a, __fmaf_rn(__fmaf_rn(-a, r, 1.0f), r, r));
 }
 
 // ---------------------------------------------------------------------------
@@ -277,7 +298,7 @@ __device__ __forceinline__ void update(const Args& a, const Block& k, float (&w)
         const float gg = __fmul_rn(ONE ? g[j] : mean_of(g[j], a), k.factor);
         m[j] = __fadd_rn(__fmul_rn(m[j], a.b1), __fmul_rn(gg, a.omb1));
         v[j] = __fadd_rn(__fmul_rn(v[j], a.b2), __fmul_rn(__fmul_rn(gg, gg), a.omb2));
-        const float root = fast_sqrt(v[j]);
+        const float root = BITS == 8 ? exact_sqrt(v[j]) : fast_sqrt(v[j]);
         const float inv = fast_rcp(__fadd_rn(__fmul_rn(root, a.c2), a.eps));
         w[j] = __fsub_rn(w[j], __fmul_rn(k.decay, w[j]));
         w[j] = __fsub_rn(w[j], __fmul_rn(k.lr, __fmul_rn(__fmul_rn(m[j], a.r1), inv)));
@@ -291,7 +312,7 @@ __device__ __forceinline__ void update(const Args& a, const Block& k, float (&w)
         high_m = __reduce_max_sync(0xffffffffu, high_m);
         high_r = __reduce_max_sync(0xffffffffu, high_r);
         const float am = __uint_as_float(high_m), ar = __uint_as_float(high_r);
-        const float im = am < kTiny ? 0.0f : divide(kMax8, am, fast_rcp(am)), ir = ar < kTiny ? 0.0f : divide(kMax8, ar, fast_rcp(ar));
+        const float im = am < kTiny ? 0.0f : scale_inverse(am), ir = ar < kTiny ? 0.0f : scale_inverse(ar);
         if ((threadIdx.x & 31) == 0) {
             const float nan = __int_as_float(0x7fffffff);
             *k.ms_out = am < kTiny ? 0.0f : isfinite(am) ? __fmul_rn(am, kInvMax8) : nan;
@@ -515,8 +536,8 @@ __global__ void __launch_bounds__(kThreads, 3) zero_adamw_kernel(const __grid_co
 // copies in flight do not depend on the warps' registers or on how far their
 // arithmetic has come, which is what bounds the vector kernel.
 // Measured, 1.3e9 parameters, P = 1: 32-bit moments 5.50 ms (6620 GB/s, 0.975 of
-// the measured copy bandwidth; vector kernel 6.2 ms), 8-bit ones 3.37 ms (6200
-// GB/s, 0.914; vector kernel 3.7 ms), where the arithmetic, about 75
+// the measured copy bandwidth; vector kernel 6.2 ms), 8-bit ones 3.45 ms (6060
+// GB/s, 0.893; vector kernel 3.7 ms), where the arithmetic, about 80
 // instructions an element, takes nearly the time of the bytes.
 constexpr int kGroups = 3;
 constexpr int kPipeThreads = 32 + kGroups * kThreads;
