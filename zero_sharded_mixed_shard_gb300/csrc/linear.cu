@@ -1103,10 +1103,11 @@ struct PrepArgs {
 // them were no faster: the copies' time is latency).
 __device__ __forceinline__ void copy_rows(const Copy& c, int cta)
 {
-    const int vecs = (c.cols + 7) / 8;
+    const unsigned int vecs = (c.cols + 7) / 8;
     const long long total = c.rows * vecs;
+    const bool narrow = total <= 0xffffffffll; // a 64-bit division costs as much as the rest
     for (long long i = cta * 256ll + threadIdx.x; i < total; i += c.ctas * 256ll) {
-        const long long r = i / vecs;
+        const long long r = narrow ? static_cast<unsigned int>(i) / vecs : i / vecs;
         const int at = static_cast<int>(i - r * vecs) * 8;
         const uint16_t* p = c.src + r * c.lds + at;
         uint32_t h[8];
@@ -1406,7 +1407,8 @@ Variant choose(const Product* p, int count, int sms, double* estimate)
             longest = std::max(longest, one);
         }
         const double rounds = std::ceil(ctas / (v.pair ? sms / 2 : v.per_sm * sms));
-        const double time = base + std::max(work / ctas * rounds, longest);
+        // a CTA that follows another one has its own start
+        const double time = base + std::max(work / ctas * rounds, longest) + (v.pair ? 0.0 : 1.6 * (rounds - 1.0));
         if (time < best) best = time, out = v;
     };
     if (!swapped) consider({true, 256, 1, 1}, 6.3, 1.5, 0.30);
@@ -1426,13 +1428,12 @@ Variant choose(const Product* p, int count, int sms, double* estimate)
     return out;
 }
 
-// Whether the gradients' two products go into launches of their own.  With few
-// tokens they want tiles of different shapes, and one launch is not always the
-// quicker form (64 tokens, 2048 -> 2048: 10 us in one, 24 in two; 4 tokens,
-// 2048 -> 8192: 30 in one, 27 in two).
+// Whether the gradients' two products go into launches of their own: where
+// they want tiles of different shapes, one launch is not always the quicker
+// form (64 tokens, 2048 -> 2048: 10 us in one, 24 in two; 4 tokens, 2048 ->
+// 8192: 30 in one, 27 in two).
 bool apart(const Product* p, int sms)
 {
-    if (!p[0].o.swap) return false;
     double one, first, second;
     choose(p, 2, sms, &one);
     choose(p, 1, sms, &first);
@@ -1589,7 +1590,7 @@ void add_copy(PrepArgs* a, int* ctas, int slot, Matrix* x, void* to)
     c.ldd = ld;
     c.rows = x->rows;
     c.cols = static_cast<int>(x->cols);
-    c.ctas = static_cast<int>(std::min<int64_t>(1216, (vecs + 255) / 256));
+    c.ctas = static_cast<int>(std::min<int64_t>(4864, (vecs + 255) / 256));
     *ctas += c.ctas;
     x->p = to;
     x->ld = ld;
