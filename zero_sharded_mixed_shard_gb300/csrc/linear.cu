@@ -12,9 +12,9 @@
 //
 // Two kernels.  zero_gemm_pair_kernel (many tiles): persistent pairs of CTAs
 // that share one product of 256 rows (each holds half of the rows and half of
-// the columns' operand), one TMA warp, one MMA warp, four epilogue warps,
-// accumulators doubled in tensor memory so that a tile's epilogue runs under
-// the next tile's products.  zero_gemm_split_kernel (few tiles): the
+// the columns' operand), one TMA warp, one MMA warp, eight epilogue
+// warps, accumulators doubled in tensor memory so that a tile's epilogue runs
+// under the next tile's products.  zero_gemm_split_kernel (few tiles): the
 // contraction is cut over the CTAs of a cluster, whose partial tiles are added
 // through distributed shared memory in a fixed order; with few tokens the
 // operands change sides (m = feature), so that a tile holds 128 rows of the
