@@ -101,17 +101,17 @@ int zero_grad_norm(const zero_adamw_plan_t* plan, void* table, float grad_scale,
                    float* stats, void* cuda_stream);
 
 /* One AdamW step (decoupled weight decay) over every tensor of the plan, in
- * one launch.  Per element, every operation a separately rounded fp32
- * operation in this order:
+ * one launch.  Per element, in fp32 and in this order:
  *   g  = ((0 + g_0) + g_1) + ... + g_{P-1};  g = g / P;  g = g * stats[1]
  *   m  = b1*m + (1-b1)*g;   v = b2*v + (1-b2)*(g*g)
- *   w  = w - (lr_j*wd_j)*w;   w = w - lr_j * ((m*r1) / (sqrt(v)*c2 + eps))
+ *   w  = w - (lr_j*wd_j)*w;   w = w - (m*(lr_j*r1)) / (sqrt(v)*c2 + eps)
  *   param = round(w)  (nearest even)
  * with lr_j = lr * lr_scale_j, 1-b in fp32, r1 = fp32(1 / (1 - b1^t)) and
- * c2 = fp32(1 / sqrt(1 - b2^t)) (from the fp32 betas, in double).  The
- * quotient, and with 32-bit moments the square root, are within 2 ulp (they
- * enter the update, which is small against the weight); every other operation
- * is correctly rounded (the root for v >= 2^-126).
+ * c2 = fp32(1 / sqrt(1 - b2^t)) (from the fp32 betas, in double).  In the
+ * lines of g, m and v every operation is rounded by itself; in the line of w
+ * the products are fused with the sums, and the quotient and, with 32-bit
+ * moments, the square root are within 2 ulp (they enter the update, which is
+ * small against the weight).
  * stats NULL: no factor.  stats (of zero_grad_norm, on the same stream):
  * g is multiplied by stats[1], and when stats[2] is 0 the step leaves
  * everything as it was (a gradient overflowed).

@@ -247,6 +247,13 @@ __device__ __forceinline__ float fast_rcp(float x)
     return y;
 }
 
+__device__ __forceinline__ float max_or_nan(float x, float y)
+{
+    float z;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+    return z;
+}
+
 // 448 / a correctly rounded: the reciprocal refined to the nearest one, then
 // the quotient.
 __device__ __forceinline__ float scale_inverse(float a)
@@ -292,26 +299,27 @@ __device__ __forceinline__ void update(const Args& a, const Block& k, float (&w)
             v[2 * q + 1] = __fmul_rn(ry, ry);
         }
     }
-    unsigned int high_m = 0, high_r = 0; // largest magnitudes, as bits: ordered like the values, NaN above infinity
+    float high_m = 0.0f, high_r = 0.0f; // largest magnitudes, or NaN
+    const float minus_rate = -__fmul_rn(k.lr, a.r1);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const float gg = __fmul_rn(ONE ? g[j] : mean_of(g[j], a), k.factor);
         m[j] = __fadd_rn(__fmul_rn(m[j], a.b1), __fmul_rn(gg, a.omb1));
         v[j] = __fadd_rn(__fmul_rn(v[j], a.b2), __fmul_rn(__fmul_rn(gg, gg), a.omb2));
         const float root = BITS == 8 ? exact_sqrt(v[j]) : fast_sqrt(v[j]);
-        const float inv = fast_rcp(__fadd_rn(__fmul_rn(root, a.c2), a.eps));
-        w[j] = __fsub_rn(w[j], __fmul_rn(k.decay, w[j]));
-        w[j] = __fsub_rn(w[j], __fmul_rn(k.lr, __fmul_rn(__fmul_rn(m[j], a.r1), inv)));
+        const float inv = fast_rcp(__fmaf_rn(root, a.c2, a.eps));
+        w[j] = __fmaf_rn(-k.decay, w[j], w[j]);
+        w[j] = __fmaf_rn(__fmul_rn(m[j], minus_rate), inv, w[j]);
         if constexpr (BITS == 8) {
             v[j] = root;
-            high_m = max(high_m, __float_as_uint(m[j]) & 0x7fffffffu);
-            high_r = max(high_r, __float_as_uint(root));
+            high_m = max_or_nan(high_m, fabsf(m[j]));
+            high_r = max_or_nan(high_r, root);
         }
     }
     if constexpr (BITS == 8) {
-        high_m = __reduce_max_sync(0xffffffffu, high_m);
-        high_r = __reduce_max_sync(0xffffffffu, high_r);
-        const float am = __uint_as_float(high_m), ar = __uint_as_float(high_r);
+        // as bits the magnitudes are ordered like the values, NaN above infinity
+        const float am = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(high_m) & 0x7fffffffu));
+        const float ar = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(high_r) & 0x7fffffffu));
         const float im = am < kTiny ? 0.0f : scale_inverse(am), ir = ar < kTiny ? 0.0f : scale_inverse(ar);
         if ((threadIdx.x & 31) == 0) {
             const float nan = __int_as_float(0x7fffffff);
@@ -336,10 +344,11 @@ __device__ __forceinline__ void update(const Args& a, const Block& k, float (&w)
             // form (bits 30..20; E4M3's subnormals are fp32's), and adding
             // random bits below bit 20 before cutting there rounds up with
             // the probability of what is cut.  A zero stays 0, a root above
-            // zero is at least 1.
+            // zero is at least 1, and the largest, 448, has no bits below its
+            // code 0x7e (a block with the scale NaN may hold any codes).
             const float y = __fmul_rn(v[j], ir);
             const unsigned int cut = (__float_as_uint(__fmul_rn(y, 7.52316384526264e-37f)) + (random << 4)) >> 20;
-            code[j] = min(max(cut, min(__float_as_uint(y), 1u)), 0x7eu);
+            code[j] = max(cut, min(__float_as_uint(y), 1u));
         }
 #pragma unroll
         for (int q = 0; q < 2; ++q)
@@ -415,7 +424,7 @@ __device__ __noinline__ void step_by_elements(const Args& a, const Tensor* x, fl
 // spill (P = 2, 2.0e8 elements 1019 against 900 us).  Measured: eight bf16
 // ranks of 2.0e8 parameters 1.30 ms (6490 GB/s, 0.957 of the measured copy
 // bandwidth), 50 thousand parameters 6.2 us, 4.2e6 parameters of odd sizes with
-// 8-bit moments and fp32 gradients 18.2 us (3950 GB/s).
+// 8-bit moments and fp32 gradients 17.9 us (4010 GB/s).
 template <int GT, int PT, int BITS, bool ONE>
 __global__ void __launch_bounds__(kThreads, 3) zero_adamw_kernel(const __grid_constant__ Args a)
 {
@@ -536,8 +545,8 @@ __global__ void __launch_bounds__(kThreads, 3) zero_adamw_kernel(const __grid_co
 // copies in flight do not depend on the warps' registers or on how far their
 // arithmetic has come, which is what bounds the vector kernel.
 // Measured, 1.3e9 parameters, P = 1: 32-bit moments 5.50 ms (6620 GB/s, 0.975 of
-// the measured copy bandwidth; vector kernel 6.2 ms), 8-bit ones 3.45 ms (6060
-// GB/s, 0.893; vector kernel 3.7 ms), where the arithmetic, about 80
+// the measured copy bandwidth; vector kernel 6.2 ms), 8-bit ones 3.31 ms (6300
+// GB/s, 0.929; vector kernel 3.7 ms), where the arithmetic, about 75
 // instructions an element, takes nearly the time of the bytes.
 constexpr int kGroups = 3;
 constexpr int kPipeThreads = 32 + kGroups * kThreads;
@@ -546,8 +555,9 @@ constexpr int kPipeThreads = 32 + kGroups * kThreads;
 // only by parity).
 constexpr int kMaxStages = 15;
 constexpr int kPipeSmem = 224 * 1024;
-// More copies in flight than this cost the stores: 32-bit moments, P = 1,
-// 3 stages of 28 KB 6620 GB/s, 6 stages 6410 GB/s.
+// More copies in flight than this cost the stores (32-bit moments, P = 1: 3
+// stages of 28 KB 6620 GB/s, 6 stages 6410), fewer leave reads waiting (8-bit,
+// fp32 gradients: 3 stages of 20 KB 5510 GB/s, 6 stages 6730).
 constexpr int kPipeTarget = 112 * 1024;
 static_assert(kMaxStages % kGroups == 0, "stages by groups");
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;
@@ -979,18 +989,20 @@ Kernel pick_norm(int grad)
     }
 }
 
-// Stages of the pipeline: about 112 KB, and three at least where they fit.
+// Stages of the pipeline: the multiple of the groups nearest to 112 KB, one
+// each at least where they fit.
 int pipeline_stages(int64_t stage)
 {
-    const int64_t n = std::min<int64_t>(kMaxStages, kPipeTarget / stage) / kGroups * kGroups;
-    return static_cast<int>(std::max<int64_t>(n, kGroups * stage <= kPipeSmem ? kGroups : 0));
+    const int64_t most = std::min<int64_t>(kMaxStages, kPipeSmem / stage) / kGroups;
+    const int64_t near = std::max<int64_t>(1, (2 * kPipeTarget / (stage * kGroups) + 1) / 2);
+    return static_cast<int>(std::min(near, most)) * kGroups;
 }
 
 // Where the pipeline beats the vector kernel.  Measured (GB/s, vector against
 // pipeline): 32-bit moments, P = 1, 3.0e8 elements 6070 / 6640, 1.2e7 5560 /
 // 5690, 3.9e6 4920 / 4350; P = 2 6740 / 6660, P = 4 6730 / 6740, P = 8 6640 /
 // 6470 (more ranks read more than they write and leave the vector kernel
-// enough copies in flight).  8-bit moments, P = 1, 3.0e8 elements 5860 / 6070,
+// enough copies in flight).  8-bit moments, P = 1, 3.0e8 elements 5860 / 6300,
 // 9.4e6 4170 / 4080, 3.9e6 3160 / 2730; P = 4 9.4e6 4550 / 5000; P = 8 5.0e7
 // 5580 / 6990.
 bool takes_pipeline(int64_t chunks, int bits, int P) { return chunks >= 4096 && (bits == 8 || P == 1); }
