@@ -69,6 +69,7 @@ struct Out {
 
 struct Problem {
     CUtensorMap a, b;
+    CUtensorMap y, z;    // pairs, where o.vec: the outputs
     Out o;
     int a_mn, b_mn;      // 0: the operand's contiguous index is k; 1: it is m (n); 2: that, in whole blocks of 64
     int m, n;            // extents on the A and the B side
@@ -212,6 +213,16 @@ __device__ __forceinline__ void tma_load3(void* dst, const CUtensorMap* map, int
                  " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
                  "l"(map), "r"(0), "r"(k), "r"(block), "r"(smem_addr(bar))
                  : "memory");
+}
+
+// 32 rows x 64 columns of shared memory (128-byte swizzle) to an output; what
+// lies past its extents is not written.
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, int x, int y, const void* src)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x), "r"(y),
+                 "r"(smem_addr(src))
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
 __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
@@ -664,7 +675,100 @@ __device__ __forceinline__ void bias_sum(const GemmArgs& args, int lane)
 // arithmetic took longer than the products it runs under (234 us).
 template <int BN> constexpr int kPairStage = kATile + BN / 2 * kBK * 2;
 constexpr int kPieceBytes = 32 * 32 * 2;
-constexpr int kEpilogueBytes = kEpilogueWarps * kPieceBytes;
+constexpr int kStoreBytes = 32 * 64 * 2; // a warp's staging for stores by TMA
+constexpr int kEpilogueBytes = kEpilogueWarps * kStoreBytes;
+
+// The staging is free again once the last store has read it.  The elected lane
+// is the same every time, so that it waits for its own stores.
+__device__ __forceinline__ void staging_free()
+{
+    if (elect_one()) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
+}
+
+// This lane's row of a half (32 columns) of the staging: 16-byte chunk q at
+// q ^ (row & 7), the 128-byte swizzle.
+template <int BF16> __device__ __forceinline__ void stage_row(uint4* staging, int half, const float (&v)[32], int lane)
+{
+#pragma unroll
+    for (int q = 0; q < 4; ++q) staging[lane * 8 + ((half * 4 + q) ^ (lane & 7))] = pack8(v + 8 * q, BF16);
+}
+
+__device__ __forceinline__ void send_staging(const CUtensorMap* map, int col, int row, const uint4* staging)
+{
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (elect_one()) tma_store(map, col, row, staging);
+    __syncwarp();
+}
+
+template <int BF16> __device__ __forceinline__ void add_bias(const Out& o, int col, float (&v)[32])
+{
+    if (!o.bias) return;
+    const uint4* b = reinterpret_cast<const uint4*>(at16(o.bias, 0, 0, col));
+#pragma unroll
+    for (int q = 0; q < 4; ++q) add8(v + 8 * q, __ldg(b + q), BF16);
+}
+
+// 32 rows x 64 whole columns of a tile, from tensor memory to the outputs by
+// TMA stores: the lanes only compute, and memory gets full lines (16384 x 64
+// -> 8192, bf16, bound by its output: 64 us, with stores by the lanes 82 us).
+// The accumulators are read a second time where the pre-activation is kept;
+// `release` is called when they have been read for the last time.
+template <int BF16, class Release>
+__device__ __forceinline__ void emit_block_as(const Problem& g, uint32_t acc, int row0, int rows, int col, uint4* staging, int lane,
+                                              Release release)
+{
+    const Out& o = g.o;
+    if (o.z) {
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+            float v[32];
+            tmem_load(acc + h * 32, v);
+            add_bias<BF16>(o, col + h * 32, v);
+            if (h == 0) staging_free();
+            stage_row<BF16>(staging, h, v, lane);
+        }
+        send_staging(&g.z, col, row0, staging);
+    }
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+        uint4 res[4] = {};
+        if (o.res) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if ((lane >> 2) + 8 * k < rows)
+                    res[k] = *reinterpret_cast<const uint4*>(
+                        at16(o.res, o.ldr, row0 + (lane >> 2) + 8 * k, col + h * 32 + (lane & 3) * 8));
+        }
+        float v[32];
+        tmem_load(acc + h * 32, v);
+        if (h == 1) release();
+        add_bias<BF16>(o, col + h * 32, v);
+        activate_all(v, o.act);
+        if (h == 0) staging_free();
+        if (o.res) { // lanes along the rows read it, each lane needs its own row
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = (lane >> 2) + 8 * k;
+                staging[r * 8 + ((h * 4 + (lane & 3)) ^ (r & 7))] = res[k];
+            }
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) add8(v + 8 * q, staging[lane * 8 + ((h * 4 + q) ^ (lane & 7))], BF16);
+        }
+        stage_row<BF16>(staging, h, v, lane);
+    }
+    send_staging(&g.y, col, row0, staging);
+}
+
+template <class Release>
+__device__ __forceinline__ void emit_block(const Problem& g, uint32_t acc, int row0, int rows, int col, uint4* staging, int lane,
+                                           Release release)
+{
+    if (g.o.bf16) emit_block_as<1>(g, acc, row0, rows, col, staging, lane, release);
+    else emit_block_as<0>(g, acc, row0, rows, col, staging, lane, release);
+}
 
 template <int BN, int STAGES, int COUNT>
 __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_pair_kernel(const __grid_constant__ GemmArgs args)
@@ -775,7 +879,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_pair_kernel(const _
     } else if (warp >= 4) {
         // two warps for each 32 rows, each with half of the columns
         const int q = warp & 3, c0 = ((warp - 4) >> 2) * (BN / 2);
-        uint4* piece = reinterpret_cast<uint4*>(smem + STAGES * kPairStage<BN> + (warp - 4) * kPieceBytes);
+        uint4* staging = reinterpret_cast<uint4*>(smem + STAGES * kPairStage<BN> + (warp - 4) * kStoreBytes);
         int n = 0;
         for (int t = pair; t < args.tiles; t += pairs, ++n) {
             const Problem& g = args.p[COUNT == 1 ? 0 : t >= args.tiles0];
@@ -787,19 +891,38 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_pair_kernel(const _
             fence_after();
             const int row0 = mt * 256 + rank * kBM + q * 32;
             const int rows = min(32, g.m - row0); // that exist; may be 0 or less
+            auto release = [&] {                  // this warp's part is read: the next tile but one may have it
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_at(peer_addr(smem_addr(&acc_empty[acc]), 0));
+            };
 #pragma unroll 1
-            for (int c = c0; c < c0 + BN / 2; c += 32) {
-                float v[32];
-                tmem_load(base + acc * BN + c + (static_cast<uint32_t>(q * 32) << 16), v);
-                if (c + 32 == c0 + BN / 2) { // this warp's part is read: the next tile but one may have it
-                    fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_at(peer_addr(smem_addr(&acc_empty[acc]), 0));
+            for (int c = c0; c < c0 + BN / 2; c += 64) {
+                const bool last = c + 64 == c0 + BN / 2;
+                const uint32_t at = base + acc * BN + c + (static_cast<uint32_t>(q * 32) << 16);
+                const int col = nt * BN + c;
+                if (g.o.vec && rows > 0 && col + 64 <= g.n) {
+                    emit_block(g, at, row0, rows, col, staging, lane, [&] {
+                        if (last) release();
+                    });
+                    continue;
                 }
-                const int cols = min(32, g.n - (nt * BN + c));
-                if (rows > 0 && cols > 0) emit_piece(g.o, row0, rows, nt * BN + c, cols, v, piece, lane);
+                staging_free();
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    const int cols = min(32, g.n - (col + h * 32));
+                    if (rows > 0 && cols > 0) {
+                        float v[32];
+                        tmem_load(at + h * 32, v);
+                        emit_piece(g.o, row0, rows, col + h * 32, cols, v, staging, lane);
+                    }
+                }
+                if (last) release();
             }
         }
+        // the stores have left before the CTA ends
+        if (elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
     }
     __syncthreads();
     __syncwarp();
@@ -1473,6 +1596,10 @@ int gemm(const Product* p, int count, int type, const BiasSum* bias, cudaStream_
                   (static_cast<unsigned int>(bm >> 4) << 24);
         if ((rc = make_map(&g.a, p[k].a, g.a_mn, g.a_mn == 2 ? kBM / 64 : g.a_mn ? 64 : kBM))) return rc;
         if ((rc = make_map(&g.b, p[k].b, g.b_mn, g.b_mn == 2 ? b_rows / 64 : g.b_mn ? 64 : b_rows))) return rc;
+        if (v.pair && g.o.vec) {
+            if ((rc = make_map(&g.y, Matrix{g.o.y, g.o.ldy, p[k].m, p[k].n}, 0, 32))) return rc;
+            if (g.o.z && (rc = make_map(&g.z, Matrix{g.o.z, g.o.ldz, p[k].m, p[k].n}, 0, 32))) return rc;
+        }
         if (tiles_of(p[k], v) > INT32_MAX - 64) return ZERO_EINVAL;
         tiles += clusters_of(p[k], v);
         if (tiles * v.parts > INT32_MAX) return ZERO_EINVAL;
