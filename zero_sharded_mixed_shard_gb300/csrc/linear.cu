@@ -671,7 +671,7 @@ __device__ __forceinline__ void bias_sum(const GemmArgs& args, int lane)
 // Measured: x [16384, 8192] -> 2048 with residual, fp16: 314 us alone (1750
 // TFLOP/s; the library's product without residual 320 us), 372 us back to back
 // at the power limit (1480 TFLOP/s; the library 349 us); [8192, 2048] -> 8192
-// with GELU 154 us (1790 TFLOP/s).  Eight epilogue warps: with four, GELU's
+// with GELU 152 us (1810 TFLOP/s).  Eight epilogue warps: with four, GELU's
 // arithmetic took longer than the products it runs under (234 us).
 template <int BN> constexpr int kPairStage = kATile + BN / 2 * kBK * 2;
 constexpr int kPieceBytes = 32 * 32 * 2;
@@ -1242,7 +1242,7 @@ __device__ __forceinline__ void copy_rows(const Copy& c, int cta)
 }
 
 // Bound by HBM and, with an activation, nearly by its arithmetic: dz and its
-// sums of 8192 x 8192 bf16 with GELU 78 us (403 MB, 5150 GB/s), the sums alone
+// sums of 8192 x 8192 bf16 with GELU 64 us (403 MB, 6300 GB/s), the sums alone
 // without activation 24 us (134 MB).
 template <int ACT, int BF16>
 __global__ void __launch_bounds__(256) zero_linear_prep_kernel(const __grid_constant__ PrepArgs a)
