@@ -58,7 +58,7 @@ typedef struct {
     int32_t state_bits; /* 32, 8, or 0: gradients only (zero_grad_norm) */
     int32_t vector_tensors; /* tensors whose streams share one 16-byte phase: whole-vector accesses */
     int32_t pipeline;       /* 1: all of them do (8-bit codes on 16 bytes), a large step may copy in bulk */
-    int32_t reserved;
+    int32_t norm_vecs;      /* size of the norm's units of work */
     int64_t elements;   /* of all tensors */
     int64_t chunks;     /* units of work of a step */
     int64_t norm_chunks;

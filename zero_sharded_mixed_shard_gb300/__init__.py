@@ -100,7 +100,7 @@ class zero_adamw_plan_t(ctypes.Structure):
     _fields_ = [("n_tensors", ctypes.c_int32), ("P", ctypes.c_int32),
                 ("grad_type", ctypes.c_int32), ("param_type", ctypes.c_int32),
                 ("state_bits", ctypes.c_int32), ("vector_tensors", ctypes.c_int32),
-                ("pipeline", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("pipeline", ctypes.c_int32), ("norm_vecs", ctypes.c_int32),
                 ("elements", ctypes.c_int64), ("chunks", ctypes.c_int64),
                 ("norm_chunks", ctypes.c_int64), ("table_bytes", ctypes.c_int64)]
 

@@ -40,8 +40,9 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBlock = 256;                    // elements of a warp's unit, and of an 8-bit scale
 constexpr int kChunk = kWarps * kBlock;        // elements of a CTA's unit of the step
-constexpr int kNormVecs = 4;                   // 8-element vectors a thread of the norm has in flight
-constexpr int kNormChunk = kThreads * 8 * kNormVecs;
+constexpr int kNormVecs = 4;                   // 8-element vectors of a thread in a chunk of the norm; 1 in a short list
+constexpr int kNormStep = kThreads * 8;        // elements of a chunk for each of them
+constexpr int kShortNorm = 400;                // chunks (of 4) up to which a list counts as short
 constexpr int kMaxPartials = 2048;             // CTAs of the norm at most
 constexpr float kMax8 = 448.0f;                // largest E4M3 value
 constexpr float kInvMax8 = 1.0f / 448.0f;
@@ -810,11 +811,16 @@ __global__ void __launch_bounds__(kPipeThreads, 1) zero_adamw_pipeline_kernel(co
 // number of elements.  The CTAs' sums are joined in fp64 by the last CTA to
 // finish, in CTA order, so the bits do not depend on which one that is.
 // Bound by HBM reads: eight fp16 ranks of 3.0e8 parameters 675 us (7160 GB/s,
-// 1.06 of the measured copy bandwidth); 50 thousand parameters 6.6 us.
-template <int GT>
+// 1.06 of the measured copy bandwidth); 50 thousand parameters 5.8 us.
+// Short lists take small chunks, so that every SM has some, and read four
+// ranks at once instead of four vectors of one (eight bf16 ranks of 2.4e5
+// parameters 11.4 against 8.1 us; long lists lose, 4.0e8 parameters of one rank
+// 124 against 233 us).
+template <int GT, int VECS>
 __global__ void __launch_bounds__(kThreads, 4) zero_grad_norm_kernel(const __grid_constant__ Args a)
 {
     using G = typename Elem<GT>::type;
+    constexpr int kNormChunk = VECS * kNormStep, kRanks = VECS == 1 ? 4 : 1;
     const int tid = threadIdx.x;
     let_successor_start();
     wait_for_predecessor();
@@ -839,24 +845,26 @@ __global__ void __launch_bounds__(kThreads, 4) zero_grad_norm_kernel(const __gri
             gp = static_cast<const G*>(x->g);
         }
         const long long c0 = (c - lo) * kNormChunk - max(phase, 0);
-        float acc[kNormVecs][8];
+        float acc[VECS][8];
 #pragma unroll
-        for (int k = 0; k < kNormVecs; ++k)
+        for (int k = 0; k < VECS; ++k)
 #pragma unroll
             for (int j = 0; j < 8; ++j) acc[k][j] = 0.0f;
         if (phase >= 0 && c0 >= 0 && c0 + kNormChunk <= n) {
+#pragma unroll kRanks
             for (int r = 0; r < a.P; ++r) {
-                Raw8<GT> raw[kNormVecs];
+                Raw8<GT> raw[VECS];
 #pragma unroll
-                for (int k = 0; k < kNormVecs; ++k) raw[k] = load8<GT>(gp + r * stride + c0 + (k * kThreads + tid) * 8);
+                for (int k = 0; k < VECS; ++k) raw[k] = load8<GT>(gp + r * stride + c0 + (k * kThreads + tid) * 8);
 #pragma unroll
-                for (int k = 0; k < kNormVecs; ++k) add8<GT>(acc[k], raw[k]);
+                for (int k = 0; k < VECS; ++k) add8<GT>(acc[k], raw[k]);
             }
         } else { // a tensor's end, or rows off 16 bytes: one element an access, lanes side by side, the loads of a rank together
+#pragma unroll kRanks
             for (int r = 0; r < a.P; ++r) {
                 const G* row = gp + r * stride + c0 + tid;
 #pragma unroll
-                for (int k = 0; k < kNormVecs; ++k) {
+                for (int k = 0; k < VECS; ++k) {
                     float e[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
@@ -869,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 4) zero_grad_norm_kernel(const __gri
             }
         }
 #pragma unroll
-        for (int k = 0; k < kNormVecs; ++k) {
+        for (int k = 0; k < VECS; ++k) {
             float s = 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -980,12 +988,17 @@ StepKernels pick_step(int grad, int param, int bits, int P)
     }
 }
 
-Kernel pick_norm(int grad)
+template <int GT> Kernel pick_vecs(int vecs)
+{
+    return vecs == 1 ? zero_grad_norm_kernel<GT, 1> : zero_grad_norm_kernel<GT, kNormVecs>;
+}
+
+Kernel pick_norm(int grad, int vecs)
 {
     switch (grad) {
-    case ZERO_TYPE_FP16: return zero_grad_norm_kernel<ZERO_TYPE_FP16>;
-    case ZERO_TYPE_BF16: return zero_grad_norm_kernel<ZERO_TYPE_BF16>;
-    default: return zero_grad_norm_kernel<ZERO_TYPE_FP32>;
+    case ZERO_TYPE_FP16: return pick_vecs<ZERO_TYPE_FP16>(vecs);
+    case ZERO_TYPE_BF16: return pick_vecs<ZERO_TYPE_BF16>(vecs);
+    default: return pick_vecs<ZERO_TYPE_FP32>(vecs);
     }
 }
 
@@ -1017,7 +1030,7 @@ static_assert(sizeof(Header) % 16 == 0 && sizeof(Tensor) % 8 == 0, "table layout
 bool good_plan(const zero_adamw_plan_t* p, const void* table)
 {
     return p && table && p->n_tensors >= 1 && p->P >= 1 && p->P <= ZERO_MAX_RANKS && p->grad_type >= 0 &&
-           p->grad_type <= 2 && p->elements >= 0 && p->chunks >= 0 && p->norm_chunks >= 0 &&
+           p->grad_type <= 2 && p->elements >= 0 && p->chunks >= 0 && p->norm_chunks >= 0 && (p->norm_vecs == 1 || p->norm_vecs == kNormVecs) &&
            p->table_bytes == table_size(p->n_tensors);
 }
 
@@ -1078,6 +1091,13 @@ int plan_tensors(const zero_adamw_tensor_t* tensors, int32_t n_tensors, int32_t 
 {
     const int gs = grad_type == ZERO_TYPE_FP32 ? 4 : 2, ss = bits == 32 ? 4 : 1;
     std::vector<Span> written, read;
+    int64_t most = 0; // chunks of the norm of the larger size
+    for (int32_t j = 0; j < n_tensors && most <= kShortNorm; ++j) {
+        if (tensors[j].n < 0 || tensors[j].n > (INT64_MAX >> 5)) return ZERO_EINVAL;
+        most += (tensors[j].n + kNormVecs * kNormStep - 1) / (kNormVecs * kNormStep);
+    }
+    plan->norm_vecs = most <= kShortNorm ? 1 : kNormVecs;
+    const int64_t norm_chunk = static_cast<int64_t>(plan->norm_vecs) * kNormStep;
     long long* first = nullptr;
     Tensor* rec = nullptr;
     if (table) {
@@ -1134,7 +1154,7 @@ int plan_tensors(const zero_adamw_tensor_t* tensors, int32_t n_tensors, int32_t 
                 chunks = (t.n + std::max(x.phase, 0) + kChunk - 1) / kChunk;
                 plan->vector_tensors += x.phase >= 0;
             }
-            norm_chunks = (t.n + std::max(x.gphase, 0) + kNormChunk - 1) / kNormChunk;
+            norm_chunks = (t.n + std::max(x.gphase, 0) + norm_chunk - 1) / norm_chunk;
         }
         if (table) {
             first[j] = plan->chunks;
@@ -1205,7 +1225,7 @@ extern "C" int zero_grad_norm(const zero_adamw_plan_t* plan, void* table, float 
     a.grad_scale = grad_scale;
     a.max_norm = max_norm;
     a.out = stats;
-    return launch(pick_norm(plan->grad_type), a, kMaxPartials, kThreads, 0, cuda_stream);
+    return launch(pick_norm(plan->grad_type, plan->norm_vecs), a, kMaxPartials, kThreads, 0, cuda_stream);
 }
 
 extern "C" int zero_adamw_step(const zero_adamw_plan_t* plan, void* table, const float* stats, int64_t t, float lr,
