@@ -647,10 +647,11 @@ __device__ __forceinline__ void tile_at(const Problem& g, int t, int* mt, int* n
     *mt = group * kGroup + in - *nt * rows;
 }
 
-// The bias gradient's last sum, by warp 3 of every CTA.
+// The bias gradient's last sum, by warp 3 of every CTA.  A column and a step
+// together may pass 2^31.
 __device__ __forceinline__ void bias_sum(const GemmArgs& args, int lane)
 {
-    for (int c = blockIdx.x * 32 + lane; c < args.n_db; c += gridDim.x * 32) {
+    for (long long c = blockIdx.x * 32ll + lane; c < args.n_db; c += gridDim.x * 32ll) {
         float s = 0.0f;
 #pragma unroll 16
         for (int k = 0; k < args.chunks; ++k) s += args.sums[static_cast<long long>(k) * args.n_db + c];
