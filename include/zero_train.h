@@ -204,6 +204,19 @@ int zero_linear_plan(int64_t T, int64_t K, int64_t N, int32_t products, int32_t*
  * run, reading it synchronises). */
 int zero_train_timeouts(int64_t* count, int32_t reset);
 
+/* Diagnostic of those waits, like zero_selftest_wait_timeout: enqueues the step
+ * of zero_adamw_step (without stats) through the pipeline of bulk copies, whose
+ * first CTA never hands a stage of its ring back, while half of the lanes of its
+ * copying warp are told that it did.  That warp's wait runs out after 2 seconds,
+ * the CTA adds 1 to the count of zero_train_timeouts and returns; every other
+ * CTA finishes and the context stays usable.  The first CTA's part of the
+ * tensors is left partly updated.
+ * Errors: as zero_adamw_step, and ZERO_EINVAL unless the plan has fp16 gradients
+ * of one rank, fp16 parameters, fp32 moments, and takes the pipeline (4096
+ * chunks). */
+int zero_selftest_adamw_wait(const zero_adamw_plan_t* plan, void* table, int64_t t, float lr,
+                             float beta1, float beta2, float eps, void* cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif

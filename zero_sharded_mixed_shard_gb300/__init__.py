@@ -52,7 +52,7 @@ EXPORTED = ("zero_init_layout", "zero_free_layout", "zero_shard_range", "zero_me
             "zero_last_cuda_error", "zero_last_cuda_error_string",
             "zero_adamw_plan", "zero_grad_norm", "zero_adamw_step",
             "zero_linear_plan", "zero_linear_workspace", "zero_linear_forward", "zero_linear_backward",
-            "zero_train_timeouts")
+            "zero_train_timeouts", "zero_selftest_adamw_wait")
 
 
 class ZeroError(RuntimeError):
@@ -198,6 +198,8 @@ def lib() -> ctypes.CDLL:
     L.zero_linear_backward.restype = ctypes.c_int
     L.zero_train_timeouts.argtypes = [ctypes.POINTER(ctypes.c_int64), i32]
     L.zero_train_timeouts.restype = ctypes.c_int
+    L.zero_selftest_adamw_wait.argtypes = [plan_p, vp, i64, f32, f32, f32, f32, vp]
+    L.zero_selftest_adamw_wait.restype = ctypes.c_int
     L.zero_strerror.argtypes = [ctypes.c_int]
     L.zero_strerror.restype = ctypes.c_char_p
     L.zero_last_cuda_error.argtypes = []
@@ -603,3 +605,12 @@ def zero_train_timeouts(reset: bool = False) -> int:
     if rc:
         raise ZeroError(rc, "zero_train_timeouts")
     return n.value
+
+
+def zero_selftest_adamw_wait(plan: AdamWPlan, t: int, lr: float, beta1: float, beta2: float, eps: float,
+                             stream=None) -> None:
+    """Enqueue the diagnostic of the pipeline's bounded waits (see include/zero_train.h)."""
+    rc = lib().zero_selftest_adamw_wait(ctypes.byref(plan.info), _addr(plan.table), t, lr, beta1, beta2, eps,
+                                        _stream(stream))
+    if rc:
+        raise ZeroError(rc, "zero_selftest_adamw_wait")

@@ -635,7 +635,10 @@ struct Chunk {
     unsigned int key;
 };
 
-template <int GT, int PT, int BITS, bool ONE>
+// STARVED: the instance of zero_selftest_adamw_wait alone.  Its first CTA never
+// hands a stage back, and half of the copying warp's lanes ask for a phase that
+// is over, so that the lanes of one warp get different answers.
+template <int GT, int PT, int BITS, bool ONE, bool STARVED = false>
 __global__ void __launch_bounds__(kPipeThreads, 1) zero_adamw_pipeline_kernel(const __grid_constant__ Args a)
 {
     using G = typename Elem<GT>::type;
@@ -685,7 +688,10 @@ __global__ void __launch_bounds__(kPipeThreads, 1) zero_adamw_pipeline_kernel(co
                 k.key = BITS == 8 ? mix32(mix32(a.seed) + 0x9e3779b9u * static_cast<unsigned int>(ti + 1)) : 0u;
             }
             const int s = it % a.stages;
-            ok = wait(&empty[s], ((it / a.stages) & 1) ^ 1, abort);
+            uint32_t parity = ((it / a.stages) & 1) ^ 1;
+            if (STARVED && blockIdx.x == 0 && it >= a.stages && lane >= 16) parity ^= 1;
+            // one answer for the warp: below it works together, and so it must give up together
+            ok = __all_sync(0xffffffffu, wait(&empty[s], parity, abort));
             if (!ok) break;
             k.b0 = (c - lo) * kChunk - max(x.phase, 0);
             k.from = k.b0 < 0 ? 1 : 0;
@@ -722,6 +728,11 @@ __global__ void __launch_bounds__(kPipeThreads, 1) zero_adamw_pipeline_kernel(co
         return;
     }
     const int group = (warp - 1) / kWarps, mine = (warp - 1) % kWarps;
+    auto hand_back = [&](int s) {
+        __syncwarp();
+        if (lane == 0 && !(STARVED && blockIdx.x == 0))
+            asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&empty[s])) : "memory");
+    };
     int it = 0;
     for (long long c = blockIdx.x; c < a.chunks; c += gridDim.x, ++it) {
         if (it % kGroups != group) continue;
@@ -731,8 +742,7 @@ __global__ void __launch_bounds__(kPipeThreads, 1) zero_adamw_pipeline_kernel(co
         const Chunk ch = meta[s];
         const long long b0 = ch.b0 + mine * kBlock;
         if (mine < ch.from || mine >= ch.to) {
-            __syncwarp();
-            if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&empty[s])) : "memory");
+            hand_back(s);
             if (b0 < ch.n) step_by_elements<GT, PT, BITS>(a, ch.x, ch.lr, ch.decay, factor, ch.key, b0, 1.0f);
             continue;
         }
@@ -779,8 +789,7 @@ __global__ void __launch_bounds__(kPipeThreads, 1) zero_adamw_pipeline_kernel(co
 #pragma unroll
                 for (int j = 0; j < 4; ++j) g[4 * h + j] = ONE ? f[j] : __fadd_rn(g[4 * h + j], f[j]);
             }
-        __syncwarp();
-        if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&empty[s])) : "memory");
+        hand_back(s);
         const long long i0 = b0 + lane * 4;
         update<BITS, ONE>(a, k, w, m, v, g, mc, vc,
                           [&](int j) { return static_cast<unsigned int>(i0 >> 1) + (j >> 1) + (j >= 4 ? 62u : 0u); },
@@ -1228,8 +1237,11 @@ extern "C" int zero_grad_norm(const zero_adamw_plan_t* plan, void* table, float 
     return launch(pick_norm(plan->grad_type, plan->norm_vecs), a, kMaxPartials, kThreads, 0, cuda_stream);
 }
 
-extern "C" int zero_adamw_step(const zero_adamw_plan_t* plan, void* table, const float* stats, int64_t t, float lr,
-                               float beta1, float beta2, float eps, uint32_t seed, void* cuda_stream)
+namespace {
+
+// The arguments of a step, checked.
+int step_args(const zero_adamw_plan_t* plan, void* table, const float* stats, int64_t t, float lr, float beta1, float beta2,
+              float eps, uint32_t seed, Args* out)
 {
     if (!good_plan(plan, table) || (plan->state_bits != 8 && plan->state_bits != 32) || t < 1 ||
         !std::isfinite(lr) || !(beta1 >= 0.0f && beta1 < 1.0f) || !(beta2 >= 0.0f && beta2 < 1.0f) ||
@@ -1237,8 +1249,8 @@ extern "C" int zero_adamw_step(const zero_adamw_plan_t* plan, void* table, const
         (plan->param_type != ZERO_TYPE_FP16 && plan->param_type != ZERO_TYPE_BF16))
         return ZERO_EINVAL;
     if (addr(table) % 16 || addr(stats) % 4) return ZERO_EALIGN;
-    if (plan->chunks == 0) return ZERO_OK; // no elements
-    Args a = base_args(plan, table, false);
+    Args& a = *out;
+    a = base_args(plan, table, false);
     a.stats = stats;
     a.lr = lr;
     a.b1 = beta1;
@@ -1249,13 +1261,45 @@ extern "C" int zero_adamw_step(const zero_adamw_plan_t* plan, void* table, const
     a.c2 = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(static_cast<double>(beta2), static_cast<double>(t))));
     a.eps = eps;
     a.seed = seed;
-    const StepKernels fn = pick_step(plan->grad_type, plan->param_type, plan->state_bits, plan->P);
     const int64_t stage = kChunk * (4 + plan->state_bits / 4 + (plan->grad_type == ZERO_TYPE_FP32 ? 4 : 2) * int64_t{plan->P});
     a.stages = pipeline_stages(stage);
     a.stage_bytes = static_cast<int>(std::min<int64_t>(stage, kPipeSmem));
-    if (plan->pipeline && a.stages > 0 && takes_pipeline(plan->chunks, plan->state_bits, plan->P))
-        return launch(fn.pipeline, a, INT64_MAX, kPipeThreads, kPipeSmem, cuda_stream);
+    return ZERO_OK;
+}
+
+bool step_takes_pipeline(const zero_adamw_plan_t* plan, const Args& a)
+{
+    return plan->pipeline && a.stages > 0 && takes_pipeline(plan->chunks, plan->state_bits, plan->P);
+}
+
+} // namespace
+
+extern "C" int zero_adamw_step(const zero_adamw_plan_t* plan, void* table, const float* stats, int64_t t, float lr,
+                               float beta1, float beta2, float eps, uint32_t seed, void* cuda_stream)
+{
+    Args a{};
+    const int rc = step_args(plan, table, stats, t, lr, beta1, beta2, eps, seed, &a);
+    if (rc) return rc;
+    if (plan->chunks == 0) return ZERO_OK; // no elements
+    const StepKernels fn = pick_step(plan->grad_type, plan->param_type, plan->state_bits, plan->P);
+    if (step_takes_pipeline(plan, a)) return launch(fn.pipeline, a, INT64_MAX, kPipeThreads, kPipeSmem, cuda_stream);
     return launch(fn.vector, a, INT64_MAX, kThreads, 0, cuda_stream);
+}
+
+extern "C" int zero_selftest_adamw_wait(const zero_adamw_plan_t* plan, void* table, int64_t t, float lr, float beta1,
+                                        float beta2, float eps, void* cuda_stream)
+{
+    Args a{};
+    int rc = step_args(plan, table, nullptr, t, lr, beta1, beta2, eps, 0, &a);
+    if (rc) return rc;
+    if (plan->grad_type != ZERO_TYPE_FP16 || plan->param_type != ZERO_TYPE_FP16 || plan->state_bits != 32 || plan->P != 1 ||
+        !step_takes_pipeline(plan, a))
+        return ZERO_EINVAL;
+    const Kernel fn = zero_adamw_pipeline_kernel<ZERO_TYPE_FP16, ZERO_TYPE_FP16, 32, true, true>;
+    int ctas = 0;
+    if ((rc = resident_ctas(fn, kPipeThreads, kPipeSmem, &ctas))) return rc;
+    if (plan->chunks <= int64_t{ctas} * a.stages) return ZERO_EINVAL; // the first CTA must come back to a stage
+    return launch(fn, a, INT64_MAX, kPipeThreads, kPipeSmem, cuda_stream);
 }
 
 // Bounded waits of the pipeline that gave up (zero_train_timeouts adds them).
