@@ -1,0 +1,130 @@
+"""AdamW and the gradient norm at the ends of their ranges: moments whose squares leave fp32's normal range, gradients whose
+squares do, the random bits of every tensor of a list.
+
+AdamW's references are the header's formulas in fp32 with every operation rounded by itself (numpy, which keeps
+subnormals); codes and scales have to be equal to theirs bit for bit.  The weight's line has fused products and a
+quotient within 2 ulp: it is held to 8 roundings of the update and 4 of the weight (u = 2^-24)."""
+import math
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+B1, B2 = 0.9, 0.999
+F = np.float32
+
+
+@pytest.fixture(scope="module")
+def z(zlib):
+    if not torch.cuda.is_available():
+        pytest.fail("the GPU tests need a CUDA device")
+    yield zlib
+    assert zlib.zero_train_timeouts() == 0
+
+
+def mix(h):
+    """MurmurHash3's 32-bit finaliser (A. Appleby)."""
+    h = np.asarray(h, np.uint64)
+    h = ((h ^ (h >> np.uint64(16))) * np.uint64(0x85EBCA6B)) & np.uint64(0xFFFFFFFF)
+    h = ((h ^ (h >> np.uint64(13))) * np.uint64(0xC2B2AE35)) & np.uint64(0xFFFFFFFF)
+    return h ^ (h >> np.uint64(16))
+
+
+def widen(codes, scale, n):
+    """fp32 values of E4M3 codes and their blocks' scales."""
+    x = torch.from_numpy(codes.copy()).view(torch.float8_e4m3fn).float().numpy()
+    return x * np.repeat(scale, 256)[:n]
+
+
+class List8:
+    """Tensors with 8-bit moments on the GPU, and the step's formulas on the host."""
+
+    def __init__(self, z, sizes, grads, m=None, v=None, ms=None, vs=None, shift=0):
+        self.z, self.sizes = z, sizes
+        self.g = [np.ascontiguousarray(g, F) for g in grads]
+        rng = np.random.default_rng(sum(sizes))
+        self.w = [rng.standard_normal(n).astype(F) for n in sizes]
+        nb = [-(-n // 256) for n in sizes]
+        zeros = lambda k, dt: [np.zeros(k[j], dt) for j in range(len(k))]  # noqa: E731
+        self.m, self.v = m or zeros(sizes, np.uint8), v or zeros(sizes, np.uint8)
+        self.ms, self.vs = ms or zeros(nb, F), vs or zeros(nb, F)
+
+        def put(a):  # `shift` elements into a buffer of its own
+            t = torch.empty(a.size + shift + 16, dtype=torch.from_numpy(a).dtype, device="cuda")[shift:shift + a.size]
+            return t.copy_(torch.from_numpy(a))
+
+        self.dev = [{k: put(a[j]) for k, a in (("grad", self.g), ("master", self.w), ("m", self.m), ("v", self.v), ("m_scale", self.ms),
+                                               ("v_scale", self.vs))} for j in range(len(sizes))]
+        rows = []
+        for d, n in zip(self.dev, sizes):
+            d["param"] = torch.empty(n + shift, dtype=torch.float16, device="cuda")[shift:]
+            rows.append(dict(d, n=n))
+        self.plan = z.zero_adamw_plan(rows, 1, z.TYPE_FP32, z.TYPE_FP16, 8)
+
+    def formulas(self, j, t, lr, eps, seed):
+        """(weight, bound of its error, m codes, v codes, m scales, v scales) of tensor j after the step."""
+        n, nb = self.sizes[j], -(-self.sizes[j] // 256)
+        b1, b2 = F(B1), F(B2)
+        g, w = self.g[j], self.w[j]
+        with np.errstate(all="ignore"):
+            m = b1 * widen(self.m[j], self.ms[j], n) + (F(1) - b1) * g
+            r = widen(self.v[j], self.vs[j], n)
+            v = b2 * (r * r) + (F(1) - b2) * (g * g)
+            root = np.sqrt(v)
+            r1 = F(1 / (1 - float(b1) ** t))
+            c2 = F(1 / math.sqrt(1 - float(b2) ** t))
+            up = m.astype(np.float64) * float(F(lr) * r1) / (root.astype(np.float64) * float(c2) + float(F(eps)))
+            want = w.astype(np.float64) - up
+            pad = lambda a: np.pad(a, (0, nb * 256 - n)).reshape(nb, 256)  # noqa: E731
+            m, root = pad(m), pad(root)
+            hm, hr = np.abs(m).max(1, keepdims=True), root.max(1, keepdims=True)
+            tiny = F(2.0 ** -96)
+            im, ir = (np.where(h < tiny, F(0), F(448) / h) for h in (hm, hr))
+            sm, sr = (np.where(h < tiny, F(0), np.where(np.isfinite(h), h * F(1 / 448), F(np.nan))).reshape(-1) for h in (hm, hr))
+            mc = torch.from_numpy((m * im).reshape(-1)[:n]).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+            h = mix(np.arange(nb * 128, dtype=np.uint64) + mix((int(mix(seed)) + 0x9E3779B9 * (j + 1)) & 0xFFFFFFFF) & np.uint64(0xFFFFFFFF))
+            rnd = np.stack((h & np.uint64(0xFFFF), h >> np.uint64(16)), 1).reshape(-1).astype(np.uint32)
+            y = (root * ir).reshape(-1)
+            cut = ((y * F(2.0 ** -120)).view(np.uint32) + (rnd << np.uint32(4))) >> np.uint32(20)
+            vc = np.where(y > 0, np.clip(cut, 1, 0x7E), 0).astype(np.uint8)[:n]
+        return want, 8 * U * np.abs(up) + 4 * U * np.abs(w), mc, vc, sm.astype(F), sr.astype(F)
+
+    def step_and_check(self, t, lr, eps, seed):
+        self.z.zero_adamw_step(self.plan, None, t, lr, B1, B2, eps, seed)
+        for j, n in enumerate(self.sizes):
+            if n == 0:
+                continue
+            want, bound, mc, vc, sm, sr = self.formulas(j, t, lr, eps, seed)
+            got = {k: x.cpu().numpy() for k, x in self.dev[j].items()}
+            for k, ref in (("m_scale", sm), ("v_scale", sr)):
+                assert np.array_equal(got[k], ref, equal_nan=True), (j, k, got[k], ref)
+            for k, ref, s in (("m", mc, sm), ("v", vc, sr)):       # a block whose scale is NaN may hold any codes
+                ok = np.repeat(~np.isnan(s), 256)[:n]
+                assert np.array_equal(got[k][ok], ref[ok]), (j, k, int((got[k] != ref)[ok].sum()))
+            err = np.abs(got["master"].astype(np.float64) - want)
+            assert bool((err <= bound).all()), (j, float((err - bound).max()))
+            assert np.array_equal(got["param"].view(np.uint16), got["master"].astype(np.float16).view(np.uint16))
+
+
+def magnitudes(sizes, lo, hi, seed):
+    """Gradients of either sign whose blocks of 256 have magnitudes spread over 10^lo .. 10^hi."""
+    rng = np.random.default_rng(seed)
+    out = []
+    for n in sizes:
+        e = np.repeat(rng.uniform(lo, hi, -(-n // 256)), 256)[:n]
+        out.append((10.0 ** e * rng.uniform(0.5, 1.0, n) * rng.choice([-1.0, 1.0], n)).astype(F))
+    return out
+
+
+LISTS = [([10317, 0, 256, 700], 0), ([10317, 0, 256, 700], 1), ([8400000, 301], 0)]  # vectors, elements, the pipeline
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-8])
+@pytest.mark.parametrize("sizes,shift", LISTS)
+def test_root_of_a_variance_below_the_normal_range(z, sizes, shift, eps):
+    """First steps from a zero state with gradients of 1e-20.3 to 1e-15: their squares' thousandth is subnormal below
+    3.4e-18, and with eps = 0 the update divides by its root alone."""
+    List8(z, sizes, magnitudes(sizes, -20.3, -15, 3), shift=shift).step_and_check(1, 1e-2, eps, 5)

@@ -231,14 +231,23 @@ __device__ __forceinline__ float fast_sqrt(float x)
 // The root correctly rounded from the approximate one, s = x y: s plus half of
 // y times the exact remainder x - s^2 (P. Markstein, as above).  A stored code
 // follows from the root's bits, so that a step on equal states gives equal
-// codes wherever the same fp32 operations are done.  x >= 0; below 2^-126 the
-// result is only between 0 and 2^-63.
+// codes wherever the same fp32 operations are done.  x is 0 or at least 2^-101,
+// where the remainder, a multiple of x 2^-48 or more, is still exact.
 __device__ __forceinline__ float exact_sqrt(float x)
 {
     float y;
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaxf(x, 1.17549435e-38f)));
     const float s = __fmul_rn(x, y);
     return __fmaf_rn(__fmaf_rn(-s, s, x), __fmul_rn(0.5f, y), s);
+}
+
+// The same for any x >= 0: what is below 2^-96 is scaled by 2^64, its root by
+// 2^-32 (both exact; the smallest root is above 2^-75).
+__device__ __forceinline__ float exact_sqrt_any(float x)
+{
+    const bool low = x < kTiny;
+    const float s = exact_sqrt(low ? __fmul_rn(x, 1.8446744073709552e19f) : x);
+    return low ? __fmul_rn(s, 2.3283064365386963e-10f) : s;
 }
 
 __device__ __forceinline__ float fast_rcp(float x)
@@ -301,20 +310,34 @@ __device__ __forceinline__ void update(const Args& a, const Block& k, float (&w)
         }
     }
     float high_m = 0.0f, high_r = 0.0f; // largest magnitudes, or NaN
+    float low_v = kTiny;
     const float minus_rate = -__fmul_rn(k.lr, a.r1);
+    auto weight = [&](int j, float root) {
+        const float inv = fast_rcp(__fmaf_rn(root, a.c2, a.eps));
+        w[j] = __fmaf_rn(-k.decay, w[j], w[j]);
+        w[j] = __fmaf_rn(__fmul_rn(m[j], minus_rate), inv, w[j]);
+    };
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const float gg = __fmul_rn(ONE ? g[j] : mean_of(g[j], a), k.factor);
         m[j] = __fadd_rn(__fmul_rn(m[j], a.b1), __fmul_rn(gg, a.omb1));
         v[j] = __fadd_rn(__fmul_rn(v[j], a.b2), __fmul_rn(__fmul_rn(gg, gg), a.omb2));
-        const float root = BITS == 8 ? exact_sqrt(v[j]) : fast_sqrt(v[j]);
-        const float inv = fast_rcp(__fmaf_rn(root, a.c2, a.eps));
-        w[j] = __fmaf_rn(-k.decay, w[j], w[j]);
-        w[j] = __fmaf_rn(__fmul_rn(m[j], minus_rate), inv, w[j]);
-        if constexpr (BITS == 8) {
-            v[j] = root;
+        if constexpr (BITS == 8) low_v = fminf(low_v, v[j]);
+        else weight(j, fast_sqrt(v[j]));
+    }
+    if constexpr (BITS == 8) { // the rare values (zeros among them) apart: one comparison for a lane's eight
+        if (low_v < kTiny) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = exact_sqrt_any(v[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = exact_sqrt(v[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            weight(j, v[j]);
             high_m = max_or_nan(high_m, fabsf(m[j]));
-            high_r = max_or_nan(high_r, root);
+            high_r = max_or_nan(high_r, v[j]);
         }
     }
     if constexpr (BITS == 8) {
