@@ -128,3 +128,27 @@ def test_root_of_a_variance_below_the_normal_range(z, sizes, shift, eps):
     """First steps from a zero state with gradients of 1e-20.3 to 1e-15: their squares' thousandth is subnormal below
     3.4e-18, and with eps = 0 the update divides by its root alone."""
     List8(z, sizes, magnitudes(sizes, -20.3, -15, 3), shift=shift).step_and_check(1, 1e-2, eps, 5)
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("n", [700, 8400000])
+def test_infinite_variance_leaves_the_weight(z, bits, n):
+    """A finite gradient whose square is infinite, without stats: m / (inf + eps) is 0, so the weight stays; the block's
+    8-bit variance gets the scale NaN, its momentum keeps its scale."""
+    rng = np.random.default_rng(n)
+    g = (rng.standard_normal(n) * 1e-2).astype(F)
+    hit = [3, 300, n - 1]
+    g[hit] = [2.5e19, -3e20, 1e25]
+    if bits == 8:
+        c = List8(z, [n], [g])
+        c.step_and_check(1, 1e-2, 1e-8, 2)
+        d, w0 = c.dev[0], c.w[0]
+        assert bool(torch.isnan(d["v_scale"][[0, 1, (n - 1) // 256]]).all()) and bool(torch.isfinite(d["m_scale"]).all())
+    else:
+        w0 = rng.standard_normal(n).astype(F)
+        d = {k: torch.from_numpy(a).cuda() for k, a in (("grad", g), ("master", w0.copy()), ("m", np.zeros(n, F)), ("v", np.zeros(n, F)))}
+        d["param"] = torch.empty(n, dtype=torch.float16, device="cuda")
+        z.zero_adamw_step(z.zero_adamw_plan([dict(d, n=n)], 1, z.TYPE_FP32, z.TYPE_FP16, 32), None, 1, 1e-2, B1, B2, 1e-8, 2)
+        assert bool(torch.isinf(d["v"][hit]).all())
+    w = d["master"].cpu().numpy()
+    assert np.isfinite(w).all() and np.array_equal(w[hit], w0[hit])

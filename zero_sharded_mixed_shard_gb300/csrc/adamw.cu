@@ -232,7 +232,7 @@ __device__ __forceinline__ float fast_sqrt(float x)
 // y times the exact remainder x - s^2 (P. Markstein, as above).  A stored code
 // follows from the root's bits, so that a step on equal states gives equal
 // codes wherever the same fp32 operations are done.  x is 0 or at least 2^-101,
-// where the remainder, a multiple of x 2^-48 or more, is still exact.
+// where the remainder, a multiple of x 2^-48 or more, is still exact, and finite.
 __device__ __forceinline__ float exact_sqrt(float x)
 {
     float y;
@@ -242,11 +242,13 @@ __device__ __forceinline__ float exact_sqrt(float x)
 }
 
 // The same for any x >= 0: what is below 2^-96 is scaled by 2^64, its root by
-// 2^-32 (both exact; the smallest root is above 2^-75).
+// 2^-32 (both exact; the smallest root is above 2^-75), and infinity, whose
+// remainder is no number, is its own root.
 __device__ __forceinline__ float exact_sqrt_any(float x)
 {
     const bool low = x < kTiny;
     const float s = exact_sqrt(low ? __fmul_rn(x, 1.8446744073709552e19f) : x);
+    if (x == __int_as_float(0x7f800000)) return x;
     return low ? __fmul_rn(s, 2.3283064365386963e-10f) : s;
 }
 
@@ -310,7 +312,7 @@ __device__ __forceinline__ void update(const Args& a, const Block& k, float (&w)
         }
     }
     float high_m = 0.0f, high_r = 0.0f; // largest magnitudes, or NaN
-    float low_v = kTiny;
+    float low_v = kTiny, high_v = 0.0f;
     const float minus_rate = -__fmul_rn(k.lr, a.r1);
     auto weight = [&](int j, float root) {
         const float inv = fast_rcp(__fmaf_rn(root, a.c2, a.eps));
@@ -322,11 +324,15 @@ __device__ __forceinline__ void update(const Args& a, const Block& k, float (&w)
         const float gg = __fmul_rn(ONE ? g[j] : mean_of(g[j], a), k.factor);
         m[j] = __fadd_rn(__fmul_rn(m[j], a.b1), __fmul_rn(gg, a.omb1));
         v[j] = __fadd_rn(__fmul_rn(v[j], a.b2), __fmul_rn(__fmul_rn(gg, gg), a.omb2));
-        if constexpr (BITS == 8) low_v = fminf(low_v, v[j]);
-        else weight(j, fast_sqrt(v[j]));
+        if constexpr (BITS == 8) {
+            low_v = fminf(low_v, v[j]);
+            high_v = fmaxf(high_v, v[j]);
+        } else {
+            weight(j, fast_sqrt(v[j]));
+        }
     }
-    if constexpr (BITS == 8) { // the rare values (zeros among them) apart: one comparison for a lane's eight
-        if (low_v < kTiny) {
+    if constexpr (BITS == 8) { // the rare values (zeros among them) apart: one branch for a lane's eight
+        if (low_v < kTiny || high_v == __int_as_float(0x7f800000)) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = exact_sqrt_any(v[j]);
         } else {
