@@ -106,7 +106,9 @@ class List8:
                 assert np.array_equal(got[k][ok], ref[ok]), (j, k, int((got[k] != ref)[ok].sum()))
             err = np.abs(got["master"].astype(np.float64) - want)
             assert bool((err <= bound).all()), (j, float((err - bound).max()))
-            assert np.array_equal(got["param"].view(np.uint16), got["master"].astype(np.float16).view(np.uint16))
+            with np.errstate(over="ignore"):
+                half = got["master"].astype(np.float16)
+            assert np.array_equal(got["param"].view(np.uint16), half.view(np.uint16))
 
 
 def magnitudes(sizes, lo, hi, seed):
@@ -152,3 +154,15 @@ def test_infinite_variance_leaves_the_weight(z, bits, n):
         assert bool(torch.isinf(d["v"][hit]).all())
     w = d["master"].cpu().numpy()
     assert np.isfinite(w).all() and np.array_equal(w[hit], w0[hit])
+
+
+@pytest.mark.parametrize("sizes,shift", LISTS)
+def test_codes_of_a_momentum_at_the_far_end(z, sizes, shift):
+    """Blocks whose largest momentum lies between 2^120 and fp32's end: the nearest codes of m * (448 / a)."""
+    rng = np.random.default_rng(11)
+    m = [rng.integers(0, 0x7F, n).astype(np.uint8) | (rng.integers(0, 2, n).astype(np.uint8) << 7) for n in sizes]
+    ms = [(10.0 ** rng.uniform(33.5, 35.85, -(-n // 256))).astype(F) for n in sizes]  # times at most 448
+    c = List8(z, sizes, [np.zeros(n, F) for n in sizes], m=m, ms=ms, v=[np.full(n, 0x38, np.uint8) for n in sizes],
+              vs=[np.full(-(-n // 256), 1.0, F) for n in sizes], shift=shift)
+    assert max(float(np.abs(widen(a, s, n)).max()) for a, s, n in zip(m, ms, sizes) if n) > 2.0 ** 127
+    c.step_and_check(1000, 1e-30, 1e-8, 7)

@@ -267,11 +267,14 @@ __device__ __forceinline__ float max_or_nan(float x, float y)
 }
 
 // 448 / a correctly rounded: the reciprocal refined to the nearest one, then
-// the quotient.
+// the quotient.  Above 2^120 both sides are scaled by 2^-8 (exact): the
+// reciprocal of what is above 2^126 would be flushed to 0.
 __device__ __forceinline__ float scale_inverse(float a)
 {
+    const float f = a > 1.329227995784916e36f ? 0.00390625f : 1.0f;
+    a *= f;
     const float r = fast_rcp(a);
-    return divide(kMax8, a, __fmaf_rn(__fmaf_rn(-a, r, 1.0f), r, r));
+    return divide(kMax8 * f, a, __fmaf_rn(__fmaf_rn(-a, r, 1.0f), r, r));
 }
 
 // ---------------------------------------------------------------------------
