@@ -139,7 +139,7 @@ int zero_adamw_step(const zero_adamw_plan_t* plan, void* table, const float* sta
 /* ------------------------------------------------------------------------ */
 
 #define ZERO_ACT_NONE 0
-#define ZERO_ACT_RELU 1 /* NaN stays NaN; derivative 0 at 0 */
+#define ZERO_ACT_RELU 1 /* NaN stays NaN; the gradient passes where z > 0, and is 0 elsewhere whatever it holds */
 #define ZERO_ACT_GELU 2 /* tanh's form: z / (1 + exp(-2 sqrt(2/pi) (z + 0.044715 z^3))) */
 #define ZERO_ACT_SILU 3 /* z / (1 + exp(-z)) */
 

@@ -448,13 +448,20 @@ template <int ACT> __device__ __forceinline__ float activate(float z)
 // The activation's derivative at z: s + z s (1 - s) u'(z).
 template <int ACT> __device__ __forceinline__ float slope(float z)
 {
-    if constexpr (ACT == ZERO_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
-    else if constexpr (ACT == ZERO_ACT_NONE) return 1.0f;
+    if constexpr (ACT == ZERO_ACT_NONE) return 1.0f;
     else {
         const float p = logistic<ACT>(z), q = fmaf(-p, p, p);
         const float d = fmaf(q, ACT == ZERO_ACT_GELU ? z * fmaf(z * z, 3.0f * kGelu3, kGelu) : z, p);
         return q == 0.0f ? p : d; // far out, where z's powers may be infinite
     }
+}
+
+// dz from dy.  ReLU's is a choice, not a product: what dy holds where z is not
+// above 0, an infinity or NaN too, does not pass.
+template <int ACT> __device__ __forceinline__ float through(float dy, float z)
+{
+    if constexpr (ACT == ZERO_ACT_RELU) return z > 0.0f ? dy : 0.0f;
+    else return dy * slope<ACT>(z);
 }
 
 // N values at once: the choice of the activation stands outside the loop.
@@ -1287,8 +1294,8 @@ __global__ void __launch_bounds__(256) zero_linear_prep_kernel(const __grid_cons
                 float2 d = unpack16(g[j], BF16);
                 if (ACT != ZERO_ACT_NONE) {
                     const float2 p = unpack16(h[j], BF16);
-                    d.x *= slope<ACT>(p.x);
-                    d.y *= slope<ACT>(p.y);
+                    d.x = through<ACT>(d.x, p.x);
+                    d.y = through<ACT>(d.y, p.y);
                 }
                 sum[2 * j] += d.x;
                 sum[2 * j + 1] += d.y;
@@ -1305,7 +1312,7 @@ __global__ void __launch_bounds__(256) zero_linear_prep_kernel(const __grid_cons
                 d[j] = 0.0f;
                 if (col + j < a.N) {
                     d[j] = load16(dy, r * a.lddy + col + j, BF16);
-                    if (ACT != ZERO_ACT_NONE) d[j] *= slope<ACT>(load16(z, r * a.ldz + col + j, BF16));
+                    if (ACT != ZERO_ACT_NONE) d[j] = through<ACT>(d[j], load16(z, r * a.ldz + col + j, BF16));
                 }
                 sum[j] += d[j];
             }
