@@ -92,9 +92,10 @@ int zero_adamw_plan(const zero_adamw_tensor_t* tensors, int32_t n_tensors, int32
  *              norm is not finite
  *   stats[2] = 1 when the norm is finite, else 0.
  * grad_scale undoes a loss scale (1 / loss scale); max_norm applies to the
- * scaled norm.  Squares are summed in fp32 with compensation and joined in
- * fp64 in a fixed order: the same gradients give the same bits on one device
- * model.  A gradient whose square leaves fp32's range counts as not finite.
+ * scaled norm.  Squares are summed in fp32 with compensation, those that leave
+ * its range in fp64, and joined in fp64 in a fixed order: the same gradients
+ * give the same bits on one device model.  Means (fp32) of any size count; the
+ * norm is not finite when one of them or stats[0] itself is not.
  * Errors: ZERO_EINVAL (null pointer, grad_scale not finite and positive,
  * max_norm NaN), ZERO_EALIGN, ZERO_ECUDA. */
 int zero_grad_norm(const zero_adamw_plan_t* plan, void* table, float grad_scale, float max_norm,

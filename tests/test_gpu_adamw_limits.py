@@ -166,3 +166,53 @@ def test_codes_of_a_momentum_at_the_far_end(z, sizes, shift):
               vs=[np.full(-(-n // 256), 1.0, F) for n in sizes], shift=shift)
     assert max(float(np.abs(widen(a, s, n)).max()) for a, s, n in zip(m, ms, sizes) if n) > 2.0 ** 127
     c.step_and_check(1000, 1e-30, 1e-8, 7)
+
+
+NORMS = [(0, 3e4), (0, 6e-8), (1, 1e18), (1, 1.5e19), (1, 1e30), (1, 1e-25), (1, 1e-38), (2, 2e18), (2, 1e37), (2, 3e-24), (2, 1e-41)]
+
+
+@pytest.mark.parametrize("gt,size", NORMS)
+@pytest.mark.parametrize("sizes,P", [([5], 1), ([3000, 7], 3), ([400001, 0, 8192], 1), ([5000000], 2)])
+def test_norm_over_the_range_of_its_gradients(z, gt, size, sizes, P):
+    """Finite gradients whose squares, or sums of squares, leave fp32's range: the norm is theirs all the same, and the step
+    that reads the statistics is not skipped.  Off by (P + 1) u a mean (at least half of the smallest subnormal), twice
+    that for its square, the sums of eight and the joins a few u."""
+    dt = (torch.float16, torch.bfloat16, torch.float32)[gt]
+    gen = torch.Generator(device="cuda").manual_seed(P)
+    total = sum(sizes)
+    g = ((torch.rand((P, total + 3), generator=gen, device="cuda") + 0.5) * size).to(dt)
+    if size > 1:
+        g[:, ::7] = 1e-3                                       # small ones among them
+    else:
+        g[:, ::5] = 0
+    if total > 5:                                              # the last quarter's scale is its own
+        g[:, total - total // 4:] = g[:, total - total // 4:] * (2.0 ** -30 if size > 1 else 1.0)
+    rows, at = [], 0
+    for n in sizes:
+        rows.append(dict(grad=g[0, at:], rank_stride=total + 3, n=n))
+        at += n
+    stats = torch.zeros(3, device="cuda")
+    z.zero_grad_norm(z.zero_grad_plan(rows, P, gt), 1.0, 1.0, stats)
+    mean = g[:, :total].double().mean(0)
+    top = float(mean.abs().max())
+    norm = float((mean / top).square().sum().sqrt() * top)
+    s = stats.double().cpu()
+    if norm > torch.finfo(torch.float32).max:                  # the norm itself has no fp32 value
+        assert math.isinf(float(s[0])) and float(s[1]) == 0 and float(s[2]) == 0
+        return
+    assert float(s[2]) == 1.0
+    half = 2.0 ** -150 * math.sqrt(total) if P > 1 else 0.0
+    assert abs(float(s[0]) - norm) <= norm * (P + 16) * U + half + 2.0 ** -150, (float(s[0]), norm)
+    want = min(1.0, 1.0 / (norm + 1e-6))
+    assert abs(float(s[1]) - want) <= want * (P + 24) * U + 2.0 ** -149
+
+
+def test_norm_that_is_not_finite(z):
+    """The norm itself above fp32's range, an infinite and a NaN gradient: not finite, factor 0."""
+    for fill, bad in ((3e38, 3e38), (1.0, math.inf), (1e30, math.nan), (0.0, -math.inf)):
+        g = torch.full((20000,), fill, device="cuda")
+        g[12345] = bad
+        stats = torch.zeros(3, device="cuda")
+        z.zero_grad_norm(z.zero_grad_plan([dict(grad=g, n=20000)], 1, z.TYPE_FP32), 1.0, 1.0, stats)
+        s = stats.cpu()
+        assert not math.isfinite(float(s[0])) and float(s[1]) == 0 and float(s[2]) == 0

@@ -47,6 +47,8 @@ constexpr int kMaxPartials = 2048;             // CTAs of the norm at most
 constexpr float kMax8 = 448.0f;                // largest E4M3 value
 constexpr float kInvMax8 = 1.0f / 448.0f;
 constexpr float kTiny = 1.262177448353619e-29f; // 2^-96
+constexpr float kLowSquares = 8.271806125530277e-25f;  // 2^-80
+constexpr float kHighSquares = 1.2676506002282294e30f; // 2^100
 
 struct Tensor {
     const void* g;
@@ -263,6 +265,13 @@ __device__ __forceinline__ float max_or_nan(float x, float y)
 {
     float z;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+    return z;
+}
+
+__device__ __forceinline__ float min_or_nan(float x, float y)
+{
+    float z;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
     return z;
 }
 
@@ -849,7 +858,9 @@ __global__ void __launch_bounds__(kPipeThreads, 1) zero_adamw_pipeline_kernel(co
 
 // Each thread squares eight means at a time and adds their sum to a
 // compensated fp32 sum (Kahan): the rounding error does not grow with the
-// number of elements.  The CTAs' sums are joined in fp64 by the last CTA to
+// number of elements.  Eights whose sum is outside [2^-80, 2^100] (below, small
+// squares are lost; above, the sums of many may overflow) are squared again
+// after scaling and added in fp64.  The CTAs' sums are joined in fp64 by the last CTA to
 // finish, in CTA order, so the bits do not depend on which one that is.
 // Bound by HBM reads: eight fp16 ranks of 3.0e8 parameters 675 us (7160 GB/s,
 // 1.06 of the measured copy bandwidth); 50 thousand parameters 5.8 us.
@@ -870,6 +881,23 @@ __global__ void __launch_bounds__(kThreads, 4) zero_grad_norm_kernel(const __gri
         const float y = __fsub_rn(s, comp), t = __fadd_rn(sum, y);
         comp = __fsub_rn(__fsub_rn(t, sum), y);
         sum = t;
+    };
+    double wide = 0.0;
+    bool scaled = false; // fp64 operations are few a cycle: not even one more where none is needed
+    auto add_scaled = [&](const float (&g)[8], bool low) {
+        unsigned int any = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) any |= __float_as_uint(g[j]);
+        if ((any & 0x7fffffffu) == 0) return; // zeros
+        const float f = low ? 1.2676506002282294e30f : 8.470329472543003e-22f; // 2^100 (means below 2^-40), 2^-70
+        float s = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float x = __fmul_rn(g[j], f);
+            s = fmaf(x, x, s);
+        }
+        wide += static_cast<double>(s) * (low ? 6.223015277861142e-61 : 1.393796574908164e42); // 2^-200, 2^140
+        scaled = true;
     };
     long long lo = 0, hi = 0, n = 0, stride = 0;
     int phase = 0;
@@ -917,15 +945,27 @@ __global__ void __launch_bounds__(kThreads, 4) zero_grad_norm_kernel(const __gri
                 }
             }
         }
+        float s[VECS], low = kHighSquares, high = 0.0f;
 #pragma unroll
         for (int k = 0; k < VECS; ++k) {
-            float s = 0.0f;
+            s[k] = 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float g = mean_of(acc[k][j], a);
-                s = fmaf(g, g, s);
+                acc[k][j] = mean_of(acc[k][j], a);
+                s[k] = fmaf(acc[k][j], acc[k][j], s[k]);
             }
-            add(s);
+            low = min_or_nan(low, s[k]);
+            high = max_or_nan(high, s[k]);
+        }
+        if (__builtin_expect(low >= kLowSquares && high <= kHighSquares, 1)) {
+#pragma unroll
+            for (int k = 0; k < VECS; ++k) add(s[k]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < VECS; ++k) {
+                if (s[k] >= kLowSquares && s[k] <= kHighSquares) add(s[k]);
+                else add_scaled(acc[k], s[k] < kLowSquares);
+            }
         }
     }
 
@@ -940,9 +980,9 @@ __global__ void __launch_bounds__(kThreads, 4) zero_grad_norm_kernel(const __gri
             for (int k = 0; k < kWarps; ++k) d += part[k];
         return d;
     };
-    // an infinite or NaN sum has no compensation: it stands for itself
-    const double mine = block_sum(isfinite(sum) ? static_cast<double>(sum) - static_cast<double>(comp)
-                                                : static_cast<double>(sum));
+    double mine = static_cast<double>(sum) - static_cast<double>(comp);
+    if (scaled) mine += wide;
+    mine = block_sum(mine);
     if (tid == 0) {
         a.head->partial[blockIdx.x] = mine;
         __threadfence();
