@@ -129,8 +129,8 @@ int zero_grad_norm(const zero_adamw_plan_t* plan, void* table, float grad_scale,
  * The random bits are those of seed (vary it per step, for instance t), the
  * tensor's index and the element's index alone: a step can be repeated.
  * Errors: ZERO_EINVAL (null pointer, plan with state_bits 0, t < 1, a
- * hyper-parameter that is not finite, beta outside [0, 1), eps < 0),
- * ZERO_EALIGN, ZERO_ECUDA. */
+ * hyper-parameter that is not finite, beta outside [0, 1), eps neither 0 nor
+ * at least 2^-126), ZERO_EALIGN, ZERO_ECUDA. */
 int zero_adamw_step(const zero_adamw_plan_t* plan, void* table, const float* stats, int64_t t,
                     float lr, float beta1, float beta2, float eps, uint32_t seed,
                     void* cuda_stream);

@@ -1317,7 +1317,7 @@ int step_args(const zero_adamw_plan_t* plan, void* table, const float* stats, in
 {
     if (!good_plan(plan, table) || (plan->state_bits != 8 && plan->state_bits != 32) || t < 1 ||
         !std::isfinite(lr) || !(beta1 >= 0.0f && beta1 < 1.0f) || !(beta2 >= 0.0f && beta2 < 1.0f) ||
-        !std::isfinite(eps) || eps < 0.0f ||
+        !std::isfinite(eps) || eps < 0.0f || (eps > 0.0f && !std::isnormal(eps)) || // the kernels' reciprocal flushes
         (plan->param_type != ZERO_TYPE_FP16 && plan->param_type != ZERO_TYPE_BF16))
         return ZERO_EINVAL;
     if (addr(table) % 16 || addr(stats) % 4) return ZERO_EALIGN;
