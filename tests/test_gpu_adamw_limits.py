@@ -216,3 +216,25 @@ def test_norm_that_is_not_finite(z):
         z.zero_grad_norm(z.zero_grad_plan([dict(grad=g, n=20000)], 1, z.TYPE_FP32), 1.0, 1.0, stats)
         s = stats.cpu()
         assert not math.isfinite(float(s[0])) and float(s[1]) == 0 and float(s[2]) == 0
+
+
+@pytest.mark.parametrize("sizes,shift", [([513, 0, 1, 10317, 0, 256, 700], 0), ([513, 0, 1, 10317, 0, 256, 700], 1), ([0, 4300001, 257, 4200000], 0)])
+def test_random_bits_of_every_tensor_and_seed(z, sizes, shift):
+    """Codes of several steps over lists with empty tensors and ragged ends, bit for bit: the random bits are those of the
+    seed, the tensor's place in the list (empty ones count) and the element.  Tensors of equal states and gradients get
+    different codes, and so does another seed."""
+    rng = np.random.default_rng(1)
+    g = [(rng.standard_normal(n) * 1e-2).astype(F) for n in sizes]
+    for seed in (0, 1, 2 ** 32 - 1):
+        c = List8(z, sizes, g, shift=shift)
+        assert shift or c.plan.info.vector_tensors == sum(n > 0 for n in sizes)
+        c.step_and_check(1, 1e-2, 1e-8, seed)
+    same = (rng.standard_normal(5000) * 1e-2).astype(F)
+    codes = []
+    for seed in (4, 4, 5):
+        c = List8(z, [5000, 5000], [same, same])
+        c.step_and_check(1, 1e-2, 1e-8, seed)
+        codes.append([d["v"].cpu().numpy() for d in c.dev])
+    assert np.array_equal(codes[0][0], codes[1][0]) and np.array_equal(codes[0][1], codes[1][1])
+    # a root lies strictly between two codes almost always, so that other bits round about half of the codes otherwise
+    assert (codes[0][0] != codes[0][1]).sum() > 1000 and (codes[0][0] != codes[2][0]).sum() > 1000
