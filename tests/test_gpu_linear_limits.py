@@ -1,5 +1,5 @@
 """The linear layer at the ends of their ranges: outputs of more than 2^30 columns, infinite and NaN gradients
-in places that ReLU masks; and matrices on boundaries of their own."""
+in places that ReLU masks; matrices on boundaries of their own; the one rounding of dz."""
 import math
 import random
 
@@ -135,3 +135,37 @@ def test_every_gradient_on_a_boundary_of_its_own(z, T, K, N, ty):
         place = {k: rng.choice([(0, 0), (8, 8), (2, 0), (0, 2), (1, 0), (0, 1), (3, 5)]) for k in shapes}
         for a, b in zip(run(place), want):
             assert torch.equal(a, b), place
+
+
+@pytest.mark.parametrize("act,ty", [(2, 0), (2, 1), (3, 1), (0, 1)])
+@pytest.mark.parametrize("T,K,N", [(2048, 512, 1024), (77, 136, 264)])
+def test_gradients_are_those_of_dz_rounded_once(z, T, K, N, act, ty):
+    """The gradients against the formulas with dz rounded to the type once, as the header has it: the same bits in every
+    call, and no further off than the roundings of dz that fall otherwise.  A dz whose fp32 value is off by a few 2^-23
+    falls to the other neighbour, twice the largest error away, in less than one case of 192; of N (T) independent ones
+    the sums are then off by less than 2 sqrt(3 / 192) = 1/4 of what the roundings themselves do."""
+    dt = (torch.float16, torch.bfloat16)[ty]
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    x, w, dy, pre = ((torch.randn(s, generator=gen, device="cuda") * k).to(dt) for s, k in (((T, K), 1), ((N, K), 0.05), ((T, N), 0.1), ((T, N), 1)))
+    n = z.zero_linear_workspace(T, K, N, act, True, True)
+    ws = torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")
+    runs = []
+    for _ in range(3):
+        dx, dw, db = (torch.full(s, math.nan, dtype=dt, device="cuda") for s in ((T, K), (N, K), (N,)))
+        z.zero_linear_backward(dy, N, pre if act else None, N, x, K, w, K, dx, K, dw, K, db, T, K, N, act, ty, ws, n)
+        runs.append((dx, dw, db))
+    for again in runs[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(runs[0], again))
+    p = pre.double().requires_grad_()
+    y = (p, None, torch.nn.functional.gelu(p, approximate="tanh"), p * torch.sigmoid(p))[act]
+    dz = torch.autograd.grad(y, p, dy.double())[0]
+    rounded = dz.to(dt).double()
+    rms = lambda a: float(a.square().mean().sqrt())  # noqa: E731
+    for got, f in ((runs[0][0], lambda d: d @ w.double()), (runs[0][1], lambda d: d.T @ x.double())):
+        want = f(rounded)
+        moved = rms(want - f(dz)) if act else 0.0
+        # the result's own rounding is spread evenly within half an ulp, at most u of it; fp32's sums are off by far less
+        u = (2.0 ** -11, 2.0 ** -8)[ty]
+        off = rms(got.double() - want)
+        assert off <= rms(want) * (u / math.sqrt(3) + 2.0 ** -18) + moved / 4, (off, moved)
+    assert bool((runs[0][2].double() - dz.sum(0)).abs().le((T + 8) * 2.0 ** -18 * dz.abs().sum(0) + (2.0 ** -11, 2.0 ** -8)[ty] * dz.sum(0).abs() + 2.0 ** -25).all())
