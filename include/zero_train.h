@@ -180,8 +180,9 @@ int zero_linear_forward(const void* x, int64_t ldx, const void* w, int64_t ldw, 
  * The residual's gradient is dy itself.  dx, dw and db may each be NULL (not
  * computed; w is unused without dx, x without dw).  dw and db may lie
  * anywhere, for instance in a rank's gradients of the flat vector that
- * zero_adam_step takes.  dz is rounded to `type` once, before the products;
- * sums are in fp32.  With T = 0 dw and db become 0.
+ * zero_adam_step takes.  dz is rounded to `type` once, before the products (in
+ * fp16 above 65504 it becomes infinite, below 3e-8 zero: scale the loss), and db
+ * is summed from it unrounded; sums are in fp32.  With T = 0 dw and db become 0.
  * workspace, errors: as zero_linear_forward (also ZERO_EINVAL when dx, dw and
  * db are all NULL). */
 int zero_linear_backward(const void* dy, int64_t lddy, const void* z, int64_t ldz, const void* x,

@@ -510,7 +510,9 @@ def zero_adamw_plan(tensors, P: int, grad_type: int, param_type: int, state_bits
     ``n``, ``grad`` (rank 0's gradient) and, with ``P > 1``, ``rank_stride``;
     ``master``, ``m``, ``v``, ``param`` and for 8-bit moments ``m_scale`` and
     ``v_scale``; ``weight_decay`` (default 0) and ``lr_scale`` (default 1).
-    The device table is allocated and filled here, on the current stream."""
+    The device table is allocated and filled here, on the current stream.  Make a
+    plan once and keep it: it costs about 0.05 ms of host time for a dozen
+    tensors, 0.5 ms for 290, 1.6 ms for a thousand, and a synchronous copy."""
     import torch
     n = len(tensors)
     arr = (zero_adamw_tensor_t * max(n, 1))()

@@ -462,11 +462,15 @@ __device__ __noinline__ void step_by_elements(const Args& a, const Tensor* x, fl
 // element.  The two differ in which lane holds an element and in nothing
 // else: results are the same.
 // Bound by HBM on large lists, by the launch and three dependent reads (place,
-// tensor, elements) on small ones.  Three CTAs an SM: at four the registers
-// spill (P = 2, 2.0e8 elements 1019 against 900 us).  Measured: eight bf16
-// ranks of 2.0e8 parameters 1.30 ms (6490 GB/s, 0.957 of the measured copy
-// bandwidth), 50 thousand parameters 6.2 us, 4.2e6 parameters of odd sizes with
-// 8-bit moments and fp32 gradients 17.9 us (4010 GB/s).
+// tensor, elements) on small ones.  Three CTAs an SM: at four the main path's
+// registers spill (P = 2, 2.0e8 elements 1019 against 900 us).  At three the
+// instances with 16-bit gradients keep theirs (fp16, 8-bit moments and several
+// ranks: 4 bytes); fp32 gradients of several ranks spill 88 bytes with 32-bit
+// moments and 64 with 8-bit ones.  Measured: eight bf16
+// ranks of 2.0e8 parameters 1.30 ms (6500 GB/s, 0.958 of the measured copy
+// bandwidth), 50 thousand parameters 6.2 us, 4.0e6 parameters of odd sizes with
+// 8-bit moments and fp32 gradients 18.2 us (3940 GB/s; 16 us where one list's 72
+// MB stay in L2).
 template <int GT, int PT, int BITS, bool ONE>
 __global__ void __launch_bounds__(kThreads, 3) zero_adamw_kernel(const __grid_constant__ Args a)
 {
@@ -587,8 +591,8 @@ __global__ void __launch_bounds__(kThreads, 3) zero_adamw_kernel(const __grid_co
 // copies in flight do not depend on the warps' registers or on how far their
 // arithmetic has come, which is what bounds the vector kernel.
 // Measured, 1.3e9 parameters, P = 1: 32-bit moments 5.50 ms (6620 GB/s, 0.975 of
-// the measured copy bandwidth; vector kernel 6.2 ms), 8-bit ones 3.31 ms (6300
-// GB/s, 0.929; vector kernel 3.7 ms), where the arithmetic, about 75
+// the measured copy bandwidth; vector kernel 6.2 ms), 8-bit ones 3.29 ms (6350
+// GB/s, 0.936; vector kernel 3.7 ms), where the arithmetic, about 75
 // instructions an element, takes nearly the time of the bytes.
 constexpr int kGroups = 3;
 constexpr int kPipeThreads = 32 + kGroups * kThreads;
@@ -862,8 +866,11 @@ __global__ void __launch_bounds__(kPipeThreads, 1) zero_adamw_pipeline_kernel(co
 // squares are lost; above, the sums of many may overflow) are squared again
 // after scaling and added in fp64.  The CTAs' sums are joined in fp64 by the last CTA to
 // finish, in CTA order, so the bits do not depend on which one that is.
-// Bound by HBM reads: eight fp16 ranks of 3.0e8 parameters 675 us (7160 GB/s,
-// 1.06 of the measured copy bandwidth); 50 thousand parameters 5.8 us.
+// Bound by HBM reads: eight fp16 ranks of 3.0e8 parameters 671 us (7200 GB/s,
+// 1.06 of the measured copy bandwidth); 50 thousand parameters 6.3 us.  The
+// check of the range costs 0.15 us of those, and 1 % of one bf16 rank's 3.0e8
+// (91.7 to 92.8 us; all zeros 97 us, all of 1e-25 153 us).  The branch for
+// the others is kept out of the main path's way and spills 10 to 74 bytes.
 // Short lists take small chunks, so that every SM has some, and read four
 // ranks at once instead of four vectors of one (eight bf16 ranks of 2.4e5
 // parameters 11.4 against 8.1 us; long lists lose, 4.0e8 parameters of one rank
@@ -1092,13 +1099,15 @@ int pipeline_stages(int64_t stage)
     return static_cast<int>(std::min(near, most)) * kGroups;
 }
 
-// Where the pipeline beats the vector kernel.  Measured (GB/s, vector against
-// pipeline): 32-bit moments, P = 1, 3.0e8 elements 6070 / 6640, 1.2e7 5560 /
+// Where the pipeline takes over: one threshold for all, near the crossings and not
+// on them.  Measured (GB/s, vector against pipeline): 32-bit moments, P = 1, 3.0e8 elements 6070 / 6640, 1.2e7 5560 /
 // 5690, 3.9e6 4920 / 4350; P = 2 6740 / 6660, P = 4 6730 / 6740, P = 8 6640 /
 // 6470 (more ranks read more than they write and leave the vector kernel
 // enough copies in flight).  8-bit moments, P = 1, 3.0e8 elements 5860 / 6300,
 // 9.4e6 4170 / 4080, 3.9e6 3160 / 2730; P = 4 9.4e6 4550 / 5000; P = 8 5.0e7
-// 5580 / 6990.
+// 5580 / 6990.  Repeated on one list of bf16, 8 bit, P = 1 (us): 8.4e6 20.4 / 22.5,
+// 9.4e6 23.6 / 28.0, 1.6e7 46.1 / 42.6: between 8.4e6 and some 1.3e7 elements the
+// vector kernel would be up to a sixth quicker.
 bool takes_pipeline(int64_t chunks, int bits, int P) { return chunks >= 4096 && (bits == 8 || P == 1); }
 
 int64_t table_size(int64_t n)

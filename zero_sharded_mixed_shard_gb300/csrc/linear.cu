@@ -268,7 +268,8 @@ __device__ __forceinline__ void wait_for_predecessor() { asm volatile("griddepco
 // One lane of a converged warp.  The copy and product instructions take
 // uniform registers: issued under this predicate the compiler knows that one
 // thread runs them, under `lane == 0` it does not and each of them costs
-// several hundred cycles (x [16384, 8192] W^T [2048]: 386 against 314 us).
+// several hundred cycles (x [16384, 8192] W^T [2048], single launches: 386
+// against 314 us).
 __device__ __forceinline__ bool elect_one()
 {
     uint32_t p;
@@ -655,7 +656,9 @@ __device__ __forceinline__ void tile_at(const Problem& g, int t, int* mt, int* n
 }
 
 // The bias gradient's last sum, by warp 3 of every CTA.  A column and a step
-// together may pass 2^31.
+// together may pass 2^31.  One lane adds a column's chunks, in a fixed order: with
+// few columns, which have up to 760 chunks, that is the longest chain of the launch
+// (backward of 4096 x 256 -> 256 22.0 us, without db 10.6; 16384 tokens 30.2, 23.9).
 __device__ __forceinline__ void bias_sum(const GemmArgs& args, int lane)
 {
     for (long long c = blockIdx.x * 32ll + lane; c < args.n_db; c += gridDim.x * 32ll) {
@@ -676,9 +679,10 @@ __device__ __forceinline__ void bias_sum(const GemmArgs& args, int lane)
 // Bound by the tensor cores (95 % of their cycles with 8192 inputs) and, run for
 // long, by the card's power.  A pair reads 128 products for each byte it loads,
 // a single CTA of 128 x 256 85, and has six stages of 64 instead of four.
-// Measured: x [16384, 8192] -> 2048 with residual, fp16: 314 us alone (1750
-// TFLOP/s; the library's product without residual 320 us), 372 us back to back
-// at the power limit (1480 TFLOP/s; the library 349 us); [8192, 2048] -> 8192
+// Measured: x [16384, 8192] -> 2048 with residual, fp16: 321 us for one launch
+// under ncu (1710 TFLOP/s), 365 to 377 us back to back at the power limit (1480
+// TFLOP/s; the library's product, without bias and residual, 349 to 356 us, so
+// that it is 3 to 5 % quicker there); [8192, 2048] -> 8192
 // with GELU 152 us (1810 TFLOP/s).  Eight epilogue warps: with four, GELU's
 // arithmetic took longer than the products it runs under (234 us).
 template <int BN> constexpr int kPairStage = kATile + BN / 2 * kBK * 2;
@@ -1021,8 +1025,9 @@ template <int PARTS> __device__ __forceinline__ void join(const Out& o, const Jo
     }
 }
 
-// Bound by the reads of the weights with few tokens (4 tokens, 2048 -> 8192, bf16:
-// 7.2 us for 33.6 MB, launch included), by latency in between: launch, first
+// Bound by the reads of the weights with few tokens (4 tokens, 2048 -> 8192, bf16,
+// 33.6 MB, launch included: 9.2 us from HBM, 16 weights in turn, 3650 GB/s; 7.0 us
+// from L2, one weight again and again), by latency in between: launch, first
 // copy, a handful of stages, join and stores follow on each other (1024 x 1024
 // -> 1024 7.7 us).
 // PER_SM 1: one CTA on an SM, stages as deep as they go, eight epilogue warps.
@@ -1249,6 +1254,12 @@ __device__ __forceinline__ void copy_rows(const Copy& c, int cta)
     }
 }
 
+// dz is rounded to 16 bits here, once: the products' operands are 16-bit ones
+// (fp32 operands would halve the tensor cores' rate and double their bytes, a
+// second product with what the rounding cuts off would double the products).
+// With bf16 and GELU dx and dw are off by 0.0023 of their size for it, 0.0017
+// with dz in fp32, where the rounding of dx and dw themselves is left.  The
+// column sums take dz before it is rounded.
 // Bound by HBM and, with an activation, nearly by its arithmetic: dz and its
 // sums of 8192 x 8192 bf16 with GELU 64 us (403 MB, 6300 GB/s), the sums alone
 // without activation 24 us (134 MB).
