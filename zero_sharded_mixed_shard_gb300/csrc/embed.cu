@@ -1,0 +1,510 @@
+// Embedding lookup y[t] = scale table[ids[t]] and its gradient
+// dtable[v] = scale (sum of dy[t] over the tokens t with ids[t] = v).
+//
+// The lookup is bound by HBM: a warp copies a piece of a row with all of its
+// reads in flight.
+//
+// The gradient sums each row's tokens in the tokens' order, without atomics on
+// values, so that a call repeats its bits.  The tokens are sorted by id with a
+// stable radix sort (9 bits a pass: two passes up to 2^18 ids; a block ranks
+// its tokens by the lanes' matching digits and finds its place from the blocks'
+// digit counts).  Then warps walk over the sorted tokens, a chunk of them and a
+// stripe of 256 columns each, adding rows of dy in registers; a run of equal
+// ids that lies in one chunk is written at once, the parts of a longer one go
+// to the workspace in fp32 and are added in order by a last launch.  However
+// often an id occurs, no warp has more than a chunk of rows to read.
+#include "layers.cuh"
+
+namespace {
+
+struct LookArgs {
+    const int32_t* ids;
+    const void* table;
+    void* y;
+    long long ldt, ldy, T, items;
+    int D, V, pieces;
+    float scale;
+};
+
+constexpr int kLookPiece = 1024; // columns of a warp's item: four vectors of 8 a lane
+
+// One warp per piece of a token's row.  VEC: rows lie on 16 bytes.
+template <int BF16, int VEC> __global__ void __launch_bounds__(256) zero_embed_kernel(const __grid_constant__ LookArgs a)
+{
+    const int lane = threadIdx.x & 31;
+    const long long item = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    let_successor_start();
+    wait_for_predecessor();
+    if (item >= a.items) return;
+    const long long t = item / a.pieces;
+    const int c0 = static_cast<int>(item - t * a.pieces) * kLookPiece;
+    const int id = a.ids[t];
+    const bool there = id >= 0 && id < a.V;
+    const uint16_t* from = static_cast<const uint16_t*>(a.table) + (there ? id * a.ldt : 0);
+    uint16_t* to = static_cast<uint16_t*>(a.y) + t * a.ldy;
+    if constexpr (VEC) {
+        uint4 u[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int c = c0 + (k * 32 + lane) * 8;
+            u[k] = make_uint4(0, 0, 0, 0);
+            if (there && c + 8 <= a.D) u[k] = *reinterpret_cast<const uint4*>(from + c);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int c = c0 + (k * 32 + lane) * 8;
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+            add8(v, u[k], BF16);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = there ? v[j] * a.scale : 0.0f;
+            if (c + 8 <= a.D) *reinterpret_cast<uint4*>(to + c) = pack8(v, BF16);
+        }
+    } else {
+#pragma unroll 8
+        for (int k = 0; k < kLookPiece / 32; ++k) {
+            const int c = c0 + k * 32 + lane;
+            if (c < a.D) store16(to, c, there ? load16(from, c, BF16) * a.scale : 0.0f, BF16);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Stable radix sort of (id, token)
+// ---------------------------------------------------------------------------
+
+constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
+constexpr int kSortThreads = kDigits, kSortWarps = kSortThreads / 32; // a thread per digit
+
+struct SortArgs {
+    const int32_t* ids;  // the first pass: the ids in order
+    const int2* from;    // later ones: (id, token)
+    int2* to;
+    uint32_t* counts;    // [blocks][kDigits] of this pass
+    uint32_t* next;      // the same of the next pass, null in the last
+    long long T;
+    int V, shift, blocks, all_counts;
+};
+
+// An id that names no row sorts behind every other one.
+__device__ __forceinline__ int sort_key(int id, int V) { return id >= 0 && id < V ? id : V; }
+
+// Digit counts of each block for the first pass; the later passes' counts
+// become 0 (the passes before them add to these).
+template <int ROUNDS> __global__ void __launch_bounds__(kSortThreads) zero_sort_count_kernel(const __grid_constant__ SortArgs a)
+{
+    __shared__ uint32_t count[kDigits];
+    let_successor_start();
+    count[threadIdx.x] = 0;
+    __syncthreads();
+    wait_for_predecessor();
+    const long long t0 = static_cast<long long>(blockIdx.x) * (ROUNDS * kSortThreads);
+#pragma unroll
+    for (int k = 0; k < ROUNDS; ++k) {
+        const long long t = t0 + k * kSortThreads + threadIdx.x;
+        if (t < a.T) atomicAdd(&count[sort_key(a.ids[t], a.V) & (kDigits - 1)], 1u);
+    }
+    __syncthreads();
+    a.counts[static_cast<long long>(blockIdx.x) * kDigits + threadIdx.x] = count[threadIdx.x];
+    for (int p = 1; p < a.all_counts; ++p)
+        a.counts[(static_cast<long long>(p) * a.blocks + blockIdx.x) * kDigits + threadIdx.x] = 0;
+}
+
+// One pass: each token's place is the start of its digit, the tokens with the
+// digit in earlier blocks, those in earlier warps of the block, and those
+// earlier in the warp.
+template <int ROUNDS> __global__ void __launch_bounds__(kSortThreads) zero_sort_pass_kernel(const __grid_constant__ SortArgs a)
+{
+    __shared__ uint32_t count[kSortWarps][kDigits];
+    __shared__ uint32_t warp_total[kSortWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = threadIdx.x;
+    let_successor_start();
+#pragma unroll
+    for (int k = 0; k < kSortWarps; ++k) count[k][d] = 0;
+    __syncthreads();
+    wait_for_predecessor();
+    constexpr int kTokens = ROUNDS * kSortThreads;
+    const long long t0 = static_cast<long long>(blockIdx.x) * kTokens + warp * (ROUNDS * 32);
+    int key[ROUNDS], token[ROUNDS];
+    uint32_t rank[ROUNDS];
+#pragma unroll
+    for (int k = 0; k < ROUNDS; ++k) {
+        const long long t = t0 + k * 32 + lane;
+        key[k] = token[k] = 0;
+        if (t < a.T) {
+            if (a.ids) {
+                key[k] = sort_key(a.ids[t], a.V);
+                token[k] = static_cast<int>(t);
+            } else {
+                const int2 p = a.from[t];
+                key[k] = p.x;
+                token[k] = p.y;
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < ROUNDS; ++k) {
+        const bool live = t0 + k * 32 + lane < a.T;
+        const int digit = live ? (key[k] >> a.shift) & (kDigits - 1) : kDigits;
+        const uint32_t same = __match_any_sync(0xffffffffu, digit);
+        const uint32_t before = live ? count[warp][digit] : 0;
+        rank[k] = before + __popc(same & ((1u << lane) - 1));
+        __syncwarp();
+        if (live && (same >> lane) == 1) count[warp][digit] = before + __popc(same); // the last of them
+        __syncwarp();
+    }
+    // tokens with digit d in earlier blocks and in all
+    uint32_t earlier = 0, all = 0;
+#pragma unroll 8
+    for (int b = 0; b < a.blocks; ++b) {
+        const uint32_t n = a.counts[static_cast<long long>(b) * kDigits + d];
+        all += n;
+        if (b < static_cast<int>(blockIdx.x)) earlier += n;
+    }
+    // the start of digit d: an exclusive sum over the digits
+    uint32_t sum = all;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t n = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += n;
+    }
+    if (lane == 31) warp_total[warp] = sum;
+    __syncthreads();
+    uint32_t at = earlier + sum - all;
+    for (int k = 0; k < warp; ++k) at += warp_total[k];
+#pragma unroll
+    for (int k = 0; k < kSortWarps; ++k) {
+        const uint32_t n = count[k][d];
+        count[k][d] = at;
+        at += n;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < ROUNDS; ++k) {
+        if (t0 + k * 32 + lane >= a.T) continue;
+        const uint32_t to = count[warp][(key[k] >> a.shift) & (kDigits - 1)] + rank[k];
+        a.to[to] = make_int2(key[k], token[k]);
+        if (a.next) atomicAdd(&a.next[static_cast<long long>(to / kTokens) * kDigits + ((key[k] >> (a.shift + kDigitBits)) & (kDigits - 1))], 1u);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Sums over runs of equal ids
+// ---------------------------------------------------------------------------
+
+constexpr int kStripe = 256;   // columns of a warp: 8 a lane
+constexpr int kZeroRows = 8;   // rows of the table that a warp looks up and clears where they have no token
+
+struct RunArgs {
+    const int2* sorted;
+    const void* dy;
+    void* dtable;
+    float* parts;        // [chunks][2][D]: of the run that began before the chunk, of the one that goes on behind it
+    long long lddy, lddt, T, sum_tasks, tasks;
+    int D, V, stripes, chunk, add;
+    float scale;
+};
+
+template <int VEC> __device__ __forceinline__ int stripe_column(int c0, int j, int lane) { return VEC ? c0 + lane * 8 + j : c0 + j * 32 + lane; }
+
+// This lane's eight columns of a run's sum to the table's gradient.
+template <int BF16, int VEC>
+__device__ __forceinline__ void put_row(const RunArgs& a, int key, int c0, int lane, const float (&sum)[8])
+{
+    uint16_t* row = static_cast<uint16_t*>(a.dtable) + key * a.lddt;
+    if constexpr (VEC) {
+        const int c = c0 + lane * 8;
+        if (c >= a.D) return;
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = sum[j] * a.scale;
+        if (a.add) add8(v, *reinterpret_cast<const uint4*>(row + c), BF16);
+        *reinterpret_cast<uint4*>(row + c) = pack8(v, BF16);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int c = stripe_column<0>(c0, j, lane);
+            if (c < a.D) store16(row, c, sum[j] * a.scale + (a.add ? load16(row, c, BF16) : 0.0f), BF16);
+        }
+    }
+}
+
+// Rows of the table without a token become 0: each lane looks its row up among
+// the sorted ids.
+template <int VEC> __device__ __forceinline__ void clear_rows(const RunArgs& a, long long v0, int lane)
+{
+    const int v = static_cast<int>(v0) + lane;
+    bool absent = lane < kZeroRows && v < a.V;
+    if (absent) {
+        long long lo = 0, hi = a.T; // first place whose id is v or above
+        while (lo < hi) {
+            const long long mid = (lo + hi) >> 1;
+            if (a.sorted[mid].x < v) lo = mid + 1;
+            else hi = mid;
+        }
+        absent = lo >= a.T || a.sorted[lo].x != v;
+    }
+    uint32_t todo = __ballot_sync(0xffffffffu, absent);
+    while (todo) {
+        const int k = __ffs(todo) - 1;
+        todo &= todo - 1;
+        uint16_t* row = static_cast<uint16_t*>(a.dtable) + (v0 + k) * a.lddt;
+        if (VEC) {
+            for (int c = lane * 8; c < a.D; c += 256) *reinterpret_cast<uint4*>(row + c) = make_uint4(0, 0, 0, 0);
+        } else {
+            for (int c = lane; c < a.D; c += 32) row[c] = 0;
+        }
+    }
+}
+
+template <int BF16, int VEC> __global__ void __launch_bounds__(256) zero_embed_grad_kernel(const __grid_constant__ RunArgs a)
+{
+    constexpr int kAhead = VEC ? 8 : 4; // rows in flight
+    const int lane = threadIdx.x & 31;
+    const long long task = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    let_successor_start();
+    wait_for_predecessor();
+    if (task >= a.tasks) return;
+    if (task >= a.sum_tasks) {
+        clear_rows<VEC>(a, (task - a.sum_tasks) * kZeroRows, lane);
+        return;
+    }
+    const long long chunk = task / a.stripes, first = chunk * a.chunk, end = min(a.T, first + a.chunk);
+    const int c0 = static_cast<int>(task - chunk * a.stripes) * kStripe;
+    const uint16_t* dy = static_cast<const uint16_t*>(a.dy);
+    float sum[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+    int run = first > 0 ? a.sorted[first - 1].x : -1; // the id whose run this is
+    bool begun = true;                                // it began before the chunk
+    bool open = false;                                // the sum holds a row
+    // the run that ends here: whole in this chunk, or a part of it
+    auto flush = [&](bool goes_on) {
+        if (!open) return;
+        if (!begun && !goes_on) {
+            put_row<BF16, VEC>(a, run, c0, lane, sum);
+        } else {
+            float* part = a.parts + (chunk * 2 + (begun ? 0 : 1)) * a.D;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int c = stripe_column<VEC>(c0, j, lane);
+                if (c < a.D) part[c] = sum[j];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+        open = false;
+    };
+    bool done = false;
+    for (long long s = first; s < end && !done; s += 32) {
+        const int2 mine = s + lane < end ? a.sorted[s + lane] : make_int2(a.V, 0); // a chunk ends off a multiple of 32 only at T
+        for (int i0 = 0; i0 < 32 && !done; i0 += kAhead) {
+            uint4 u[kAhead];
+            uint16_t e[kAhead][8];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int key = __shfl_sync(0xffffffffu, mine.x, i0 + i);
+                const uint16_t* row = dy + __shfl_sync(0xffffffffu, mine.y, i0 + i) * a.lddy;
+                if constexpr (VEC) {
+                    u[i] = make_uint4(0, 0, 0, 0);
+                    if (key < a.V && c0 + lane * 8 < a.D) u[i] = *reinterpret_cast<const uint4*>(row + c0 + lane * 8);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int c = stripe_column<0>(c0, j, lane);
+                        e[i][j] = key < a.V && c < a.D ? row[c] : 0;
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int key = __shfl_sync(0xffffffffu, mine.x, i0 + i);
+                if (key != run) {
+                    flush(false);
+                    run = key;
+                    begun = false;
+                }
+                if (key >= a.V) { // behind the last id
+                    done = true;
+                    break;
+                }
+                open = true;
+                if constexpr (VEC) {
+                    add8(sum, u[i], BF16);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sum[j] += load16(&e[i][j], 0, BF16);
+                }
+            }
+        }
+    }
+    flush(end < a.T && a.sorted[end].x == run);
+}
+
+// The parts of a run that passes a chunk's end, added in order by a warp of
+// the chunk that it begins in.
+template <int BF16, int VEC> __global__ void __launch_bounds__(256) zero_embed_join_kernel(const __grid_constant__ RunArgs a)
+{
+    const int lane = threadIdx.x & 31;
+    const long long task = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    let_successor_start();
+    wait_for_predecessor();
+    if (task >= a.sum_tasks) return;
+    const long long chunk = task / a.stripes, first = chunk * a.chunk, end = first + a.chunk;
+    const int c0 = static_cast<int>(task - chunk * a.stripes) * kStripe;
+    if (end >= a.T) return;
+    const int key = a.sorted[end - 1].x;
+    if (key >= a.V || a.sorted[end].x != key || (first > 0 && a.sorted[first - 1].x == key)) return;
+    // the chunks behind this one that begin with the run
+    const long long chunks = (a.T + a.chunk - 1) / a.chunk;
+    long long last = chunk; // the last chunk that holds a part
+    while (true) {
+        const long long c = last + 1 + lane;
+        const bool in = c < chunks && a.sorted[c * a.chunk].x == key;
+        const uint32_t all = __ballot_sync(0xffffffffu, in);
+        const int n = all == 0xffffffffu ? 32 : __ffs(~all) - 1;
+        last += n;
+        if (n < 32) break;
+    }
+    float sum[8];
+    auto read = [&](const float* part, float (&v)[8]) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int c = stripe_column<VEC>(c0, j, lane);
+            v[j] = c < a.D ? part[c] : 0.0f;
+        }
+    };
+    read(a.parts + (chunk * 2 + 1) * a.D, sum);
+#pragma unroll 4
+    for (long long c = chunk + 1; c <= last; ++c) {
+        float v[8];
+        read(a.parts + c * 2 * a.D, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] += v[j];
+    }
+    put_row<BF16, VEC>(a, key, c0, lane, sum);
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+constexpr int64_t kMostIds = int64_t{1} << 30;
+
+bool bad_embed(int64_t T, int64_t D, int64_t V, float scale, int32_t type)
+{
+    return T < 0 || T > kMostExtent || D < 1 || D > kMostIds || V < 1 || V > kMostIds || std::max(T, V) * D > kMostElements ||
+           !(scale > -INFINITY && scale < INFINITY) || (type != ZERO_TYPE_FP16 && type != ZERO_TYPE_BF16);
+}
+
+// The layout of a gradient's workspace and the sizes of its launches.
+struct GradPlan {
+    int rounds, blocks, passes, chunk;
+    int64_t chunks, stripes;
+    int2* pairs[2];
+    uint32_t* counts;
+    float* parts;
+    int64_t bytes;
+};
+
+GradPlan plan_grad(int64_t T, int64_t D, int64_t V, void* workspace)
+{
+    GradPlan p{};
+    // a block reads the counts of all of them: many tokens take larger blocks
+    p.rounds = T <= 65536 ? 2 : 8;
+    p.blocks = static_cast<int>((T + p.rounds * kSortThreads - 1) / (p.rounds * kSortThreads));
+    int bits = 1;
+    while ((V >> bits) != 0) ++bits; // of V itself, which stands for no row
+    p.passes = (bits + kDigitBits - 1) / kDigitBits;
+    p.stripes = (D + kStripe - 1) / kStripe;
+    // longer chunks once there are warps enough: fewer runs are cut
+    p.chunk = static_cast<int>(std::min<int64_t>(256, std::max<int64_t>(32, T * p.stripes / 8192 / 32 * 32)));
+    p.chunks = (T + p.chunk - 1) / p.chunk;
+    Carver c{static_cast<unsigned char*>(workspace)};
+    for (int2*& q : p.pairs) q = static_cast<int2*>(c.take(T * 8));
+    p.counts = static_cast<uint32_t*>(c.take(static_cast<int64_t>(p.passes) * p.blocks * kDigits * 4));
+    p.parts = static_cast<float*>(c.take(p.chunks * 2 * D * 4));
+    p.bytes = c.used;
+    return p;
+}
+
+template <class Kernel> Kernel pick(int bf16, int vec, Kernel k00, Kernel k01, Kernel k10, Kernel k11)
+{
+    return bf16 ? (vec ? k11 : k10) : (vec ? k01 : k00);
+}
+
+} // namespace
+
+extern "C" int zero_embed_forward(const int32_t* ids, const void* table, int64_t ldt, void* y, int64_t ldy, int64_t T, int64_t D,
+                                  int64_t V, float scale, int32_t type, void* cuda_stream)
+{
+    if (bad_embed(T, D, V, scale, type)) return ZERO_EINVAL;
+    if (T == 0) return ZERO_OK;
+    if (!ids || !table || !y || bad_ld(ldt, D) || bad_ld(ldy, D)) return ZERO_EINVAL;
+    if (addr(ids) % 4 || addr(table) % 2 || addr(y) % 2) return ZERO_EALIGN;
+    if (share(y, ldy, T, D, table, ldt, V, D) || share(y, ldy, T, D, ids, 2 * T, 1, 2 * T)) return ZERO_EOVERLAP;
+    LookArgs a{};
+    a.ids = ids, a.table = table, a.y = y, a.ldt = ldt, a.ldy = ldy, a.T = T, a.D = static_cast<int>(D), a.V = static_cast<int>(V);
+    a.pieces = static_cast<int>((D + kLookPiece - 1) / kLookPiece);
+    a.items = T * a.pieces;
+    a.scale = scale;
+    if ((a.items + 7) / 8 > INT32_MAX) return ZERO_EINVAL;
+    const bool vec = D % 8 == 0 && aligned16(table, ldt) && aligned16(y, ldy);
+    auto fn = pick(type == ZERO_TYPE_BF16, vec, zero_embed_kernel<0, 0>, zero_embed_kernel<0, 1>, zero_embed_kernel<1, 0>, zero_embed_kernel<1, 1>);
+    return launch_after(fn, a, (a.items + 7) / 8, 256, 0, 1, static_cast<cudaStream_t>(cuda_stream));
+}
+
+extern "C" int zero_embed_workspace(int64_t T, int64_t D, int64_t V, int64_t* bytes)
+{
+    if (!bytes || bad_embed(T, D, V, 1.0f, ZERO_TYPE_FP16)) return ZERO_EINVAL;
+    *bytes = T == 0 ? 0 : plan_grad(T, D, V, nullptr).bytes;
+    return ZERO_OK;
+}
+
+extern "C" int zero_embed_backward(const int32_t* ids, const void* dy, int64_t lddy, void* dtable, int64_t lddt, int64_t T, int64_t D,
+                                   int64_t V, float scale, int32_t add, int32_t type, void* workspace, int64_t workspace_bytes,
+                                   void* cuda_stream)
+{
+    if (bad_embed(T, D, V, scale, type) || !dtable || bad_ld(lddt, D)) return ZERO_EINVAL;
+    if (T > 0 && (!ids || !dy || bad_ld(lddy, D))) return ZERO_EINVAL;
+    if (addr(dtable) % 2 || (T > 0 && (addr(ids) % 4 || addr(dy) % 2))) return ZERO_EALIGN;
+    cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+    if (T == 0) {
+        if (add) return ZERO_OK;
+        return record(cudaMemset2DAsync(dtable, static_cast<size_t>(lddt) * 2, 0, static_cast<size_t>(D) * 2, static_cast<size_t>(V), st));
+    }
+    if (share(dtable, lddt, V, D, dy, lddy, T, D) || share(dtable, lddt, V, D, ids, 2 * T, 1, 2 * T)) return ZERO_EOVERLAP;
+    const GradPlan p = plan_grad(T, D, V, workspace);
+    if (!workspace || workspace_bytes < p.bytes) return ZERO_EINVAL;
+    if (addr(workspace) % 16) return ZERO_EALIGN;
+    if (in_workspace(workspace, p.bytes, dy, lddy, T, D) || in_workspace(workspace, p.bytes, dtable, lddt, V, D) ||
+        in_workspace(workspace, p.bytes, ids, 2 * T, 1, 2 * T))
+        return ZERO_EOVERLAP;
+    RunArgs r{};
+    r.dy = dy, r.dtable = dtable, r.parts = p.parts, r.lddy = lddy, r.lddt = lddt, r.T = T, r.D = static_cast<int>(D), r.V = static_cast<int>(V);
+    r.stripes = static_cast<int>(p.stripes), r.chunk = p.chunk, r.add = add != 0, r.scale = scale;
+    r.sum_tasks = p.chunks * p.stripes;
+    r.tasks = r.sum_tasks + (add ? 0 : (V + kZeroRows - 1) / kZeroRows);
+    if ((r.tasks + 7) / 8 > INT32_MAX) return ZERO_EINVAL;
+
+    SortArgs s{};
+    s.ids = ids, s.counts = p.counts, s.T = T, s.V = static_cast<int>(V), s.blocks = p.blocks, s.all_counts = p.passes;
+    int rc = launch_after(p.rounds == 2 ? zero_sort_count_kernel<2> : zero_sort_count_kernel<8>, s, p.blocks, kSortThreads, 0, 1, st);
+    for (int k = 0; k < p.passes && !rc; ++k) {
+        const int64_t each = static_cast<int64_t>(p.blocks) * kDigits;
+        s.ids = k == 0 ? ids : nullptr;
+        s.from = p.pairs[(k + 1) & 1], s.to = p.pairs[k & 1];
+        s.counts = p.counts + k * each, s.next = k + 1 < p.passes ? p.counts + (k + 1) * each : nullptr;
+        s.shift = k * kDigitBits;
+        rc = launch_after(p.rounds == 2 ? zero_sort_pass_kernel<2> : zero_sort_pass_kernel<8>, s, p.blocks, kSortThreads, 0, 1, st);
+    }
+    if (rc) return rc;
+    r.sorted = p.pairs[(p.passes - 1) & 1];
+    const int bf16 = type == ZERO_TYPE_BF16;
+    const bool vec = D % 8 == 0 && aligned16(dy, lddy) && aligned16(dtable, lddt);
+    auto sum = pick(bf16, vec, zero_embed_grad_kernel<0, 0>, zero_embed_grad_kernel<0, 1>, zero_embed_grad_kernel<1, 0>, zero_embed_grad_kernel<1, 1>);
+    if ((rc = launch_after(sum, r, (r.tasks + 7) / 8, 256, 0, 1, st))) return rc;
+    auto join = pick(bf16, vec, zero_embed_join_kernel<0, 0>, zero_embed_join_kernel<0, 1>, zero_embed_join_kernel<1, 0>, zero_embed_join_kernel<1, 1>);
+    return launch_after(join, r, (r.sum_tasks + 7) / 8, 256, 0, 1, st);
+}
