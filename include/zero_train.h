@@ -1,8 +1,9 @@
 /*
  * zero_train.h -- C ABI of the training operators beside the ZeRO step
  * (zero_step.h): AdamW over many separate tensors with 32-bit or 8-bit
- * moments, the global gradient norm with its clipping factor, and the linear
- * layer whose gradients the steps consume.
+ * moments, the global gradient norm with its clipping factor, and the layers
+ * whose gradients the steps consume: the linear layer, embedding, layer norm,
+ * and the loss that ends a language model.
  *
  * The general rules of zero_step.h hold: 0 or a negative ZERO_E* code, a
  * rejected call has no side effects, device memory is the caller's, kernels
@@ -22,7 +23,7 @@ extern "C" {
 /* Element types of gradients, parameters and layers. */
 #define ZERO_TYPE_FP16 0
 #define ZERO_TYPE_BF16 1
-#define ZERO_TYPE_FP32 2 /* gradients only */
+#define ZERO_TYPE_FP32 2 /* gradients of AdamW and its norm, a teacher's logits */
 
 /* ------------------------------------------------------------------------ */
 /* AdamW over many tensors, gradient norm                                   */
@@ -200,6 +201,121 @@ int zero_linear_backward(const void* dy, int64_t lddy, const void* z, int64_t ld
  * Errors: ZERO_EINVAL (also T < 1), ZERO_ECUDA. */
 int zero_linear_plan(int64_t T, int64_t K, int64_t N, int32_t products, int32_t* launches,
                      int32_t* rows, int32_t* columns, int32_t* cluster, int32_t* per_sm);
+
+/* ------------------------------------------------------------------------ */
+/* Embedding                                                                */
+/* ------------------------------------------------------------------------ */
+
+/* y[t] = scale * table[ids[t]] for T tokens: ids int32 [T], table [V][ldt]
+ * (D wide), y [T][ldy], of `type` (ZERO_TYPE_FP16 or ZERO_TYPE_BF16), rounded
+ * once.  An id outside [0, V) (padding) gives a row of zeros.  T may be 0.
+ * Errors: ZERO_EINVAL (a null pointer, T above 2^31 - 513, D or V above 2^30,
+ * a row stride below D, scale not finite, type unknown), ZERO_EALIGN (a
+ * pointer not on its element size), ZERO_EOVERLAP (y shares an element with
+ * the table or the ids), ZERO_ECUDA. */
+int zero_embed_forward(const int32_t* ids, const void* table, int64_t ldt, void* y, int64_t ldy,
+                       int64_t T, int64_t D, int64_t V, float scale, int32_t type,
+                       void* cuda_stream);
+
+/* Bytes of workspace of zero_embed_backward: about T * D / 4 + 16 T.  Host
+ * only.  Errors: ZERO_EINVAL. */
+int zero_embed_workspace(int64_t T, int64_t D, int64_t V, int64_t* bytes);
+
+/* The table's gradient, dtable[v] = scale * sum of dy[t] over the tokens with
+ * ids[t] = v, dtable [V][lddt], dy [T][lddy].  Sums are in fp32, over a row's
+ * tokens in a fixed order (the same call gives the same bits), rounded once.
+ * add 0: every row of dtable is written, those without a token with zeros.
+ * add 1: the sums are added to what dtable holds (a table whose gradient the
+ * output layer has written already) before the rounding, and rows without a
+ * token stay as they are.  Tokens outside [0, V) are passed over, whatever
+ * their rows of dy hold.  With T = 0 dtable becomes 0 (add 0) or stays.
+ * workspace: device, 16-byte aligned, zero_embed_workspace bytes; calls that
+ * share one must not overlap on the GPU.
+ * Errors: as zero_embed_forward (also a workspace too small; dtable shares an
+ * element with dy or the ids, or the workspace a byte with any of them). */
+int zero_embed_backward(const int32_t* ids, const void* dy, int64_t lddy, void* dtable,
+                        int64_t lddt, int64_t T, int64_t D, int64_t V, float scale, int32_t add,
+                        int32_t type, void* workspace, int64_t workspace_bytes,
+                        void* cuda_stream);
+
+/* ------------------------------------------------------------------------ */
+/* Layer norm                                                               */
+/* ------------------------------------------------------------------------ */
+
+/* y = (x - mean) * rstd * weight + bias over rows of D elements, with
+ * rstd = 1 / sqrt(mean((x - mean)^2) + eps): x [T][ldx], y [T][ldy], weight [D]
+ * or NULL (ones), bias [D] or NULL (zeros), all of `type`.  mean and rstd (fp32
+ * [T], each may be NULL) receive the statistics that the backward pass needs.
+ * Statistics are in fp32, the variance that of the centred values; y is
+ * rounded once.  y may be x itself (same pointer and stride).  T may be 0.
+ * Errors: ZERO_EINVAL (a null pointer, T above 2^31 - 513, D above 2^30, a row
+ * stride below D, eps not finite or below 2^-126, type unknown), ZERO_EALIGN
+ * (a pointer not on its element size), ZERO_EOVERLAP (an output shares an
+ * element with an input or another output), ZERO_ECUDA. */
+int zero_layernorm_forward(const void* x, int64_t ldx, const void* weight, const void* bias,
+                           void* y, int64_t ldy, float* mean, float* rstd, int64_t T, int64_t D,
+                           float eps, int32_t type, void* cuda_stream);
+
+/* Bytes of workspace of zero_layernorm_backward.  Host only.  Errors:
+ * ZERO_EINVAL. */
+int zero_layernorm_workspace(int64_t T, int64_t D, int64_t* bytes);
+
+/* The gradients of zero_layernorm_forward from dy [T][lddy] and the forward
+ * call's mean and rstd.  With h = (x - mean) * rstd and a = dy * weight:
+ *   dx = rstd * (a - mean(a) - h * mean(a * h)) + dres   [T][lddx]
+ *   dweight = sum over rows of dy * h;  dbias = sum over rows of dy   [D]
+ * dres [T][lddr] or NULL is the gradient that reaches x past the norm (a
+ * residual's).  dx, dweight and dbias may each be NULL (not computed).  dx may
+ * be dres itself, and dy itself where D is at most 8192 (same pointer and
+ * stride).  Sums are in fp32 and in a fixed order; each output is rounded
+ * once.  With T = 0 dweight and dbias become 0.
+ * workspace: device, 16-byte aligned, zero_layernorm_workspace bytes (may be
+ * NULL without dweight and dbias); calls that share one must not overlap on
+ * the GPU.
+ * Errors: as zero_layernorm_forward (also ZERO_EINVAL when all outputs are
+ * NULL or the workspace is too small, and ZERO_EOVERLAP when the workspace
+ * shares a byte with a matrix). */
+int zero_layernorm_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                            const void* weight, const float* mean, const float* rstd,
+                            const void* dres, int64_t lddr, void* dx, int64_t lddx, void* dweight,
+                            void* dbias, int64_t T, int64_t D, int32_t type, void* workspace,
+                            int64_t workspace_bytes, void* cuda_stream);
+
+/* ------------------------------------------------------------------------ */
+/* Loss against targets and a teacher                                       */
+/* ------------------------------------------------------------------------ */
+
+/* The loss of T rows of logits [T][ldl] (V wide) against a target token each
+ * and a teacher's K largest logits, and its gradient.  Per row, with z the
+ * temperature, q = softmax(logits), q' = softmax(logits / z), p = softmax over
+ * the row's K entries of teacher / z, j_k their indices and w the row's weight:
+ *   loss[t] = w * ((1 - alpha) * -log q[target]
+ *                  + alpha * z^2 * sum_k p_k * (log p_k - log q'[j_k]))
+ *   dlogits[t][j] = grad_scale * d loss[t] / d logits[t][j]
+ * alpha 0 is plain cross-entropy (K, index and teacher are not looked at),
+ * alpha 1 the teacher alone (targets is not looked at).
+ * targets: int32 [T]; one outside [0, V) leaves its row without the first
+ * term.  index: int32 [T][ldk]; an index outside [0, V) and a teacher's logit
+ * of minus infinity have no probability, a row without any (or K = 0) has no
+ * second term.  An index that occurs twice counts as two entries.  teacher:
+ * [T][ldk] of teacher_type (ZERO_TYPE_FP16, _BF16 or _FP32).  weights: fp32
+ * [T] or NULL (ones).  A row with weight 0 or without terms gets loss 0 and a
+ * gradient of zeros, whatever its logits hold.  Logits of minus infinity
+ * (masked) have probability 0.
+ * loss: fp32 [T].  dlogits [T][lddl], of `type` like the logits, or NULL (not
+ * computed); it may be logits itself (same pointer and stride).  Sums are in
+ * fp32, the gradient is rounded once; the same call gives the same bits.  T
+ * may be 0.
+ * Errors: ZERO_EINVAL (a null pointer, T above 2^31 - 513, V above 2^30, K
+ * outside [0, 1024], a row stride below its row, temperature outside [2^-10,
+ * 2^10], alpha outside [0, 1], grad_scale not finite, a type unknown),
+ * ZERO_EALIGN (a pointer not on its element size), ZERO_EOVERLAP (an output
+ * shares an element with an input or the other output), ZERO_ECUDA. */
+int zero_distill_loss(const void* logits, int64_t ldl, const int32_t* targets,
+                      const int32_t* index, const void* teacher, int64_t ldk,
+                      const float* weights, float* loss, void* dlogits, int64_t lddl, int64_t T,
+                      int64_t V, int64_t K, float temperature, float alpha, float grad_scale,
+                      int32_t type, int32_t teacher_type, void* cuda_stream);
 
 /* Bounded waits of the kernels of this header that gave up on the current
  * device since the last reset; like zero_device_timeouts (0 in every correct

@@ -52,6 +52,9 @@ EXPORTED = ("zero_init_layout", "zero_free_layout", "zero_shard_range", "zero_me
             "zero_last_cuda_error", "zero_last_cuda_error_string",
             "zero_adamw_plan", "zero_grad_norm", "zero_adamw_step",
             "zero_linear_plan", "zero_linear_workspace", "zero_linear_forward", "zero_linear_backward",
+            "zero_embed_forward", "zero_embed_workspace", "zero_embed_backward",
+            "zero_layernorm_forward", "zero_layernorm_workspace", "zero_layernorm_backward",
+            "zero_distill_loss",
             "zero_train_timeouts", "zero_selftest_adamw_wait")
 
 
@@ -196,6 +199,22 @@ def lib() -> ctypes.CDLL:
     L.zero_linear_backward.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp,
                                        i64, i64, i64, i32, i32, vp, i64, vp]
     L.zero_linear_backward.restype = ctypes.c_int
+    L.zero_embed_forward.argtypes = [vp, vp, i64, vp, i64, i64, i64, i64, f32, i32, vp]
+    L.zero_embed_forward.restype = ctypes.c_int
+    L.zero_embed_workspace.argtypes = [i64, i64, i64, ctypes.POINTER(ctypes.c_int64)]
+    L.zero_embed_workspace.restype = ctypes.c_int
+    L.zero_embed_backward.argtypes = [vp, vp, i64, vp, i64, i64, i64, i64, f32, i32, i32, vp, i64, vp]
+    L.zero_embed_backward.restype = ctypes.c_int
+    L.zero_layernorm_forward.argtypes = [vp, i64, vp, vp, vp, i64, vp, vp, i64, i64, f32, i32, vp]
+    L.zero_layernorm_forward.restype = ctypes.c_int
+    L.zero_layernorm_workspace.argtypes = [i64, i64, ctypes.POINTER(ctypes.c_int64)]
+    L.zero_layernorm_workspace.restype = ctypes.c_int
+    L.zero_layernorm_backward.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp, vp, i64,
+                                          i64, i32, vp, i64, vp]
+    L.zero_layernorm_backward.restype = ctypes.c_int
+    L.zero_distill_loss.argtypes = [vp, i64, vp, vp, vp, i64, vp, vp, vp, i64, i64, i64, i64, f32, f32,
+                                    f32, i32, i32, vp]
+    L.zero_distill_loss.restype = ctypes.c_int
     L.zero_train_timeouts.argtypes = [ctypes.POINTER(ctypes.c_int64), i32]
     L.zero_train_timeouts.restype = ctypes.c_int
     L.zero_selftest_adamw_wait.argtypes = [plan_p, vp, i64, f32, f32, f32, f32, vp]
@@ -600,6 +619,81 @@ def zero_linear_backward(dy, lddy: int, z, ldz: int, x, ldx: int, w, ldw: int, d
                                     _addr(workspace), workspace_bytes, _stream(stream))
     if rc:
         raise ZeroError(rc, "zero_linear_backward")
+
+
+def zero_embed_forward(ids, table, ldt: int, y, ldy: int, T: int, D: int, V: int, scale: float,
+                       type: int, stream=None) -> None:
+    """Enqueue y[t] = scale * table[ids[t]], ids int32 (see include/zero_train.h)."""
+    rc = lib().zero_embed_forward(_addr(ids), _addr(table), ldt, _addr(y), ldy, T, D, V, scale, type,
+                                  _stream(stream))
+    if rc:
+        raise ZeroError(rc, "zero_embed_forward")
+
+
+def zero_embed_workspace(T: int, D: int, V: int) -> int:
+    """Workspace bytes of zero_embed_backward (see include/zero_train.h)."""
+    n = ctypes.c_int64()
+    rc = lib().zero_embed_workspace(T, D, V, ctypes.byref(n))
+    if rc:
+        raise ZeroError(rc, "zero_embed_workspace")
+    return n.value
+
+
+def zero_embed_backward(ids, dy, lddy: int, dtable, lddt: int, T: int, D: int, V: int, scale: float,
+                        add: bool, type: int, workspace=None, workspace_bytes: int = 0,
+                        stream=None) -> None:
+    """Enqueue the gradient of the embedding's table, written or (``add``) added
+    to what ``dtable`` holds (see include/zero_train.h)."""
+    rc = lib().zero_embed_backward(_addr(ids), _addr(dy), lddy, _addr(dtable), lddt, T, D, V, scale,
+                                   1 if add else 0, type, _addr(workspace), workspace_bytes,
+                                   _stream(stream))
+    if rc:
+        raise ZeroError(rc, "zero_embed_backward")
+
+
+def zero_layernorm_forward(x, ldx: int, weight, bias, y, ldy: int, mean, rstd, T: int, D: int,
+                           eps: float, type: int, stream=None) -> None:
+    """Enqueue the layer norm of T rows; ``mean`` and ``rstd`` (fp32 [T], or None)
+    receive what the backward pass needs (see include/zero_train.h)."""
+    rc = lib().zero_layernorm_forward(_addr(x), ldx, _addr(weight), _addr(bias), _addr(y), ldy,
+                                      _addr(mean), _addr(rstd), T, D, eps, type, _stream(stream))
+    if rc:
+        raise ZeroError(rc, "zero_layernorm_forward")
+
+
+def zero_layernorm_workspace(T: int, D: int) -> int:
+    """Workspace bytes of zero_layernorm_backward (see include/zero_train.h)."""
+    n = ctypes.c_int64()
+    rc = lib().zero_layernorm_workspace(T, D, ctypes.byref(n))
+    if rc:
+        raise ZeroError(rc, "zero_layernorm_workspace")
+    return n.value
+
+
+def zero_layernorm_backward(dy, lddy: int, x, ldx: int, weight, mean, rstd, dres, lddr: int, dx,
+                            lddx: int, dweight, dbias, T: int, D: int, type: int, workspace=None,
+                            workspace_bytes: int = 0, stream=None) -> None:
+    """Enqueue the gradients of zero_layernorm_forward, dx plus the residual's
+    gradient ``dres`` (see include/zero_train.h)."""
+    rc = lib().zero_layernorm_backward(_addr(dy), lddy, _addr(x), ldx, _addr(weight), _addr(mean),
+                                       _addr(rstd), _addr(dres), lddr, _addr(dx), lddx,
+                                       _addr(dweight), _addr(dbias), T, D, type, _addr(workspace),
+                                       workspace_bytes, _stream(stream))
+    if rc:
+        raise ZeroError(rc, "zero_layernorm_backward")
+
+
+def zero_distill_loss(logits, ldl: int, targets, index, teacher, ldk: int, weights, loss, dlogits,
+                      lddl: int, T: int, V: int, K: int, temperature: float, alpha: float,
+                      grad_scale: float, type: int, teacher_type: int = TYPE_FP32,
+                      stream=None) -> None:
+    """Enqueue the rows' loss against targets and a teacher's top logits, and
+    its gradient (see include/zero_train.h)."""
+    rc = lib().zero_distill_loss(_addr(logits), ldl, _addr(targets), _addr(index), _addr(teacher), ldk,
+                                 _addr(weights), _addr(loss), _addr(dlogits), lddl, T, V, K,
+                                 temperature, alpha, grad_scale, type, teacher_type, _stream(stream))
+    if rc:
+        raise ZeroError(rc, "zero_distill_loss")
 
 
 def zero_train_timeouts(reset: bool = False) -> int:
