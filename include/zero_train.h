@@ -2,8 +2,8 @@
  * zero_train.h -- C ABI of the training operators beside the ZeRO step
  * (zero_step.h): AdamW over many separate tensors with 32-bit or 8-bit
  * moments, the global gradient norm with its clipping factor, and the layers
- * whose gradients the steps consume: the linear layer, embedding, layer norm,
- * and the loss that ends a language model.
+ * whose gradients the steps consume: the linear layer, the gated feed-forward
+ * projections, embedding, layer norm, and the loss that ends a language model.
  *
  * The general rules of zero_step.h hold: 0 or a negative ZERO_E* code, a
  * rejected call has no side effects, device memory is the caller's, kernels
@@ -201,6 +201,70 @@ int zero_linear_backward(const void* dy, int64_t lddy, const void* z, int64_t ld
  * Errors: ZERO_EINVAL (also T < 1), ZERO_ECUDA. */
 int zero_linear_plan(int64_t T, int64_t K, int64_t N, int32_t products, int32_t* launches,
                      int32_t* rows, int32_t* columns, int32_t* cluster, int32_t* per_sm);
+
+/* ------------------------------------------------------------------------ */
+/* Gated feed-forward projections                                           */
+/* ------------------------------------------------------------------------ */
+
+/* Bytes of workspace that is enough for a call of zero_gated_forward (backward
+ * 0) or zero_gated_backward (backward 1) of these sizes.  aligned != 0 when x,
+ * wg and wu start on 16 bytes and have row strides that are multiples of 8
+ * elements; otherwise room for aligned copies is counted.  May be 0 for the
+ * forward call.  Host only.  Errors: ZERO_EINVAL. */
+int zero_gated_workspace(int64_t T, int64_t K, int64_t N, int32_t backward, int32_t aligned,
+                         int64_t* bytes);
+
+/* h = act(g) * u with g = x wg^T + bg and u = x wu^T + bu for T tokens, K
+ * inputs, N features: x [T][ldx], wg [N][ldwg] and wu [N][ldwu] (both K wide;
+ * they may be halves of one matrix), bg and bu [N] or NULL, h [T][ldh], all of
+ * `type` (ZERO_TYPE_FP16 or ZERO_TYPE_BF16).  g [T][ldg] and u [T][ldu], both
+ * or neither NULL, receive the pre-activations, which the backward pass needs.
+ * Products are summed in fp32; h, g and u are each rounded once, h from the
+ * unrounded g and u.  T may be 0.  (The block's down-projection, with its
+ * residual, is zero_linear_forward on h.)
+ * workspace: device, 16-byte aligned, zero_gated_workspace bytes (may be NULL
+ * when that is 0); calls that share one must not overlap on the GPU.  The same
+ * call gives the same bits.
+ * Errors: ZERO_EINVAL (T or K above 2^31 - 513, N above half of that, a null
+ * pointer, one of g and u NULL, a row stride below its row, act or type
+ * unknown, workspace too small), ZERO_EALIGN (a pointer not on its element
+ * size, workspace not on 16 bytes), ZERO_EOVERLAP (an output shares an element
+ * with an input or another output, or the used workspace a byte with any of
+ * them), ZERO_ECUDA. */
+int zero_gated_forward(const void* x, int64_t ldx, const void* wg, int64_t ldwg, const void* wu,
+                       int64_t ldwu, const void* bg, const void* bu, void* h, int64_t ldh, void* g,
+                       int64_t ldg, void* u, int64_t ldu, int64_t T, int64_t K, int64_t N,
+                       int32_t act, int32_t type, void* workspace, int64_t workspace_bytes,
+                       void* cuda_stream);
+
+/* The gradients of zero_gated_forward from dh [T][lddh], the gradient of h,
+ * and the forward call's g and u:
+ *   du = dh * act(g);  dg = dh * u * act'(g)
+ *   dx = dg wg + du wu  [T][lddx]
+ *   dwg = dg^T x  [N][lddwg];  dwu = du^T x  [N][lddwu]
+ *   dbg = sum over tokens of dg;  dbu = sum over tokens of du  [N]
+ * Each of dx, dwg, dwu, dbg and dbu may be NULL (not computed; wg and wu are
+ * unused without dx, x without dwg and dwu).  dg and du are rounded to `type`
+ * once, before the products (in fp16 above 65504 they become infinite, below
+ * 3e-8 zero: scale the loss), and dbg and dbu are summed from them unrounded;
+ * sums are in fp32.  With ZERO_ACT_RELU dg is 0 where g is not above 0,
+ * whatever dh and u hold.  With T = 0 all of dwg, dwu, dbg and dbu become 0.
+ * workspace (never 0 bytes here, unless T is 0), errors: as zero_gated_forward
+ * (also ZERO_EINVAL when all outputs are NULL). */
+int zero_gated_backward(const void* dh, int64_t lddh, const void* g, int64_t ldg, const void* u,
+                        int64_t ldu, const void* x, int64_t ldx, const void* wg, int64_t ldwg,
+                        const void* wu, int64_t ldwu, void* dx, int64_t lddx, void* dwg,
+                        int64_t lddwg, void* dwu, int64_t lddwu, void* dbg, void* dbu, int64_t T,
+                        int64_t K, int64_t N, int32_t act, int32_t type, void* workspace,
+                        int64_t workspace_bytes, void* cuda_stream);
+
+/* Which kernel the gated projections' products would take, like
+ * zero_linear_plan: products 0 the forward product, 1 dx, 2 dwg and dwu, 3 all
+ * three; of the first launch the tile (of a forward product half of its
+ * columns are the gate's; up to 128 tokens half of its rows), the cluster and
+ * the CTAs per SM.  Errors: ZERO_EINVAL (also T < 1), ZERO_ECUDA. */
+int zero_gated_plan(int64_t T, int64_t K, int64_t N, int32_t products, int32_t* launches,
+                    int32_t* rows, int32_t* columns, int32_t* cluster, int32_t* per_sm);
 
 /* ------------------------------------------------------------------------ */
 /* Embedding                                                                */

@@ -52,6 +52,7 @@ EXPORTED = ("zero_init_layout", "zero_free_layout", "zero_shard_range", "zero_me
             "zero_last_cuda_error", "zero_last_cuda_error_string",
             "zero_adamw_plan", "zero_grad_norm", "zero_adamw_step",
             "zero_linear_plan", "zero_linear_workspace", "zero_linear_forward", "zero_linear_backward",
+            "zero_gated_workspace", "zero_gated_forward", "zero_gated_backward", "zero_gated_plan",
             "zero_embed_forward", "zero_embed_workspace", "zero_embed_backward",
             "zero_layernorm_forward", "zero_layernorm_workspace", "zero_layernorm_backward",
             "zero_distill_loss",
@@ -199,6 +200,16 @@ def lib() -> ctypes.CDLL:
     L.zero_linear_backward.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp,
                                        i64, i64, i64, i32, i32, vp, i64, vp]
     L.zero_linear_backward.restype = ctypes.c_int
+    L.zero_gated_workspace.argtypes = [i64, i64, i64, i32, i32, ctypes.POINTER(ctypes.c_int64)]
+    L.zero_gated_workspace.restype = ctypes.c_int
+    L.zero_gated_forward.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp, i64, vp, i64, i64,
+                                     i64, i64, i32, i32, vp, i64, vp]
+    L.zero_gated_forward.restype = ctypes.c_int
+    L.zero_gated_backward.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp,
+                                      i64, vp, i64, vp, vp, i64, i64, i64, i32, i32, vp, i64, vp]
+    L.zero_gated_backward.restype = ctypes.c_int
+    L.zero_gated_plan.argtypes = [i64, i64, i64, i32, i32p, i32p, i32p, i32p, i32p]
+    L.zero_gated_plan.restype = ctypes.c_int
     L.zero_embed_forward.argtypes = [vp, vp, i64, vp, i64, i64, i64, i64, f32, i32, vp]
     L.zero_embed_forward.restype = ctypes.c_int
     L.zero_embed_workspace.argtypes = [i64, i64, i64, ctypes.POINTER(ctypes.c_int64)]
@@ -619,6 +630,49 @@ def zero_linear_backward(dy, lddy: int, z, ldz: int, x, ldx: int, w, ldw: int, d
                                     _addr(workspace), workspace_bytes, _stream(stream))
     if rc:
         raise ZeroError(rc, "zero_linear_backward")
+
+
+def zero_gated_workspace(T: int, K: int, N: int, backward: bool, aligned: bool) -> int:
+    """Workspace bytes of a call of the gated projections (see include/zero_train.h)."""
+    n = ctypes.c_int64()
+    rc = lib().zero_gated_workspace(T, K, N, 1 if backward else 0, 1 if aligned else 0, ctypes.byref(n))
+    if rc:
+        raise ZeroError(rc, "zero_gated_workspace")
+    return n.value
+
+
+def zero_gated_forward(x, ldx: int, wg, ldwg: int, wu, ldwu: int, bg, bu, h, ldh: int, g, ldg: int, u,
+                       ldu: int, T: int, K: int, N: int, act: int, type: int, workspace=None,
+                       workspace_bytes: int = 0, stream=None) -> None:
+    """Enqueue h = act(x wg^T + bg) * (x wu^T + bu) (see include/zero_train.h)."""
+    rc = lib().zero_gated_forward(_addr(x), ldx, _addr(wg), ldwg, _addr(wu), ldwu, _addr(bg), _addr(bu),
+                                  _addr(h), ldh, _addr(g), ldg, _addr(u), ldu, T, K, N, act, type,
+                                  _addr(workspace), workspace_bytes, _stream(stream))
+    if rc:
+        raise ZeroError(rc, "zero_gated_forward")
+
+
+def zero_gated_backward(dh, lddh: int, g, ldg: int, u, ldu: int, x, ldx: int, wg, ldwg: int, wu,
+                        ldwu: int, dx, lddx: int, dwg, lddwg: int, dwu, lddwu: int, dbg, dbu, T: int,
+                        K: int, N: int, act: int, type: int, workspace=None, workspace_bytes: int = 0,
+                        stream=None) -> None:
+    """Enqueue the gradients of zero_gated_forward (see include/zero_train.h)."""
+    rc = lib().zero_gated_backward(_addr(dh), lddh, _addr(g), ldg, _addr(u), ldu, _addr(x), ldx,
+                                   _addr(wg), ldwg, _addr(wu), ldwu, _addr(dx), lddx, _addr(dwg), lddwg,
+                                   _addr(dwu), lddwu, _addr(dbg), _addr(dbu), T, K, N, act, type,
+                                   _addr(workspace), workspace_bytes, _stream(stream))
+    if rc:
+        raise ZeroError(rc, "zero_gated_backward")
+
+
+def zero_gated_plan(T: int, K: int, N: int, products: int) -> dict:
+    """The kernel the gated projections' products would take (0 forward, 1 dx,
+    2 dwg and dwu, 3 all): like zero_linear_plan (see include/zero_train.h)."""
+    v = [ctypes.c_int32() for _ in range(5)]
+    rc = lib().zero_gated_plan(T, K, N, products, *map(ctypes.byref, v))
+    if rc:
+        raise ZeroError(rc, "zero_gated_plan")
+    return dict(zip(("launches", "rows", "columns", "cluster", "per_sm"), (x.value for x in v)))
 
 
 def zero_embed_forward(ids, table, ldt: int, y, ldy: int, T: int, D: int, V: int, scale: float,

@@ -22,7 +22,7 @@ constexpr int kBK = 64;           // contraction per stage: 128 bytes, one swizz
 constexpr int kATile = kBM * kBK * 2;
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;
 
-__device__ unsigned int g_linear_timeouts;
+__device__ unsigned int g_gemm_timeouts;
 
 // Where and how a tile's results go.  swap: the tile's rows are the output's
 // columns.
@@ -57,7 +57,62 @@ struct GemmArgs {
     const float* sums;
     void* db;
     int chunks, n_db, bf16;
+    static constexpr int kTwin = 0;
 };
+
+// The gated projections.  Forward (kTwin 1): one product whose tile holds as
+// many columns (swapped: rows) of the gate as of the up projection, so that
+// both meet in one epilogue.  Backward (kTwin 2): dx, whose contraction runs
+// over the gate's features and then over the up projection's, and both dW.
+struct GatedProblem : Problem {
+    CUtensorMap a2, b2;  // forward: the up projection's weights; dx: those of the second part
+    CUtensorMap u;       // forward, pairs, where o.vec: like y and z (which holds the gate)
+    const void* bias2;
+    void* u_out;
+    long long ldu;
+    int wide_u;
+    int half;            // dx: blocks of the contraction in its first part, else 0
+    int second_a;        // dx: the operand of two parts is A
+};
+
+struct GatedArgs {
+    GatedProblem p;
+    int tiles;
+    static constexpr int kTwin = 1;
+};
+
+struct GatedBackArgs {
+    GatedProblem p[3];
+    int ends[2];         // tiles (clusters) up to the end of the first and of the second product
+    int tiles;
+    const float* sums;   // [chunks][n_db]: the gate's columns, then the up projection's
+    void* db;
+    void* db2;           // either may be null
+    int chunks, n_db, bf16;
+    static constexpr int kTwin = 2;
+};
+
+// The product that tile (cluster) t belongs to, and its place among that
+// product's.
+template <int COUNT> __device__ __forceinline__ const Problem& problem_of(const GemmArgs& args, int t, int* at)
+{
+    const bool second = COUNT == 2 && t >= args.tiles0;
+    *at = t - (second ? args.tiles0 : 0);
+    return args.p[COUNT == 1 ? 0 : second];
+}
+
+template <int COUNT> __device__ __forceinline__ const GatedProblem& problem_of(const GatedArgs& args, int t, int* at)
+{
+    *at = t;
+    return args.p;
+}
+
+template <int COUNT> __device__ __forceinline__ const GatedProblem& problem_of(const GatedBackArgs& args, int t, int* at)
+{
+    const int k = t < args.ends[0] ? 0 : t < args.ends[1] ? 1 : 2;
+    *at = t - (k ? args.ends[k - 1] : 0);
+    return args.p[k];
+}
 
 // ---------------------------------------------------------------------------
 // PTX
@@ -104,7 +159,7 @@ __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile 
         if (*abort) return false;
         if (global_ns() - t0 > kWaitLimitNs) break;
     }
-    if (atomicExch(const_cast<int*>(abort), 1) == 0) atomicAdd(&g_linear_timeouts, 1u);
+    if (atomicExch(const_cast<int*>(abort), 1) == 0) atomicAdd(&g_gemm_timeouts, 1u);
     return false;
 }
 
@@ -564,6 +619,21 @@ __device__ __forceinline__ void bias_sum(const GemmArgs& args, int lane)
     }
 }
 
+__device__ __forceinline__ void bias_sum(const GatedArgs&, int) {}
+
+// Both biases' gradients, one after the other in a row of sums.
+__device__ __forceinline__ void bias_sum(const GatedBackArgs& args, int lane)
+{
+    const int n = args.n_db / 2;
+    for (long long c = blockIdx.x * 32ll + lane; c < args.n_db; c += gridDim.x * 32ll) {
+        float s = 0.0f;
+#pragma unroll 16
+        for (int k = 0; k < args.chunks; ++k) s += args.sums[static_cast<long long>(k) * args.n_db + c];
+        void* db = c < n ? args.db : args.db2;
+        if (db) store16(db, c < n ? c : c - n, s, args.bf16);
+    }
+}
+
 // ---------------------------------------------------------------------------
 // Many tiles: persistent pairs of CTAs
 // ---------------------------------------------------------------------------
@@ -677,9 +747,147 @@ __device__ __forceinline__ void emit_block(const Problem& g, uint32_t acc, int r
     else emit_block_as<0>(g, acc, row0, rows, col, staging, lane, release);
 }
 
-template <int BN, int STAGES, int COUNT>
-__global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_pair_kernel(const __grid_constant__ GemmArgs args)
+// The gated projections' results: h = act(g) u, and g and u themselves where
+// they are kept.  One element, and eight neighbours.
+__device__ __forceinline__ void emit_gated(const GatedProblem& p, long long row, int col, float g, float u)
 {
+    const Out& o = p.o;
+    if (o.bias) g += load16(o.bias, col, o.bf16);
+    if (p.bias2) u += load16(p.bias2, col, o.bf16);
+    if (o.z) {
+        store16(o.z, row * o.ldz + col, g, o.bf16);
+        store16(p.u_out, row * p.ldu + col, u, o.bf16);
+    }
+    float v[1] = {g};
+    activate_all(v, o.act);
+    store16(o.y, row * o.ldy + col, v[0] * u, o.bf16);
+}
+
+__device__ __forceinline__ void emit_gated8(const GatedProblem& p, long long row, int col, float (&g)[8], float (&u)[8])
+{
+    const Out& o = p.o;
+    if (o.bias) add8(g, __ldg(reinterpret_cast<const uint4*>(at16(o.bias, 0, 0, col))), o.bf16);
+    if (p.bias2) add8(u, __ldg(reinterpret_cast<const uint4*>(at16(p.bias2, 0, 0, col))), o.bf16);
+    if (o.z) {
+        *reinterpret_cast<uint4*>(at16(o.z, o.ldz, row, col)) = pack8(g, o.bf16);
+        *reinterpret_cast<uint4*>(at16(p.u_out, p.ldu, row, col)) = pack8(u, o.bf16);
+    }
+    activate_all(g, o.act);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) g[j] *= u[j];
+    *reinterpret_cast<uint4*>(at16(o.y, o.ldy, row, col)) = pack8(g, o.bf16);
+}
+
+template <int BF16> __device__ __forceinline__ void add_bias_any(const void* bias, int vec, int col, int cols, float (&v)[32], int lane)
+{
+    if (!bias) return;
+    if (vec && cols == 32) {
+        const uint4* b = reinterpret_cast<const uint4*>(at16(bias, 0, 0, col));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) add8(v + 8 * q, __ldg(b + q), BF16);
+        return;
+    }
+    const float mine = lane < cols ? load16(bias, col + lane, BF16) : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] += __shfl_sync(0xffffffffu, mine, j);
+}
+
+// 32 x 32 results of a warp, lane l holding row row0 + l.
+template <int BF16>
+__device__ __forceinline__ void emit_gated_piece_as(const GatedProblem& p, long long row0, int rows, int col0, int cols, float (&g)[32],
+                                                    float (&u)[32], uint4* piece, int lane)
+{
+    const Out& o = p.o;
+    add_bias_any<BF16>(o.bias, o.vec, col0, cols, g, lane);
+    add_bias_any<BF16>(p.bias2, o.vec, col0, cols, u, lane);
+    auto put = [&](const float(&v)[32], void* to, long long ld, int wide) {
+        piece_row(piece, v, BF16, lane);
+        __syncwarp();
+        piece_out(piece, at16(to, ld, row0, col0), ld, rows, cols, wide, lane);
+        __syncwarp();
+    };
+    if (o.z) {
+        put(g, o.z, o.ldz, o.wide_z);
+        put(u, p.u_out, p.ldu, p.wide_u);
+    }
+    activate_all(g, o.act);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) g[j] *= u[j];
+    put(g, o.y, o.ldy, o.wide_y);
+}
+
+__device__ __forceinline__ void emit_gated_piece(const GatedProblem& p, long long row0, int rows, int col0, int cols, float (&g)[32],
+                                                 float (&u)[32], uint4* piece, int lane)
+{
+    if (p.o.bf16) emit_gated_piece_as<1>(p, row0, rows, col0, cols, g, u, piece, lane);
+    else emit_gated_piece_as<0>(p, row0, rows, col0, cols, g, u, piece, lane);
+}
+
+// 32 rows x 64 columns of a pair's tile, whole ones by TMA stores: the gate's
+// accumulators at `acc`, the up projection's BN / 2 columns on.  What is kept
+// is written first, each from the staging that the last store has left.
+template <int BN, int BF16, class Release>
+__device__ __forceinline__ void emit_gated_whole(const GatedProblem& p, uint32_t acc, int row0, int col, uint4* staging, int lane, Release release)
+{
+    const Out& o = p.o;
+    if (o.z) {
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) { // the gate, then the up projection
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+                float v[32];
+                tmem_load(acc + k * (BN / 2) + h * 32, v);
+                add_bias_any<BF16>(k ? p.bias2 : o.bias, 1, col + h * 32, 32, v, lane);
+                if (h == 0) staging_free();
+                stage_row<BF16>(staging, h, v, lane);
+            }
+            send_staging(k ? &p.u : &p.z, col, row0, staging);
+        }
+    }
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+        float g[32], u[32];
+        tmem_load(acc + h * 32, g);
+        tmem_load(acc + BN / 2 + h * 32, u);
+        if (h == 1) release();
+        add_bias_any<BF16>(o.bias, 1, col + h * 32, 32, g, lane);
+        add_bias_any<BF16>(p.bias2, 1, col + h * 32, 32, u, lane);
+        activate_all(g, o.act);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) g[j] *= u[j];
+        if (h == 0) staging_free();
+        stage_row<BF16>(staging, h, g, lane);
+    }
+    send_staging(&p.y, col, row0, staging);
+}
+
+template <int BN, class Release>
+__device__ __forceinline__ void emit_gated_block(const GatedProblem& p, uint32_t acc, int row0, int rows, int col, uint4* staging, int lane,
+                                                 Release release)
+{
+    if (p.o.vec && rows > 0 && col + 64 <= p.n) {
+        if (p.o.bf16) emit_gated_whole<BN, 1>(p, acc, row0, col, staging, lane, release);
+        else emit_gated_whole<BN, 0>(p, acc, row0, col, staging, lane, release);
+        return;
+    }
+    staging_free();
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+        const int cols = min(32, p.n - (col + h * 32));
+        if (rows > 0 && cols > 0) {
+            float g[32], u[32];
+            tmem_load(acc + h * 32, g);
+            tmem_load(acc + BN / 2 + h * 32, u);
+            emit_gated_piece(p, row0, rows, col + h * 32, cols, g, u, staging, lane);
+        }
+    }
+    release();
+}
+
+template <int BN, int STAGES, int COUNT, class Args>
+__global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_pair_kernel(const __grid_constant__ Args args)
+{
+    constexpr int kTwin = Args::kTwin;
     extern __shared__ unsigned char raw[];
     unsigned char* smem = aligned_smem(raw);
     __shared__ uint64_t full[STAGES], empty[STAGES], acc_full[2], acc_empty[2], drained;
@@ -716,10 +924,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_pair_kernel(const _
         int it = 0;
         bool ok = true;
         for (int t = pair; ok && t < args.tiles; t += pairs) {
-            const Problem& g = args.p[COUNT == 1 ? 0 : t >= args.tiles0];
-            int mt, nt;
-            tile_at(g, COUNT == 2 && t >= args.tiles0 ? t - args.tiles0 : t, &mt, &nt);
-            const int m0 = mt * 256 + rank * kBM, n0 = nt * BN + rank * (BN / 2);
+            int at, mt, nt;
+            const auto& g = problem_of<COUNT>(args, t, &at);
+            tile_at(g, at, &mt, &nt);
+            // a tile of the gated projections has half of its columns from either of them, a CTA's half each
+            const int m0 = mt * 256 + rank * kBM, n0 = kTwin == 1 ? nt * (BN / 2) : nt * BN + rank * (BN / 2);
             for (int kb = 0; kb < g.kblocks; ++kb, ++it) {
                 const int s = it % STAGES;
                 if (!wait(&empty[s], ((it / STAGES) & 1) ^ 1, abort)) {
@@ -731,6 +940,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_pair_kernel(const _
                 if (rank == 0) mbar_expect(&full[s], 2 * kPairStage<BN>);
                 unsigned char* sa = smem + s * kPairStage<BN>;
                 unsigned char* sb = sa + kATile;
+                const CUtensorMap* map_b = &g.b;
+                int k = kb * kBK; // of B: the weights' two parts start at their own 0, dz has them side by side
+                if constexpr (kTwin == 1) {
+                    if (rank) map_b = &g.b2;
+                } else if constexpr (kTwin == 2) {
+                    if (g.half && kb >= g.half) map_b = &g.b2, k -= g.half * kBK;
+                }
                 if (g.a_mn == 2) {
                     tma_load_pair3(sa, &g.a, kb * kBK, m0 / 64, bar);
                 } else if (g.a_mn) {
@@ -740,12 +956,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_pair_kernel(const _
                     tma_load_pair(sa, &g.a, kb * kBK, m0, bar);
                 }
                 if (g.b_mn == 2) {
-                    tma_load_pair3(sb, &g.b, kb * kBK, n0 / 64, bar);
+                    tma_load_pair3(sb, map_b, k, n0 / 64, bar);
                 } else if (g.b_mn) {
 #pragma unroll
-                    for (int i = 0; i < BN / 128; ++i) tma_load_pair(sb + i * 8192, &g.b, n0 + i * 64, kb * kBK, bar);
+                    for (int i = 0; i < BN / 128; ++i) tma_load_pair(sb + i * 8192, map_b, n0 + i * 64, k, bar);
                 } else {
-                    tma_load_pair(sb, &g.b, kb * kBK, n0, bar);
+                    tma_load_pair(sb, map_b, k, n0, bar);
                 }
             }
         }
@@ -756,7 +972,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_pair_kernel(const _
         int it = 0, n = 0;
         bool ok = true;
         for (int t = pair; ok && t < args.tiles; t += pairs, ++n) {
-            const Problem& g = args.p[COUNT == 1 ? 0 : t >= args.tiles0];
+            int at;
+            const auto& g = problem_of<COUNT>(args, t, &at);
             const int acc = n & 1, kblocks = g.kblocks;
             const uint64_t da = g.a_mn ? 2048 >> 4 : 32 >> 4, db = g.b_mn ? 2048 >> 4 : 32 >> 4;
             const uint64_t a0 = tile_desc(smem, g.a_mn), b0 = tile_desc(smem + kATile, g.b_mn);
@@ -789,9 +1006,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_pair_kernel(const _
         uint4* staging = reinterpret_cast<uint4*>(smem + STAGES * kPairStage<BN> + (warp - 4) * kStoreBytes);
         int n = 0;
         for (int t = pair; t < args.tiles; t += pairs, ++n) {
-            const Problem& g = args.p[COUNT == 1 ? 0 : t >= args.tiles0];
-            int mt, nt;
-            tile_at(g, COUNT == 2 && t >= args.tiles0 ? t - args.tiles0 : t, &mt, &nt);
+            int place, mt, nt;
+            const auto& g = problem_of<COUNT>(args, t, &place);
+            tile_at(g, place, &mt, &nt);
             const int acc = n & 1;
             const bool ok = wait(&acc_full[acc], (n >> 1) & 1, abort);
             if (!__all_sync(0xffffffffu, ok)) break;
@@ -803,8 +1020,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1) zero_gemm_pair_kernel(const _
                 __syncwarp();
                 if (lane == 0) mbar_arrive_at(peer_addr(smem_addr(&acc_empty[acc]), 0));
             };
+            if constexpr (kTwin == 1) {
+                // columns [64 h, 64 h + 64) of both halves, h = 0, 1
+                const int c = c0 / 2;
+                emit_gated_block<BN>(g, base + acc * BN + c + (static_cast<uint32_t>(q * 32) << 16), row0, rows, nt * (BN / 2) + c, staging,
+                                     lane, release);
+            }
 #pragma unroll 1
-            for (int c = c0; c < c0 + BN / 2; c += 64) {
+            for (int c = kTwin == 1 ? c0 + BN / 2 : c0; c < c0 + BN / 2; c += 64) {
                 const bool last = c + 64 == c0 + BN / 2;
                 const uint32_t at = base + acc * BN + c + (static_cast<uint32_t>(q * 32) << 16);
                 const int col = nt * BN + c;
@@ -920,6 +1143,42 @@ template <int PARTS> __device__ __forceinline__ void join(const Out& o, const Jo
     }
 }
 
+// The same for the gated projections, whose two sums of an element lie `up`
+// floats apart in a partial tile.
+template <int PARTS> __device__ __forceinline__ void join_gated(const GatedProblem& p, const Join& j, int up)
+{
+    const int vecs = p.o.vec ? j.fast / 8 : 0;
+    for (int e = j.self; e < vecs * j.slow; e += j.everyone) {
+        const int s = e / vecs, f = (e - s * vecs) * 8;
+        const uint32_t at = j.part + static_cast<uint32_t>(s * j.pitch + f) * 4;
+        float g[8], u[8];
+#pragma unroll
+        for (int h = 0; h < 8; ++h) g[h] = u[h] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float4 a = peer_load4(at + h * 16, j.first + k), b = peer_load4(at + up * 4 + h * 16, j.first + k);
+                g[4 * h] += a.x, g[4 * h + 1] += a.y, g[4 * h + 2] += a.z, g[4 * h + 3] += a.w;
+                u[4 * h] += b.x, u[4 * h + 1] += b.y, u[4 * h + 2] += b.z, u[4 * h + 3] += b.w;
+            }
+        }
+        emit_gated8(p, j.row0 + s, j.col0 + f, g, u);
+    }
+    const int left = j.fast - vecs * 8;
+    for (int e = j.self; e < left * j.slow; e += j.everyone) {
+        const int s = e / left, f = e - s * left + vecs * 8;
+        const uint32_t at = j.part + static_cast<uint32_t>(s * j.pitch + f) * 4;
+        float g = 0.0f, u = 0.0f;
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k) {
+            g += peer_load(at, j.first + k);
+            u += peer_load(at + up * 4, j.first + k);
+        }
+        emit_gated(p, j.row0 + s, j.col0 + f, g, u);
+    }
+}
+
 // Bound by the reads of the weights with few tokens (4 tokens, 2048 -> 8192, bf16,
 // 33.6 MB, launch included: 9.2 us from HBM, 16 weights in turn, 3650 GB/s; 7.0 us
 // from L2, one weight again and again), by latency in between: launch, first
@@ -932,9 +1191,10 @@ template <int BN, int PER_SM> constexpr int kSplitThreads = PER_SM == 2 ? 256 : 
 template <int BN, int PER_SM> constexpr int kSplitStages = PER_SM == 1 ? (BN >= 128 ? 6 : 8) : BN >= 64 ? 4 : BN >= 32 ? 5 : 6;
 template <int BN, int PER_SM> constexpr int kSplitSmem = kSplitStages<BN, PER_SM> * kStageBytes<BN> + 1024;
 
-template <int BN, int PER_SM, int COUNT>
-__global__ void __launch_bounds__((kSplitThreads<BN, PER_SM>), PER_SM) zero_gemm_split_kernel(const __grid_constant__ GemmArgs args)
+template <int BN, int PER_SM, int COUNT, class Args>
+__global__ void __launch_bounds__((kSplitThreads<BN, PER_SM>), PER_SM) zero_gemm_split_kernel(const __grid_constant__ Args args)
 {
+    constexpr int kTwin = Args::kTwin;
     constexpr int STAGES = kSplitStages<BN, PER_SM>, kThreads = kSplitThreads<BN, PER_SM>;
     extern __shared__ unsigned char raw[];
     unsigned char* smem = aligned_smem(raw);
@@ -945,9 +1205,11 @@ __global__ void __launch_bounds__((kSplitThreads<BN, PER_SM>), PER_SM) zero_gemm
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31; // warp: uniform
     const int rank = static_cast<int>(cluster_rank()), size = static_cast<int>(cluster_size());
     const int cluster = blockIdx.x / size;
-    const bool second = COUNT == 2 && cluster >= args.tiles0;
-    const Problem& g = args.p[COUNT == 1 ? 0 : second];
-    const int at = cluster - (second ? args.tiles0 : 0), t = g.cut ? at : at * size + rank;
+    int at;
+    const auto& g = problem_of<COUNT>(args, cluster, &at);
+    const int t = g.cut ? at : at * size + rank;
+    // extents of a tile in the output: half of the gated projections' features
+    const int tile_m = kTwin == 1 && g.o.swap ? kBM / 2 : kBM, tile_n = kTwin == 1 && !g.o.swap ? BN / 2 : BN;
     const bool idle = t >= g.tiles_m * g.tiles_n; // the last cluster may have CTAs without a tile
     int mt, nt;
     tile_at(g, idle ? 0 : t, &mt, &nt);
@@ -986,21 +1248,36 @@ __global__ void __launch_bounds__((kSplitThreads<BN, PER_SM>), PER_SM) zero_gemm
             mbar_expect(&full[s], kStageBytes<BN>);
             unsigned char* sa = smem + s * kStageBytes<BN>;
             unsigned char* sb = sa + kATile;
+            if constexpr (kTwin == 1) { // the gate's features and the up projection's in one operand
+                tma_load(sa, &g.a, kb * kBK, mt * tile_m, &full[s]);
+                if (g.o.swap) tma_load(sa + kATile / 2, &g.a2, kb * kBK, mt * tile_m, &full[s]);
+                tma_load(sb, &g.b, kb * kBK, nt * tile_n, &full[s]);
+                if (!g.o.swap) tma_load(sb + BN / 2 * kBK * 2, &g.b2, kb * kBK, nt * tile_n, &full[s]);
+                continue;
+            }
+            const CUtensorMap *map_a = &g.a, *map_b = &g.b;
+            int ka = kb * kBK, kbb = kb * kBK;
+            if constexpr (kTwin == 2) { // the weights' second part starts at its own 0
+                if (g.half && kb >= g.half) {
+                    if (g.second_a) map_a = &g.a2, ka -= g.half * kBK;
+                    else map_b = &g.b2, kbb -= g.half * kBK;
+                }
+            }
             if (g.a_mn == 2) {
-                tma_load3(sa, &g.a, kb * kBK, mt * (kBM / 64), &full[s]);
+                tma_load3(sa, map_a, ka, mt * (kBM / 64), &full[s]);
             } else if (g.a_mn) {
-                tma_load(sa, &g.a, mt * kBM, kb * kBK, &full[s]);
-                tma_load(sa + 8192, &g.a, mt * kBM + 64, kb * kBK, &full[s]);
+                tma_load(sa, map_a, mt * kBM, ka, &full[s]);
+                tma_load(sa + 8192, map_a, mt * kBM + 64, ka, &full[s]);
             } else {
-                tma_load(sa, &g.a, kb * kBK, mt * kBM, &full[s]);
+                tma_load(sa, map_a, ka, mt * kBM, &full[s]);
             }
             if (BN >= 64 && g.b_mn == 2) {
-                tma_load3(sb, &g.b, kb * kBK, nt * (BN / 64), &full[s]);
+                tma_load3(sb, map_b, kbb, nt * (BN / 64), &full[s]);
             } else if (BN >= 64 && g.b_mn) {
 #pragma unroll
-                for (int i = 0; i < BN / 64; ++i) tma_load(sb + i * 8192, &g.b, nt * BN + i * 64, kb * kBK, &full[s]);
+                for (int i = 0; i < BN / 64; ++i) tma_load(sb + i * 8192, map_b, nt * BN + i * 64, kbb, &full[s]);
             } else {
-                tma_load(sb, &g.b, kb * kBK, nt * BN, &full[s]);
+                tma_load(sb, map_b, kbb, nt * BN, &full[s]);
             }
         }
         if (!ok)
@@ -1034,7 +1311,7 @@ __global__ void __launch_bounds__((kSplitThreads<BN, PER_SM>), PER_SM) zero_gemm
     __syncwarp();
     // The stages are free once the last product is done.
     const Out& o = g.o;
-    const int rows = idle ? 0 : min(kBM, g.m - mt * kBM), cols = min(BN, g.n - nt * BN);
+    const int rows = idle ? 0 : min(tile_m, g.m - mt * tile_m), cols = min(tile_n, g.n - nt * tile_n);
     float* part = reinterpret_cast<float*>(smem);
     const int pitch = (o.swap ? kBM : BN) + 4; // floats; 16-byte accesses free of bank conflicts
     const bool direct = BN >= 64 && parts == 1 && !o.swap; // nothing to join: straight from tensor memory
@@ -1049,8 +1326,21 @@ __global__ void __launch_bounds__((kSplitThreads<BN, PER_SM>), PER_SM) zero_gemm
             const int row = q * 32 + lane;
             const uint32_t acc = base + (static_cast<uint32_t>(q * 32) << 16);
             constexpr int kStep = BN < 32 ? 16 : 32;
+            if constexpr (kTwin == 1 && BN >= 64) {
+                if (direct) { // 32 columns of both at a time
 #pragma unroll 1
-            for (int c = c0; c < c0 + kSpan; c += kStep) {
+                    for (int c = ((warp - 4) >> 2) * 32; c < BN / 2; c += kThreads == 384 ? 64 : 32) {
+                        if (q * 32 >= rows || c >= cols) continue;
+                        float v[32], u[32];
+                        tmem_load(acc + c, v);
+                        tmem_load(acc + BN / 2 + c, u);
+                        emit_gated_piece(g, mt * kBM + q * 32, min(32, rows - q * 32), nt * tile_n + c, min(32, cols - c), v, u,
+                                         reinterpret_cast<uint4*>(smem + (warp - 4) * kPieceBytes), lane);
+                    }
+                }
+            }
+#pragma unroll 1
+            for (int c = kTwin == 1 && direct ? BN : c0; c < c0 + kSpan; c += kStep) {
                 float v[kStep];
                 if constexpr (kStep == 16) tmem_load16(acc, v);
                 else tmem_load(acc + c, v);
@@ -1085,16 +1375,26 @@ __global__ void __launch_bounds__((kSplitThreads<BN, PER_SM>), PER_SM) zero_gemm
         j.pitch = pitch;
         j.fast = o.swap ? rows : cols; // extents along and across the output's rows
         j.slow = o.swap ? cols : rows;
-        j.row0 = o.swap ? nt * BN : mt * kBM;
-        j.col0 = o.swap ? mt * kBM : nt * BN;
+        j.row0 = o.swap ? nt * tile_n : mt * tile_m;
+        j.col0 = o.swap ? mt * tile_m : nt * tile_n;
         j.first = g.cut ? 0 : static_cast<uint32_t>(rank);
         j.self = (g.cut ? rank * kThreads : 0) + static_cast<int>(threadIdx.x);
         j.everyone = (g.cut ? size : 1) * kThreads;
-        switch (parts) {
-        case 1: join<1>(o, j); break;
-        case 2: join<2>(o, j); break;
-        case 4: join<4>(o, j); break;
-        default: join<8>(o, j); break;
+        if constexpr (kTwin == 1) {
+            const int up = o.swap ? kBM / 2 : BN / 2; // from the gate's to the up projection's, in floats
+            switch (parts) {
+            case 1: join_gated<1>(g, j, up); break;
+            case 2: join_gated<2>(g, j, up); break;
+            case 4: join_gated<4>(g, j, up); break;
+            default: join_gated<8>(g, j, up); break;
+            }
+        } else {
+            switch (parts) {
+            case 1: join<1>(o, j); break;
+            case 2: join<2>(o, j); break;
+            case 4: join<4>(o, j); break;
+            default: join<8>(o, j); break;
+            }
         }
     }
     cluster_sync(); // peers have read this CTA's part
@@ -1180,13 +1480,13 @@ inline int make_map(CUtensorMap* map, const Matrix& x, int mn, int extent)
     return r == CUDA_SUCCESS ? ZERO_OK : zero_record_cuda_error(static_cast<int>(cudaErrorInvalidValue));
 }
 
-using GemmKernel = void (*)(GemmArgs);
+template <class Args> using GemmKernel = void (*)(Args);
 
 // Dynamic shared memory above 48 KB is allowed once per kernel and device.
-inline int allow_smem(GemmKernel fn, int bytes)
+inline int allow_smem(const void* fn, int bytes)
 {
     static std::mutex mu;
-    static struct { int dev; GemmKernel fn; } known[64];
+    static struct { int dev; const void* fn; } known[64];
     static int n_known = 0;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1210,11 +1510,12 @@ struct Product {
     int a_mn, b_mn;
     int64_t m, n, k;
     Out o;
+    int twin;            // the gated projections: a tile's features are half of the one's, half of the other's
 };
 
 inline Product product(const Matrix& a, int a_mn, const Matrix& b, int b_mn, const Out& o)
 {
-    return {a, b, a_mn, b_mn, a_mn ? a.cols : a.rows, b_mn ? b.cols : b.rows, a_mn ? a.rows : a.cols, o};
+    return {a, b, a_mn, b_mn, a_mn ? a.cols : a.rows, b_mn ? b.cols : b.rows, a_mn ? a.rows : a.cols, o, 0};
 }
 
 // Which kernel takes a launch, with what tile.
@@ -1232,8 +1533,9 @@ struct BiasSum {
 
 inline int64_t tiles_of(const Product& p, const Variant& v)
 {
-    const int64_t bm = v.pair ? 256 : kBM;
-    return ((p.m + bm - 1) / bm) * ((p.n + v.bn - 1) / v.bn);
+    int64_t bm = v.pair ? 256 : kBM, bn = v.bn;
+    if (p.twin) (p.o.swap ? bm : bn) /= 2;
+    return ((p.m + bm - 1) / bm) * ((p.n + bn - 1) / bn);
 }
 
 inline int64_t kblocks_of(const Product& p) { return (p.k + kBK - 1) / kBK; }
@@ -1266,7 +1568,7 @@ inline Variant choose(const Product* p, int count, int sms, double* estimate)
     bool swapped = false;
     for (int k = 0; k < count; ++k) {
         int bn = p[k].b_mn ? 64 : 16;
-        while (bn < 128 && bn < p[k].n) bn *= 2;
+        while (bn < 128 && bn < (p[k].twin && !p[k].o.swap ? 2 * p[k].n : p[k].n)) bn *= 2;
         widest = std::max(widest, bn);
         swapped = swapped || p[k].o.swap;
     }
@@ -1305,90 +1607,24 @@ inline Variant choose(const Product* p, int count, int sms, double* estimate)
     return out;
 }
 
-// Whether the gradients' two products go into launches of their own: where
-// they want tiles of different shapes, one launch is not always the quicker
-// form (64 tokens, 2048 -> 2048: 10 us in one, 24 in two; 4 tokens, 2048 ->
-// 8192: 30 in one, 27 in two).
-inline bool apart(const Product* p, int sms)
-{
-    double one, first, second;
-    choose(p, 2, sms, &one);
-    choose(p, 1, sms, &first);
-    choose(p + 1, 1, sms, &second);
-    return first + second < one;
-}
+// The split kernel of a variant.
+template <class Args> struct SplitPick {
+    GemmKernel<Args> fn;
+    int smem, threads;
+};
 
-// One or two products in one launch, and the bias gradient's last sum.
-inline int gemm(const Product* p, int count, int type, const BiasSum* bias, cudaStream_t stream)
+template <int COUNT, class Args> SplitPick<Args> pick_split(const Variant& v)
 {
-    int sms = 0;
-    int rc = sm_count(&sms);
-    if (rc) return rc;
-    double estimate;
-    const Variant v = choose(p, count, sms, &estimate);
-    GemmArgs args{};
-    int64_t tiles = 0;
-    const unsigned int t = type == ZERO_TYPE_BF16 ? 1 : 0;
-    for (int k = 0; k < count; ++k) {
-        Problem& g = args.p[k];
-        const int bm = v.pair ? 256 : kBM, b_rows = v.pair ? v.bn / 2 : v.bn;
-        g.o = p[k].o;
-        g.o.wide_y = widest_access(g.o.y, g.o.ldy);
-        g.o.wide_z = widest_access(g.o.z, g.o.ldz);
-        g.o.wide_r = widest_access(g.o.res, g.o.ldr);
-        g.o.bf16 = type == ZERO_TYPE_BF16;
-        g.a_mn = p[k].a_mn ? (p[k].a.cols % 64 == 0 ? 2 : 1) : 0;
-        g.b_mn = p[k].b_mn ? (p[k].b.cols % 64 == 0 ? 2 : 1) : 0;
-        g.m = static_cast<int>(p[k].m);
-        g.n = static_cast<int>(p[k].n);
-        g.tiles_m = static_cast<int>((p[k].m + bm - 1) / bm);
-        g.tiles_n = static_cast<int>((p[k].n + v.bn - 1) / v.bn);
-        g.kblocks = static_cast<int>(kblocks_of(p[k]));
-        g.cut = is_cut(p[k], v);
-        g.idesc = (1u << 4) | (t << 7) | (t << 10) | (static_cast<unsigned int>(g.a_mn != 0) << 15) |
-                  (static_cast<unsigned int>(g.b_mn != 0) << 16) | (static_cast<unsigned int>(v.bn >> 3) << 17) |
-                  (static_cast<unsigned int>(bm >> 4) << 24);
-        if ((rc = make_map(&g.a, p[k].a, g.a_mn, g.a_mn == 2 ? kBM / 64 : g.a_mn ? 64 : kBM))) return rc;
-        if ((rc = make_map(&g.b, p[k].b, g.b_mn, g.b_mn == 2 ? b_rows / 64 : g.b_mn ? 64 : b_rows))) return rc;
-        if (v.pair && g.o.vec) {
-            if ((rc = make_map(&g.y, Matrix{g.o.y, g.o.ldy, p[k].m, p[k].n}, 0, 32))) return rc;
-            if (g.o.z && (rc = make_map(&g.z, Matrix{g.o.z, g.o.ldz, p[k].m, p[k].n}, 0, 32))) return rc;
-        }
-        if (tiles_of(p[k], v) > INT32_MAX - 64) return ZERO_EINVAL;
-        tiles += clusters_of(p[k], v);
-        if (tiles * v.parts > INT32_MAX) return ZERO_EINVAL;
-        if (k == 0) args.tiles0 = static_cast<int>(tiles);
-    }
-    args.tiles = static_cast<int>(tiles);
-    if (bias) {
-        args.sums = bias->sums;
-        args.db = bias->db;
-        args.chunks = bias->chunks;
-        args.n_db = bias->n;
-        args.bf16 = type == ZERO_TYPE_BF16;
-    }
-    if (v.pair) {
-        GemmKernel fn = count == 1 ? zero_gemm_pair_kernel<256, kPairStages<256>, 1> : zero_gemm_pair_kernel<256, kPairStages<256>, 2>;
-        if ((rc = allow_smem(fn, kPairSmem<256>))) return rc;
-        return launch_after(fn, args, 2 * std::min<int64_t>(tiles, sms / 2), kGemmThreads, kPairSmem<256>, 2, stream);
-    }
-    GemmKernel fn = nullptr;
-    int smem = 0;
-    int threads = 0;
-    auto pick = [&](auto columns, auto per_sm) {
+    auto pick = [](auto columns, auto per_sm) -> SplitPick<Args> {
         constexpr int BN = decltype(columns)::value, PER = decltype(per_sm)::value;
-        fn = count == 1 ? zero_gemm_split_kernel<BN, PER, 1> : zero_gemm_split_kernel<BN, PER, 2>;
-        smem = kSplitSmem<BN, PER>;
-        threads = kSplitThreads<BN, PER>;
+        return {zero_gemm_split_kernel<BN, PER, COUNT, Args>, kSplitSmem<BN, PER>, kSplitThreads<BN, PER>};
     };
     using std::integral_constant;
-    if (v.bn == 16) pick(integral_constant<int, 16>{}, integral_constant<int, 2>{});
-    else if (v.bn == 32) pick(integral_constant<int, 32>{}, integral_constant<int, 2>{});
-    else if (v.bn == 64 && v.per_sm == 2) pick(integral_constant<int, 64>{}, integral_constant<int, 2>{});
-    else if (v.bn == 64) pick(integral_constant<int, 64>{}, integral_constant<int, 1>{});
-    else pick(integral_constant<int, 128>{}, integral_constant<int, 1>{});
-    if ((rc = allow_smem(fn, smem))) return rc;
-    return launch_after(fn, args, tiles * v.parts, threads, smem, v.parts, stream);
+    if (v.bn == 16) return pick(integral_constant<int, 16>{}, integral_constant<int, 2>{});
+    if (v.bn == 32) return pick(integral_constant<int, 32>{}, integral_constant<int, 2>{});
+    if (v.bn == 64 && v.per_sm == 2) return pick(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+    if (v.bn == 64) return pick(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+    return pick(integral_constant<int, 128>{}, integral_constant<int, 1>{});
 }
 
 // Up to this many tokens a tile's rows are features (y) or inputs (dx), its columns tokens.

@@ -28,6 +28,8 @@
 
 // Defined in adamw.cu (not exported): the step's part of zero_train_timeouts.
 __attribute__((visibility("hidden"))) int zero_adamw_wait_timeouts(unsigned int* count, int reset);
+// Defined in gated.cu (not exported): the gated projections' part.
+__attribute__((visibility("hidden"))) int zero_gated_wait_timeouts(unsigned int* count, int reset);
 
 namespace {
 
@@ -159,6 +161,79 @@ PrepKernel pick_prep(int act, int type)
     case ZERO_ACT_SILU: return b ? zero_linear_prep_kernel<ZERO_ACT_SILU, 1> : zero_linear_prep_kernel<ZERO_ACT_SILU, 0>;
     default: return b ? zero_linear_prep_kernel<ZERO_ACT_NONE, 1> : zero_linear_prep_kernel<ZERO_ACT_NONE, 0>;
     }
+}
+
+// Whether the gradients' two products go into launches of their own: where
+// they want tiles of different shapes, one launch is not always the quicker
+// form (64 tokens, 2048 -> 2048: 10 us in one, 24 in two; 4 tokens, 2048 ->
+// 8192: 30 in one, 27 in two).
+bool apart(const Product* p, int sms)
+{
+    double one, first, second;
+    choose(p, 2, sms, &one);
+    choose(p, 1, sms, &first);
+    choose(p + 1, 1, sms, &second);
+    return first + second < one;
+}
+
+// One or two products in one launch, and the bias gradient's last sum.
+int gemm(const Product* p, int count, int type, const BiasSum* bias, cudaStream_t stream)
+{
+    int sms = 0;
+    int rc = sm_count(&sms);
+    if (rc) return rc;
+    double estimate;
+    const Variant v = choose(p, count, sms, &estimate);
+    GemmArgs args{};
+    int64_t tiles = 0;
+    const unsigned int t = type == ZERO_TYPE_BF16 ? 1 : 0;
+    for (int k = 0; k < count; ++k) {
+        Problem& g = args.p[k];
+        const int bm = v.pair ? 256 : kBM, b_rows = v.pair ? v.bn / 2 : v.bn;
+        g.o = p[k].o;
+        g.o.wide_y = widest_access(g.o.y, g.o.ldy);
+        g.o.wide_z = widest_access(g.o.z, g.o.ldz);
+        g.o.wide_r = widest_access(g.o.res, g.o.ldr);
+        g.o.bf16 = type == ZERO_TYPE_BF16;
+        g.a_mn = p[k].a_mn ? (p[k].a.cols % 64 == 0 ? 2 : 1) : 0;
+        g.b_mn = p[k].b_mn ? (p[k].b.cols % 64 == 0 ? 2 : 1) : 0;
+        g.m = static_cast<int>(p[k].m);
+        g.n = static_cast<int>(p[k].n);
+        g.tiles_m = static_cast<int>((p[k].m + bm - 1) / bm);
+        g.tiles_n = static_cast<int>((p[k].n + v.bn - 1) / v.bn);
+        g.kblocks = static_cast<int>(kblocks_of(p[k]));
+        g.cut = is_cut(p[k], v);
+        g.idesc = (1u << 4) | (t << 7) | (t << 10) | (static_cast<unsigned int>(g.a_mn != 0) << 15) |
+                  (static_cast<unsigned int>(g.b_mn != 0) << 16) | (static_cast<unsigned int>(v.bn >> 3) << 17) |
+                  (static_cast<unsigned int>(bm >> 4) << 24);
+        if ((rc = make_map(&g.a, p[k].a, g.a_mn, g.a_mn == 2 ? kBM / 64 : g.a_mn ? 64 : kBM))) return rc;
+        if ((rc = make_map(&g.b, p[k].b, g.b_mn, g.b_mn == 2 ? b_rows / 64 : g.b_mn ? 64 : b_rows))) return rc;
+        if (v.pair && g.o.vec) {
+            if ((rc = make_map(&g.y, Matrix{g.o.y, g.o.ldy, p[k].m, p[k].n}, 0, 32))) return rc;
+            if (g.o.z && (rc = make_map(&g.z, Matrix{g.o.z, g.o.ldz, p[k].m, p[k].n}, 0, 32))) return rc;
+        }
+        if (tiles_of(p[k], v) > INT32_MAX - 64) return ZERO_EINVAL;
+        tiles += clusters_of(p[k], v);
+        if (tiles * v.parts > INT32_MAX) return ZERO_EINVAL;
+        if (k == 0) args.tiles0 = static_cast<int>(tiles);
+    }
+    args.tiles = static_cast<int>(tiles);
+    if (bias) {
+        args.sums = bias->sums;
+        args.db = bias->db;
+        args.chunks = bias->chunks;
+        args.n_db = bias->n;
+        args.bf16 = type == ZERO_TYPE_BF16;
+    }
+    if (v.pair) {
+        GemmKernel<GemmArgs> fn = count == 1 ? zero_gemm_pair_kernel<256, kPairStages<256>, 1, GemmArgs>
+                                             : zero_gemm_pair_kernel<256, kPairStages<256>, 2, GemmArgs>;
+        if ((rc = allow_smem(reinterpret_cast<const void*>(fn), kPairSmem<256>))) return rc;
+        return launch_after(fn, args, 2 * std::min<int64_t>(tiles, sms / 2), kGemmThreads, kPairSmem<256>, 2, stream);
+    }
+    const SplitPick<GemmArgs> k = count == 1 ? pick_split<1, GemmArgs>(v) : pick_split<2, GemmArgs>(v);
+    if ((rc = allow_smem(reinterpret_cast<const void*>(k.fn), k.smem))) return rc;
+    return launch_after(k.fn, args, tiles * v.parts, k.threads, k.smem, v.parts, stream);
 }
 
 } // namespace
@@ -358,15 +433,16 @@ extern "C" int zero_train_timeouts(int64_t* count, int32_t reset)
 {
     if (!count) return ZERO_EINVAL;
     unsigned int n = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(&n, g_linear_timeouts, sizeof(n));
+    cudaError_t e = cudaMemcpyFromSymbol(&n, g_gemm_timeouts, sizeof(n));
     if (e == cudaSuccess && reset) {
         const unsigned int zero = 0;
-        e = cudaMemcpyToSymbol(g_linear_timeouts, &zero, sizeof(zero));
+        e = cudaMemcpyToSymbol(g_gemm_timeouts, &zero, sizeof(zero));
     }
     if (e != cudaSuccess) return record(e);
-    unsigned int steps = 0;
-    const int rc = zero_adamw_wait_timeouts(&steps, reset);
+    unsigned int steps = 0, gated = 0;
+    int rc = zero_adamw_wait_timeouts(&steps, reset);
+    if (!rc) rc = zero_gated_wait_timeouts(&gated, reset);
     if (rc) return rc;
-    *count = static_cast<int64_t>(n) + steps;
+    *count = static_cast<int64_t>(n) + steps + gated;
     return ZERO_OK;
 }
