@@ -95,7 +95,7 @@ def test_forward(z, T, K, N, act, ty, pad, shift):
 
 
 MANY = [(5000, 200, 500, 0), (4993, 1000, 555, 8), (6000, 72, 1027, 0), (2500, 520, 1300, 3), (20000, 64, 256, 0), (4096, 1024, 2050, 0), (3000, 256, 1600, 0)]
-WIDE = [(5, 2048, 4096), (30, 2048, 2048), (60, 2048, 2000), (128, 2048, 4096), (250, 2048, 2048), (200, 200, 9000), (400, 320, 4096), (1024, 1024, 1024), (512, 2048, 1024)]
+WIDE = [(5, 2048, 4096), (30, 2048, 2048), (60, 2048, 2000), (128, 2048, 4096), (250, 2048, 2048), (200, 200, 9000), (400, 320, 4096), (1024, 1024, 1024), (512, 2048, 1024), (2048, 512, 512), (2000, 512, 500)]
 
 
 @pytest.mark.parametrize("T,K,N,pad", MANY)
