@@ -8,11 +8,14 @@
 // values, so that a call repeats its bits.  The tokens are sorted by id with a
 // stable radix sort (9 bits a pass: two passes up to 2^18 ids; a block ranks
 // its tokens by the lanes' matching digits and finds its place from the blocks'
-// digit counts).  Then warps walk over the sorted tokens, a chunk of them and a
-// stripe of 256 columns each, adding rows of dy in registers; a run of equal
-// ids that lies in one chunk is written at once, the parts of a longer one go
-// to the workspace in fp32 and are added in order by a last launch.  However
-// often an id occurs, no warp has more than a chunk of rows to read.
+// digit counts): up to 65536 tokens by one cluster of eight CTAs, which
+// exchange counts and tokens through distributed shared memory while the other
+// SMs clear the first rows of the table, more by a launch per pass.  Then
+// warps walk over the sorted tokens, a chunk of them and a stripe of 256
+// columns each, adding rows of dy in registers; a run of equal ids that lies in
+// one chunk is written at once, the parts of a longer one go to the workspace
+// in fp32 and are added in order by a last launch.  However often an id occurs,
+// no warp has more than a chunk of rows to read.
 #include "layers.cuh"
 
 namespace {
@@ -189,6 +192,141 @@ template <int ROUNDS> __global__ void __launch_bounds__(kSortThreads) zero_sort_
     }
 }
 
+// The whole sort by one cluster: a CTA holds every eighth part of the order in
+// its shared memory, a thread ROUNDS tokens in registers.  Per pass the CTAs
+// rank their tokens, read each other's digit counts, and write the tokens to
+// their places in each other's memory.  The clusters behind the first one
+// write zeros to the table's first `clear` rows meanwhile.
+constexpr int kCluster = 8, kClusterThreads = 1024, kClusterWarps = kClusterThreads / 32;
+
+template <int ROUNDS> constexpr int kClusterSortSmem = ROUNDS * kClusterThreads * 8 + kClusterWarps * kDigits * 2 + 2 * kDigits * 4;
+
+struct ClusterSortArgs {
+    const int32_t* ids;
+    int2* to;
+    uint16_t* dtable;
+    long long lddt, clear;
+    int T, V, D, passes, vec;
+};
+
+__device__ __forceinline__ void cluster_barrier()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t at_peer(const void* p, uint32_t rank)
+{
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
+    return at;
+}
+
+template <int ROUNDS> __global__ void __launch_bounds__(kClusterThreads) zero_sort_cluster_kernel(const __grid_constant__ ClusterSortArgs a)
+{
+    extern __shared__ __align__(16) unsigned char raw[];
+    constexpr int kTokens = ROUNDS * kClusterThreads;
+    int2* pairs = reinterpret_cast<int2*>(raw);                                  // [kTokens]
+    uint16_t* count = reinterpret_cast<uint16_t*>(raw + kTokens * 8);            // [kClusterWarps][kDigits]
+    uint32_t* total = reinterpret_cast<uint32_t*>(count + kClusterWarps * kDigits); // [kDigits], read by the peers
+    uint32_t* base = total + kDigits;                                            // [kDigits]
+    __shared__ uint32_t warp_total[kDigits / 32];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    let_successor_start();
+    wait_for_predecessor();
+    if (blockIdx.x >= kCluster) {
+        const int warps = (gridDim.x - kCluster) * kClusterWarps;
+        for (long long v = (blockIdx.x - kCluster) * kClusterWarps + warp; v < a.clear; v += warps) {
+            uint16_t* row = a.dtable + v * a.lddt;
+            if (a.vec) {
+                for (int c = lane * 8; c < a.D; c += 256) *reinterpret_cast<uint4*>(row + c) = make_uint4(0, 0, 0, 0);
+            } else {
+                for (int c = lane; c < a.D; c += 32) row[c] = 0;
+            }
+        }
+        return;
+    }
+    const int rank = static_cast<int>(blockIdx.x), t0 = rank * kTokens + warp * (ROUNDS * 32);
+    int key[ROUNDS], token[ROUNDS];
+    uint32_t place[ROUNDS];
+#pragma unroll
+    for (int k = 0; k < ROUNDS; ++k) {
+        token[k] = t0 + k * 32 + lane;
+        key[k] = token[k] < a.T ? sort_key(a.ids[token[k]], a.V) : 0;
+    }
+    for (int pass = 0, shift = 0; pass < a.passes; ++pass, shift += kDigitBits) {
+        for (int i = tid; i < kClusterWarps * kDigits / 2; i += kClusterThreads) reinterpret_cast<uint32_t*>(count)[i] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < ROUNDS; ++k) {
+            const bool live = t0 + k * 32 + lane < a.T;
+            const int digit = live ? (key[k] >> shift) & (kDigits - 1) : kDigits;
+            const uint32_t same = __match_any_sync(0xffffffffu, digit);
+            const uint32_t before = live ? count[warp * kDigits + digit] : 0;
+            place[k] = before + __popc(same & ((1u << lane) - 1));
+            __syncwarp();
+            if (live && (same >> lane) == 1) count[warp * kDigits + digit] = static_cast<uint16_t>(before + __popc(same)); // the last of them
+            __syncwarp();
+        }
+        __syncthreads();
+        if (tid < kDigits) { // tokens with this digit in the warps before each one
+            uint32_t n = 0;
+#pragma unroll
+            for (int w = 0; w < kClusterWarps; ++w) {
+                const uint32_t own = count[w * kDigits + tid];
+                count[w * kDigits + tid] = static_cast<uint16_t>(n);
+                n += own;
+            }
+            total[tid] = n;
+        }
+        cluster_barrier(); // the counts are there, and every CTA has its tokens in registers
+        uint32_t all = 0, earlier = 0, sum = 0;
+        if (tid < kDigits) {
+#pragma unroll
+            for (int r = 0; r < kCluster; ++r) {
+                uint32_t n;
+                asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(n) : "r"(at_peer(total + tid, r)) : "memory");
+                all += n;
+                if (r < rank) earlier += n;
+            }
+            sum = all;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t n = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += n;
+            }
+            if (lane == 31) warp_total[warp] = sum;
+        }
+        __syncthreads();
+        if (tid < kDigits) {
+            uint32_t at = earlier + sum - all;
+            for (int w = 0; w < warp; ++w) at += warp_total[w];
+            base[tid] = at;
+        }
+        __syncthreads();
+        const bool last = pass + 1 == a.passes;
+#pragma unroll
+        for (int k = 0; k < ROUNDS; ++k) {
+            if (t0 + k * 32 + lane >= a.T) continue;
+            const int digit = (key[k] >> shift) & (kDigits - 1);
+            const uint32_t to = base[digit] + count[warp * kDigits + digit] + place[k];
+            if (last) {
+                a.to[to] = make_int2(key[k], token[k]);
+            } else {
+                asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(at_peer(pairs + to % kTokens, to / kTokens)), "r"(key[k]), "r"(token[k])
+                             : "memory");
+            }
+        }
+        cluster_barrier(); // the tokens have arrived, and no CTA reads another one's counts any more
+        if (last) break;
+#pragma unroll
+        for (int k = 0; k < ROUNDS; ++k) {
+            const int at = warp * (ROUNDS * 32) + k * 32 + lane;
+            if (rank * kTokens + at < a.T) key[k] = pairs[at].x, token[k] = pairs[at].y;
+        }
+    }
+}
+
 // ---------------------------------------------------------------------------
 // Sums over runs of equal ids
 // ---------------------------------------------------------------------------
@@ -201,31 +339,48 @@ struct RunArgs {
     const void* dy;
     void* dtable;
     float* parts;        // [chunks][2][D]: of the run that began before the chunk, of the one that goes on behind it
-    long long lddy, lddt, T, sum_tasks, tasks;
+    long long lddy, lddt, T, sum_tasks, tasks, cleared; // rows of the table below `cleared` are 0 already
     int D, V, stripes, chunk, add;
     float scale;
 };
 
 template <int VEC> __device__ __forceinline__ int stripe_column(int c0, int j, int lane) { return VEC ? c0 + lane * 8 + j : c0 + j * 32 + lane; }
 
-// This lane's eight columns of a run's sum to the table's gradient.
-template <int BF16, int VEC>
-__device__ __forceinline__ void put_row(const RunArgs& a, int key, int c0, int lane, const float (&sum)[8])
+// This lane's eight elements of a row from memory, as pairs.
+template <int VEC> __device__ __forceinline__ uint4 get_row(const uint16_t* row, int c0, int lane, int D)
 {
-    uint16_t* row = static_cast<uint16_t*>(a.dtable) + key * a.lddt;
     if constexpr (VEC) {
         const int c = c0 + lane * 8;
-        if (c >= a.D) return;
-        float v[8];
+        return c < D ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0);
+    } else {
+        uint32_t h[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = sum[j] * a.scale;
-        if (a.add) add8(v, *reinterpret_cast<const uint4*>(row + c), BF16);
-        *reinterpret_cast<uint4*>(row + c) = pack8(v, BF16);
+        for (int j = 0; j < 8; ++j) {
+            const int c = stripe_column<0>(c0, j, lane);
+            h[j] = c < D ? row[c] : 0;
+        }
+        return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+    }
+}
+
+// A run's sum, plus what the table's gradient held (zeros where it does not
+// count), to its row.
+template <int BF16, int VEC>
+__device__ __forceinline__ void put_row(const RunArgs& a, int key, int c0, int lane, const float (&sum)[8], const uint4& old)
+{
+    uint16_t* row = static_cast<uint16_t*>(a.dtable) + key * a.lddt;
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = sum[j] * a.scale;
+    if (a.add) add8(v, old, BF16);
+    if constexpr (VEC) {
+        const int c = c0 + lane * 8;
+        if (c < a.D) *reinterpret_cast<uint4*>(row + c) = pack8(v, BF16);
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int c = stripe_column<0>(c0, j, lane);
-            if (c < a.D) store16(row, c, sum[j] * a.scale + (a.add ? load16(row, c, BF16) : 0.0f), BF16);
+            if (c < a.D) store16(row, c, v[j], BF16);
         }
     }
 }
@@ -258,16 +413,16 @@ template <int VEC> __device__ __forceinline__ void clear_rows(const RunArgs& a, 
     }
 }
 
-template <int BF16, int VEC> __global__ void __launch_bounds__(256) zero_embed_grad_kernel(const __grid_constant__ RunArgs a)
+template <int BF16, int VEC, int ADD> __global__ void __launch_bounds__(256) zero_embed_grad_kernel(const __grid_constant__ RunArgs a)
 {
-    constexpr int kAhead = VEC ? 8 : 4; // rows in flight
+    constexpr int kAhead = VEC && !ADD ? 8 : 4; // rows in flight
     const int lane = threadIdx.x & 31;
     const long long task = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
     let_successor_start();
     wait_for_predecessor();
     if (task >= a.tasks) return;
     if (task >= a.sum_tasks) {
-        clear_rows<VEC>(a, (task - a.sum_tasks) * kZeroRows, lane);
+        clear_rows<VEC>(a, a.cleared + (task - a.sum_tasks) * kZeroRows, lane);
         return;
     }
     const long long chunk = task / a.stripes, first = chunk * a.chunk, end = min(a.T, first + a.chunk);
@@ -279,11 +434,12 @@ template <int BF16, int VEC> __global__ void __launch_bounds__(256) zero_embed_g
     int run = first > 0 ? a.sorted[first - 1].x : -1; // the id whose run this is
     bool begun = true;                                // it began before the chunk
     bool open = false;                                // the sum holds a row
+    uint4 old = make_uint4(0, 0, 0, 0);               // what the run's row of the table's gradient held
     // the run that ends here: whole in this chunk, or a part of it
     auto flush = [&](bool goes_on) {
         if (!open) return;
         if (!begun && !goes_on) {
-            put_row<BF16, VEC>(a, run, c0, lane, sum);
+            put_row<BF16, VEC>(a, run, c0, lane, sum, old);
         } else {
             float* part = a.parts + (chunk * 2 + (begun ? 0 : 1)) * a.D;
 #pragma unroll
@@ -298,27 +454,25 @@ template <int BF16, int VEC> __global__ void __launch_bounds__(256) zero_embed_g
     };
     bool done = false;
     for (long long s = first; s < end && !done; s += 32) {
-        const int2 mine = s + lane < end ? a.sorted[s + lane] : make_int2(a.V, 0); // a chunk ends off a multiple of 32 only at T
-        for (int i0 = 0; i0 < 32 && !done; i0 += kAhead) {
-            uint4 u[kAhead];
-            uint16_t e[kAhead][8];
+        const int n = static_cast<int>(min(32ll, end - s));
+        const int2 mine = lane < n ? a.sorted[s + lane] : make_int2(a.V, 0);
+        for (int i0 = 0; i0 < n && !done; i0 += kAhead) {
+            uint4 u[kAhead], o[ADD ? kAhead : 1];
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
                 const int key = __shfl_sync(0xffffffffu, mine.x, i0 + i);
                 const uint16_t* row = dy + __shfl_sync(0xffffffffu, mine.y, i0 + i) * a.lddy;
-                if constexpr (VEC) {
-                    u[i] = make_uint4(0, 0, 0, 0);
-                    if (key < a.V && c0 + lane * 8 < a.D) u[i] = *reinterpret_cast<const uint4*>(row + c0 + lane * 8);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int c = stripe_column<0>(c0, j, lane);
-                        e[i][j] = key < a.V && c < a.D ? row[c] : 0;
-                    }
+                u[i] = key < a.V ? get_row<VEC>(row, c0, lane, a.D) : make_uint4(0, 0, 0, 0);
+                // the table's row as it was: read with the others, for the last token that may end a run
+                if constexpr (ADD) {
+                    const int next = __shfl_sync(0xffffffffu, mine.x, min(i0 + i + 1, 31));
+                    o[i] = key < a.V && (key != next || i0 + i + 1 >= n) ? get_row<VEC>(static_cast<const uint16_t*>(a.dtable) + key * a.lddt, c0, lane, a.D)
+                                                                        : make_uint4(0, 0, 0, 0);
                 }
             }
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
+                if (i0 + i >= n) break;
                 const int key = __shfl_sync(0xffffffffu, mine.x, i0 + i);
                 if (key != run) {
                     flush(false);
@@ -330,12 +484,8 @@ template <int BF16, int VEC> __global__ void __launch_bounds__(256) zero_embed_g
                     break;
                 }
                 open = true;
-                if constexpr (VEC) {
-                    add8(sum, u[i], BF16);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) sum[j] += load16(&e[i][j], 0, BF16);
-                }
+                if constexpr (ADD) old = o[i];
+                add8(sum, u[i], BF16);
             }
         }
     }
@@ -368,22 +518,30 @@ template <int BF16, int VEC> __global__ void __launch_bounds__(256) zero_embed_j
         if (n < 32) break;
     }
     float sum[8];
+    // volatile: all of a batch's reads are issued before the first is used
     auto read = [&](const float* part, float (&v)[8]) {
+        if constexpr (VEC) {
+            const int c = min(c0 + lane * 8, a.D - 8); // lanes behind the row read its end, and write nothing
+            asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "l"(part + c));
+            asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]) : "l"(part + c + 4));
+        } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int c = stripe_column<VEC>(c0, j, lane);
-            v[j] = c < a.D ? part[c] : 0.0f;
+            for (int j = 0; j < 8; ++j) asm volatile("ld.global.f32 %0, [%1];" : "=f"(v[j]) : "l"(part + min(stripe_column<0>(c0, j, lane), a.D - 1)));
         }
     };
+    uint4 old = make_uint4(0, 0, 0, 0);
+    if (a.add) old = get_row<VEC>(static_cast<const uint16_t*>(a.dtable) + key * a.lddt, c0, lane, a.D);
     read(a.parts + (chunk * 2 + 1) * a.D, sum);
-#pragma unroll 4
-    for (long long c = chunk + 1; c <= last; ++c) {
-        float v[8];
-        read(a.parts + c * 2 * a.D, v);
+    for (long long c = chunk + 1; c <= last; c += 8) {
+        float v[8][8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] += v[j];
+        for (int k = 0; k < 8; ++k) read(a.parts + min(c + k, last) * 2 * a.D, v[k]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[j] += c + k <= last ? v[k][j] : 0.0f;
     }
-    put_row<BF16, VEC>(a, key, c0, lane, sum);
+    put_row<BF16, VEC>(a, key, c0, lane, sum, old);
 }
 
 // ---------------------------------------------------------------------------
@@ -400,6 +558,7 @@ bool bad_embed(int64_t T, int64_t D, int64_t V, float scale, int32_t type)
 
 // The layout of a gradient's workspace and the sizes of its launches.
 struct GradPlan {
+    int cluster;         // rounds of the sort by one cluster, 0: a launch per pass
     int rounds, blocks, passes, chunk;
     int64_t chunks, stripes;
     int2* pairs[2];
@@ -411,27 +570,62 @@ struct GradPlan {
 GradPlan plan_grad(int64_t T, int64_t D, int64_t V, void* workspace)
 {
     GradPlan p{};
-    // a block reads the counts of all of them: many tokens take larger blocks
-    p.rounds = T <= 65536 ? 2 : 8;
-    p.blocks = static_cast<int>((T + p.rounds * kSortThreads - 1) / (p.rounds * kSortThreads));
+    for (int r = 1; r <= 8 && !p.cluster; r *= 2)
+        if (T <= r * kCluster * kClusterThreads) p.cluster = r;
+    p.rounds = 8;
+    p.blocks = p.cluster ? 0 : static_cast<int>((T + p.rounds * kSortThreads - 1) / (p.rounds * kSortThreads));
     int bits = 1;
     while ((V >> bits) != 0) ++bits; // of V itself, which stands for no row
     p.passes = (bits + kDigitBits - 1) / kDigitBits;
     p.stripes = (D + kStripe - 1) / kStripe;
-    // longer chunks once there are warps enough: fewer runs are cut
-    p.chunk = static_cast<int>(std::min<int64_t>(256, std::max<int64_t>(32, T * p.stripes / 8192 / 32 * 32)));
+    // short chunks where there are few: a chunk's rows follow on each other; longer ones once there are warps
+    // enough: fewer runs are cut
+    p.chunk = 4;
+    while (p.chunk < 32 && T * p.stripes > 2432 * p.chunk) p.chunk *= 2;
+    if (p.chunk == 32) p.chunk = static_cast<int>(std::min<int64_t>(256, std::max<int64_t>(32, T * p.stripes / 8192 / 32 * 32)));
     p.chunks = (T + p.chunk - 1) / p.chunk;
     Carver c{static_cast<unsigned char*>(workspace)};
-    for (int2*& q : p.pairs) q = static_cast<int2*>(c.take(T * 8));
+    p.pairs[0] = static_cast<int2*>(c.take(T * 8));
+    p.pairs[1] = p.cluster ? p.pairs[0] : static_cast<int2*>(c.take(T * 8));
     p.counts = static_cast<uint32_t*>(c.take(static_cast<int64_t>(p.passes) * p.blocks * kDigits * 4));
     p.parts = static_cast<float*>(c.take(p.chunks * 2 * D * 4));
     p.bytes = c.used;
     return p;
 }
 
+constexpr int64_t kClearBytes = 40 << 20; // of the table's gradient that is cleared during a sort by one cluster
+constexpr int kClearCtas = 136;
+
+using ClusterSort = void (*)(ClusterSortArgs);
+
+template <int ROUNDS> int sort_by_cluster(const ClusterSortArgs& a, cudaStream_t stream)
+{
+    const int rc = allow_smem(reinterpret_cast<const void*>(static_cast<ClusterSort>(zero_sort_cluster_kernel<ROUNDS>)), kClusterSortSmem<ROUNDS>);
+    if (rc) return rc;
+    return launch_after(static_cast<ClusterSort>(zero_sort_cluster_kernel<ROUNDS>), a, a.clear ? kCluster + kClearCtas : kCluster, kClusterThreads,
+                        kClusterSortSmem<ROUNDS>, kCluster, stream);
+}
+
 template <class Kernel> Kernel pick(int bf16, int vec, Kernel k00, Kernel k01, Kernel k10, Kernel k11)
 {
     return bf16 ? (vec ? k11 : k10) : (vec ? k01 : k00);
+}
+
+// A launch for the first counts, then one per pass; ends in pairs[(passes - 1) & 1].
+int sort_by_passes(const GradPlan& p, const int32_t* ids, int64_t T, int64_t V, cudaStream_t st)
+{
+    SortArgs s{};
+    s.ids = ids, s.counts = p.counts, s.T = T, s.V = static_cast<int>(V), s.blocks = p.blocks, s.all_counts = p.passes;
+    int rc = launch_after(zero_sort_count_kernel<8>, s, p.blocks, kSortThreads, 0, 1, st);
+    for (int k = 0; k < p.passes && !rc; ++k) {
+        const int64_t each = static_cast<int64_t>(p.blocks) * kDigits;
+        s.ids = k == 0 ? ids : nullptr;
+        s.from = p.pairs[(k + 1) & 1], s.to = p.pairs[k & 1];
+        s.counts = p.counts + k * each, s.next = k + 1 < p.passes ? p.counts + (k + 1) * each : nullptr;
+        s.shift = k * kDigitBits;
+        rc = launch_after(zero_sort_pass_kernel<8>, s, p.blocks, kSortThreads, 0, 1, st);
+    }
+    return rc;
 }
 
 } // namespace
@@ -485,25 +679,28 @@ extern "C" int zero_embed_backward(const int32_t* ids, const void* dy, int64_t l
     r.dy = dy, r.dtable = dtable, r.parts = p.parts, r.lddy = lddy, r.lddt = lddt, r.T = T, r.D = static_cast<int>(D), r.V = static_cast<int>(V);
     r.stripes = static_cast<int>(p.stripes), r.chunk = p.chunk, r.add = add != 0, r.scale = scale;
     r.sum_tasks = p.chunks * p.stripes;
-    r.tasks = r.sum_tasks + (add ? 0 : (V + kZeroRows - 1) / kZeroRows);
+    if (!add && p.cluster) r.cleared = std::min<int64_t>(V, kClearBytes / (2 * D));
+    r.tasks = r.sum_tasks + (add ? 0 : (V - r.cleared + kZeroRows - 1) / kZeroRows);
     if ((r.tasks + 7) / 8 > INT32_MAX) return ZERO_EINVAL;
-
-    SortArgs s{};
-    s.ids = ids, s.counts = p.counts, s.T = T, s.V = static_cast<int>(V), s.blocks = p.blocks, s.all_counts = p.passes;
-    int rc = launch_after(p.rounds == 2 ? zero_sort_count_kernel<2> : zero_sort_count_kernel<8>, s, p.blocks, kSortThreads, 0, 1, st);
-    for (int k = 0; k < p.passes && !rc; ++k) {
-        const int64_t each = static_cast<int64_t>(p.blocks) * kDigits;
-        s.ids = k == 0 ? ids : nullptr;
-        s.from = p.pairs[(k + 1) & 1], s.to = p.pairs[k & 1];
-        s.counts = p.counts + k * each, s.next = k + 1 < p.passes ? p.counts + (k + 1) * each : nullptr;
-        s.shift = k * kDigitBits;
-        rc = launch_after(p.rounds == 2 ? zero_sort_pass_kernel<2> : zero_sort_pass_kernel<8>, s, p.blocks, kSortThreads, 0, 1, st);
-    }
-    if (rc) return rc;
-    r.sorted = p.pairs[(p.passes - 1) & 1];
     const int bf16 = type == ZERO_TYPE_BF16;
     const bool vec = D % 8 == 0 && aligned16(dy, lddy) && aligned16(dtable, lddt);
-    auto sum = pick(bf16, vec, zero_embed_grad_kernel<0, 0>, zero_embed_grad_kernel<0, 1>, zero_embed_grad_kernel<1, 0>, zero_embed_grad_kernel<1, 1>);
+    int rc = ZERO_OK;
+    if (p.cluster) {
+        ClusterSortArgs s{};
+        s.ids = ids, s.to = p.pairs[0], s.dtable = static_cast<uint16_t*>(dtable), s.lddt = lddt, s.clear = r.cleared;
+        s.T = static_cast<int>(T), s.V = static_cast<int>(V), s.D = static_cast<int>(D), s.passes = p.passes, s.vec = vec;
+        rc = p.cluster == 1   ? sort_by_cluster<1>(s, st)
+             : p.cluster == 2 ? sort_by_cluster<2>(s, st)
+             : p.cluster == 4 ? sort_by_cluster<4>(s, st)
+                              : sort_by_cluster<8>(s, st);
+    } else {
+        rc = sort_by_passes(p, ids, T, V, st);
+    }
+    if (rc) return rc;
+
+    r.sorted = p.pairs[(p.passes - 1) & 1];
+    auto sum = add ? pick(bf16, vec, zero_embed_grad_kernel<0, 0, 1>, zero_embed_grad_kernel<0, 1, 1>, zero_embed_grad_kernel<1, 0, 1>, zero_embed_grad_kernel<1, 1, 1>)
+                   : pick(bf16, vec, zero_embed_grad_kernel<0, 0, 0>, zero_embed_grad_kernel<0, 1, 0>, zero_embed_grad_kernel<1, 0, 0>, zero_embed_grad_kernel<1, 1, 0>);
     if ((rc = launch_after(sum, r, (r.tasks + 7) / 8, 256, 0, 1, st))) return rc;
     auto join = pick(bf16, vec, zero_embed_join_kernel<0, 0>, zero_embed_join_kernel<0, 1>, zero_embed_join_kernel<1, 0>, zero_embed_join_kernel<1, 1>);
     return launch_after(join, r, (r.sum_tasks + 7) / 8, 256, 0, 1, st);

@@ -7,7 +7,6 @@
 #include <cuda.h> // driver types only: the tensor-map encoder is found through the runtime
 
 #include <cmath>
-#include <mutex>
 #include <type_traits>
 #include <utility>
 
@@ -1481,24 +1480,6 @@ inline int make_map(CUtensorMap* map, const Matrix& x, int mn, int extent)
 }
 
 template <class Args> using GemmKernel = void (*)(Args);
-
-// Dynamic shared memory above 48 KB is allowed once per kernel and device.
-inline int allow_smem(const void* fn, int bytes)
-{
-    static std::mutex mu;
-    static struct { int dev; const void* fn; } known[64];
-    static int n_known = 0;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return record(e);
-    std::lock_guard<std::mutex> lock(mu);
-    for (int k = 0; k < n_known; ++k)
-        if (known[k].dev == dev && known[k].fn == fn) return ZERO_OK;
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return record(e);
-    if (n_known < 64) known[n_known++] = {dev, fn};
-    return ZERO_OK;
-}
 
 template <int BN> constexpr int kPairStages = BN >= 256 ? 6 : 8;
 

@@ -9,6 +9,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
 #include "zero_train.h"
 
@@ -115,6 +116,24 @@ inline bool aligned16(const void* p, int64_t ld) { return addr(p) % 16 == 0 && l
 
 // Elements of the widest access that every row start allows.
 inline int widest_access(const void* p, int64_t ld) { return aligned16(p, ld) ? 8 : addr(p) % 4 == 0 && ld % 2 == 0 ? 2 : 1; }
+
+// Dynamic shared memory above 48 KB is allowed once per kernel and device.
+inline int allow_smem(const void* fn, int bytes)
+{
+    static std::mutex mu;
+    static struct { int dev; const void* fn; } known[64];
+    static int n_known = 0;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return record(e);
+    std::lock_guard<std::mutex> lock(mu);
+    for (int k = 0; k < n_known; ++k)
+        if (known[k].dev == dev && known[k].fn == fn) return ZERO_OK;
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return record(e);
+    if (n_known < 64) known[n_known++] = {dev, fn};
+    return ZERO_OK;
+}
 
 // A launch whose start may overlap the preceding kernel's end.
 template <class Kernel, class Args>
