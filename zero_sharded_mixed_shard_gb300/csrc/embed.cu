@@ -339,7 +339,7 @@ struct RunArgs {
     const void* dy;
     void* dtable;
     float* parts;        // [chunks][2][D]: of the run that began before the chunk, of the one that goes on behind it
-    long long lddy, lddt, T, sum_tasks, tasks, cleared; // rows of the table below `cleared` are 0 already
+    long long lddy, lddt, T, sum_tasks, join_tasks, tasks, cleared; // rows of the table below `cleared` are 0 already
     int D, V, stripes, chunk, add;
     float scale;
 };
@@ -431,81 +431,72 @@ template <int BF16, int VEC, int ADD> __global__ void __launch_bounds__(256) zer
     float sum[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
-    int run = first > 0 ? a.sorted[first - 1].x : -1; // the id whose run this is
-    bool begun = true;                                // it began before the chunk
-    bool open = false;                                // the sum holds a row
-    uint4 old = make_uint4(0, 0, 0, 0);               // what the run's row of the table's gradient held
-    // the run that ends here: whole in this chunk, or a part of it
-    auto flush = [&](bool goes_on) {
-        if (!open) return;
-        if (!begun && !goes_on) {
-            put_row<BF16, VEC>(a, run, c0, lane, sum, old);
-        } else {
-            float* part = a.parts + (chunk * 2 + (begun ? 0 : 1)) * a.D;
+    bool begun = first > 0 && a.sorted[first - 1].x == a.sorted[first].x; // the run began before the chunk
+    bool open = false;                                                     // the sum holds a row
+    auto put_part = [&]() {
+        float* part = a.parts + (chunk * 2 + (begun ? 0 : 1)) * a.D;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int c = stripe_column<VEC>(c0, j, lane);
-                if (c < a.D) part[c] = sum[j];
-            }
+        for (int j = 0; j < 8; ++j) {
+            const int c = stripe_column<VEC>(c0, j, lane);
+            if (c < a.D) part[c] = sum[j];
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
-        open = false;
     };
-    bool done = false;
-    for (long long s = first; s < end && !done; s += 32) {
-        const int n = static_cast<int>(min(32ll, end - s));
-        const int2 mine = lane < n ? a.sorted[s + lane] : make_int2(a.V, 0);
-        for (int i0 = 0; i0 < n && !done; i0 += kAhead) {
-            uint4 u[kAhead], o[ADD ? kAhead : 1];
+    for (long long s = first; s < end; s += 32) {
+        const int2 none = make_int2(a.V, 0);
+        const int2 mine = s + lane < end ? a.sorted[s + lane] : none;
+        // which tokens are there, and which end their run: one bit each, so that the sums below shuffle nothing
+        const int next = s + lane + 1 < a.T ? a.sorted[s + lane + 1].x : a.V;
+        const int n = __popc(__ballot_sync(0xffffffffu, mine.x < a.V));
+        const uint32_t ends = __ballot_sync(0xffffffffu, mine.x != next);
+        for (int i0 = 0; i0 < n; i0 += kAhead) {
+            uint4 u[kAhead], o[ADD ? kAhead : 1] = {};
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
-                const int key = __shfl_sync(0xffffffffu, mine.x, i0 + i);
                 const uint16_t* row = dy + __shfl_sync(0xffffffffu, mine.y, i0 + i) * a.lddy;
-                u[i] = key < a.V ? get_row<VEC>(row, c0, lane, a.D) : make_uint4(0, 0, 0, 0);
-                // the table's row as it was: read with the others, for the last token that may end a run
+                u[i] = i0 + i < n ? get_row<VEC>(row, c0, lane, a.D) : make_uint4(0, 0, 0, 0);
+                // the table's row as it was: read with the others, for the token that ends its run
                 if constexpr (ADD) {
-                    const int next = __shfl_sync(0xffffffffu, mine.x, min(i0 + i + 1, 31));
-                    o[i] = key < a.V && (key != next || i0 + i + 1 >= n) ? get_row<VEC>(static_cast<const uint16_t*>(a.dtable) + key * a.lddt, c0, lane, a.D)
-                                                                        : make_uint4(0, 0, 0, 0);
+                    const int key = __shfl_sync(0xffffffffu, mine.x, i0 + i);
+                    o[i] = i0 + i < n && (ends >> (i0 + i) & 1) ? get_row<VEC>(static_cast<const uint16_t*>(a.dtable) + key * a.lddt, c0, lane, a.D)
+                                                                : make_uint4(0, 0, 0, 0);
                 }
             }
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
                 if (i0 + i >= n) break;
-                const int key = __shfl_sync(0xffffffffu, mine.x, i0 + i);
-                if (key != run) {
-                    flush(false);
-                    run = key;
-                    begun = false;
-                }
-                if (key >= a.V) { // behind the last id
-                    done = true;
-                    break;
-                }
-                open = true;
-                if constexpr (ADD) old = o[i];
                 add8(sum, u[i], BF16);
+                open = true;
+                if (!(ends >> (i0 + i) & 1)) continue;
+                const int key = __shfl_sync(0xffffffffu, mine.x, i0 + i);
+                if (begun) put_part();
+                else put_row<BF16, VEC>(a, key, c0, lane, sum, o[ADD ? i : 0]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+                begun = open = false;
             }
         }
+        if (n < 32) break; // behind the last id, or at the chunk's end
     }
-    flush(end < a.T && a.sorted[end].x == run);
+    if (open) put_part(); // the run goes on behind the chunk
 }
 
 // The parts of a run that passes a chunk's end, added in order by a warp of
-// the chunk that it begins in.
-template <int BF16, int VEC> __global__ void __launch_bounds__(256) zero_embed_join_kernel(const __grid_constant__ RunArgs a)
+// the chunk that it begins in: four columns a lane, sixteen parts in flight.
+// Bound by latency (16384 tokens, 2048 columns, runs of up to 33 parts).
+constexpr int kJoinStripe = 128, kJoinAhead = 16;
+
+template <int BF16, int VEC> __global__ void __launch_bounds__(128) zero_embed_join_kernel(const __grid_constant__ RunArgs a)
 {
     const int lane = threadIdx.x & 31;
-    const long long task = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const long long task = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
     let_successor_start();
     wait_for_predecessor();
-    if (task >= a.sum_tasks) return;
-    const long long chunk = task / a.stripes, first = chunk * a.chunk, end = first + a.chunk;
-    const int c0 = static_cast<int>(task - chunk * a.stripes) * kStripe;
+    if (task >= a.join_tasks) return;
+    const int stripes = (a.D + kJoinStripe - 1) / kJoinStripe;
+    const long long chunk = task / stripes, first = chunk * a.chunk, end = first + a.chunk;
     if (end >= a.T) return;
-    const int key = a.sorted[end - 1].x;
-    if (key >= a.V || a.sorted[end].x != key || (first > 0 && a.sorted[first - 1].x == key)) return;
+    const int key = a.sorted[end - 1].x, next = a.sorted[end].x, previous = first > 0 ? a.sorted[first - 1].x : -1;
+    if (key >= a.V || next != key || previous == key) return;
     // the chunks behind this one that begin with the run
     const long long chunks = (a.T + a.chunk - 1) / a.chunk;
     long long last = chunk; // the last chunk that holds a part
@@ -517,31 +508,50 @@ template <int BF16, int VEC> __global__ void __launch_bounds__(256) zero_embed_j
         last += n;
         if (n < 32) break;
     }
-    float sum[8];
-    // volatile: all of a batch's reads are issued before the first is used
-    auto read = [&](const float* part, float (&v)[8]) {
-        if constexpr (VEC) {
-            const int c = min(c0 + lane * 8, a.D - 8); // lanes behind the row read its end, and write nothing
-            asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "l"(part + c));
-            asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]) : "l"(part + c + 4));
-        } else {
+    const int c0 = static_cast<int>(task - chunk * stripes) * kJoinStripe;
+    // columns; lanes behind the row read its end, and write nothing
+    int at[4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) asm volatile("ld.global.f32 %0, [%1];" : "=f"(v[j]) : "l"(part + min(stripe_column<0>(c0, j, lane), a.D - 1)));
-        }
-    };
-    uint4 old = make_uint4(0, 0, 0, 0);
-    if (a.add) old = get_row<VEC>(static_cast<const uint16_t*>(a.dtable) + key * a.lddt, c0, lane, a.D);
-    read(a.parts + (chunk * 2 + 1) * a.D, sum);
-    for (long long c = chunk + 1; c <= last; c += 8) {
-        float v[8][8];
+    for (int j = 0; j < 4; ++j) at[j] = VEC ? min(c0 + lane * 4, a.D - 4) + j : min(c0 + j * 32 + lane, a.D - 1);
+    uint16_t* row = static_cast<uint16_t*>(a.dtable) + key * a.lddt;
+    float sum[4], old[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) read(a.parts + min(c + k, last) * 2 * a.D, v[k]);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sum[j] += c + k <= last ? v[k][j] : 0.0f;
+    for (int j = 0; j < 4; ++j) {
+        sum[j] = a.parts[(chunk * 2 + 1) * a.D + at[j]];
+        old[j] = a.add ? load16(row, at[j], BF16) : 0.0f;
     }
-    put_row<BF16, VEC>(a, key, c0, lane, sum, old);
+    for (long long c = chunk + 1; c <= last; c += kJoinAhead) {
+        const int n = static_cast<int>(min(static_cast<long long>(kJoinAhead), last + 1 - c));
+        float v[kJoinAhead][4];
+#pragma unroll
+        for (int k = 0; k < kJoinAhead; ++k) {
+            const float* part = a.parts + (c + k) * 2 * a.D;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[k][j] = 0.0f;
+            if (k >= n) continue;
+            if constexpr (VEC) {
+                const float4 f = __ldcg(reinterpret_cast<const float4*>(part + at[0]));
+                v[k][0] = f.x, v[k][1] = f.y, v[k][2] = f.z, v[k][3] = f.w;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[k][j] = __ldcg(part + at[j]);
+            }
+        }
+        __syncwarp(); // keeps the reads before it: the compiler adds each part before it reads the next else (15 us instead of 6)
+#pragma unroll
+        for (int k = 0; k < kJoinAhead; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum[j] += v[k][j];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum[j] = sum[j] * a.scale + old[j];
+    if constexpr (VEC) {
+        if (c0 + lane * 4 < a.D) *reinterpret_cast<uint2*>(row + at[0]) = make_uint2(pack16(sum[0], sum[1], BF16), pack16(sum[2], sum[3], BF16));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (c0 + j * 32 + lane < a.D) store16(row, at[j], sum[j], BF16);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -679,9 +689,10 @@ extern "C" int zero_embed_backward(const int32_t* ids, const void* dy, int64_t l
     r.dy = dy, r.dtable = dtable, r.parts = p.parts, r.lddy = lddy, r.lddt = lddt, r.T = T, r.D = static_cast<int>(D), r.V = static_cast<int>(V);
     r.stripes = static_cast<int>(p.stripes), r.chunk = p.chunk, r.add = add != 0, r.scale = scale;
     r.sum_tasks = p.chunks * p.stripes;
+    r.join_tasks = p.chunks * ((D + kJoinStripe - 1) / kJoinStripe);
     if (!add && p.cluster) r.cleared = std::min<int64_t>(V, kClearBytes / (2 * D));
     r.tasks = r.sum_tasks + (add ? 0 : (V - r.cleared + kZeroRows - 1) / kZeroRows);
-    if ((r.tasks + 7) / 8 > INT32_MAX) return ZERO_EINVAL;
+    if ((r.tasks + 7) / 8 > INT32_MAX || (r.join_tasks + 3) / 4 > INT32_MAX) return ZERO_EINVAL;
     const int bf16 = type == ZERO_TYPE_BF16;
     const bool vec = D % 8 == 0 && aligned16(dy, lddy) && aligned16(dtable, lddt);
     int rc = ZERO_OK;
@@ -703,5 +714,5 @@ extern "C" int zero_embed_backward(const int32_t* ids, const void* dy, int64_t l
                    : pick(bf16, vec, zero_embed_grad_kernel<0, 0, 0>, zero_embed_grad_kernel<0, 1, 0>, zero_embed_grad_kernel<1, 0, 0>, zero_embed_grad_kernel<1, 1, 0>);
     if ((rc = launch_after(sum, r, (r.tasks + 7) / 8, 256, 0, 1, st))) return rc;
     auto join = pick(bf16, vec, zero_embed_join_kernel<0, 0>, zero_embed_join_kernel<0, 1>, zero_embed_join_kernel<1, 0>, zero_embed_join_kernel<1, 1>);
-    return launch_after(join, r, (r.sum_tasks + 7) / 8, 256, 0, 1, st);
+    return launch_after(join, r, (r.join_tasks + 3) / 4, 128, 0, 1, st);
 }
