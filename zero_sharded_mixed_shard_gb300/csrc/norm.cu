@@ -39,7 +39,7 @@ struct NormBackArgs {
     const float* rstd;
     const void* res;
     void* dx;
-    float* sums;         // [groups][2][D], null: no gradients of the weights
+    float* sums;         // [groups][2][D], a part of each CTA, null: no gradients of the weights
     long long lddy, ldx, ldr, lddx, T;
     int D, groups;
     float inv_d;
@@ -231,17 +231,38 @@ __global__ void __launch_bounds__(kNormCta<GROUP>) zero_layernorm_kernel(const _
     }
 }
 
-// Rows of a group taken together: their reads are in flight at once and their
-// sums share a barrier.
-template <int GROUP, int VPT> constexpr int kNormRows = GROUP > 256 ? 1 : VPT == 1 ? 4 : 2;
+// The gradient: a CTA of kGradThreads on every SM, as many groups as fit in it,
+// a row per group at a time.  VEC: the rows to come are copied to shared
+// memory ahead, kAhead of them, each thread its own vectors, so that it waits
+// for nobody's copies but its own; else the row is read where it is used.
+// A group joins its two sums of a row by one barrier of its own.  16384 rows of
+// 2048 bf16 elements with the residual (269 MB): NORM_GRAD_TIME.
+constexpr int kGradThreads = 512;
+template <int VPT> constexpr int kNormAhead = VPT == 1 ? 6 : 4;
+template <int GROUP, int VPT, int VEC>
+constexpr int kNormSmem = (VEC ? kNormAhead<VPT> * 3 * kGradThreads * VPT * 16 : 0) > 2 * kGradThreads * VPT * 8 * 4
+                              ? kNormAhead<VPT> * 3 * kGradThreads * VPT * 16
+                              : 2 * kGradThreads * VPT * 8 * 4;
+
+template <int GROUP> __device__ __forceinline__ void group_barrier(int group)
+{
+    if constexpr (GROUP == 32) __syncwarp();
+    else if constexpr (GROUP == kGradThreads) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(GROUP) : "memory");
+}
+
+__device__ __forceinline__ void copy16(void* to, const void* from)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
+}
 
 template <int BF16, int VEC, int GROUP, int VPT>
-__global__ void __launch_bounds__(kNormCta<GROUP>) zero_layernorm_grad_kernel(const __grid_constant__ NormBackArgs a)
+__global__ void __launch_bounds__(kGradThreads, 1) zero_layernorm_grad_kernel(const __grid_constant__ NormBackArgs a)
 {
-    constexpr int R = kNormRows<GROUP, VPT>, kGroups = kNormCta<GROUP> / GROUP;
-    __shared__ float part[kNormCta<GROUP> / 32 * 2 * R];
-    const int self = threadIdx.x % GROUP;
-    const long long group = static_cast<long long>(blockIdx.x) * kGroups + threadIdx.x / GROUP;
+    extern __shared__ __align__(16) unsigned char raw[];
+    constexpr int kGroups = kGradThreads / GROUP, kWarps = GROUP / 32, S = kNormAhead<VPT>;
+    __shared__ float part[2][kGradThreads / 32][2];
+    const int self = threadIdx.x % GROUP, in_cta = threadIdx.x / GROUP;
     let_successor_start();
     wait_for_predecessor();
     const uint16_t* dy = static_cast<const uint16_t*>(a.dy);
@@ -257,85 +278,141 @@ __global__ void __launch_bounds__(kNormCta<GROUP>) zero_layernorm_grad_kernel(co
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[k][j] = db[k][j] = 0.0f;
     }
-    // every group of a CTA goes round equally often, for the barriers' sake
-    const long long first = static_cast<long long>(blockIdx.x) * kGroups * R, step = static_cast<long long>(gridDim.x) * kGroups * R;
-    for (long long at = first; at < a.T; at += step) {
-        const long long r0 = at + threadIdx.x / GROUP * R;
-        Packed px[R][VPT], pd[R][VPT], pr[R][VPT];
-        float mean[R], rstd[R], sum[2 * R];
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const bool live = r0 + i < a.T;
-            const long long r = live ? r0 + i : a.T - 1;
-            mean[i] = -0.5f * a.mean[r];
-            rstd[i] = 2.0f * a.rstd[r];
+    // this thread's place in slot s: three streams of VPT vectors
+    auto slot = [&](int s, int stream, int k) {
+        return reinterpret_cast<uint4*>(raw) + ((s * 3 + stream) * VPT + k) * kGradThreads + threadIdx.x;
+    };
+    auto copy_row = [&](int s, long long r) {
+        if (r < a.T) {
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                px[i][k] = load_row<VEC, GROUP>(x + r * a.ldx, k, self, a.D);
-                pd[i][k] = load_row<VEC, GROUP>(dy + r * a.lddy, k, self, live ? a.D : 0);
-                if (res && dx) pr[i][k] = load_row<VEC, GROUP>(res + r * a.ldr, k, self, a.D);
+                const int c = column<1, GROUP>(k, 0, self);
+                if (c >= a.D) continue;
+                copy16(slot(s, 0, k), x + r * a.ldx + c);
+                copy16(slot(s, 1, k), dy + r * a.lddy + c);
+                if (res) copy16(slot(s, 2, k), res + r * a.ldr + c);
             }
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto held = [&](int s, int stream, int k) {
+        const uint4 v = *slot(s, stream, k);
+        Packed p;
+        p.u[0] = v.x, p.u[1] = v.y, p.u[2] = v.z, p.u[3] = v.w;
+        return p;
+    };
+    const long long first = static_cast<long long>(blockIdx.x) * kGroups + in_cta, step = static_cast<long long>(gridDim.x) * kGroups;
+    float mean_next = 0.0f, rstd_next = 0.0f;
+    if (first < a.T) mean_next = a.mean[first], rstd_next = a.rstd[first];
+    if constexpr (VEC) {
+        // columns past the last are never copied: zeros
+        for (int s = 0; s < S; ++s)
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const bool live = r0 + i < a.T;
-            float s0 = 0.0f, s1 = 0.0f;
+            for (int k = 0; k < VPT; ++k)
+                if (column<1, GROUP>(k, 0, self) >= a.D)
+                    for (int i = 0; i < 3; ++i) *slot(s, i, k) = make_uint4(0, 0, 0, 0);
+        for (int s = 0; s < S - 1; ++s) copy_row(s, first + s * step);
+    }
+    int s = 0, turn = 0;
+    for (long long r = first; r < a.T; r += step) {
+        const float mean = -0.5f * mean_next, rstd = 2.0f * rstd_next;
+        if (r + step < a.T) mean_next = a.mean[r + step], rstd_next = a.rstd[r + step];
+        Packed px[VPT], pd[VPT], pr[VPT];
+        if constexpr (VEC) {
+            copy_row(s == 0 ? S - 1 : s - 1, r + (S - 1) * step); // into the slot that the last row has left
+            asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) px[k] = held(s, 0, k), pd[k] = held(s, 1, k);
+        } else {
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                float vx[8], vd[8], vw[8];
-                widen<BF16>(px[i][k], vx);
-                widen<BF16>(pd[i][k], vd);
-                widen<BF16>(w[k], vw);
+                px[k] = load_row<0, GROUP>(x + r * a.ldx, k, self, a.D);
+                pd[k] = load_row<0, GROUP>(dy + r * a.lddy, k, self, a.D);
+                if (res) pr[k] = load_row<0, GROUP>(res + r * a.ldr, k, self, a.D);
+            }
+        }
+        float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    // columns past the last are no column's: what they add goes nowhere, and their dy is 0
-                    const bool in = live && column<VEC, GROUP>(k, j, self) < a.D;
-                    const float h = in ? fmaf(vx[j], 0.5f, mean[i]) * rstd[i] : 0.0f;
-                    const float g = vd[j] * vw[j];
-                    dw[k][j] = fmaf(vd[j], h, dw[k][j]);
-                    db[k][j] += vd[j];
-                    s0 += g;
-                    s1 = fmaf(g, h, s1);
+        for (int k = 0; k < VPT; ++k) {
+            float vx[8], vd[8], vw[8];
+            widen<BF16>(px[k], vx);
+            widen<BF16>(pd[k], vd);
+            widen<BF16>(w[k], vw);
+            // vectors past the last have dy 0: their sums go nowhere, so long as their h is finite
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float h = fmaf(vx[j], 0.5f, mean) * rstd;
+                if (column<VEC, GROUP>(k, j, self) >= a.D) h = 0.0f;
+                const float g = vd[j] * vw[j];
+                dw[k][j] = fmaf(vd[j], h, dw[k][j]);
+                db[k][j] += vd[j];
+                sum[0] += g;
+                sum[1] = fmaf(g, h, sum[1]);
+            }
+        }
+        if (dx) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], o);
+                sum[1] += __shfl_xor_sync(0xffffffffu, sum[1], o);
+            }
+            if constexpr (GROUP > 32) { // two buffers in turn: a thread passes the next barrier only when all have read this one
+                if ((threadIdx.x & 31) == 0) part[turn][threadIdx.x / 32][0] = sum[0], part[turn][threadIdx.x / 32][1] = sum[1];
+                group_barrier<GROUP>(in_cta);
+                sum[0] = sum[1] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < kWarps; ++i) {
+                    sum[0] += part[turn][in_cta * kWarps + i][0];
+                    sum[1] += part[turn][in_cta * kWarps + i][1];
                 }
+                turn ^= 1;
             }
-            sum[2 * i] = s0;
-            sum[2 * i + 1] = s1;
-        }
-        if (!dx) continue;
-        group_sum<GROUP>(sum, part);
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            if (r0 + i >= a.T) break;
-            const float c0 = sum[2 * i] * a.inv_d, c1 = sum[2 * i + 1] * a.inv_d, s = 0.5f * rstd[i];
+            const float c0 = sum[0] * a.inv_d, c1 = sum[1] * a.inv_d, half = 0.5f * rstd;
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 float vx[8], vd[8], vw[8], o[8];
-                widen<BF16>(px[i][k], vx);
-                widen<BF16>(pd[i][k], vd);
+                widen<BF16>(px[k], vx);
+                widen<BF16>(pd[k], vd);
                 widen<BF16>(w[k], vw);
-                if (res) widen<BF16>(pr[i][k], o);
+                if (res) {
+                    if constexpr (VEC) pr[k] = held(s, 2, k);
+                    widen<BF16>(pr[k], o);
+                }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float h = fmaf(vx[j], 0.5f, mean[i]) * rstd[i];
-                    const float d = s * (vd[j] * vw[j] - c0 - h * c1);
+                    const float h = fmaf(vx[j], 0.5f, mean) * rstd;
+                    const float d = half * (vd[j] * vw[j] - c0 - h * c1);
                     o[j] = res ? o[j] + d : d;
                 }
-                store_row<VEC, GROUP, BF16>(dx + (r0 + i) * a.lddx, k, self, a.D, o);
+                store_row<VEC, GROUP, BF16>(dx + r * a.lddx, k, self, a.D, o);
             }
         }
+        if (++s == S) s = 0;
     }
     if (!a.sums) return;
-    float* to = a.sums + group * 2 * a.D;
+    // the groups' sums, joined in the groups' order
+    if constexpr (VEC) asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    float* all = reinterpret_cast<float*>(raw); // [kGroups][2][8 GROUP VPT]
+    constexpr int kWidth = 8 * GROUP * VPT;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int c = column<VEC, GROUP>(k, j, self);
-            if (c < a.D) {
-                to[c] = dw[k][j];
-                to[a.D + c] = db[k][j];
-            }
+            all[(in_cta * 2) * kWidth + c] = dw[k][j];
+            all[(in_cta * 2 + 1) * kWidth + c] = db[k][j];
         }
+    }
+    __syncthreads();
+    float* to = a.sums + static_cast<long long>(blockIdx.x) * 2 * a.D;
+    for (int i = threadIdx.x; i < 2 * kWidth; i += kGradThreads) {
+        const int which = i / kWidth, c = i - which * kWidth;
+        if (c >= a.D) continue;
+        float v = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) v += all[(k * 2 + which) * kWidth + c];
+        to[which * static_cast<long long>(a.D) + c] = v;
     }
 }
 
@@ -493,13 +570,12 @@ constexpr int64_t kNormWide = 8192; // rows above it take the wide kernels
 
 struct NormBackPick {
     NormBackKernel fn;
-    int group, rows;     // threads that share a row, rows a group takes together
-    int per_sm;          // CTAs on an SM
+    int group, smem;     // threads that share a row, bytes of shared memory
 };
 
 template <int BF16, int VEC, int GROUP, int VPT> NormBackPick back_pick()
 {
-    return {zero_layernorm_grad_kernel<BF16, VEC, GROUP, VPT>, GROUP, kNormRows<GROUP, VPT>, GROUP <= 256 ? 2 : 1};
+    return {zero_layernorm_grad_kernel<BF16, VEC, GROUP, VPT>, GROUP, kNormSmem<GROUP, VPT, VEC>};
 }
 
 template <int BF16, int VEC> NormBackPick pick_back(int64_t D)
@@ -507,7 +583,7 @@ template <int BF16, int VEC> NormBackPick pick_back(int64_t D)
     if (D <= 256) return back_pick<BF16, VEC, 32, 1>();
     if (D <= 512) return back_pick<BF16, VEC, 64, 1>();
     if (D <= 1024) return back_pick<BF16, VEC, 128, 1>();
-    if (D <= 2048) return back_pick<BF16, VEC, 256, 1>();
+    if (D <= 2048) return back_pick<BF16, VEC, 128, 2>();
     if (D <= 4096) return back_pick<BF16, VEC, 256, 2>();
     return back_pick<BF16, VEC, 512, 2>();
 }
@@ -518,15 +594,13 @@ NormBackPick pick_back(int64_t D, int bf16, int vec)
     return vec ? pick_back<0, 1>(D) : pick_back<0, 0>(D);
 }
 
-constexpr int kMostNormCtas = 304; // of the gradient: two on each SM
+constexpr int kMostNormCtas = 192; // of the gradient: one on each SM
 
-// Groups whose sums a gradient's second launch adds, a bound that holds on any device.
+// Parts of the columns' sums that a gradient's second launch adds, a bound that holds on any device.
 int64_t most_groups(int64_t T, int64_t D)
 {
     if (D > kNormWide) return std::max<int64_t>(1, std::min<int64_t>(64, T / 64));
-    const int64_t group = pick_back(D, 0, 0).group;
-    const int64_t per_cta = std::max<int64_t>(1, kNormThreads / group);
-    return kMostNormCtas * per_cta;
+    return std::min<int64_t>(kMostNormCtas, T);
 }
 
 constexpr int64_t kMostWidth = int64_t{1} << 30; // columns are counted in 32 bits, past the last one too
@@ -645,11 +719,10 @@ extern "C" int zero_layernorm_backward(const void* dy, int64_t lddy, const void*
         if (sums && (rc = launch_after(columns, a, stripes * a.groups, 256, 0, 1, st))) return rc;
     } else {
         const NormBackPick k = pick_back(D, bf16, vec);
-        const int threads = std::max(k.group, kNormThreads), per_cta = threads / k.group;
-        const int64_t need = (T + static_cast<int64_t>(per_cta) * k.rows - 1) / (static_cast<int64_t>(per_cta) * k.rows);
-        const int64_t ctas = std::min<int64_t>({need, static_cast<int64_t>(sms) * k.per_sm, kMostNormCtas});
-        a.groups = static_cast<int>(ctas * per_cta);
-        if ((rc = launch_after(k.fn, a, ctas, threads, 0, 1, st))) return rc;
+        const int64_t per_cta = kGradThreads / k.group, ctas = std::min<int64_t>({(T + per_cta - 1) / per_cta, sms, kMostNormCtas});
+        a.groups = static_cast<int>(ctas);
+        if ((rc = allow_smem(reinterpret_cast<const void*>(k.fn), k.smem))) return rc;
+        if ((rc = launch_after(k.fn, a, ctas, kGradThreads, k.smem, 1, st))) return rc;
     }
     if (!sums) return ZERO_OK;
     NormSumArgs s{};
