@@ -12,16 +12,16 @@
 // A CTA takes a row.  One pass over it finds the largest logit and the sums of
 // exponentials (each thread's own largest so far, joined at the end), a second
 // one writes the gradient; the second reads the row from L2.  Both sums share
-// the largest logit, since it is the same for s / z.  The gradient's few
-// elements at the target and the indices are written last, after the CTA's
-// barrier, from logits read before the second pass: logits and gradient may be
-// one matrix.
+// the largest logit, since it is the same for s / z.  One warp stays out of
+// both passes where there is a teacher: its distribution, the loss, and the
+// gradient's elements at the target and the indices are that warp's, and are
+// stored last, after the CTA's barrier, from logits read before the second
+// pass: logits and gradient may be one matrix.
+// Bound by issue and exponentials, nearly by HBM: DISTILL_TIME.
 #include "layers.cuh"
 
 namespace {
 
-constexpr int kLossThreads = 512;
-constexpr int kLossWarps = kLossThreads / 32;
 constexpr int kMostTeacher = 1024; // entries of a row's teacher
 
 struct LossArgs {
@@ -49,9 +49,6 @@ struct Tops {
     float top, sum, soft;
 };
 
-// x - top without the difference of two infinities of one sign.
-__device__ __forceinline__ float below(float x, float top) { return top == -INFINITY ? x : x - top; }
-
 __device__ __forceinline__ Tops join(const Tops& p, const Tops& q, float l, float lz)
 {
     Tops o;
@@ -62,53 +59,95 @@ __device__ __forceinline__ Tops join(const Tops& p, const Tops& q, float l, floa
     return o;
 }
 
-__device__ __forceinline__ float block_sum(float v, float* part)
+__device__ __forceinline__ float warp_sum(float v)
 {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float s = 0.0f;
-#pragma unroll
-    for (int k = 0; k < kLossWarps; ++k) s += part[k];
-    return s;
+    return v;
 }
 
-__device__ __forceinline__ float block_max(float v, float* part)
+__device__ __forceinline__ float warp_max(float v)
 {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float s = part[0];
-#pragma unroll
-    for (int k = 1; k < kLossWarps; ++k) s = fmaxf(s, part[k]);
-    return s;
+    return v;
 }
 
-__device__ __forceinline__ void widen8(const uint4& u, float (&v)[8], int bf16)
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
 {
-    const uint32_t h[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float2 f = unpack16(h[j], bf16);
-        v[2 * j] = f.x;
-        v[2 * j + 1] = f.y;
+    float2 d;
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\tfma.rn.f32x2 a, a, b, c;\n\t"
+        "mov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
+__device__ __forceinline__ float2 exp2_2(float2 a) { return make_float2(fast_exp2(a.x), fast_exp2(a.y)); }
+
+// The larger of each half; a NaN loses.
+template <int BF16> __device__ __forceinline__ uint32_t max16(uint32_t a, uint32_t b)
+{
+    if constexpr (BF16) {
+        const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+        return *reinterpret_cast<const uint32_t*>(&m);
+    } else {
+        const __half2 m = __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+        return *reinterpret_cast<const uint32_t*>(&m);
     }
 }
 
-// VEC: a row of the gradient starts as far from a boundary of 16 bytes as its
-// row of logits.  BOTH: two sums at different temperatures; otherwise one that
-// serves the term in use (or both, at temperature 1).
-template <int BF16, int VEC, int BOTH>
-__global__ void __launch_bounds__(kLossThreads) zero_distill_kernel(const __grid_constant__ LossArgs a)
+// The exponentials of two logits below the largest: `hard` 2^(l d), `soft`
+// 2^(lz d).  SUMS 0: one serves both (in `hard`).  1: two of them.  2 and 4: the
+// temperature is that, and e^d is a power of e^(d / z): half of the
+// exponentials.
+template <int SUMS> __device__ __forceinline__ void exponentials(float2 d, float l, float lz, float2* hard, float2* soft)
 {
-    __shared__ float part[kLossWarps];
+    if constexpr (SUMS == 0) {
+        *hard = exp2_2(mul2(d, make_float2(l, l)));
+        return;
+    }
+    *soft = exp2_2(mul2(d, make_float2(lz, lz)));
+    if constexpr (SUMS == 1) {
+        *hard = exp2_2(mul2(d, make_float2(l, l)));
+    } else {
+        *hard = mul2(*soft, *soft);
+        if constexpr (SUMS == 4) *hard = mul2(*hard, *hard);
+    }
+}
+
+constexpr int kAtOnce = 4;         // vectors of a thread in flight
+constexpr int kFewTeachers = 256;  // up to these the teacher's warp merges its entries alone
+
+// VEC: a row of the gradient starts as far from a boundary of 16 bytes as its
+// row of logits.
+template <int BF16, int VEC, int SUMS, int kLossThreads>
+__global__ void __launch_bounds__(kLossThreads, kLossThreads == 128 ? 10 : 4) zero_distill_kernel(const __grid_constant__ LossArgs a)
+{
+    constexpr int kLossWarps = kLossThreads / 32;
     __shared__ Tops tops[kLossWarps];
-    __shared__ float p_of[kMostTeacher], s_of[kMostTeacher];
-    __shared__ int j_of[kMostTeacher];
+    __shared__ float p_of[kMostTeacher], s_of[kMostTeacher], v_of[kMostTeacher];
+    __shared__ __align__(16) int j_of[kMostTeacher];
+    __shared__ int soft_flag;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long row = blockIdx.x;
     let_successor_start();
@@ -118,13 +157,22 @@ __global__ void __launch_bounds__(kLossThreads) zero_distill_kernel(const __grid
     const float w = a.weights ? a.weights[row] : 1.0f;
     const int target = a.targets ? a.targets[row] : -1;
     const bool hard = a.hard != 0.0f && w != 0.0f && target >= 0 && target < a.V;
+    const bool teacher = a.soft != 0.0f && w != 0.0f && a.K > 0;
+    // the row's vectors lie in [head, rest); without them everything is rest
+    const int head = VEC ? min(a.V, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(s) & 15)) & 15) / 2) : 0;
+    const int rest = VEC ? head + (a.V - head) / 8 * 8 : 0;
+    const float s_target = hard ? load16(s, target, BF16) : 0.0f;
+    const float l1 = kLog2e, lz = kLog2e / a.z;
+    const float l = SUMS || hard ? l1 : lz; // one sum: the temperature of the term in use
+    // the threads that go over the row
+    const int self = teacher ? tid - 32 : tid, everyone = teacher ? kLossThreads - 32 : kLossThreads;
 
-    // the teacher's distribution
-    bool soft = a.soft != 0.0f && w != 0.0f && a.K > 0;
+    Tops mine = {-INFINITY, 0.0f, 0.0f};
     float entropy = 0.0f; // sum p log p
-    if (soft) {
+    if (self < 0) {
+        // the teacher's distribution
         float top = -INFINITY, bad = 0.0f;
-        for (int k = tid; k < a.K; k += kLossThreads) {
+        for (int k = lane; k < a.K; k += 32) {
             const int j = a.index[row * a.ldk + k];
             const bool in = j >= 0 && j < a.V;
             const float r = in ? teacher_at(a.teacher, row * a.ldk + k, a.teacher_type) : -INFINITY;
@@ -134,25 +182,88 @@ __global__ void __launch_bounds__(kLossThreads) zero_distill_kernel(const __grid
             top = fmaxf(top, r);
             if (r != r) bad = 1.0f;
         }
-        top = block_max(top, part);
-        bad = block_max(bad, part);
-        soft = top != -INFINITY || bad != 0.0f; // some entry has a probability
+        top = warp_max(top);
+        bad = warp_max(bad);
         float sum = 0.0f;
-        for (int k = tid; k < a.K; k += kLossThreads) sum += j_of[k] < 0 ? 0.0f : expf((p_of[k] - top) / a.z);
-        sum = block_sum(sum, part);
+        for (int k = lane; k < a.K; k += 32) sum += j_of[k] < 0 ? 0.0f : expf((p_of[k] - top) / a.z);
+        sum = warp_sum(sum);
         const float log_sum = logf(sum);
         float h = 0.0f;
-        for (int k = tid; k < a.K; k += kLossThreads) {
+        for (int k = lane; k < a.K; k += 32) {
             const float d = (p_of[k] - top) / a.z, p = j_of[k] < 0 ? 0.0f : expf(d) / sum;
             if (p != 0.0f) h += p * (d - log_sum); // NaN goes on
             p_of[k] = p;
         }
-        entropy = block_sum(h, part);
+        entropy = warp_sum(h);
+        if (lane == 0) soft_flag = top != -INFINITY || bad != 0.0f; // some entry has a probability
+    } else if (hard || teacher) {
+        // the largest logit and the sums
+        float base = 0.0f; // what is subtracted: the largest, while there is a finite one
+        float2 sum = make_float2(0.0f, 0.0f), sum_soft = sum;
+        auto raise = [&](float top) {
+            if (top > mine.top) {
+                const float d = mine.top - top;
+                const float f = fast_exp2(d * l), g = fast_exp2(d * lz);
+                sum = make_float2(sum.x * f, sum.y * f);
+                if (SUMS) sum_soft = make_float2(sum_soft.x * g, sum_soft.y * g);
+                base = mine.top = top;
+            }
+        };
+        auto take = [&](float2 v) {
+            float2 e, f;
+            exponentials<SUMS>(add2(v, make_float2(-base, -base)), l, lz, &e, &f);
+            sum = add2(sum, e);
+            if (SUMS) sum_soft = add2(sum_soft, f);
+        };
+        auto take8 = [&](const uint4& u) {
+            const float2 m = unpack16(max16<BF16>(max16<BF16>(u.x, u.y), max16<BF16>(u.z, u.w)), BF16);
+            raise(fmaxf(m.x, m.y));
+            take(unpack16(u.x, BF16));
+            take(unpack16(u.y, BF16));
+            take(unpack16(u.z, BF16));
+            take(unpack16(u.w, BF16));
+        };
+        if (VEC) {
+            int c = head + self * 8;
+            for (; c + (kAtOnce - 1) * everyone * 8 < rest; c += kAtOnce * everyone * 8) {
+                uint4 u[kAtOnce];
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k) u[k] = *reinterpret_cast<const uint4*>(s + c + k * everyone * 8);
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k) take8(u[k]);
+            }
+            for (; c < rest; c += everyone * 8) take8(*reinterpret_cast<const uint4*>(s + c));
+        }
+        // what lies before and behind the vectors: fewer than 16 elements where there are any
+        for (int c = self < head ? self : rest + self - head; c < a.V; c += everyone * 8) {
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int at = c + j * everyone;
+                v[j] = at < a.V && (j == 0 || !VEC) ? load16(s, at, BF16) : -INFINITY;
+            }
+            float top = v[0];
+#pragma unroll
+            for (int j = 1; j < 8; ++j) top = fmaxf(top, v[j]);
+            raise(top);
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) take(make_float2(v[j], v[j + 1]));
+            if (VEC) break;
+        }
+        mine.sum = sum.x + sum.y;
+        mine.soft = sum_soft.x + sum_soft.y;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            Tops other;
+            other.top = __shfl_xor_sync(0xffffffffu, mine.top, o);
+            other.sum = __shfl_xor_sync(0xffffffffu, mine.sum, o);
+            other.soft = __shfl_xor_sync(0xffffffffu, mine.soft, o);
+            mine = join(mine, other, l, lz);
+        }
     }
-    // the row's vectors lie in [head, rest); without them everything is rest
-    const int head = VEC ? min(a.V, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(s) & 15)) & 15) / 2) : 0;
-    const int rest = VEC ? head + (a.V - head) / 8 * 8 : 0;
-    const float s_target = hard ? load16(s, target, BF16) : 0.0f;
+    if (lane == 0) tops[warp] = mine;
+    __syncthreads();
+    const bool soft = teacher && soft_flag;
 
     if (!hard && !soft) { // nothing to learn from this row, whatever it holds
         if (tid == 0) a.loss[row] = 0.0f;
@@ -163,123 +274,86 @@ __global__ void __launch_bounds__(kLossThreads) zero_distill_kernel(const __grid
         }
         return;
     }
-
-    // the largest logit and the sums
-    const float l1 = kLog2e, lz = kLog2e / a.z;
-    const float l = BOTH || hard ? l1 : lz; // not BOTH: the one that is in use
-    Tops mine = {-INFINITY, 0.0f, 0.0f};
-    auto take = [&](const float (&v)[8]) {
-        float top = v[0];
-#pragma unroll
-        for (int j = 1; j < 8; ++j) top = fmaxf(top, v[j]);
-        if (top > mine.top) {
-            const float d = mine.top - top;
-            mine.sum *= fast_exp2(d * l);
-            if (BOTH) mine.soft *= fast_exp2(d * lz);
-            mine.top = top;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float d = below(v[j], mine.top);
-            mine.sum += fast_exp2(d * l);
-            if (BOTH) mine.soft += fast_exp2(d * lz);
-        }
-    };
-    if (VEC) {
-#pragma unroll 4
-        for (int c = head + tid * 8; c < rest; c += kLossThreads * 8) {
-            float v[8];
-            widen8(*reinterpret_cast<const uint4*>(s + c), v, BF16);
-            take(v);
-        }
-    }
-    // what lies before and behind the vectors: fewer than 16 elements where there are any
-    for (int c = tid < head ? tid : rest + tid - head; c < a.V; c += kLossThreads * 8) {
-        float v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int at = c + j * kLossThreads;
-            v[j] = at < a.V && (j == 0 || !VEC) ? load16(s, at, BF16) : -INFINITY;
-        }
-        take(v);
-        if (VEC) break;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        Tops other;
-        other.top = __shfl_xor_sync(0xffffffffu, mine.top, o);
-        other.sum = __shfl_xor_sync(0xffffffffu, mine.sum, o);
-        other.soft = __shfl_xor_sync(0xffffffffu, mine.soft, o);
-        mine = join(mine, other, l, lz);
-    }
-    if (lane == 0) tops[warp] = mine;
-    __syncthreads();
     Tops all = tops[0];
 #pragma unroll
     for (int k = 1; k < kLossWarps; ++k) all = join(all, tops[k], l, lz);
-    const float sum_hard = all.sum, sum_soft = BOTH ? all.soft : all.sum;
+    const float sum_hard = all.sum, sum_soft = SUMS ? all.soft : all.sum;
+    const float base = all.top == -INFINITY ? 0.0f : all.top;
+    // the gradient: f_hard 2^(l1 (s - top)) + f_soft 2^(lz (s - top))
+    const float g = w * a.scale, g_soft = g * a.soft * a.z;
+    const float f_hard = hard ? g * a.hard / sum_hard : 0.0f, f_soft = soft ? g_soft / sum_soft : 0.0f;
+    auto slope = [&](float2 v) {
+        float2 e, f;
+        exponentials<SUMS>(add2(v, make_float2(-base, -base)), l, lz, &e, &f);
+        if (SUMS) return fma2(make_float2(f_hard, f_hard), e, mul2(make_float2(f_soft, f_soft), f));
+        return mul2(make_float2(f_hard + f_soft, f_hard + f_soft), e);
+    };
+    auto slope1 = [&](float v) { return slope(make_float2(v, v)).x; };
+    // the gradient's value at an entry: an index that occurs twice has the same, whole value both times
+    auto merged = [&](int k) {
+        const int j = j_of[k];
+        float p = 0.0f;
+        for (int i = 0; i < a.K; ++i)
+            if (j_of[i] == j) p += p_of[i];
+        float v = slope1(s_of[k]) - g_soft * p;
+        if (hard && j == target) v -= g * a.hard;
+        return v;
+    };
 
-    // the loss
-    float cross = 0.0f; // sum p log q'
-    if (soft) {
-        float h = 0.0f;
-        const float log_sum = logf(sum_soft);
-        for (int k = tid; k < a.K; k += kLossThreads) {
-            const float p = p_of[k];
-            if (p != 0.0f) h += p * ((s_of[k] - all.top) / a.z - log_sum);
+    bool listed = false; // the target is among the teacher's
+    if (self < 0 || (!teacher && warp == 0)) {
+        float cross = 0.0f; // sum p log q'
+        if (soft) {
+            float h = 0.0f;
+            const float log_sum = logf(sum_soft);
+            for (int k = lane; k < a.K; k += 32) {
+                const float p = p_of[k];
+                if (p != 0.0f) h += p * ((s_of[k] - all.top) / a.z - log_sum);
+                listed = listed || j_of[k] == target;
+            }
+            cross = warp_sum(h);
+            listed = __any_sync(0xffffffffu, listed);
+            if (a.grad && a.K <= kFewTeachers)
+                for (int k = lane; k < a.K; k += 32) v_of[k] = merged(k);
         }
-        cross = block_sum(h, part);
-    }
-    if (tid == 0) {
-        float v = 0.0f;
-        if (hard) v += a.hard * (logf(sum_hard) - (s_target - all.top));
-        if (soft) v += a.soft * a.z * a.z * (entropy - cross);
-        a.loss[row] = w * v;
+        if (lane == 0) {
+            float v = 0.0f;
+            if (hard) v += a.hard * (logf(sum_hard) - (s_target - all.top));
+            if (soft) v += a.soft * a.z * a.z * (entropy - cross);
+            a.loss[row] = w * v;
+        }
     }
     if (!a.grad) return;
-
-    // the gradient: f_hard 2^(l1 (s - top)) + f_soft 2^(lz (s - top))
-    const float g = w * a.scale;
-    const float f_hard = hard ? g * a.hard / sum_hard : 0.0f, f_soft = soft ? g * a.soft * a.z / sum_soft : 0.0f;
-    const float f_one = f_hard + f_soft;
-    auto slope = [&](float x) {
-        const float d = below(x, all.top);
-        if (BOTH) return fmaf(f_hard, fast_exp2(d * l1), f_soft * fast_exp2(d * lz));
-        return f_one * fast_exp2(d * l);
-    };
-    if (VEC) {
-#pragma unroll 4
-        for (int c = head + tid * 8; c < rest; c += kLossThreads * 8) {
-            float v[8];
-            widen8(*reinterpret_cast<const uint4*>(s + c), v, BF16);
+    if (self >= 0) {
+        auto write8 = [&](int c, const uint4& u) {
+            const float2 v0 = slope(unpack16(u.x, BF16)), v1 = slope(unpack16(u.y, BF16)), v2 = slope(unpack16(u.z, BF16)), v3 = slope(unpack16(u.w, BF16));
+            *reinterpret_cast<uint4*>(ds + c) = make_uint4(pack16(v0.x, v0.y, BF16), pack16(v1.x, v1.y, BF16), pack16(v2.x, v2.y, BF16), pack16(v3.x, v3.y, BF16));
+        };
+        if (VEC) {
+            int c = head + self * 8;
+            for (; c + (kAtOnce - 1) * everyone * 8 < rest; c += kAtOnce * everyone * 8) {
+                uint4 u[kAtOnce];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = slope(v[j]);
-            *reinterpret_cast<uint4*>(ds + c) = pack8(v, BF16);
+                for (int k = 0; k < kAtOnce; ++k) u[k] = *reinterpret_cast<const uint4*>(s + c + k * everyone * 8);
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k) write8(c + k * everyone * 8, u[k]);
+            }
+            for (; c < rest; c += everyone * 8) write8(c, *reinterpret_cast<const uint4*>(s + c));
+            if (self < head) store16(ds, self, slope1(load16(s, self, BF16)), BF16);
         }
-        if (tid < head) store16(ds, tid, slope(load16(s, tid, BF16)), BF16);
-    }
 #pragma unroll 8
-    for (int c = rest + tid; c < a.V; c += kLossThreads) store16(ds, c, slope(load16(s, c, BF16)), BF16);
+        for (int c = rest + self; c < a.V; c += everyone) store16(ds, c, slope1(load16(s, c, BF16)), BF16);
+    }
     __syncthreads(); // every element has its sum's part
-    const float g_soft = g * a.soft * a.z;
-    if (soft) {
-        for (int k = tid; k < a.K; k += kLossThreads) {
-            const int j = j_of[k];
-            if (j < 0) continue;
-            float p = 0.0f; // an index that occurs twice: each writes the same whole value
-            for (int i = 0; i < a.K; ++i)
-                if (j_of[i] == j) p += p_of[i];
-            float v = slope(s_of[k]) - g_soft * p;
-            if (hard && j == target) v -= g * a.hard;
-            store16(ds, j, v, BF16);
-        }
+    if (soft && a.K <= kFewTeachers) {
+        if (self < 0)
+            for (int k = lane; k < a.K; k += 32)
+                if (j_of[k] >= 0) store16(ds, j_of[k], v_of[k], BF16);
+    } else if (soft) {
+        for (int k = tid; k < a.K; k += kLossThreads)
+            if (j_of[k] >= 0) store16(ds, j_of[k], merged(k), BF16);
     }
-    if (hard && tid == 0) {
-        bool listed = false;
-        if (soft)
-            for (int i = 0; i < a.K; ++i) listed = listed || j_of[i] == target;
-        if (!listed) store16(ds, target, slope(s_target) - g * a.hard, BF16);
-    }
+    if (hard && !listed && tid == 0) store16(ds, target, slope1(s_target) - g * a.hard, BF16);
 }
 
 // ---------------------------------------------------------------------------
@@ -288,11 +362,23 @@ __global__ void __launch_bounds__(kLossThreads) zero_distill_kernel(const __grid
 
 using LossKernel = void (*)(LossArgs);
 
-template <int BF16> LossKernel pick_loss(bool vec, bool both)
+template <int BF16, int VEC, int THREADS> LossKernel pick_loss(int sums)
 {
-    if (vec) return both ? zero_distill_kernel<BF16, 1, 1> : zero_distill_kernel<BF16, 1, 0>;
-    return both ? zero_distill_kernel<BF16, 0, 1> : zero_distill_kernel<BF16, 0, 0>;
+    switch (sums) {
+    case 0: return zero_distill_kernel<BF16, VEC, 0, THREADS>;
+    case 2: return zero_distill_kernel<BF16, VEC, 2, THREADS>;
+    case 4: return zero_distill_kernel<BF16, VEC, 4, THREADS>;
+    default: return zero_distill_kernel<BF16, VEC, 1, THREADS>;
+    }
 }
+
+// Rows below this take 128 threads, ten rows an SM: a row's time is then the
+// latency of its steps (18280 rows of 5000 with 64 teacher's logits 129 us, 256
+// threads 280; without a teacher 74, 150).  Rows above it 256, four an SM, so
+// that L2 holds all of them for the second pass (8192 rows of 44629 with 64:
+// 280 us, 128 threads 390, 512 threads 380; the row in shared memory instead,
+// two CTAs an SM, 375).
+constexpr int64_t kShortRows = 16384;
 
 // A matrix for share(), which counts in 16 bits.
 struct Extent {
@@ -341,8 +427,15 @@ extern "C" int zero_distill_loss(const void* logits, int64_t ldl, const int32_t*
     a.ldl = ldl, a.ldk = ldk, a.ldg = lddl, a.V = static_cast<int>(V), a.K = static_cast<int>(K), a.teacher_type = teacher_type;
     a.hard = 1.0f - alpha, a.soft = alpha, a.z = temperature, a.scale = grad_scale;
     const bool both = alpha > 0.0f && alpha < 1.0f && K > 0 && temperature != 1.0f;
+    const int sums = !both ? 0 : temperature == 2.0f ? 2 : temperature == 4.0f ? 4 : 1;
     // every row of the gradient starts as far from a boundary of 16 bytes as that of the logits
     const bool vec = !dlogits || ((addr(logits) - addr(dlogits)) % 16 == 0 && (ldl - lddl) % 8 == 0);
-    return launch_after(type == ZERO_TYPE_BF16 ? pick_loss<1>(vec, both) : pick_loss<0>(vec, both), a, T, kLossThreads, 0, 1,
-                        static_cast<cudaStream_t>(cuda_stream));
+    const int bf16 = type == ZERO_TYPE_BF16;
+    LossKernel fn;
+    const bool few = V < kShortRows;
+    if (few && vec) fn = bf16 ? pick_loss<1, 1, 128>(sums) : pick_loss<0, 1, 128>(sums);
+    else if (few) fn = bf16 ? pick_loss<1, 0, 128>(sums) : pick_loss<0, 0, 128>(sums);
+    else if (vec) fn = bf16 ? pick_loss<1, 1, 256>(sums) : pick_loss<0, 1, 256>(sums);
+    else fn = bf16 ? pick_loss<1, 0, 256>(sums) : pick_loss<0, 0, 256>(sums);
+    return launch_after(fn, a, T, few ? 128 : 256, 0, 1, static_cast<cudaStream_t>(cuda_stream));
 }
