@@ -45,31 +45,24 @@ template <int BF16, int VEC> __global__ void __launch_bounds__(256) zero_embed_k
     const bool there = id >= 0 && id < a.V;
     const uint16_t* from = static_cast<const uint16_t*>(a.table) + (there ? id * a.ldt : 0);
     uint16_t* to = static_cast<uint16_t*>(a.y) + t * a.ldy;
-    if constexpr (VEC) {
-        uint4 u[4];
+    uint4 u[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int c = c0 + (k * 32 + lane) * 8;
-            u[k] = make_uint4(0, 0, 0, 0);
-            if (there && c + 8 <= a.D) u[k] = *reinterpret_cast<const uint4*>(from + c);
-        }
+    for (int k = 0; k < 4; ++k) {
+        const int c = c0 + (k * 32 + lane) * 8;
+        u[k] = make_uint4(0, 0, 0, 0);
+        if (there && c < a.D) u[k] = VEC ? *reinterpret_cast<const uint4*>(from + c) : load_any(from, c, a.D);
+    }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int c = c0 + (k * 32 + lane) * 8;
-            float v[8];
+    for (int k = 0; k < 4; ++k) {
+        const int c = c0 + (k * 32 + lane) * 8;
+        float v[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-            add8(v, u[k], BF16);
+        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+        add8(v, u[k], BF16);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = there ? v[j] * a.scale : 0.0f;
-            if (c + 8 <= a.D) *reinterpret_cast<uint4*>(to + c) = pack8(v, BF16);
-        }
-    } else {
-#pragma unroll 8
-        for (int k = 0; k < kLookPiece / 32; ++k) {
-            const int c = c0 + k * 32 + lane;
-            if (c < a.D) store16(to, c, there ? load16(from, c, BF16) * a.scale : 0.0f, BF16);
-        }
+        for (int j = 0; j < 8; ++j) v[j] = there ? v[j] * a.scale : 0.0f;
+        if (!VEC) store_any(to, c, a.D, pack8(v, BF16), lane == 0, lane == 31);
+        else if (c < a.D) *reinterpret_cast<uint4*>(to + c) = pack8(v, BF16);
     }
 }
 
@@ -192,6 +185,17 @@ template <int ROUNDS> __global__ void __launch_bounds__(kSortThreads) zero_sort_
     }
 }
 
+// Zeros to a row, by a warp.
+template <int VEC> __device__ __forceinline__ void clear_row(uint16_t* row, int D, int lane)
+{
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    for (int c0 = 0; c0 < D; c0 += 256) {
+        const int c = c0 + lane * 8;
+        if (!VEC) store_any(row, c, D, zero, lane == 0, lane == 31);
+        else if (c < D) *reinterpret_cast<uint4*>(row + c) = zero;
+    }
+}
+
 // The whole sort by one cluster: a CTA holds every eighth part of the order in
 // its shared memory, a thread ROUNDS tokens in registers.  Per pass the CTAs
 // rank their tokens, read each other's digit counts, and write the tokens to
@@ -238,11 +242,8 @@ template <int ROUNDS> __global__ void __launch_bounds__(kClusterThreads) zero_so
         const int warps = (gridDim.x - kCluster) * kClusterWarps;
         for (long long v = (blockIdx.x - kCluster) * kClusterWarps + warp; v < a.clear; v += warps) {
             uint16_t* row = a.dtable + v * a.lddt;
-            if (a.vec) {
-                for (int c = lane * 8; c < a.D; c += 256) *reinterpret_cast<uint4*>(row + c) = make_uint4(0, 0, 0, 0);
-            } else {
-                for (int c = lane; c < a.D; c += 32) row[c] = 0;
-            }
+            if (a.vec) clear_row<1>(row, a.D, lane);
+            else clear_row<0>(row, a.D, lane);
         }
         return;
     }
@@ -338,51 +339,31 @@ struct RunArgs {
     const int2* sorted;
     const void* dy;
     void* dtable;
-    float* parts;        // [chunks][2][D]: of the run that began before the chunk, of the one that goes on behind it
+    float* parts;        // [chunks][2][pitch]: of the run that began before the chunk, of the one that goes on behind it
     long long lddy, lddt, T, sum_tasks, join_tasks, tasks, cleared; // rows of the table below `cleared` are 0 already
-    int D, V, stripes, chunk, add;
+    int D, V, stripes, chunk, add, pitch;
     float scale;
 };
 
-template <int VEC> __device__ __forceinline__ int stripe_column(int c0, int j, int lane) { return VEC ? c0 + lane * 8 + j : c0 + j * 32 + lane; }
-
-// This lane's eight elements of a row from memory, as pairs.
-template <int VEC> __device__ __forceinline__ uint4 get_row(const uint16_t* row, int c0, int lane, int D)
+// This lane's eight elements of a row from memory.
+template <int VEC> __device__ __forceinline__ uint4 get_row(const uint16_t* row, int c, int D)
 {
-    if constexpr (VEC) {
-        const int c = c0 + lane * 8;
-        return c < D ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0);
-    } else {
-        uint32_t h[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int c = stripe_column<0>(c0, j, lane);
-            h[j] = c < D ? row[c] : 0;
-        }
-        return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
-    }
+    if constexpr (!VEC) return load_any(row, c, D);
+    return c < D ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0);
 }
 
 // A run's sum, plus what the table's gradient held (zeros where it does not
 // count), to its row.
 template <int BF16, int VEC>
-__device__ __forceinline__ void put_row(const RunArgs& a, int key, int c0, int lane, const float (&sum)[8], const uint4& old)
+__device__ __forceinline__ void put_row(const RunArgs& a, int key, int c, int lane, const float (&sum)[8], const uint4& old)
 {
     uint16_t* row = static_cast<uint16_t*>(a.dtable) + key * a.lddt;
     float v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = sum[j] * a.scale;
     if (a.add) add8(v, old, BF16);
-    if constexpr (VEC) {
-        const int c = c0 + lane * 8;
-        if (c < a.D) *reinterpret_cast<uint4*>(row + c) = pack8(v, BF16);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int c = stripe_column<0>(c0, j, lane);
-            if (c < a.D) store16(row, c, v[j], BF16);
-        }
-    }
+    if constexpr (!VEC) store_any(row, c, a.D, pack8(v, BF16), lane == 0, lane == 31);
+    else if (c < a.D) *reinterpret_cast<uint4*>(row + c) = pack8(v, BF16);
 }
 
 // Rows of the table without a token become 0: each lane looks its row up among
@@ -405,17 +386,13 @@ template <int VEC> __device__ __forceinline__ void clear_rows(const RunArgs& a, 
         const int k = __ffs(todo) - 1;
         todo &= todo - 1;
         uint16_t* row = static_cast<uint16_t*>(a.dtable) + (v0 + k) * a.lddt;
-        if (VEC) {
-            for (int c = lane * 8; c < a.D; c += 256) *reinterpret_cast<uint4*>(row + c) = make_uint4(0, 0, 0, 0);
-        } else {
-            for (int c = lane; c < a.D; c += 32) row[c] = 0;
-        }
+        clear_row<VEC>(row, a.D, lane);
     }
 }
 
 template <int BF16, int VEC, int ADD> __global__ void __launch_bounds__(256) zero_embed_grad_kernel(const __grid_constant__ RunArgs a)
 {
-    constexpr int kAhead = VEC && !ADD ? 8 : 4; // rows in flight
+    constexpr int kAhead = VEC && !ADD ? 8 : 4; // rows in flight (two granules each off 16 bytes)
     const int lane = threadIdx.x & 31;
     const long long task = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
     let_successor_start();
@@ -426,7 +403,7 @@ template <int BF16, int VEC, int ADD> __global__ void __launch_bounds__(256) zer
         return;
     }
     const long long chunk = task / a.stripes, first = chunk * a.chunk, end = min(a.T, first + a.chunk);
-    const int c0 = static_cast<int>(task - chunk * a.stripes) * kStripe;
+    const int col = static_cast<int>(task - chunk * a.stripes) * kStripe + lane * 8;
     const uint16_t* dy = static_cast<const uint16_t*>(a.dy);
     float sum[8];
 #pragma unroll
@@ -434,12 +411,10 @@ template <int BF16, int VEC, int ADD> __global__ void __launch_bounds__(256) zer
     bool begun = first > 0 && a.sorted[first - 1].x == a.sorted[first].x; // the run began before the chunk
     bool open = false;                                                     // the sum holds a row
     auto put_part = [&]() {
-        float* part = a.parts + (chunk * 2 + (begun ? 0 : 1)) * a.D;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int c = stripe_column<VEC>(c0, j, lane);
-            if (c < a.D) part[c] = sum[j];
-        }
+        if (col >= a.D) return; // a part has room for whole vectors
+        float4* part = reinterpret_cast<float4*>(a.parts + (chunk * 2 + (begun ? 0 : 1)) * a.pitch + col);
+        part[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+        part[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
     };
     for (long long s = first; s < end; s += 32) {
         const int2 none = make_int2(a.V, 0);
@@ -453,11 +428,11 @@ template <int BF16, int VEC, int ADD> __global__ void __launch_bounds__(256) zer
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
                 const uint16_t* row = dy + __shfl_sync(0xffffffffu, mine.y, i0 + i) * a.lddy;
-                u[i] = i0 + i < n ? get_row<VEC>(row, c0, lane, a.D) : make_uint4(0, 0, 0, 0);
+                u[i] = i0 + i < n ? get_row<VEC>(row, col, a.D) : make_uint4(0, 0, 0, 0);
                 // the table's row as it was: read with the others, for the token that ends its run
                 if constexpr (ADD) {
                     const int key = __shfl_sync(0xffffffffu, mine.x, i0 + i);
-                    o[i] = i0 + i < n && (ends >> (i0 + i) & 1) ? get_row<VEC>(static_cast<const uint16_t*>(a.dtable) + key * a.lddt, c0, lane, a.D)
+                    o[i] = i0 + i < n && (ends >> (i0 + i) & 1) ? get_row<VEC>(static_cast<const uint16_t*>(a.dtable) + key * a.lddt, col, a.D)
                                                                 : make_uint4(0, 0, 0, 0);
                 }
             }
@@ -469,7 +444,7 @@ template <int BF16, int VEC, int ADD> __global__ void __launch_bounds__(256) zer
                 if (!(ends >> (i0 + i) & 1)) continue;
                 const int key = __shfl_sync(0xffffffffu, mine.x, i0 + i);
                 if (begun) put_part();
-                else put_row<BF16, VEC>(a, key, c0, lane, sum, o[ADD ? i : 0]);
+                else put_row<BF16, VEC>(a, key, col, lane, sum, o[ADD ? i : 0]);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
                 begun = open = false;
@@ -509,33 +484,21 @@ template <int BF16, int VEC> __global__ void __launch_bounds__(128) zero_embed_j
         if (n < 32) break;
     }
     const int c0 = static_cast<int>(task - chunk * stripes) * kJoinStripe;
-    // columns; lanes behind the row read its end, and write nothing
-    int at[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) at[j] = VEC ? min(c0 + lane * 4, a.D - 4) + j : min(c0 + j * 32 + lane, a.D - 1);
+    const int at = min(c0 + lane * 4, a.pitch - 4); // lanes behind the row read its end, and write nothing
     uint16_t* row = static_cast<uint16_t*>(a.dtable) + key * a.lddt;
     float sum[4], old[4];
+    const float4 tail = *reinterpret_cast<const float4*>(a.parts + (chunk * 2 + 1) * a.pitch + at);
+    sum[0] = tail.x, sum[1] = tail.y, sum[2] = tail.z, sum[3] = tail.w;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        sum[j] = a.parts[(chunk * 2 + 1) * a.D + at[j]];
-        old[j] = a.add ? load16(row, at[j], BF16) : 0.0f;
-    }
+    for (int j = 0; j < 4; ++j) old[j] = a.add && at + j < a.D ? load16(row, at + j, BF16) : 0.0f;
     for (long long c = chunk + 1; c <= last; c += kJoinAhead) {
         const int n = static_cast<int>(min(static_cast<long long>(kJoinAhead), last + 1 - c));
         float v[kJoinAhead][4];
 #pragma unroll
         for (int k = 0; k < kJoinAhead; ++k) {
-            const float* part = a.parts + (c + k) * 2 * a.D;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[k][j] = 0.0f;
-            if (k >= n) continue;
-            if constexpr (VEC) {
-                const float4 f = __ldcg(reinterpret_cast<const float4*>(part + at[0]));
-                v[k][0] = f.x, v[k][1] = f.y, v[k][2] = f.z, v[k][3] = f.w;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[k][j] = __ldcg(part + at[j]);
-            }
+            float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (k < n) f = __ldcg(reinterpret_cast<const float4*>(a.parts + (c + k) * 2 * a.pitch + at));
+            v[k][0] = f.x, v[k][1] = f.y, v[k][2] = f.z, v[k][3] = f.w;
         }
         __syncwarp(); // keeps the reads before it: the compiler adds each part before it reads the next else (15 us instead of 6)
 #pragma unroll
@@ -545,12 +508,13 @@ template <int BF16, int VEC> __global__ void __launch_bounds__(128) zero_embed_j
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) sum[j] = sum[j] * a.scale + old[j];
-    if constexpr (VEC) {
-        if (c0 + lane * 4 < a.D) *reinterpret_cast<uint2*>(row + at[0]) = make_uint2(pack16(sum[0], sum[1], BF16), pack16(sum[2], sum[3], BF16));
+    if (c0 + lane * 4 >= a.D) return;
+    if (VEC) {
+        *reinterpret_cast<uint2*>(row + at) = make_uint2(pack16(sum[0], sum[1], BF16), pack16(sum[2], sum[3], BF16));
     } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (c0 + j * 32 + lane < a.D) store16(row, at[j], sum[j], BF16);
+            if (at + j < a.D) store16(row, at + j, sum[j], BF16);
     }
 }
 
@@ -598,7 +562,7 @@ GradPlan plan_grad(int64_t T, int64_t D, int64_t V, void* workspace)
     p.pairs[0] = static_cast<int2*>(c.take(T * 8));
     p.pairs[1] = p.cluster ? p.pairs[0] : static_cast<int2*>(c.take(T * 8));
     p.counts = static_cast<uint32_t*>(c.take(static_cast<int64_t>(p.passes) * p.blocks * kDigits * 4));
-    p.parts = static_cast<float*>(c.take(p.chunks * 2 * D * 4));
+    p.parts = static_cast<float*>(c.take(p.chunks * 2 * up(D, 8) * 4));
     p.bytes = c.used;
     return p;
 }
@@ -687,7 +651,7 @@ extern "C" int zero_embed_backward(const int32_t* ids, const void* dy, int64_t l
         return ZERO_EOVERLAP;
     RunArgs r{};
     r.dy = dy, r.dtable = dtable, r.parts = p.parts, r.lddy = lddy, r.lddt = lddt, r.T = T, r.D = static_cast<int>(D), r.V = static_cast<int>(V);
-    r.stripes = static_cast<int>(p.stripes), r.chunk = p.chunk, r.add = add != 0, r.scale = scale;
+    r.stripes = static_cast<int>(p.stripes), r.chunk = p.chunk, r.pitch = static_cast<int>(up(D, 8)), r.add = add != 0, r.scale = scale;
     r.sum_tasks = p.chunks * p.stripes;
     r.join_tasks = p.chunks * ((D + kJoinStripe - 1) / kJoinStripe);
     if (!add && p.cluster) r.cleared = std::min<int64_t>(V, kClearBytes / (2 * D));

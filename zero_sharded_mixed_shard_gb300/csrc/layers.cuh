@@ -95,6 +95,77 @@ __device__ __forceinline__ uint16_t* at16(const void* p, long long ld, long long
 }
 
 // ---------------------------------------------------------------------------
+// Rows that start anywhere: reads and writes by whole 16-byte granules
+// ---------------------------------------------------------------------------
+
+// Elements before p in its 16-byte granule.
+__device__ __forceinline__ int phase_of(const uint16_t* p) { return static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15) >> 1; }
+
+// Elements e .. e + 7 of the sixteen in a and b, 0 <= e < 8.
+__device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, int e)
+{
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int j = 0; j < 6; ++j) w[j] = e & 4 ? w[j + 2] : w[j];
+#pragma unroll
+    for (int j = 0; j < 5; ++j) w[j] = e & 2 ? w[j + 1] : w[j];
+    const int half = (e & 1) * 16;
+    return make_uint4(__funnelshift_r(w[0], w[1], half), __funnelshift_r(w[1], w[2], half), __funnelshift_r(w[2], w[3], half),
+                      __funnelshift_r(w[3], w[4], half));
+}
+
+// The first n of eight elements, zeros behind them.
+__device__ __forceinline__ uint4 first_of(const uint4& v, int n)
+{
+    if (n >= 8) return v;
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = n >= 2 * j + 2 ? w[j] : n == 2 * j + 1 ? w[j] & 0xffffu : 0u;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Elements [c, c + 8) of a row of D, zeros past its end.  Reads only granules
+// that hold an element of the row.
+__device__ __forceinline__ uint4 load_any(const uint16_t* row, int c, int D)
+{
+    uint4 a = make_uint4(0, 0, 0, 0), b = a;
+    const int e = phase_of(row + c);
+    const uint4* from = reinterpret_cast<const uint4*>(row + c - e);
+    if (c < D) a = from[0];
+    if (e && c + 8 - e < D) b = from[1];
+    return first_of(shifted(a, b, e), D - c);
+}
+
+// Elements [c, c + 8) of a row of D from each of a run of lanes with
+// neighbouring c, all of which call this; `first` and `last` mark its ends.  A
+// granule is written whole where the run holds all of it, else by elements.
+__device__ __forceinline__ void store_any(uint16_t* row, int c, int D, const uint4& v, bool first, bool last)
+{
+    const int e = phase_of(row + c);
+    uint4 before;
+    before.x = __shfl_up_sync(0xffffffffu, v.x, 1);
+    before.y = __shfl_up_sync(0xffffffffu, v.y, 1);
+    before.z = __shfl_up_sync(0xffffffffu, v.z, 1);
+    before.w = __shfl_up_sync(0xffffffffu, v.w, 1);
+    const uint4 g = e ? shifted(before, v, 8 - e) : v; // the granule that holds element c
+    const int at = c - e;
+    if (at < D && at + 8 <= D && (!first || !e)) {
+        *reinterpret_cast<uint4*>(row + at) = g;
+    } else if (at < D) {
+        const uint32_t w[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (at + j < D && (!first || j >= e)) row[at + j] = static_cast<uint16_t>(w[j >> 1] >> (j & 1) * 16);
+    }
+    if (last && e) { // what lies in the granule behind
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 1; j < 8; ++j)
+            if (j >= 8 - e && c + j < D) row[c + j] = static_cast<uint16_t>(w[j >> 1] >> (j & 1) * 16);
+    }
+}
+
+// ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
 

@@ -7,17 +7,15 @@
 //             dw = sum over rows of dy h,   db = sum over rows of dy
 //
 // Both are bound by HBM: a row is read once, held in registers between its
-// statistics and its use, and written once.  A group of threads shares a row
-// (a warp for narrow ones, a CTA for wide ones), each with vectors of 8
-// elements; the variance is that of the centred values, not a difference of
+// statistics and its use, and written once, while the rows to come are on their
+// way to shared memory.  A group of threads shares a row (eight lanes for
+// narrow ones, a CTA for wide ones), each with vectors of 8 elements; the variance is that of the centred values, not a difference of
 // large sums.  In the backward pass a thread keeps its columns' sums of dw and
 // db over all rows of its group; the groups' sums go to the workspace and a
 // second launch adds them in a fixed order, so that a call repeats its bits.
 #include "layers.cuh"
 
 namespace {
-
-constexpr int kNormThreads = 256; // of a CTA, unless a row takes more
 
 struct NormArgs {
     const void* x;
@@ -52,119 +50,169 @@ struct NormSumArgs {
     int D, groups, bf16;
 };
 
-// Eight elements of a row as they are held between two uses.
-struct Packed {
-    uint32_t u[4];
-};
+// A row's columns among the GROUP threads that share it: eight neighbours a
+// thread, GROUP threads beside each other, then the next vector of each.
+template <int GROUP> __device__ __forceinline__ int column(int k, int self) { return (k * GROUP + self) * 8; }
 
-// Column j of a thread's vector k: 8 neighbours where rows lie on 16 bytes,
-// else elements a group's width apart, so that a warp's accesses stay next to
-// each other.
-template <int VEC, int GROUP> __device__ __forceinline__ int column(int k, int j, int self)
+// VEC: rows lie on 16 bytes and hold whole vectors.  Else they start anywhere.
+template <int VEC> __device__ __forceinline__ uint4 load_row(const uint16_t* row, int c, int D)
 {
-    return VEC ? (k * GROUP + self) * 8 + j : (k * 8 + j) * GROUP + self;
+    if constexpr (!VEC) return load_any(row, c, D);
+    return c < D ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0);
 }
 
-template <int VEC, int GROUP>
-__device__ __forceinline__ Packed load_row(const uint16_t* row, int k, int self, int D)
+// By whole warps: lanes of a group that has no row pass D 0.
+template <int VEC, int GROUP> __device__ __forceinline__ void store_row(uint16_t* row, int c, int self, int D, const uint4& v)
 {
-    Packed p;
-    if constexpr (VEC) {
-        const int c = column<1, GROUP>(k, 0, self);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (c < D) v = *reinterpret_cast<const uint4*>(row + c);
-        p.u[0] = v.x, p.u[1] = v.y, p.u[2] = v.z, p.u[3] = v.w;
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int c0 = column<0, GROUP>(k, 2 * j, self), c1 = column<0, GROUP>(k, 2 * j + 1, self);
-            const uint32_t lo = c0 < D ? row[c0] : 0, hi = c1 < D ? row[c1] : 0;
-            p.u[j] = lo | hi << 16;
-        }
-    }
-    return p;
+    constexpr int kRun = GROUP < 32 ? GROUP : 32; // lanes beside each other in a row
+    if constexpr (!VEC) store_any(row, c, D, v, self % kRun == 0, self % kRun == kRun - 1);
+    else if (c < D) *reinterpret_cast<uint4*>(row + c) = v;
 }
 
-template <int VEC, int GROUP, int BF16>
-__device__ __forceinline__ void store_row(uint16_t* row, int k, int self, int D, const float (&v)[8])
+template <int BF16> __device__ __forceinline__ void widen(const uint4& u, float (&v)[8])
 {
-    if constexpr (VEC) {
-        const int c = column<1, GROUP>(k, 0, self);
-        if (c < D) *reinterpret_cast<uint4*>(row + c) = pack8(v, BF16);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int c = column<0, GROUP>(k, j, self);
-            if (c < D) store16(row, c, v[j], BF16);
-        }
-    }
-}
-
-template <int BF16> __device__ __forceinline__ void widen(const Packed& p, float (&v)[8])
-{
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const float2 f = unpack16(p.u[j], BF16);
+        const float2 f = unpack16(w[j], BF16);
         v[2 * j] = f.x;
         v[2 * j + 1] = f.y;
     }
 }
 
-// Sums over a group's threads of N values, the same in every thread.  `part`
-// has N floats for each of the group's warps; the barriers are the whole CTA's,
-// so every thread of it calls this the same number of times.
-template <int GROUP, int N> __device__ __forceinline__ void group_sum(float (&v)[N], float* part)
+// Rows to come, copied to shared memory ahead of their use: AHEAD of them,
+// STREAMS matrices, VPT vectors of each of the CTA's threads.  VEC: a thread
+// copies what it reads itself, and waits for nobody else.  Else the granules
+// that hold a run's columns (a run: the lanes of a warp that share a row) are
+// copied by its lanes, one more than there are lanes, and a lane reads two.
+template <int VEC, int GROUP, int VPT, int STREAMS, int AHEAD, int THREADS> struct Rows {
+    static constexpr int kRun = GROUP < 32 ? GROUP : 32, kSlots = THREADS / kRun * (VEC ? kRun : kRun + 1);
+    static constexpr int kBytes = AHEAD * STREAMS * VPT * kSlots * 16;
+    uint4* base;
+    int self, place; // within the group; of this thread's first granule among kSlots
+
+    __device__ __forceinline__ Rows(unsigned char* raw, int self_) : base(reinterpret_cast<uint4*>(raw)), self(self_)
+    {
+        place = VEC ? threadIdx.x : threadIdx.x / kRun * (kRun + 1) + threadIdx.x % kRun;
+    }
+    __device__ __forceinline__ uint4* at(int slot, int stream, int k) { return base + ((slot * STREAMS + stream) * VPT + k) * kSlots + place; }
+    static __device__ __forceinline__ void copy16(void* to, const void* from)
+    {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
+    }
+    // Granules that hold no element of the row are not read.
+    __device__ __forceinline__ void copy(int slot, int stream, const uint16_t* row, int D)
+    {
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int c = column<GROUP>(k, self);
+            if constexpr (VEC) {
+                if (c < D) copy16(at(slot, stream, k), row + c);
+            } else {
+                const int e = phase_of(row + c);
+                if (c - e < D) copy16(at(slot, stream, k), row + c - e);
+                if (self % kRun == kRun - 1 && e && c + 8 - e < D) copy16(at(slot, stream, k) + 1, row + c - e + 8);
+            }
+        }
+    }
+    static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    static __device__ __forceinline__ void wait()
+    {
+        asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
+        if (!VEC) __syncwarp();
+    }
+    // Before a slot that has been read is copied to again.
+    static __device__ __forceinline__ void read()
+    {
+        if (!VEC) __syncwarp();
+    }
+    __device__ __forceinline__ uint4 get(int slot, int stream, int k, const uint16_t* row, int D)
+    {
+        const uint4* p = at(slot, stream, k);
+        const int c = column<GROUP>(k, self);
+        if constexpr (VEC) return c < D ? p[0] : make_uint4(0, 0, 0, 0);
+        return first_of(shifted(p[0], p[1], phase_of(row + c)), D - c);
+    }
+};
+
+// Sum over a group of up to a warp.
+template <int GROUP> __device__ __forceinline__ float lanes_sum(float v)
 {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
+    for (int o = (GROUP < 32 ? GROUP : 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+template <int GROUP, int THREADS> __device__ __forceinline__ void group_barrier(int group)
+{
+    if constexpr (GROUP == THREADS) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(GROUP) : "memory");
+}
+
+// Sums over a group's threads of N values, the same in all of them.  `part`
+// has room for two turns: a thread passes the next barrier only when all have
+// read this turn's values.
+template <int GROUP, int N, int THREADS>
+__device__ __forceinline__ void group_sum(float (&v)[N], float (*part)[THREADS / 32][N], int group, int* turn)
+{
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-    }
+    for (int i = 0; i < N; ++i) v[i] = lanes_sum<GROUP>(v[i]);
     if constexpr (GROUP > 32) {
         constexpr int kWarps = GROUP / 32;
-        const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, first = warp / kWarps * kWarps;
-        __syncthreads(); // the last call's values have been read
-        if (lane == 0) {
+        if ((threadIdx.x & 31) == 0)
 #pragma unroll
-            for (int i = 0; i < N; ++i) part[warp * N + i] = v[i];
-        }
-        __syncthreads();
+            for (int i = 0; i < N; ++i) part[*turn][threadIdx.x / 32][i] = v[i];
+        group_barrier<GROUP, THREADS>(group);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            float s = 0.0f;
+            v[i] = 0.0f;
 #pragma unroll
-            for (int k = 0; k < kWarps; ++k) s += part[(first + k) * N + i];
-            v[i] = s;
+            for (int k = 0; k < kWarps; ++k) v[i] += part[*turn][group * kWarps + k][i];
         }
+        *turn ^= 1;
     }
 }
 
-template <int GROUP> constexpr int kNormCta = GROUP > kNormThreads ? GROUP : kNormThreads;
+// Forward: CTAs that stay, two on an SM, as many groups as fit in each, a row
+// per group at a time.  Bound by HBM: NORM_TIME.
+constexpr int kNormThreads = 512;
+template <int VPT> constexpr int kForwardAhead = VPT == 1 ? 8 : VPT == 2 ? 5 : 3;
 
-// One row per group of GROUP threads, VPT vectors of 8 a thread (D <= 8 GROUP
-// VPT).  HELD 0: wider rows, read again for each of the three passes (from L2).
-template <int BF16, int VEC, int GROUP, int VPT, int HELD>
-__global__ void __launch_bounds__(kNormCta<GROUP>) zero_layernorm_kernel(const __grid_constant__ NormArgs a)
+template <int BF16, int VEC, int GROUP, int VPT>
+__global__ void __launch_bounds__(kNormThreads, 2) zero_layernorm_kernel(const __grid_constant__ NormArgs a)
 {
-    __shared__ float part[kNormCta<GROUP> / 32];
-    constexpr int kGroups = kNormCta<GROUP> / GROUP;
-    const int self = threadIdx.x % GROUP;
-    const long long t = static_cast<long long>(blockIdx.x) * kGroups + threadIdx.x / GROUP;
-    const bool live = t < a.T; // a group without a row goes through the barriers with the others
-    const long long row = live ? t : a.T - 1;
+    extern __shared__ __align__(16) unsigned char raw[];
+    constexpr int kGroups = kNormThreads / GROUP, S = kForwardAhead<VPT>;
+    __shared__ float part[2][kNormThreads / 32][1];
+    const int self = threadIdx.x % GROUP, group = threadIdx.x / GROUP;
     let_successor_start();
     wait_for_predecessor();
-    const uint16_t* x = static_cast<const uint16_t*>(a.x) + row * a.ldx;
-    const int steps = HELD ? 1 : (a.D + GROUP * 8 * VPT - 1) / (GROUP * 8 * VPT);
-    Packed p[VPT];
-    auto fetch = [&](int s) {
-#pragma unroll
-        for (int k = 0; k < VPT; ++k) p[k] = load_row<VEC, GROUP>(x, s * VPT + k, self, a.D);
+    const uint16_t* x = static_cast<const uint16_t*>(a.x);
+    const uint16_t* w = static_cast<const uint16_t*>(a.w);
+    const uint16_t* b = static_cast<const uint16_t*>(a.b);
+    uint16_t* y = static_cast<uint16_t*>(a.y);
+    Rows<VEC, GROUP, VPT, 1, S, kNormThreads> rows(raw, self);
+    const long long step = static_cast<long long>(gridDim.x) * kGroups;
+    // the groups of a warp go round equally often: a group without a row works on none
+    constexpr int kTogether = GROUP < 32 ? 32 / GROUP : 1;
+    const long long first = static_cast<long long>(blockIdx.x) * kGroups + group, leader = first / kTogether * kTogether;
+    auto ahead = [&](int slot, long long r) {
+        if (r < a.T) rows.copy(slot, 0, x + r * a.ldx, a.D);
+        rows.commit();
     };
-    // the mean as a sum of x / D: no partial sum is above the largest value
-    float sum[1] = {0.0f};
-    for (int s = 0; s < steps; ++s) {
-        fetch(s);
+    for (int s = 0; s < S - 1; ++s) ahead(s, first + s * step);
+    int s = 0, turn = 0;
+    for (long long lead = leader, r = first; lead < a.T; lead += step, r += step) {
+        const int D = r < a.T ? a.D : 0;
+        const uint16_t* from = x + r * a.ldx;
+        rows.read();
+        ahead(s == 0 ? S - 1 : s - 1, r + (S - 1) * step); // into the slot that the last row has left
+        rows.wait();
+        uint4 p[VPT];
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) p[k] = rows.get(s, 0, k, from, D);
+        // the mean as a sum of x / D: no partial sum is above the largest value
+        float sum[1] = {0.0f};
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             float v[8];
@@ -172,97 +220,145 @@ __global__ void __launch_bounds__(kNormCta<GROUP>) zero_layernorm_kernel(const _
 #pragma unroll
             for (int j = 0; j < 8; ++j) sum[0] = fmaf(v[j], a.inv_d, sum[0]);
         }
-    }
-    group_sum<GROUP>(sum, part);
-    const float mean = sum[0], half_mean = -0.5f * mean;
-    // half of the centred value: a difference of two values of bf16's range may pass fp32's
-    auto squares = [&](float scale) {
-        float q[1] = {0.0f};
-        for (int s = 0; s < steps; ++s) {
-            if (!HELD) fetch(s);
+        group_sum<GROUP, 1, kNormThreads>(sum, part, group, &turn);
+        const float mean = sum[0], half_mean = -0.5f * mean;
+        // half of the centred value: a difference of two values of bf16's range may pass fp32's
+        auto squares = [&](float scale) {
+            float q[1] = {0.0f};
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 float v[8];
                 widen<BF16>(p[k], v);
+                const int there = D - column<GROUP>(k, self);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float d = fmaf(v[j], 0.5f, half_mean) * scale;
-                    if (column<VEC, GROUP>(s * VPT + k, j, self) < a.D) q[0] = fmaf(d, d, q[0]);
+                    if (VEC ? there > 0 : there > j) q[0] = fmaf(d, d, q[0]);
                 }
             }
+            group_sum<GROUP, 1, kNormThreads>(q, part, group, &turn);
+            return q[0];
+        };
+        const float q = squares(1.0f) * a.inv_d;
+        float rstd = __frsqrt_rn(fmaf(4.0f, q, a.eps));
+        // squares of values above 2^63 leave fp32's range: taken again with the values scaled down (by the whole warp where
+        // groups share one: the sum's shuffles are the warp's)
+        const int over = !(q < 2e37f);
+        if (BF16 && (GROUP < 32 ? __any_sync(0xffffffffu, over) : over)) {
+            const float small = squares(1.262177448353619e-29f) * a.inv_d; // 2^-96; eps does not count beside them
+            if (over) rstd = __frsqrt_rn(4.0f * small) * 1.262177448353619e-29f;
         }
-        group_sum<GROUP>(q, part);
-        return q[0];
-    };
-    const float q = squares(1.0f) * a.inv_d;
-    float rstd = __frsqrt_rn(fmaf(4.0f, q, a.eps));
-    // squares of values above 2^63 leave fp32's range: taken again with the values scaled down
-    const int over = !(q < 2e37f);
-    const bool again = GROUP <= 32 ? __any_sync(0xffffffffu, over) : __syncthreads_or(over);
-    if (BF16 && again) {
-        const float small = squares(1.262177448353619e-29f) * a.inv_d; // 2^-96; eps does not count beside them
-        if (over) rstd = __frsqrt_rn(4.0f * small) * 1.262177448353619e-29f;
-    }
-    if (!live) return;
-    if (self == 0) {
-        if (a.mean) a.mean[t] = mean;
-        if (a.rstd) a.rstd[t] = rstd;
-    }
-    uint16_t* y = static_cast<uint16_t*>(a.y) + row * a.ldy;
-    const uint16_t* w = static_cast<const uint16_t*>(a.w);
-    const uint16_t* b = static_cast<const uint16_t*>(a.b);
-    const float twice = 2.0f * rstd;
-    for (int s = 0; s < steps; ++s) {
-        if (!HELD) fetch(s);
+        if (self == 0 && D) {
+            if (a.mean) a.mean[r] = mean;
+            if (a.rstd) a.rstd[r] = rstd;
+        }
+        const float twice = 2.0f * rstd;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            float v[8], g[8], c[8];
+            const int c = column<GROUP>(k, self);
+            float v[8], g[8], h[8];
             widen<BF16>(p[k], v);
-            if (w) widen<BF16>(load_row<VEC, GROUP>(w, s * VPT + k, self, a.D), g);
-            if (b) widen<BF16>(load_row<VEC, GROUP>(b, s * VPT + k, self, a.D), c);
+            if (w) widen<BF16>(load_row<VEC>(w, c, a.D), g);
+            if (b) widen<BF16>(load_row<VEC>(b, c, a.D), h);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 v[j] = fmaf(v[j], 0.5f, half_mean) * twice;
                 if (w) v[j] *= g[j];
-                if (b) v[j] += c[j];
+                if (b) v[j] += h[j];
             }
-            store_row<VEC, GROUP, BF16>(y, s * VPT + k, self, a.D, v);
+            store_row<VEC, GROUP>(y + r * a.ldy, c, self, D, pack8(v, BF16));
         }
+        if (++s == S) s = 0;
+    }
+}
+
+// Forward of rows above 16384 elements: a CTA per row, which reads it three
+// times (from L2 after the first).
+constexpr int kWideThreads = 1024;
+
+template <int BF16, int VEC>
+__global__ void __launch_bounds__(kWideThreads) zero_layernorm_wide_kernel(const __grid_constant__ NormArgs a)
+{
+    __shared__ float part[2][kWideThreads / 32][1];
+    const int self = threadIdx.x;
+    const long long r = blockIdx.x;
+    let_successor_start();
+    wait_for_predecessor();
+    const uint16_t* x = static_cast<const uint16_t*>(a.x) + r * a.ldx;
+    const uint16_t* w = static_cast<const uint16_t*>(a.w);
+    const uint16_t* b = static_cast<const uint16_t*>(a.b);
+    uint16_t* y = static_cast<uint16_t*>(a.y) + r * a.ldy;
+    const int steps = (a.D + kWideThreads * 8 - 1) / (kWideThreads * 8);
+    int turn = 0;
+    float sum[1] = {0.0f};
+#pragma unroll 2
+    for (int k = 0; k < steps; ++k) {
+        float v[8];
+        widen<BF16>(load_row<VEC>(x, column<kWideThreads>(k, self), a.D), v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[0] = fmaf(v[j], a.inv_d, sum[0]);
+    }
+    group_sum<kWideThreads, 1, kWideThreads>(sum, part, 0, &turn);
+    const float mean = sum[0], half_mean = -0.5f * mean;
+    auto squares = [&](float scale) {
+        float q[1] = {0.0f};
+#pragma unroll 2
+        for (int k = 0; k < steps; ++k) {
+            float v[8];
+            const int c = column<kWideThreads>(k, self);
+            widen<BF16>(load_row<VEC>(x, c, a.D), v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float d = fmaf(v[j], 0.5f, half_mean) * scale;
+                if (c + j < a.D) q[0] = fmaf(d, d, q[0]);
+            }
+        }
+        group_sum<kWideThreads, 1, kWideThreads>(q, part, 0, &turn);
+        return q[0];
+    };
+    const float q = squares(1.0f) * a.inv_d;
+    float rstd = __frsqrt_rn(fmaf(4.0f, q, a.eps));
+    if (BF16 && !(q < 2e37f)) { // the same in every thread
+        const float small = squares(1.262177448353619e-29f) * a.inv_d;
+        rstd = __frsqrt_rn(4.0f * small) * 1.262177448353619e-29f;
+    }
+    if (self == 0) {
+        if (a.mean) a.mean[r] = mean;
+        if (a.rstd) a.rstd[r] = rstd;
+    }
+    const float twice = 2.0f * rstd;
+    for (int k = 0; k < steps; ++k) {
+        const int c = column<kWideThreads>(k, self);
+        float v[8], g[8], h[8];
+        widen<BF16>(load_row<VEC>(x, c, a.D), v);
+        if (w) widen<BF16>(load_row<VEC>(w, c, a.D), g);
+        if (b) widen<BF16>(load_row<VEC>(b, c, a.D), h);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            v[j] = fmaf(v[j], 0.5f, half_mean) * twice;
+            if (w) v[j] *= g[j];
+            if (b) v[j] += h[j];
+        }
+        store_row<VEC, kWideThreads>(y, c, self, a.D, pack8(v, BF16));
     }
 }
 
 // The gradient: a CTA of kGradThreads on every SM, as many groups as fit in it,
-// a row per group at a time.  VEC: the rows to come are copied to shared
-// memory ahead, kAhead of them, each thread its own vectors, so that it waits
-// for nobody's copies but its own; else the row is read where it is used.
-// A group joins its two sums of a row by one barrier of its own.  16384 rows of
-// 2048 bf16 elements with the residual (269 MB): NORM_GRAD_TIME.
+// a row per group at a time.  A group joins its two sums of a row by one
+// barrier of its own.  16384 rows of 2048 bf16 elements with the residual (269
+// MB): NORM_GRAD_TIME.
 constexpr int kGradThreads = 512;
-template <int VPT> constexpr int kNormAhead = VPT == 1 ? 6 : 4;
-template <int GROUP, int VPT, int VEC>
-constexpr int kNormSmem = (VEC ? kNormAhead<VPT> * 3 * kGradThreads * VPT * 16 : 0) > 2 * kGradThreads * VPT * 8 * 4
-                              ? kNormAhead<VPT> * 3 * kGradThreads * VPT * 16
-                              : 2 * kGradThreads * VPT * 8 * 4;
-
-template <int GROUP> __device__ __forceinline__ void group_barrier(int group)
-{
-    if constexpr (GROUP == 32) __syncwarp();
-    else if constexpr (GROUP == kGradThreads) __syncthreads();
-    else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(GROUP) : "memory");
-}
-
-__device__ __forceinline__ void copy16(void* to, const void* from)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
-}
+template <int VPT> constexpr int kGradAhead = VPT == 1 ? 6 : 4;
+template <int VEC, int GROUP, int VPT> using GradRows = Rows<VEC, GROUP, VPT, 3, kGradAhead<VPT>, kGradThreads>;
+constexpr int kGradSums = 2 * kGradThreads * 8 * 4; // bytes of the groups' sums, for each vector of a thread
 
 template <int BF16, int VEC, int GROUP, int VPT>
 __global__ void __launch_bounds__(kGradThreads, 1) zero_layernorm_grad_kernel(const __grid_constant__ NormBackArgs a)
 {
     extern __shared__ __align__(16) unsigned char raw[];
-    constexpr int kGroups = kGradThreads / GROUP, kWarps = GROUP / 32, S = kNormAhead<VPT>;
+    constexpr int kGroups = kGradThreads / GROUP, S = kGradAhead<VPT>;
     __shared__ float part[2][kGradThreads / 32][2];
-    const int self = threadIdx.x % GROUP, in_cta = threadIdx.x / GROUP;
+    const int self = threadIdx.x % GROUP, group = threadIdx.x / GROUP;
     let_successor_start();
     wait_for_predecessor();
     const uint16_t* dy = static_cast<const uint16_t*>(a.dy);
@@ -270,66 +366,42 @@ __global__ void __launch_bounds__(kGradThreads, 1) zero_layernorm_grad_kernel(co
     const uint16_t* res = static_cast<const uint16_t*>(a.res);
     uint16_t* dx = static_cast<uint16_t*>(a.dx);
     float dw[VPT][8], db[VPT][8];
-    Packed w[VPT];
+    uint4 w[VPT];
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-        if (a.w) w[k] = load_row<VEC, GROUP>(static_cast<const uint16_t*>(a.w), k, self, a.D);
-        else w[k].u[0] = w[k].u[1] = w[k].u[2] = w[k].u[3] = BF16 ? 0x3f803f80u : 0x3c003c00u; // ones
+        const uint32_t one = BF16 ? 0x3f803f80u : 0x3c003c00u;
+        w[k] = a.w ? load_row<VEC>(static_cast<const uint16_t*>(a.w), column<GROUP>(k, self), a.D) : make_uint4(one, one, one, one);
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[k][j] = db[k][j] = 0.0f;
     }
-    // this thread's place in slot s: three streams of VPT vectors
-    auto slot = [&](int s, int stream, int k) {
-        return reinterpret_cast<uint4*>(raw) + ((s * 3 + stream) * VPT + k) * kGradThreads + threadIdx.x;
-    };
-    auto copy_row = [&](int s, long long r) {
+    GradRows<VEC, GROUP, VPT> rows(raw, self);
+    const long long step = static_cast<long long>(gridDim.x) * kGroups;
+    constexpr int kTogether = GROUP < 32 ? 32 / GROUP : 1;
+    const long long first = static_cast<long long>(blockIdx.x) * kGroups + group, leader = first / kTogether * kTogether;
+    auto ahead = [&](int slot, long long r) {
         if (r < a.T) {
-#pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                const int c = column<1, GROUP>(k, 0, self);
-                if (c >= a.D) continue;
-                copy16(slot(s, 0, k), x + r * a.ldx + c);
-                copy16(slot(s, 1, k), dy + r * a.lddy + c);
-                if (res) copy16(slot(s, 2, k), res + r * a.ldr + c);
-            }
+            rows.copy(slot, 0, x + r * a.ldx, a.D);
+            rows.copy(slot, 1, dy + r * a.lddy, a.D);
+            if (res) rows.copy(slot, 2, res + r * a.ldr, a.D);
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
+        rows.commit();
     };
-    auto held = [&](int s, int stream, int k) {
-        const uint4 v = *slot(s, stream, k);
-        Packed p;
-        p.u[0] = v.x, p.u[1] = v.y, p.u[2] = v.z, p.u[3] = v.w;
-        return p;
-    };
-    const long long first = static_cast<long long>(blockIdx.x) * kGroups + in_cta, step = static_cast<long long>(gridDim.x) * kGroups;
     float mean_next = 0.0f, rstd_next = 0.0f;
     if (first < a.T) mean_next = a.mean[first], rstd_next = a.rstd[first];
-    if constexpr (VEC) {
-        // columns past the last are never copied: zeros
-        for (int s = 0; s < S; ++s)
-#pragma unroll
-            for (int k = 0; k < VPT; ++k)
-                if (column<1, GROUP>(k, 0, self) >= a.D)
-                    for (int i = 0; i < 3; ++i) *slot(s, i, k) = make_uint4(0, 0, 0, 0);
-        for (int s = 0; s < S - 1; ++s) copy_row(s, first + s * step);
-    }
+    for (int s = 0; s < S - 1; ++s) ahead(s, first + s * step);
     int s = 0, turn = 0;
-    for (long long r = first; r < a.T; r += step) {
+    for (long long lead = leader, r = first; lead < a.T; lead += step, r += step) {
+        const int D = r < a.T ? a.D : 0; // a group without a row works on none
         const float mean = -0.5f * mean_next, rstd = 2.0f * rstd_next;
         if (r + step < a.T) mean_next = a.mean[r + step], rstd_next = a.rstd[r + step];
-        Packed px[VPT], pd[VPT], pr[VPT];
-        if constexpr (VEC) {
-            copy_row(s == 0 ? S - 1 : s - 1, r + (S - 1) * step); // into the slot that the last row has left
-            asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+        rows.read();
+        ahead(s == 0 ? S - 1 : s - 1, r + (S - 1) * step); // into the slot that the last row has left
+        rows.wait();
+        uint4 px[VPT], pd[VPT];
 #pragma unroll
-            for (int k = 0; k < VPT; ++k) px[k] = held(s, 0, k), pd[k] = held(s, 1, k);
-        } else {
-#pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                px[k] = load_row<0, GROUP>(x + r * a.ldx, k, self, a.D);
-                pd[k] = load_row<0, GROUP>(dy + r * a.lddy, k, self, a.D);
-                if (res) pr[k] = load_row<0, GROUP>(res + r * a.ldr, k, self, a.D);
-            }
+        for (int k = 0; k < VPT; ++k) {
+            px[k] = rows.get(s, 0, k, x + r * a.ldx, D);
+            pd[k] = rows.get(s, 1, k, dy + r * a.lddy, D);
         }
         float sum[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -338,11 +410,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) zero_layernorm_grad_kernel(co
             widen<BF16>(px[k], vx);
             widen<BF16>(pd[k], vd);
             widen<BF16>(w[k], vw);
-            // vectors past the last have dy 0: their sums go nowhere, so long as their h is finite
+            // past the row's end dy is 0: such sums go nowhere, so long as their h is finite
+            const int there = D - column<GROUP>(k, self);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 float h = fmaf(vx[j], 0.5f, mean) * rstd;
-                if (column<VEC, GROUP>(k, j, self) >= a.D) h = 0.0f;
+                if (VEC ? there <= 0 : there <= j) h = 0.0f;
                 const float g = vd[j] * vw[j];
                 dw[k][j] = fmaf(vd[j], h, dw[k][j]);
                 db[k][j] += vd[j];
@@ -351,22 +424,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) zero_layernorm_grad_kernel(co
             }
         }
         if (dx) {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], o);
-                sum[1] += __shfl_xor_sync(0xffffffffu, sum[1], o);
-            }
-            if constexpr (GROUP > 32) { // two buffers in turn: a thread passes the next barrier only when all have read this one
-                if ((threadIdx.x & 31) == 0) part[turn][threadIdx.x / 32][0] = sum[0], part[turn][threadIdx.x / 32][1] = sum[1];
-                group_barrier<GROUP>(in_cta);
-                sum[0] = sum[1] = 0.0f;
-#pragma unroll
-                for (int i = 0; i < kWarps; ++i) {
-                    sum[0] += part[turn][in_cta * kWarps + i][0];
-                    sum[1] += part[turn][in_cta * kWarps + i][1];
-                }
-                turn ^= 1;
-            }
+            group_sum<GROUP, 2, kGradThreads>(sum, part, group, &turn);
             const float c0 = sum[0] * a.inv_d, c1 = sum[1] * a.inv_d, half = 0.5f * rstd;
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
@@ -374,24 +432,21 @@ __global__ void __launch_bounds__(kGradThreads, 1) zero_layernorm_grad_kernel(co
                 widen<BF16>(px[k], vx);
                 widen<BF16>(pd[k], vd);
                 widen<BF16>(w[k], vw);
-                if (res) {
-                    if constexpr (VEC) pr[k] = held(s, 2, k);
-                    widen<BF16>(pr[k], o);
-                }
+                if (res) widen<BF16>(rows.get(s, 2, k, res + r * a.ldr, D), o);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float h = fmaf(vx[j], 0.5f, mean) * rstd;
                     const float d = half * (vd[j] * vw[j] - c0 - h * c1);
                     o[j] = res ? o[j] + d : d;
                 }
-                store_row<VEC, GROUP, BF16>(dx + r * a.lddx, k, self, a.D, o);
+                store_row<VEC, GROUP>(dx + r * a.lddx, column<GROUP>(k, self), self, D, pack8(o, BF16));
             }
         }
         if (++s == S) s = 0;
     }
     if (!a.sums) return;
     // the groups' sums, joined in the groups' order
-    if constexpr (VEC) asm volatile("cp.async.wait_all;" ::: "memory");
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
     float* all = reinterpret_cast<float*>(raw); // [kGroups][2][8 GROUP VPT]
     constexpr int kWidth = 8 * GROUP * VPT;
@@ -399,9 +454,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) zero_layernorm_grad_kernel(co
     for (int k = 0; k < VPT; ++k) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int c = column<VEC, GROUP>(k, j, self);
-            all[(in_cta * 2) * kWidth + c] = dw[k][j];
-            all[(in_cta * 2 + 1) * kWidth + c] = db[k][j];
+            const int c = column<GROUP>(k, self) + j;
+            all[(group * 2) * kWidth + c] = dw[k][j];
+            all[(group * 2 + 1) * kWidth + c] = db[k][j];
         }
     }
     __syncthreads();
@@ -410,7 +465,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) zero_layernorm_grad_kernel(co
         const int which = i / kWidth, c = i - which * kWidth;
         if (c >= a.D) continue;
         float v = 0.0f;
-#pragma unroll
+#pragma unroll 8
         for (int k = 0; k < kGroups; ++k) v += all[(k * 2 + which) * kWidth + c];
         to[which * static_cast<long long>(a.D) + c] = v;
     }
@@ -419,10 +474,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) zero_layernorm_grad_kernel(co
 // Rows of more than 8192 elements: dx with a CTA per row that reads it twice
 // (the second time from L2), the sums of dw and db by stripes of columns.
 template <int BF16, int VEC>
-__global__ void __launch_bounds__(1024) zero_layernorm_wide_grad_kernel(const __grid_constant__ NormBackArgs a)
+__global__ void __launch_bounds__(kWideThreads) zero_layernorm_wide_grad_kernel(const __grid_constant__ NormBackArgs a)
 {
-    constexpr int GROUP = 1024;
-    __shared__ float part[GROUP / 32 * 2];
+    __shared__ float part[2][kWideThreads / 32][2];
     const int self = threadIdx.x;
     const long long r = blockIdx.x;
     let_successor_start();
@@ -433,37 +487,41 @@ __global__ void __launch_bounds__(1024) zero_layernorm_wide_grad_kernel(const __
     const uint16_t* res = static_cast<const uint16_t*>(a.res) + (a.res ? r * a.ldr : 0);
     uint16_t* dx = static_cast<uint16_t*>(a.dx) + r * a.lddx;
     const float mean = -0.5f * a.mean[r], rstd = 2.0f * a.rstd[r];
-    const int steps = (a.D + GROUP * 8 - 1) / (GROUP * 8);
+    const int steps = (a.D + kWideThreads * 8 - 1) / (kWideThreads * 8);
+    int turn = 0;
     float sum[2] = {0.0f, 0.0f};
+#pragma unroll 2
     for (int k = 0; k < steps; ++k) {
         float vx[8], vd[8], vw[8];
-        widen<BF16>(load_row<VEC, GROUP>(x, k, self, a.D), vx);
-        widen<BF16>(load_row<VEC, GROUP>(dy, k, self, a.D), vd);
-        if (w) widen<BF16>(load_row<VEC, GROUP>(w, k, self, a.D), vw);
+        const int c = column<kWideThreads>(k, self);
+        widen<BF16>(load_row<VEC>(x, c, a.D), vx);
+        widen<BF16>(load_row<VEC>(dy, c, a.D), vd);
+        if (w) widen<BF16>(load_row<VEC>(w, c, a.D), vw);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            if (column<VEC, GROUP>(k, j, self) < a.D) {
+            if (c + j < a.D) {
                 const float g = w ? vd[j] * vw[j] : vd[j];
                 sum[0] += g;
                 sum[1] = fmaf(g, fmaf(vx[j], 0.5f, mean) * rstd, sum[1]);
             }
         }
     }
-    group_sum<GROUP>(sum, part);
+    group_sum<kWideThreads, 2, kWideThreads>(sum, part, 0, &turn);
     const float c0 = sum[0] * a.inv_d, c1 = sum[1] * a.inv_d, s = 0.5f * rstd;
     for (int k = 0; k < steps; ++k) {
         float vx[8], vd[8], vw[8], o[8];
-        widen<BF16>(load_row<VEC, GROUP>(x, k, self, a.D), vx);
-        widen<BF16>(load_row<VEC, GROUP>(dy, k, self, a.D), vd);
-        if (w) widen<BF16>(load_row<VEC, GROUP>(w, k, self, a.D), vw);
-        if (a.res) widen<BF16>(load_row<VEC, GROUP>(res, k, self, a.D), o);
+        const int c = column<kWideThreads>(k, self);
+        widen<BF16>(load_row<VEC>(x, c, a.D), vx);
+        widen<BF16>(load_row<VEC>(dy, c, a.D), vd);
+        if (w) widen<BF16>(load_row<VEC>(w, c, a.D), vw);
+        if (a.res) widen<BF16>(load_row<VEC>(res, c, a.D), o);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float g = w ? vd[j] * vw[j] : vd[j], h = fmaf(vx[j], 0.5f, mean) * rstd;
             const float d = s * (g - c0 - h * c1);
             o[j] = a.res ? o[j] + d : d;
         }
-        store_row<VEC, GROUP, BF16>(dx, k, self, a.D, o);
+        store_row<VEC, kWideThreads>(dx, c, self, a.D, pack8(o, BF16));
     }
 }
 
@@ -487,8 +545,8 @@ __global__ void __launch_bounds__(256) zero_layernorm_columns_kernel(const __gri
 #pragma unroll 4
     for (long long r = r0 + line; r < r1; r += 8) {
         float vx[8], vd[8];
-        widen<BF16>(load_row<VEC, 32>(x + r * a.ldx, 0, lane, cols), vx);
-        widen<BF16>(load_row<VEC, 32>(dy + r * a.lddy, 0, lane, cols), vd);
+        widen<BF16>(load_row<VEC>(x + r * a.ldx, lane * 8, cols), vx);
+        widen<BF16>(load_row<VEC>(dy + r * a.lddy, lane * 8, cols), vd);
         const float mean = -0.5f * a.mean[r], rstd = 2.0f * a.rstd[r];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -498,8 +556,8 @@ __global__ void __launch_bounds__(256) zero_layernorm_columns_kernel(const __gri
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        part[0][line][column<VEC, 32>(0, j, lane)] = dw[j];
-        part[1][line][column<VEC, 32>(0, j, lane)] = db[j];
+        part[0][line][lane * 8 + j] = dw[j];
+        part[1][line][lane * 8 + j] = db[j];
     }
     __syncthreads();
     const int c = threadIdx.x;
@@ -549,24 +607,36 @@ using NormBackKernel = void (*)(NormBackArgs);
 
 struct NormPick {
     NormKernel fn;
-    int group;           // threads that share a row
+    int group, smem;     // threads that share a row, bytes of shared memory
 };
 
-// The narrowest group that holds a row: fewer threads have less to join; a
-// warp's row needs no barrier.
-template <int BF16, int VEC> NormPick pick_norm(int64_t D)
+template <int BF16, int VEC, int GROUP, int VPT> NormPick norm_pick()
 {
-    if (D <= 256) return {zero_layernorm_kernel<BF16, VEC, 32, 1, 1>, 32};
-    if (D <= 512) return {zero_layernorm_kernel<BF16, VEC, 32, 2, 1>, 32};
-    if (D <= 1024) return {zero_layernorm_kernel<BF16, VEC, 32, 4, 1>, 32};
-    if (D <= 2048) return {zero_layernorm_kernel<BF16, VEC, 256, 1, 1>, 256};
-    if (D <= 4096) return {zero_layernorm_kernel<BF16, VEC, 256, 2, 1>, 256};
-    if (D <= 8192) return {zero_layernorm_kernel<BF16, VEC, 256, 4, 1>, 256};
-    if (D <= 16384) return {zero_layernorm_kernel<BF16, VEC, 1024, 2, 1>, 1024};
-    return {zero_layernorm_kernel<BF16, VEC, 1024, 2, 0>, 1024};
+    return {zero_layernorm_kernel<BF16, VEC, GROUP, VPT>, GROUP, Rows<VEC, GROUP, VPT, 1, kForwardAhead<VPT>, kNormThreads>::kBytes};
 }
 
-constexpr int64_t kNormWide = 8192; // rows above it take the wide kernels
+// The narrowest group that holds a row in one or two vectors a thread: fewer
+// threads have less to join.
+template <int BF16, int VEC> NormPick pick_norm(int64_t D)
+{
+    if (D <= 64) return norm_pick<BF16, VEC, 8, 1>();
+    if (D <= 256) return norm_pick<BF16, VEC, 32, 1>();
+    if (D <= 512) return norm_pick<BF16, VEC, 32, 2>();
+    if (D <= 1024) return norm_pick<BF16, VEC, 64, 2>();
+    if (D <= 2048) return norm_pick<BF16, VEC, 128, 2>();
+    if (D <= 4096) return norm_pick<BF16, VEC, 256, 2>();
+    if (D <= 8192) return norm_pick<BF16, VEC, 512, 2>();
+    return norm_pick<BF16, VEC, 512, 4>();
+}
+
+NormPick pick_norm(int64_t D, int bf16, int vec)
+{
+    if (bf16) return vec ? pick_norm<1, 1>(D) : pick_norm<1, 0>(D);
+    return vec ? pick_norm<0, 1>(D) : pick_norm<0, 0>(D);
+}
+
+constexpr int64_t kForwardWide = 16384; // rows above it take the wide forward kernel
+constexpr int64_t kNormWide = 8192;     // rows above it the wide gradient kernels
 
 struct NormBackPick {
     NormBackKernel fn;
@@ -575,11 +645,12 @@ struct NormBackPick {
 
 template <int BF16, int VEC, int GROUP, int VPT> NormBackPick back_pick()
 {
-    return {zero_layernorm_grad_kernel<BF16, VEC, GROUP, VPT>, GROUP, kNormSmem<GROUP, VPT, VEC>};
+    return {zero_layernorm_grad_kernel<BF16, VEC, GROUP, VPT>, GROUP, std::max(GradRows<VEC, GROUP, VPT>::kBytes, VPT * kGradSums)};
 }
 
 template <int BF16, int VEC> NormBackPick pick_back(int64_t D)
 {
+    if (D <= 64) return back_pick<BF16, VEC, 8, 1>();
     if (D <= 256) return back_pick<BF16, VEC, 32, 1>();
     if (D <= 512) return back_pick<BF16, VEC, 64, 1>();
     if (D <= 1024) return back_pick<BF16, VEC, 128, 1>();
@@ -637,14 +708,24 @@ extern "C" int zero_layernorm_forward(const void* x, int64_t ldx, const void* we
             floats_share(s, T, y, ldy, T, D))
             return ZERO_EOVERLAP;
     const bool vec = D % 8 == 0 && aligned16(x, ldx) && aligned16(y, ldy) && addr(weight) % 16 == 0 && addr(bias) % 16 == 0;
-    NormPick k;
-    if (type == ZERO_TYPE_BF16) k = vec ? pick_norm<1, 1>(D) : pick_norm<1, 0>(D);
-    else k = vec ? pick_norm<0, 1>(D) : pick_norm<0, 0>(D);
+    const int bf16 = type == ZERO_TYPE_BF16;
+    cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
     NormArgs a{};
     a.x = x, a.w = weight, a.b = bias, a.y = y, a.mean = mean, a.rstd = rstd, a.ldx = ldx, a.ldy = ldy, a.T = T;
     a.D = static_cast<int>(D), a.eps = eps, a.inv_d = 1.0f / static_cast<float>(D);
-    const int threads = std::max(k.group, kNormThreads), rows = threads / k.group;
-    return launch_after(k.fn, a, (T + rows - 1) / rows, threads, 0, 1, static_cast<cudaStream_t>(cuda_stream));
+    if (D > kForwardWide) {
+        NormKernel fn;
+        if (bf16) fn = vec ? zero_layernorm_wide_kernel<1, 1> : zero_layernorm_wide_kernel<1, 0>;
+        else fn = vec ? zero_layernorm_wide_kernel<0, 1> : zero_layernorm_wide_kernel<0, 0>;
+        return launch_after(fn, a, T, kWideThreads, 0, 1, st);
+    }
+    int sms = 0;
+    int rc = sm_count(&sms);
+    if (rc) return rc;
+    const NormPick k = pick_norm(D, bf16, vec);
+    const int64_t per_cta = kNormThreads / k.group, ctas = std::min<int64_t>((T + per_cta - 1) / per_cta, 2ll * sms);
+    if ((rc = allow_smem(reinterpret_cast<const void*>(k.fn), k.smem))) return rc;
+    return launch_after(k.fn, a, ctas, kNormThreads, k.smem, 1, st);
 }
 
 extern "C" int zero_layernorm_workspace(int64_t T, int64_t D, int64_t* bytes)
@@ -715,7 +796,7 @@ extern "C" int zero_layernorm_backward(const void* dy, int64_t lddy, const void*
         else columns = vec ? zero_layernorm_columns_kernel<0, 1> : zero_layernorm_columns_kernel<0, 0>;
         const int64_t stripes = (D + kNormStripe - 1) / kNormStripe;
         if (stripes * a.groups > INT32_MAX) return ZERO_EINVAL;
-        if (dx && (rc = launch_after(rows, a, T, 1024, 0, 1, st))) return rc;
+        if (dx && (rc = launch_after(rows, a, T, kWideThreads, 0, 1, st))) return rc;
         if (sums && (rc = launch_after(columns, a, stripes * a.groups, 256, 0, 1, st))) return rc;
     } else {
         const NormBackPick k = pick_back(D, bf16, vec);
