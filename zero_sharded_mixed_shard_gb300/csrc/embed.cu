@@ -2,7 +2,9 @@
 // dtable[v] = scale (sum of dy[t] over the tokens t with ids[t] = v).
 //
 // The lookup is bound by HBM: a warp copies a piece of a row with all of its
-// reads in flight.
+// reads in flight.  Off 16 bytes both directions go by the 16-byte granules of
+// the row that is written (its phase: the elements before it in its first
+// granule), and the rows that are read are shifted to them.
 //
 // The gradient sums each row's tokens in the tokens' order, without atomics on
 // values, so that a call repeats its bits.  The tokens are sorted by id with a
@@ -45,23 +47,24 @@ template <int BF16, int VEC> __global__ void __launch_bounds__(256) zero_embed_k
     const bool there = id >= 0 && id < a.V;
     const uint16_t* from = static_cast<const uint16_t*>(a.table) + (there ? id * a.ldt : 0);
     uint16_t* to = static_cast<uint16_t*>(a.y) + t * a.ldy;
+    const int phase = VEC ? 0 : phase_of(to);
     uint4 u[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        const int c = c0 + (k * 32 + lane) * 8;
+        const int c = c0 + (k * 32 + lane) * 8 - phase;
         u[k] = make_uint4(0, 0, 0, 0);
         if (there && c < a.D) u[k] = VEC ? *reinterpret_cast<const uint4*>(from + c) : load_any(from, c, a.D);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        const int c = c0 + (k * 32 + lane) * 8;
+        const int c = c0 + (k * 32 + lane) * 8 - phase;
         float v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = 0.0f;
         add8(v, u[k], BF16);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = there ? v[j] * a.scale : 0.0f;
-        if (!VEC) store_any(to, c, a.D, pack8(v, BF16), lane == 0, lane == 31);
+        if (!VEC) put_granule(to, c, a.D, pack8(v, BF16));
         else if (c < a.D) *reinterpret_cast<uint4*>(to + c) = pack8(v, BF16);
     }
 }
@@ -189,10 +192,9 @@ template <int ROUNDS> __global__ void __launch_bounds__(kSortThreads) zero_sort_
 template <int VEC> __device__ __forceinline__ void clear_row(uint16_t* row, int D, int lane)
 {
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    for (int c0 = 0; c0 < D; c0 += 256) {
-        const int c = c0 + lane * 8;
-        if (!VEC) store_any(row, c, D, zero, lane == 0, lane == 31);
-        else if (c < D) *reinterpret_cast<uint4*>(row + c) = zero;
+    for (int c = lane * 8 - (VEC ? 0 : phase_of(row)); c < D; c += 256) {
+        if (!VEC) put_granule(row, c, D, zero);
+        else *reinterpret_cast<uint4*>(row + c) = zero;
     }
 }
 
@@ -339,13 +341,13 @@ struct RunArgs {
     const int2* sorted;
     const void* dy;
     void* dtable;
-    float* parts;        // [chunks][2][pitch]: of the run that began before the chunk, of the one that goes on behind it
+    float* parts;        // [chunks][2][pitch], by granules of the row: of the run that began before the chunk, of the one that goes on behind it
     long long lddy, lddt, T, sum_tasks, join_tasks, tasks, cleared; // rows of the table below `cleared` are 0 already
     int D, V, stripes, chunk, add, pitch;
     float scale;
 };
 
-// This lane's eight elements of a row from memory.
+// Eight elements of a row from column c on.
 template <int VEC> __device__ __forceinline__ uint4 get_row(const uint16_t* row, int c, int D)
 {
     if constexpr (!VEC) return load_any(row, c, D);
@@ -355,14 +357,13 @@ template <int VEC> __device__ __forceinline__ uint4 get_row(const uint16_t* row,
 // A run's sum, plus what the table's gradient held (zeros where it does not
 // count), to its row.
 template <int BF16, int VEC>
-__device__ __forceinline__ void put_row(const RunArgs& a, int key, int c, int lane, const float (&sum)[8], const uint4& old)
+__device__ __forceinline__ void put_row(const RunArgs& a, uint16_t* row, int c, const float (&sum)[8], const uint4& old)
 {
-    uint16_t* row = static_cast<uint16_t*>(a.dtable) + key * a.lddt;
     float v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = sum[j] * a.scale;
     if (a.add) add8(v, old, BF16);
-    if constexpr (!VEC) store_any(row, c, a.D, pack8(v, BF16), lane == 0, lane == 31);
+    if constexpr (!VEC) put_granule(row, c, a.D, pack8(v, BF16));
     else if (c < a.D) *reinterpret_cast<uint4*>(row + c) = pack8(v, BF16);
 }
 
@@ -390,9 +391,9 @@ template <int VEC> __device__ __forceinline__ void clear_rows(const RunArgs& a, 
     }
 }
 
-template <int BF16, int VEC, int ADD> __global__ void __launch_bounds__(256) zero_embed_grad_kernel(const __grid_constant__ RunArgs a)
+template <int BF16, int VEC, int ADD> __global__ void __launch_bounds__(256, 2) zero_embed_grad_kernel(const __grid_constant__ RunArgs a)
 {
-    constexpr int kAhead = VEC && !ADD ? 8 : 4; // rows in flight (two granules each off 16 bytes)
+    constexpr int kAhead = VEC ? 8 : 4; // rows in flight (two granules each off 16 bytes)
     const int lane = threadIdx.x & 31;
     const long long task = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
     let_successor_start();
@@ -411,7 +412,7 @@ template <int BF16, int VEC, int ADD> __global__ void __launch_bounds__(256) zer
     bool begun = first > 0 && a.sorted[first - 1].x == a.sorted[first].x; // the run began before the chunk
     bool open = false;                                                     // the sum holds a row
     auto put_part = [&]() {
-        if (col >= a.D) return; // a part has room for whole vectors
+        if (col >= a.pitch) return;
         float4* part = reinterpret_cast<float4*>(a.parts + (chunk * 2 + (begun ? 0 : 1)) * a.pitch + col);
         part[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
         part[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
@@ -428,12 +429,18 @@ template <int BF16, int VEC, int ADD> __global__ void __launch_bounds__(256) zer
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
                 const uint16_t* row = dy + __shfl_sync(0xffffffffu, mine.y, i0 + i) * a.lddy;
-                u[i] = i0 + i < n ? get_row<VEC>(row, col, a.D) : make_uint4(0, 0, 0, 0);
-                // the table's row as it was: read with the others, for the token that ends its run
-                if constexpr (ADD) {
-                    const int key = __shfl_sync(0xffffffffu, mine.x, i0 + i);
-                    o[i] = i0 + i < n && (ends >> (i0 + i) & 1) ? get_row<VEC>(static_cast<const uint16_t*>(a.dtable) + key * a.lddt, col, a.D)
-                                                                : make_uint4(0, 0, 0, 0);
+                u[i] = make_uint4(0, 0, 0, 0);
+                o[ADD ? i : 0] = make_uint4(0, 0, 0, 0);
+                if (VEC && !ADD) {
+                    if (i0 + i < n) u[i] = get_row<VEC>(row, col, a.D);
+                    continue;
+                }
+                const uint16_t* to = static_cast<const uint16_t*>(a.dtable) + __shfl_sync(0xffffffffu, mine.x, i0 + i) * a.lddt;
+                const int c = VEC ? col : col - phase_of(to);
+                if (i0 + i < n) {
+                    u[i] = get_row<VEC>(row, c, a.D);
+                    // the table's row as it was: read with the others, for the token that ends its run
+                    if (ADD && (ends >> (i0 + i) & 1)) o[ADD ? i : 0] = get_row<VEC>(to, c, a.D);
                 }
             }
 #pragma unroll
@@ -442,9 +449,9 @@ template <int BF16, int VEC, int ADD> __global__ void __launch_bounds__(256) zer
                 add8(sum, u[i], BF16);
                 open = true;
                 if (!(ends >> (i0 + i) & 1)) continue;
-                const int key = __shfl_sync(0xffffffffu, mine.x, i0 + i);
+                uint16_t* to = static_cast<uint16_t*>(a.dtable) + __shfl_sync(0xffffffffu, mine.x, i0 + i) * a.lddt;
                 if (begun) put_part();
-                else put_row<BF16, VEC>(a, key, col, lane, sum, o[ADD ? i : 0]);
+                else put_row<BF16, VEC>(a, to, VEC ? col : col - phase_of(to), sum, o[ADD ? i : 0]);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
                 begun = open = false;
@@ -455,9 +462,34 @@ template <int BF16, int VEC, int ADD> __global__ void __launch_bounds__(256) zer
     if (open) put_part(); // the run goes on behind the chunk
 }
 
+// The same place of eight parts (the first n; later ones are not read): one
+// statement, since the compiler adds each part before it reads the next
+// otherwise (16384 tokens, 2048 columns, runs of up to 33 parts: 20 us).
+__device__ __forceinline__ void read_eight(const float* from, long long pitch, int n, float (&v)[8][4])
+{
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k][0] = v[k][1] = v[k][2] = v[k][3] = 0.0f;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.gt.s32 p, %40, 0;\n\t@p ld.global.v4.f32 {%0, %1, %2, %3}, [%32];\n\t"
+                 "setp.gt.s32 p, %40, 1;\n\t@p ld.global.v4.f32 {%4, %5, %6, %7}, [%33];\n\t"
+                 "setp.gt.s32 p, %40, 2;\n\t@p ld.global.v4.f32 {%8, %9, %10, %11}, [%34];\n\t"
+                 "setp.gt.s32 p, %40, 3;\n\t@p ld.global.v4.f32 {%12, %13, %14, %15}, [%35];\n\t"
+                 "setp.gt.s32 p, %40, 4;\n\t@p ld.global.v4.f32 {%16, %17, %18, %19}, [%36];\n\t"
+                 "setp.gt.s32 p, %40, 5;\n\t@p ld.global.v4.f32 {%20, %21, %22, %23}, [%37];\n\t"
+                 "setp.gt.s32 p, %40, 6;\n\t@p ld.global.v4.f32 {%24, %25, %26, %27}, [%38];\n\t"
+                 "setp.gt.s32 p, %40, 7;\n\t@p ld.global.v4.f32 {%28, %29, %30, %31}, [%39];\n\t}"
+                 : "+f"(v[0][0]), "+f"(v[0][1]), "+f"(v[0][2]), "+f"(v[0][3]), "+f"(v[1][0]), "+f"(v[1][1]), "+f"(v[1][2]), "+f"(v[1][3]),
+                   "+f"(v[2][0]), "+f"(v[2][1]), "+f"(v[2][2]), "+f"(v[2][3]), "+f"(v[3][0]), "+f"(v[3][1]), "+f"(v[3][2]), "+f"(v[3][3]),
+                   "+f"(v[4][0]), "+f"(v[4][1]), "+f"(v[4][2]), "+f"(v[4][3]), "+f"(v[5][0]), "+f"(v[5][1]), "+f"(v[5][2]), "+f"(v[5][3]),
+                   "+f"(v[6][0]), "+f"(v[6][1]), "+f"(v[6][2]), "+f"(v[6][3]), "+f"(v[7][0]), "+f"(v[7][1]), "+f"(v[7][2]), "+f"(v[7][3])
+                 : "l"(from), "l"(from + pitch), "l"(from + 2 * pitch), "l"(from + 3 * pitch), "l"(from + 4 * pitch), "l"(from + 5 * pitch),
+                   "l"(from + 6 * pitch), "l"(from + 7 * pitch), "r"(n)
+                 : "memory");
+}
+
 // The parts of a run that passes a chunk's end, added in order by a warp of
 // the chunk that it begins in: four columns a lane, sixteen parts in flight.
-// Bound by latency (16384 tokens, 2048 columns, runs of up to 33 parts).
+// Bound by latency.
 constexpr int kJoinStripe = 128, kJoinAhead = 16;
 
 template <int BF16, int VEC> __global__ void __launch_bounds__(128) zero_embed_join_kernel(const __grid_constant__ RunArgs a)
@@ -467,7 +499,7 @@ template <int BF16, int VEC> __global__ void __launch_bounds__(128) zero_embed_j
     let_successor_start();
     wait_for_predecessor();
     if (task >= a.join_tasks) return;
-    const int stripes = (a.D + kJoinStripe - 1) / kJoinStripe;
+    const int stripes = (a.pitch + kJoinStripe - 1) / kJoinStripe;
     const long long chunk = task / stripes, first = chunk * a.chunk, end = first + a.chunk;
     if (end >= a.T) return;
     const int key = a.sorted[end - 1].x, next = a.sorted[end].x, previous = first > 0 ? a.sorted[first - 1].x : -1;
@@ -484,37 +516,33 @@ template <int BF16, int VEC> __global__ void __launch_bounds__(128) zero_embed_j
         if (n < 32) break;
     }
     const int c0 = static_cast<int>(task - chunk * stripes) * kJoinStripe;
-    const int at = min(c0 + lane * 4, a.pitch - 4); // lanes behind the row read its end, and write nothing
+    const int at = min(c0 + lane * 4, a.pitch - 4); // lanes behind the parts read their end, and write nothing
     uint16_t* row = static_cast<uint16_t*>(a.dtable) + key * a.lddt;
+    const int col = VEC ? at : at - phase_of(row);
     float sum[4], old[4];
     const float4 tail = *reinterpret_cast<const float4*>(a.parts + (chunk * 2 + 1) * a.pitch + at);
     sum[0] = tail.x, sum[1] = tail.y, sum[2] = tail.z, sum[3] = tail.w;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) old[j] = a.add && at + j < a.D ? load16(row, at + j, BF16) : 0.0f;
+    for (int j = 0; j < 4; ++j) old[j] = a.add && col + j >= 0 && col + j < a.D ? load16(row, col + j, BF16) : 0.0f;
     for (long long c = chunk + 1; c <= last; c += kJoinAhead) {
         const int n = static_cast<int>(min(static_cast<long long>(kJoinAhead), last + 1 - c));
-        float v[kJoinAhead][4];
+        float v[kJoinAhead / 8][8][4];
 #pragma unroll
-        for (int k = 0; k < kJoinAhead; ++k) {
-            float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (k < n) f = __ldcg(reinterpret_cast<const float4*>(a.parts + (c + k) * 2 * a.pitch + at));
-            v[k][0] = f.x, v[k][1] = f.y, v[k][2] = f.z, v[k][3] = f.w;
-        }
-        __syncwarp(); // keeps the reads before it: the compiler adds each part before it reads the next else (15 us instead of 6)
+        for (int h = 0; h < kJoinAhead / 8; ++h) read_eight(a.parts + (c + 8 * h) * 2 * a.pitch + at, 2ll * a.pitch, n - 8 * h, v[h]);
 #pragma unroll
         for (int k = 0; k < kJoinAhead; ++k)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) sum[j] += v[k][j];
+            for (int j = 0; j < 4; ++j) sum[j] += v[k / 8][k % 8][j];
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) sum[j] = sum[j] * a.scale + old[j];
-    if (c0 + lane * 4 >= a.D) return;
+    if (c0 + lane * 4 >= a.pitch) return;
     if (VEC) {
         *reinterpret_cast<uint2*>(row + at) = make_uint2(pack16(sum[0], sum[1], BF16), pack16(sum[2], sum[3], BF16));
     } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (at + j < a.D) store16(row, at + j, sum[j], BF16);
+            if (col + j >= 0 && col + j < a.D) store16(row, col + j, sum[j], BF16);
     }
 }
 
@@ -534,7 +562,7 @@ bool bad_embed(int64_t T, int64_t D, int64_t V, float scale, int32_t type)
 struct GradPlan {
     int cluster;         // rounds of the sort by one cluster, 0: a launch per pass
     int rounds, blocks, passes, chunk;
-    int64_t chunks, stripes;
+    int64_t chunks, stripes, pitch;
     int2* pairs[2];
     uint32_t* counts;
     float* parts;
@@ -551,7 +579,8 @@ GradPlan plan_grad(int64_t T, int64_t D, int64_t V, void* workspace)
     int bits = 1;
     while ((V >> bits) != 0) ++bits; // of V itself, which stands for no row
     p.passes = (bits + kDigitBits - 1) / kDigitBits;
-    p.stripes = (D + kStripe - 1) / kStripe;
+    p.pitch = up(D + 7, 8); // granules of a row that starts anywhere
+    p.stripes = (p.pitch + kStripe - 1) / kStripe;
     // short chunks where there are few: a chunk's rows follow on each other; longer ones once there are warps
     // enough: fewer runs are cut
     p.chunk = 4;
@@ -562,7 +591,7 @@ GradPlan plan_grad(int64_t T, int64_t D, int64_t V, void* workspace)
     p.pairs[0] = static_cast<int2*>(c.take(T * 8));
     p.pairs[1] = p.cluster ? p.pairs[0] : static_cast<int2*>(c.take(T * 8));
     p.counts = static_cast<uint32_t*>(c.take(static_cast<int64_t>(p.passes) * p.blocks * kDigits * 4));
-    p.parts = static_cast<float*>(c.take(p.chunks * 2 * up(D, 8) * 4));
+    p.parts = static_cast<float*>(c.take(p.chunks * 2 * p.pitch * 4));
     p.bytes = c.used;
     return p;
 }
@@ -614,11 +643,11 @@ extern "C" int zero_embed_forward(const int32_t* ids, const void* table, int64_t
     if (share(y, ldy, T, D, table, ldt, V, D) || share(y, ldy, T, D, ids, 2 * T, 1, 2 * T)) return ZERO_EOVERLAP;
     LookArgs a{};
     a.ids = ids, a.table = table, a.y = y, a.ldt = ldt, a.ldy = ldy, a.T = T, a.D = static_cast<int>(D), a.V = static_cast<int>(V);
-    a.pieces = static_cast<int>((D + kLookPiece - 1) / kLookPiece);
+    const bool vec = D % 8 == 0 && aligned16(table, ldt) && aligned16(y, ldy);
+    a.pieces = static_cast<int>((D + (vec ? 0 : 7) + kLookPiece - 1) / kLookPiece);
     a.items = T * a.pieces;
     a.scale = scale;
     if ((a.items + 7) / 8 > INT32_MAX) return ZERO_EINVAL;
-    const bool vec = D % 8 == 0 && aligned16(table, ldt) && aligned16(y, ldy);
     auto fn = pick(type == ZERO_TYPE_BF16, vec, zero_embed_kernel<0, 0>, zero_embed_kernel<0, 1>, zero_embed_kernel<1, 0>, zero_embed_kernel<1, 1>);
     return launch_after(fn, a, (a.items + 7) / 8, 256, 0, 1, static_cast<cudaStream_t>(cuda_stream));
 }
@@ -649,16 +678,16 @@ extern "C" int zero_embed_backward(const int32_t* ids, const void* dy, int64_t l
     if (in_workspace(workspace, p.bytes, dy, lddy, T, D) || in_workspace(workspace, p.bytes, dtable, lddt, V, D) ||
         in_workspace(workspace, p.bytes, ids, 2 * T, 1, 2 * T))
         return ZERO_EOVERLAP;
+    const int bf16 = type == ZERO_TYPE_BF16;
+    const bool vec = D % 8 == 0 && aligned16(dy, lddy) && aligned16(dtable, lddt);
     RunArgs r{};
     r.dy = dy, r.dtable = dtable, r.parts = p.parts, r.lddy = lddy, r.lddt = lddt, r.T = T, r.D = static_cast<int>(D), r.V = static_cast<int>(V);
-    r.stripes = static_cast<int>(p.stripes), r.chunk = p.chunk, r.pitch = static_cast<int>(up(D, 8)), r.add = add != 0, r.scale = scale;
-    r.sum_tasks = p.chunks * p.stripes;
-    r.join_tasks = p.chunks * ((D + kJoinStripe - 1) / kJoinStripe);
+    r.pitch = static_cast<int>(vec ? D : p.pitch), r.stripes = (r.pitch + kStripe - 1) / kStripe, r.chunk = p.chunk, r.add = add != 0, r.scale = scale;
+    r.sum_tasks = p.chunks * r.stripes;
+    r.join_tasks = p.chunks * ((r.pitch + kJoinStripe - 1) / kJoinStripe);
     if (!add && p.cluster) r.cleared = std::min<int64_t>(V, kClearBytes / (2 * D));
     r.tasks = r.sum_tasks + (add ? 0 : (V - r.cleared + kZeroRows - 1) / kZeroRows);
     if ((r.tasks + 7) / 8 > INT32_MAX || (r.join_tasks + 3) / 4 > INT32_MAX) return ZERO_EINVAL;
-    const int bf16 = type == ZERO_TYPE_BF16;
-    const bool vec = D % 8 == 0 && aligned16(dy, lddy) && aligned16(dtable, lddt);
     int rc = ZERO_OK;
     if (p.cluster) {
         ClusterSortArgs s{};

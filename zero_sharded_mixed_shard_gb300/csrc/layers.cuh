@@ -124,46 +124,115 @@ __device__ __forceinline__ uint4 first_of(const uint4& v, int n)
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Elements [c, c + 8) of a row of D, zeros past its end.  Reads only granules
-// that hold an element of the row.
+// Elements [c, c + 8) of a row of D, c above -8, zeros past its end (what lies
+// before the row is anything).  Reads only granules that hold an element of
+// the row.
 __device__ __forceinline__ uint4 load_any(const uint16_t* row, int c, int D)
 {
     uint4 a = make_uint4(0, 0, 0, 0), b = a;
     const int e = phase_of(row + c);
     const uint4* from = reinterpret_cast<const uint4*>(row + c - e);
-    if (c < D) a = from[0];
+    if (c < D && c - e > -8) a = from[0];
     if (e && c + 8 - e < D) b = from[1];
     return first_of(shifted(a, b, e), D - c);
 }
 
+// The first n (0 to 7) elements of a granule, and those from e (1 to 7) on, in
+// three stores at most.
+__device__ __forceinline__ void put_first(uint16_t* p, const uint4& g, int n)
+{
+    if (n & 4) *reinterpret_cast<uint2*>(p) = make_uint2(g.x, g.y);
+    if (n & 2) *reinterpret_cast<uint32_t*>(p + (n & 4)) = n & 4 ? g.z : g.x;
+    if (n & 1) p[n - 1] = static_cast<uint16_t>(n & 4 ? (n & 2 ? g.w : g.z) : (n & 2 ? g.y : g.x));
+}
+
+__device__ __forceinline__ void put_from(uint16_t* p, const uint4& g, int e)
+{
+    if (e <= 4) *reinterpret_cast<uint2*>(p + 4) = make_uint2(g.z, g.w);
+    if (e <= 2 || e == 5 || e == 6) *reinterpret_cast<uint32_t*>(p + (e <= 2 ? 2 : 6)) = e <= 2 ? g.y : g.w;
+    if (e & 1) p[e] = static_cast<uint16_t>((e & 4 ? (e & 2 ? g.w : g.z) : (e & 2 ? g.y : g.x)) >> 16);
+}
+
+// The granule whose first element is `at` (above -8) of a row of D: what
+// belongs to the row.
+__device__ __forceinline__ void put_granule(uint16_t* row, int at, int D, const uint4& g)
+{
+    uint16_t* p = row + at;
+    if (at >= 0 && at + 8 <= D) {
+        *reinterpret_cast<uint4*>(p) = g;
+    } else if (at >= 0) {
+        if (at < D) put_first(p, g, D - at);
+    } else if (at + 8 <= D) {
+        put_from(p, g, -at);
+    } else { // a row that begins and ends in one granule
+        const uint32_t w[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+        for (int j = 1; j < 8; ++j)
+            if (at + j >= 0 && at + j < D) p[j] = static_cast<uint16_t>(w[j >> 1] >> (j & 1) * 16);
+    }
+}
+
 // Elements [c, c + 8) of a row of D from each of a run of lanes with
-// neighbouring c, all of which call this; `first` and `last` mark its ends.  A
-// granule is written whole where the run holds all of it, else by elements.
+// neighbouring c, by whole warps; `first` and `last` mark the run's ends.  A
+// granule is written whole where the run holds all of it.
 __device__ __forceinline__ void store_any(uint16_t* row, int c, int D, const uint4& v, bool first, bool last)
 {
-    const int e = phase_of(row + c);
+    const int e = phase_of(row + c), at = c - e;
     uint4 before;
     before.x = __shfl_up_sync(0xffffffffu, v.x, 1);
     before.y = __shfl_up_sync(0xffffffffu, v.y, 1);
     before.z = __shfl_up_sync(0xffffffffu, v.z, 1);
     before.w = __shfl_up_sync(0xffffffffu, v.w, 1);
     const uint4 g = e ? shifted(before, v, 8 - e) : v; // the granule that holds element c
-    const int at = c - e;
-    if (at < D && at + 8 <= D && (!first || !e)) {
-        *reinterpret_cast<uint4*>(row + at) = g;
-    } else if (at < D) {
+    uint16_t* p = row + at;
+    if (at + 8 <= D && (!first || !e)) {
+        *reinterpret_cast<uint4*>(p) = g;
+    } else if (!first || !e) {
+        if (at < D) put_first(p, g, D - at);
+    } else if (at + 8 <= D) {
+        put_from(p, g, e);
+    } else { // a row that begins and ends in one granule
         const uint32_t w[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (at + j < D && (!first || j >= e)) row[at + j] = static_cast<uint16_t>(w[j >> 1] >> (j & 1) * 16);
-    }
-    if (last && e) { // what lies in the granule behind
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
         for (int j = 1; j < 8; ++j)
-            if (j >= 8 - e && c + j < D) row[c + j] = static_cast<uint16_t>(w[j >> 1] >> (j & 1) * 16);
+            if (j >= e && at + j < D) p[j] = static_cast<uint16_t>(w[j >> 1] >> (j & 1) * 16);
     }
+    if (last && e && at + 8 < D) put_first(p + 8, shifted(v, make_uint4(0, 0, 0, 0), 8 - e), min(e, D - at - 8));
 }
+
+// ---------------------------------------------------------------------------
+// Two fp32 operations in one instruction
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\tfma.rn.f32x2 a, a, b, c;\n\t"
+        "mov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // ---------------------------------------------------------------------------
 // Host side

@@ -69,15 +69,22 @@ template <int VEC, int GROUP> __device__ __forceinline__ void store_row(uint16_t
     else if (c < D) *reinterpret_cast<uint4*>(row + c) = v;
 }
 
+template <int BF16> __device__ __forceinline__ void widen(const uint4& u, float2 (&v)[4])
+{
+    v[0] = unpack16(u.x, BF16), v[1] = unpack16(u.y, BF16), v[2] = unpack16(u.z, BF16), v[3] = unpack16(u.w, BF16);
+}
+
 template <int BF16> __device__ __forceinline__ void widen(const uint4& u, float (&v)[8])
 {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    float2 p[4];
+    widen<BF16>(u, p);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float2 f = unpack16(w[j], BF16);
-        v[2 * j] = f.x;
-        v[2 * j + 1] = f.y;
-    }
+    for (int j = 0; j < 4; ++j) v[2 * j] = p[j].x, v[2 * j + 1] = p[j].y;
+}
+
+template <int BF16> __device__ __forceinline__ uint4 narrow(const float2 (&v)[4])
+{
+    return make_uint4(pack16(v[0].x, v[0].y, BF16), pack16(v[1].x, v[1].y, BF16), pack16(v[2].x, v[2].y, BF16), pack16(v[3].x, v[3].y, BF16));
 }
 
 // Rows to come, copied to shared memory ahead of their use: AHEAD of them,
@@ -173,13 +180,16 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float (*part)[THREADS /
     }
 }
 
-// Forward: CTAs that stay, two on an SM, as many groups as fit in each, a row
-// per group at a time.  Bound by HBM: NORM_TIME.
+// Forward: a CTA that stays on every SM, as many groups as fit in it, a row per
+// group at a time.  A thread has four vectors of a row where it is wide enough:
+// fewer threads have less to join.  Its weights and biases stay in its
+// registers.  Bound by HBM and by latency: NORM_TIME.
 constexpr int kNormThreads = 512;
-template <int VPT> constexpr int kForwardAhead = VPT == 1 ? 8 : VPT == 2 ? 5 : 3;
+template <int VPT> constexpr int kForwardAhead = VPT == 4 ? 5 : 8;
+template <int VEC, int GROUP, int VPT> using ForwardRows = Rows<VEC, GROUP, VPT, 1, kForwardAhead<VPT>, kNormThreads>;
 
 template <int BF16, int VEC, int GROUP, int VPT>
-__global__ void __launch_bounds__(kNormThreads, 2) zero_layernorm_kernel(const __grid_constant__ NormArgs a)
+__global__ void __launch_bounds__(kNormThreads, 1) zero_layernorm_kernel(const __grid_constant__ NormArgs a)
 {
     extern __shared__ __align__(16) unsigned char raw[];
     constexpr int kGroups = kNormThreads / GROUP, S = kForwardAhead<VPT>;
@@ -191,7 +201,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) zero_layernorm_kernel(const _
     const uint16_t* w = static_cast<const uint16_t*>(a.w);
     const uint16_t* b = static_cast<const uint16_t*>(a.b);
     uint16_t* y = static_cast<uint16_t*>(a.y);
-    Rows<VEC, GROUP, VPT, 1, S, kNormThreads> rows(raw, self);
+    ForwardRows<VEC, GROUP, VPT> rows(raw, self);
     const long long step = static_cast<long long>(gridDim.x) * kGroups;
     // the groups of a warp go round equally often: a group without a row works on none
     constexpr int kTogether = GROUP < 32 ? 32 / GROUP : 1;
@@ -201,6 +211,13 @@ __global__ void __launch_bounds__(kNormThreads, 2) zero_layernorm_kernel(const _
         rows.commit();
     };
     for (int s = 0; s < S - 1; ++s) ahead(s, first + s * step);
+    uint4 weight[VPT], bias[VPT];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        const uint32_t one = BF16 ? 0x3f803f80u : 0x3c003c00u;
+        weight[k] = w ? load_row<VEC>(w, column<GROUP>(k, self), a.D) : make_uint4(one, one, one, one);
+        bias[k] = b ? load_row<VEC>(b, column<GROUP>(k, self), a.D) : make_uint4(0, 0, 0, 0);
+    }
     int s = 0, turn = 0;
     for (long long lead = leader, r = first; lead < a.T; lead += step, r += step) {
         const int D = r < a.T ? a.D : 0;
@@ -208,34 +225,39 @@ __global__ void __launch_bounds__(kNormThreads, 2) zero_layernorm_kernel(const _
         rows.read();
         ahead(s == 0 ? S - 1 : s - 1, r + (S - 1) * step); // into the slot that the last row has left
         rows.wait();
-        uint4 p[VPT];
-#pragma unroll
-        for (int k = 0; k < VPT; ++k) p[k] = rows.get(s, 0, k, from, D);
+        float2 v[VPT][4];
         // the mean as a sum of x / D: no partial sum is above the largest value
-        float sum[1] = {0.0f};
+        float2 total = both(0.0f);
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            float v[8];
-            widen<BF16>(p[k], v);
+            widen<BF16>(rows.get(s, 0, k, from, D), v[k]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum[0] = fmaf(v[j], a.inv_d, sum[0]);
+            for (int j = 0; j < 4; ++j) total = fma2(v[k][j], both(a.inv_d), total);
         }
+        float sum[1] = {total.x + total.y};
         group_sum<GROUP, 1, kNormThreads>(sum, part, group, &turn);
-        const float mean = sum[0], half_mean = -0.5f * mean;
-        // half of the centred value: a difference of two values of bf16's range may pass fp32's
-        auto squares = [&](float scale) {
-            float q[1] = {0.0f};
+        const float mean = sum[0];
+        // half of the centred values: a difference of two values of bf16's range may pass fp32's; 0 past the row's end
 #pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                float v[8];
-                widen<BF16>(p[k], v);
-                const int there = D - column<GROUP>(k, self);
+        for (int k = 0; k < VPT; ++k) {
+            const int there = D - column<GROUP>(k, self);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float d = fmaf(v[j], 0.5f, half_mean) * scale;
-                    if (VEC ? there > 0 : there > j) q[0] = fmaf(d, d, q[0]);
-                }
+            for (int j = 0; j < 4; ++j) {
+                v[k][j] = fma2(v[k][j], both(0.5f), both(-0.5f * mean));
+                if (VEC ? there <= 0 : there <= 2 * j) v[k][j].x = 0.0f;
+                if (VEC ? there <= 0 : there <= 2 * j + 1) v[k][j].y = 0.0f;
             }
+        }
+        auto squares = [&](float scale) {
+            float2 all = both(0.0f);
+#pragma unroll
+            for (int k = 0; k < VPT; ++k)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 d = mul2(v[k][j], both(scale));
+                    all = fma2(d, d, all);
+                }
+            float q[1] = {all.x + all.y};
             group_sum<GROUP, 1, kNormThreads>(q, part, group, &turn);
             return q[0];
         };
@@ -252,21 +274,15 @@ __global__ void __launch_bounds__(kNormThreads, 2) zero_layernorm_kernel(const _
             if (a.mean) a.mean[r] = mean;
             if (a.rstd) a.rstd[r] = rstd;
         }
-        const float twice = 2.0f * rstd;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const int c = column<GROUP>(k, self);
-            float v[8], g[8], h[8];
-            widen<BF16>(p[k], v);
-            if (w) widen<BF16>(load_row<VEC>(w, c, a.D), g);
-            if (b) widen<BF16>(load_row<VEC>(b, c, a.D), h);
+            float2 g[4], h[4];
+            widen<BF16>(weight[k], g);
+            widen<BF16>(bias[k], h);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                v[j] = fmaf(v[j], 0.5f, half_mean) * twice;
-                if (w) v[j] *= g[j];
-                if (b) v[j] += h[j];
-            }
-            store_row<VEC, GROUP>(y + r * a.ldy, c, self, D, pack8(v, BF16));
+            for (int j = 0; j < 4; ++j) v[k][j] = fma2(mul2(v[k][j], both(2.0f * rstd)), g[j], h[j]);
+            store_row<VEC, GROUP>(y + r * a.ldy, c, self, D, narrow<BF16>(v[k]));
         }
         if (++s == S) s = 0;
     }
@@ -365,14 +381,14 @@ __global__ void __launch_bounds__(kGradThreads, 1) zero_layernorm_grad_kernel(co
     const uint16_t* x = static_cast<const uint16_t*>(a.x);
     const uint16_t* res = static_cast<const uint16_t*>(a.res);
     uint16_t* dx = static_cast<uint16_t*>(a.dx);
-    float dw[VPT][8], db[VPT][8];
+    float2 dw[VPT][4], db[VPT][4];
     uint4 w[VPT];
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
         const uint32_t one = BF16 ? 0x3f803f80u : 0x3c003c00u;
         w[k] = a.w ? load_row<VEC>(static_cast<const uint16_t*>(a.w), column<GROUP>(k, self), a.D) : make_uint4(one, one, one, one);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dw[k][j] = db[k][j] = 0.0f;
+        for (int j = 0; j < 4; ++j) dw[k][j] = db[k][j] = both(0.0f);
     }
     GradRows<VEC, GROUP, VPT> rows(raw, self);
     const long long step = static_cast<long long>(gridDim.x) * kGroups;
@@ -403,43 +419,47 @@ __global__ void __launch_bounds__(kGradThreads, 1) zero_layernorm_grad_kernel(co
             px[k] = rows.get(s, 0, k, x + r * a.ldx, D);
             pd[k] = rows.get(s, 1, k, dy + r * a.lddy, D);
         }
-        float sum[2] = {0.0f, 0.0f};
+        float2 sum_g = both(0.0f), sum_gh = both(0.0f);
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            float vx[8], vd[8], vw[8];
+            float2 vx[4], vd[4], vw[4];
             widen<BF16>(px[k], vx);
             widen<BF16>(pd[k], vd);
             widen<BF16>(w[k], vw);
             // past the row's end dy is 0: such sums go nowhere, so long as their h is finite
             const int there = D - column<GROUP>(k, self);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float h = fmaf(vx[j], 0.5f, mean) * rstd;
-                if (VEC ? there <= 0 : there <= j) h = 0.0f;
-                const float g = vd[j] * vw[j];
-                dw[k][j] = fmaf(vd[j], h, dw[k][j]);
-                db[k][j] += vd[j];
-                sum[0] += g;
-                sum[1] = fmaf(g, h, sum[1]);
+            for (int j = 0; j < 4; ++j) {
+                float2 h = mul2(fma2(vx[j], both(0.5f), both(mean)), both(rstd));
+                if (VEC ? there <= 0 : there <= 2 * j) h.x = 0.0f;
+                if (VEC ? there <= 0 : there <= 2 * j + 1) h.y = 0.0f;
+                const float2 g = mul2(vd[j], vw[j]);
+                dw[k][j] = fma2(vd[j], h, dw[k][j]);
+                db[k][j] = add2(db[k][j], vd[j]);
+                sum_g = add2(sum_g, g);
+                sum_gh = fma2(g, h, sum_gh);
             }
         }
         if (dx) {
+            float sum[2] = {sum_g.x + sum_g.y, sum_gh.x + sum_gh.y};
             group_sum<GROUP, 2, kGradThreads>(sum, part, group, &turn);
             const float c0 = sum[0] * a.inv_d, c1 = sum[1] * a.inv_d, half = 0.5f * rstd;
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                float vx[8], vd[8], vw[8], o[8];
+                float2 vx[4], vd[4], vw[4], o[4];
                 widen<BF16>(px[k], vx);
                 widen<BF16>(pd[k], vd);
                 widen<BF16>(w[k], vw);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[j] = both(0.0f);
                 if (res) widen<BF16>(rows.get(s, 2, k, res + r * a.ldr, D), o);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float h = fmaf(vx[j], 0.5f, mean) * rstd;
-                    const float d = half * (vd[j] * vw[j] - c0 - h * c1);
-                    o[j] = res ? o[j] + d : d;
+                for (int j = 0; j < 4; ++j) {
+                    const float2 h = mul2(fma2(vx[j], both(0.5f), both(mean)), both(rstd));
+                    const float2 t = add2(fma2(vd[j], vw[j], both(-c0)), mul2(h, both(-c1)));
+                    o[j] = fma2(t, both(half), o[j]);
                 }
-                store_row<VEC, GROUP>(dx + r * a.lddx, column<GROUP>(k, self), self, D, pack8(o, BF16));
+                store_row<VEC, GROUP>(dx + r * a.lddx, column<GROUP>(k, self), self, D, narrow<BF16>(o));
             }
         }
         if (++s == S) s = 0;
@@ -453,10 +473,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) zero_layernorm_grad_kernel(co
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int c = column<GROUP>(k, self) + j;
-            all[(group * 2) * kWidth + c] = dw[k][j];
-            all[(group * 2 + 1) * kWidth + c] = db[k][j];
+        for (int j = 0; j < 4; ++j) {
+            const int c = column<GROUP>(k, self) + 2 * j;
+            *reinterpret_cast<float2*>(all + (group * 2) * kWidth + c) = dw[k][j];
+            *reinterpret_cast<float2*>(all + (group * 2 + 1) * kWidth + c) = db[k][j];
         }
     }
     __syncthreads();
@@ -612,20 +632,19 @@ struct NormPick {
 
 template <int BF16, int VEC, int GROUP, int VPT> NormPick norm_pick()
 {
-    return {zero_layernorm_kernel<BF16, VEC, GROUP, VPT>, GROUP, Rows<VEC, GROUP, VPT, 1, kForwardAhead<VPT>, kNormThreads>::kBytes};
+    return {zero_layernorm_kernel<BF16, VEC, GROUP, VPT>, GROUP, ForwardRows<VEC, GROUP, VPT>::kBytes};
 }
 
-// The narrowest group that holds a row in one or two vectors a thread: fewer
-// threads have less to join.
 template <int BF16, int VEC> NormPick pick_norm(int64_t D)
 {
     if (D <= 64) return norm_pick<BF16, VEC, 8, 1>();
-    if (D <= 256) return norm_pick<BF16, VEC, 32, 1>();
-    if (D <= 512) return norm_pick<BF16, VEC, 32, 2>();
-    if (D <= 1024) return norm_pick<BF16, VEC, 64, 2>();
-    if (D <= 2048) return norm_pick<BF16, VEC, 128, 2>();
-    if (D <= 4096) return norm_pick<BF16, VEC, 256, 2>();
-    if (D <= 8192) return norm_pick<BF16, VEC, 512, 2>();
+    if (D <= 128) return norm_pick<BF16, VEC, 8, 2>();
+    if (D <= 256) return norm_pick<BF16, VEC, 8, 4>();
+    if (D <= 512) return norm_pick<BF16, VEC, 16, 4>();
+    if (D <= 1024) return norm_pick<BF16, VEC, 32, 4>();
+    if (D <= 2048) return norm_pick<BF16, VEC, 64, 4>();
+    if (D <= 4096) return norm_pick<BF16, VEC, 128, 4>();
+    if (D <= 8192) return norm_pick<BF16, VEC, 256, 4>();
     return norm_pick<BF16, VEC, 512, 4>();
 }
 
@@ -723,7 +742,7 @@ extern "C" int zero_layernorm_forward(const void* x, int64_t ldx, const void* we
     int rc = sm_count(&sms);
     if (rc) return rc;
     const NormPick k = pick_norm(D, bf16, vec);
-    const int64_t per_cta = kNormThreads / k.group, ctas = std::min<int64_t>((T + per_cta - 1) / per_cta, 2ll * sms);
+    const int64_t per_cta = kNormThreads / k.group, ctas = std::min<int64_t>((T + per_cta - 1) / per_cta, sms);
     if ((rc = allow_smem(reinterpret_cast<const void*>(k.fn), k.smem))) return rc;
     return launch_after(k.fn, a, ctas, kNormThreads, k.smem, 1, st);
 }
