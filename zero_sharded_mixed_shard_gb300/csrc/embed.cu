@@ -391,7 +391,7 @@ template <int VEC> __device__ __forceinline__ void clear_rows(const RunArgs& a, 
     }
 }
 
-template <int BF16, int VEC, int ADD> __global__ void __launch_bounds__(256, 2) zero_embed_grad_kernel(const __grid_constant__ RunArgs a)
+template <int BF16, int VEC, int ADD> __global__ void __launch_bounds__(256, VEC ? (ADD ? 2 : 3) : 4) zero_embed_grad_kernel(const __grid_constant__ RunArgs a)
 {
     constexpr int kAhead = VEC ? 8 : 4; // rows in flight (two granules each off 16 bytes)
     const int lane = threadIdx.x & 31;
