@@ -12,7 +12,7 @@
 // its tokens by the lanes' matching digits and finds its place from the blocks'
 // digit counts): up to 65536 tokens by one cluster of eight CTAs, which
 // exchange counts and tokens through distributed shared memory while the other
-// SMs clear the first rows of the table, more by a launch per pass.  Then
+// SMs clear the first rows of the table, more by two launches per pass.  Then
 // warps walk over the sorted tokens, a chunk of them and a stripe of 256
 // columns each, adding rows of dy in registers; a run of equal ids that lies in
 // one chunk is written at once, the parts of a longer one go to the workspace
@@ -75,12 +75,13 @@ template <int BF16, int VEC> __global__ void __launch_bounds__(256) zero_embed_k
 
 constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
 constexpr int kSortThreads = kDigits, kSortWarps = kSortThreads / 32; // a thread per digit
+constexpr int kRounds = 8, kSortTokens = kRounds * kSortThreads;       // tokens of a block
 
 struct SortArgs {
     const int32_t* ids;  // the first pass: the ids in order
     const int2* from;    // later ones: (id, token)
     int2* to;
-    uint32_t* counts;    // [blocks][kDigits] of this pass
+    uint32_t* counts;    // [blocks + 1][kDigits] of this pass: each block's tokens with a digit, then sums of them
     uint32_t* next;      // the same of the next pass, null in the last
     long long T;
     int V, shift, blocks, all_counts;
@@ -91,29 +92,52 @@ __device__ __forceinline__ int sort_key(int id, int V) { return id >= 0 && id < 
 
 // Digit counts of each block for the first pass; the later passes' counts
 // become 0 (the passes before them add to these).
-template <int ROUNDS> __global__ void __launch_bounds__(kSortThreads) zero_sort_count_kernel(const __grid_constant__ SortArgs a)
+__global__ void __launch_bounds__(kSortThreads) zero_sort_count_kernel(const __grid_constant__ SortArgs a)
 {
     __shared__ uint32_t count[kDigits];
     let_successor_start();
     count[threadIdx.x] = 0;
     __syncthreads();
     wait_for_predecessor();
-    const long long t0 = static_cast<long long>(blockIdx.x) * (ROUNDS * kSortThreads);
+    const long long t0 = static_cast<long long>(blockIdx.x) * kSortTokens;
 #pragma unroll
-    for (int k = 0; k < ROUNDS; ++k) {
+    for (int k = 0; k < kRounds; ++k) {
         const long long t = t0 + k * kSortThreads + threadIdx.x;
         if (t < a.T) atomicAdd(&count[sort_key(a.ids[t], a.V) & (kDigits - 1)], 1u);
     }
     __syncthreads();
     a.counts[static_cast<long long>(blockIdx.x) * kDigits + threadIdx.x] = count[threadIdx.x];
     for (int p = 1; p < a.all_counts; ++p)
-        a.counts[(static_cast<long long>(p) * a.blocks + blockIdx.x) * kDigits + threadIdx.x] = 0;
+        a.counts[(static_cast<long long>(p) * (a.blocks + 1) + blockIdx.x) * kDigits + threadIdx.x] = 0;
+}
+
+// A warp per digit: its tokens in each block become those in the blocks before
+// it, and behind the last block stands the sum of all.
+__global__ void __launch_bounds__(256) zero_sort_scan_kernel(const __grid_constant__ SortArgs a)
+{
+    const int lane = threadIdx.x & 31, d = static_cast<int>(blockIdx.x) * 8 + static_cast<int>(threadIdx.x >> 5);
+    let_successor_start();
+    wait_for_predecessor();
+    uint32_t before = 0;
+    for (long long b0 = 0; b0 < a.blocks; b0 += 32) {
+        uint32_t* p = a.counts + (b0 + lane) * kDigits + d;
+        const uint32_t own = b0 + lane < a.blocks ? *p : 0;
+        uint32_t sum = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t n = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += n;
+        }
+        if (b0 + lane < a.blocks) *p = before + sum - own;
+        before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0) a.counts[static_cast<long long>(a.blocks) * kDigits + d] = before;
 }
 
 // One pass: each token's place is the start of its digit, the tokens with the
 // digit in earlier blocks, those in earlier warps of the block, and those
 // earlier in the warp.
-template <int ROUNDS> __global__ void __launch_bounds__(kSortThreads) zero_sort_pass_kernel(const __grid_constant__ SortArgs a)
+__global__ void __launch_bounds__(kSortThreads) zero_sort_pass_kernel(const __grid_constant__ SortArgs a)
 {
     __shared__ uint32_t count[kSortWarps][kDigits];
     __shared__ uint32_t warp_total[kSortWarps];
@@ -123,12 +147,11 @@ template <int ROUNDS> __global__ void __launch_bounds__(kSortThreads) zero_sort_
     for (int k = 0; k < kSortWarps; ++k) count[k][d] = 0;
     __syncthreads();
     wait_for_predecessor();
-    constexpr int kTokens = ROUNDS * kSortThreads;
-    const long long t0 = static_cast<long long>(blockIdx.x) * kTokens + warp * (ROUNDS * 32);
-    int key[ROUNDS], token[ROUNDS];
-    uint32_t rank[ROUNDS];
+    const long long t0 = static_cast<long long>(blockIdx.x) * kSortTokens + warp * (kRounds * 32);
+    int key[kRounds], token[kRounds];
+    uint32_t rank[kRounds];
 #pragma unroll
-    for (int k = 0; k < ROUNDS; ++k) {
+    for (int k = 0; k < kRounds; ++k) {
         const long long t = t0 + k * 32 + lane;
         key[k] = token[k] = 0;
         if (t < a.T) {
@@ -143,7 +166,7 @@ template <int ROUNDS> __global__ void __launch_bounds__(kSortThreads) zero_sort_
         }
     }
 #pragma unroll
-    for (int k = 0; k < ROUNDS; ++k) {
+    for (int k = 0; k < kRounds; ++k) {
         const bool live = t0 + k * 32 + lane < a.T;
         const int digit = live ? (key[k] >> a.shift) & (kDigits - 1) : kDigits;
         const uint32_t same = __match_any_sync(0xffffffffu, digit);
@@ -154,13 +177,7 @@ template <int ROUNDS> __global__ void __launch_bounds__(kSortThreads) zero_sort_
         __syncwarp();
     }
     // tokens with digit d in earlier blocks and in all
-    uint32_t earlier = 0, all = 0;
-#pragma unroll 8
-    for (int b = 0; b < a.blocks; ++b) {
-        const uint32_t n = a.counts[static_cast<long long>(b) * kDigits + d];
-        all += n;
-        if (b < static_cast<int>(blockIdx.x)) earlier += n;
-    }
+    const uint32_t earlier = a.counts[static_cast<long long>(blockIdx.x) * kDigits + d], all = a.counts[static_cast<long long>(a.blocks) * kDigits + d];
     // the start of digit d: an exclusive sum over the digits
     uint32_t sum = all;
 #pragma unroll
@@ -180,11 +197,11 @@ template <int ROUNDS> __global__ void __launch_bounds__(kSortThreads) zero_sort_
     }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < ROUNDS; ++k) {
+    for (int k = 0; k < kRounds; ++k) {
         if (t0 + k * 32 + lane >= a.T) continue;
         const uint32_t to = count[warp][(key[k] >> a.shift) & (kDigits - 1)] + rank[k];
         a.to[to] = make_int2(key[k], token[k]);
-        if (a.next) atomicAdd(&a.next[static_cast<long long>(to / kTokens) * kDigits + ((key[k] >> (a.shift + kDigitBits)) & (kDigits - 1))], 1u);
+        if (a.next) atomicAdd(&a.next[static_cast<long long>(to / kSortTokens) * kDigits + ((key[k] >> (a.shift + kDigitBits)) & (kDigits - 1))], 1u);
     }
 }
 
@@ -561,7 +578,7 @@ bool bad_embed(int64_t T, int64_t D, int64_t V, float scale, int32_t type)
 // The layout of a gradient's workspace and the sizes of its launches.
 struct GradPlan {
     int cluster;         // rounds of the sort by one cluster, 0: a launch per pass
-    int rounds, blocks, passes, chunk;
+    int blocks, passes, chunk;
     int64_t chunks, stripes, pitch;
     int2* pairs[2];
     uint32_t* counts;
@@ -574,8 +591,7 @@ GradPlan plan_grad(int64_t T, int64_t D, int64_t V, void* workspace)
     GradPlan p{};
     for (int r = 1; r <= 8 && !p.cluster; r *= 2)
         if (T <= r * kCluster * kClusterThreads) p.cluster = r;
-    p.rounds = 8;
-    p.blocks = p.cluster ? 0 : static_cast<int>((T + p.rounds * kSortThreads - 1) / (p.rounds * kSortThreads));
+    p.blocks = p.cluster ? 0 : static_cast<int>((T + kSortTokens - 1) / kSortTokens);
     int bits = 1;
     while ((V >> bits) != 0) ++bits; // of V itself, which stands for no row
     p.passes = (bits + kDigitBits - 1) / kDigitBits;
@@ -590,7 +606,7 @@ GradPlan plan_grad(int64_t T, int64_t D, int64_t V, void* workspace)
     Carver c{static_cast<unsigned char*>(workspace)};
     p.pairs[0] = static_cast<int2*>(c.take(T * 8));
     p.pairs[1] = p.cluster ? p.pairs[0] : static_cast<int2*>(c.take(T * 8));
-    p.counts = static_cast<uint32_t*>(c.take(static_cast<int64_t>(p.passes) * p.blocks * kDigits * 4));
+    p.counts = static_cast<uint32_t*>(c.take(p.cluster ? 0 : static_cast<int64_t>(p.passes) * (p.blocks + 1) * kDigits * 4));
     p.parts = static_cast<float*>(c.take(p.chunks * 2 * p.pitch * 4));
     p.bytes = c.used;
     return p;
@@ -614,19 +630,21 @@ template <class Kernel> Kernel pick(int bf16, int vec, Kernel k00, Kernel k01, K
     return bf16 ? (vec ? k11 : k10) : (vec ? k01 : k00);
 }
 
-// A launch for the first counts, then one per pass; ends in pairs[(passes - 1) & 1].
+// A launch for the first counts, then two per pass (the blocks' sums, the
+// tokens' places); ends in pairs[(passes - 1) & 1].
 int sort_by_passes(const GradPlan& p, const int32_t* ids, int64_t T, int64_t V, cudaStream_t st)
 {
     SortArgs s{};
     s.ids = ids, s.counts = p.counts, s.T = T, s.V = static_cast<int>(V), s.blocks = p.blocks, s.all_counts = p.passes;
-    int rc = launch_after(zero_sort_count_kernel<8>, s, p.blocks, kSortThreads, 0, 1, st);
+    int rc = launch_after(zero_sort_count_kernel, s, p.blocks, kSortThreads, 0, 1, st);
     for (int k = 0; k < p.passes && !rc; ++k) {
-        const int64_t each = static_cast<int64_t>(p.blocks) * kDigits;
+        const int64_t each = static_cast<int64_t>(p.blocks + 1) * kDigits;
         s.ids = k == 0 ? ids : nullptr;
         s.from = p.pairs[(k + 1) & 1], s.to = p.pairs[k & 1];
         s.counts = p.counts + k * each, s.next = k + 1 < p.passes ? p.counts + (k + 1) * each : nullptr;
         s.shift = k * kDigitBits;
-        rc = launch_after(zero_sort_pass_kernel<8>, s, p.blocks, kSortThreads, 0, 1, st);
+        if (!(rc = launch_after(zero_sort_scan_kernel, s, kDigits / 8, 256, 0, 1, st)))
+            rc = launch_after(zero_sort_pass_kernel, s, p.blocks, kSortThreads, 0, 1, st);
     }
     return rc;
 }
