@@ -17,7 +17,10 @@
 // gradient's elements at the target and the indices are that warp's, and are
 // stored last, after the CTA's barrier, from logits read before the second
 // pass: logits and gradient may be one matrix.
-// Bound by issue and exponentials, nearly by HBM: DISTILL_TIME.
+// Bound by HBM and, nearly, by issue and exponentials: 8192 rows of 44629 bf16
+// logits with 64 of a teacher's at temperature 2 (1.47 GB) 278 us, 5270 GB/s;
+// without a teacher 258 us.  (Each block's barrier for the teacher's sums, scalar
+// arithmetic and two exponentials an element 466 us.)
 #include "layers.cuh"
 
 namespace {

@@ -16,6 +16,12 @@
 //                                             runs over Wg's features, then over Wu's
 //   dWg = dg^T x,  dWu = du^T x
 // All three products go into one launch where they take the same kernel.
+//
+// Bound by the tensor cores: x [8192, 2048], 8192 features, SiLU, bf16, g and u
+// kept: forward 292 us (1880 TFLOP/s; 350 back to back at the card's power
+// limit), the backward pass's products 605 us (1820 TFLOP/s, tensor pipe 97 %
+// busy; in all 745, back to back 782).  With few tokens by the reads of the
+// weights: 4 tokens 14 us (67 MB).
 #include "gemm.cuh"
 
 namespace {
@@ -37,7 +43,9 @@ struct GatePrepArgs {
 
 // dg and du are rounded to 16 bits here, once, as operands of the products;
 // their column sums take them before that.
-// Bound by HBM: it reads three elements and writes two for each of T x N.
+// Bound by HBM: it reads three elements and writes two for each of T x N (8192 x
+// 8192 bf16, SiLU, 671 MB 107 us, 6270 GB/s; one, two or four rows of a thread in
+// flight make no difference).
 template <int ACT, int BF16>
 __global__ void __launch_bounds__(256) zero_gated_prep_kernel(const __grid_constant__ GatePrepArgs a)
 {

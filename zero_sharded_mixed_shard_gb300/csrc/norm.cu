@@ -183,7 +183,10 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float (*part)[THREADS /
 // Forward: a CTA that stays on every SM, as many groups as fit in it, a row per
 // group at a time.  A thread has four vectors of a row where it is wide enough:
 // fewer threads have less to join.  Its weights and biases stay in its
-// registers.  Bound by HBM and by latency: NORM_TIME.
+// registers.  16384 rows of 2048 bf16 elements (134 MB) 23 us, 5700 GB/s (two
+// vectors a thread, two CTAs an SM, weights in shared memory 35 us: twice the
+// joins; a CTA of 256 threads per row that does not stay 40); off 16 bytes 49 us,
+// bound by shifting the granules.
 constexpr int kNormThreads = 512;
 template <int VPT> constexpr int kForwardAhead = VPT == 4 ? 5 : 8;
 template <int VEC, int GROUP, int VPT> using ForwardRows = Rows<VEC, GROUP, VPT, 1, kForwardAhead<VPT>, kNormThreads>;
@@ -362,7 +365,8 @@ __global__ void __launch_bounds__(kWideThreads) zero_layernorm_wide_kernel(const
 // The gradient: a CTA of kGradThreads on every SM, as many groups as fit in it,
 // a row per group at a time.  A group joins its two sums of a row by one
 // barrier of its own.  16384 rows of 2048 bf16 elements with the residual (269
-// MB): NORM_GRAD_TIME.
+// MB) 46 us with the sums' launch, 5850 GB/s (rows read where they are used,
+// the CTA's barrier twice per four rows: 81 us); off 16 bytes 71 us.
 constexpr int kGradThreads = 512;
 template <int VPT> constexpr int kGradAhead = VPT == 1 ? 6 : 4;
 template <int VEC, int GROUP, int VPT> using GradRows = Rows<VEC, GROUP, VPT, 3, kGradAhead<VPT>, kGradThreads>;
