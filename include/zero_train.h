@@ -330,7 +330,7 @@ int zero_layernorm_workspace(int64_t T, int64_t D, int64_t* bytes);
  *   dweight = sum over rows of dy * h;  dbias = sum over rows of dy   [D]
  * dres [T][lddr] or NULL is the gradient that reaches x past the norm (a
  * residual's).  dx, dweight and dbias may each be NULL (not computed).  dx may
- * be dres itself, and dy itself where D is at most 8192 (same pointer and
+ * be dres itself, and dy itself where D is at most 16384 (same pointer and
  * stride).  Sums are in fp32 and in a fixed order; each output is rounded
  * once.  With T = 0 dweight and dbias become 0.
  * workspace: device, 16-byte aligned, zero_layernorm_workspace bytes (may be

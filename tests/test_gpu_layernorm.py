@@ -57,7 +57,7 @@ def check_forward(z, T, D, ty, pad=0, shift=0, weight=True, bias=True, stats=Tru
         assert bool(torch.isnan(mean[T:]).all()) and bool(torch.isnan(rstd[T:]).all())
 
 
-WIDTHS = [1, 7, 8, 64, 255, 256, 264, 513, 1000, 1024, 1032, 2048, 2049, 4096, 5000, 8192, 8200, 16384, 16392, 40000]
+WIDTHS = [1, 7, 8, 64, 255, 256, 264, 513, 1000, 1024, 1032, 2048, 2049, 4096, 5000, 8192, 8200, 12289, 16384, 16392, 40000]
 
 
 @pytest.mark.parametrize("D", WIDTHS)
@@ -158,7 +158,7 @@ def test_backward(z, T, D, ty, pad, shift):
     check_backward(z, T, D, ty, pad, shift)
 
 
-@pytest.mark.parametrize("T,D", [(5000, 100), (3001, 331), (2600, 2048), (4000, 1000), (700, 4096), (650, 9000)])
+@pytest.mark.parametrize("T,D", [(5000, 100), (3001, 331), (2600, 2048), (4000, 1000), (700, 4096), (650, 9000), (320, 17000)])
 @pytest.mark.parametrize("ty", [0, 1])
 def test_backward_many_rows(z, T, D, ty):
     check_backward(z, T, D, ty)
@@ -171,7 +171,7 @@ def test_backward_parts(z, want, res, weight, T, D):
     check_backward(z, T, D, 1, 0, 0, res, weight, want)
 
 
-@pytest.mark.parametrize("inplace,T,D", [("dy", 100, 333), ("res", 100, 333), ("dy", 50, 2048), ("res", 50, 8192), ("res", 20, 9001), ("dy", 1000, 64)])
+@pytest.mark.parametrize("inplace,T,D", [("dy", 100, 333), ("res", 100, 333), ("dy", 50, 2048), ("res", 50, 8192), ("res", 20, 9001), ("dy", 20, 16000), ("res", 10, 17001), ("dy", 1000, 64)])
 def test_backward_in_place(z, inplace, T, D):
     check_backward(z, T, D, 0, inplace=inplace)
 

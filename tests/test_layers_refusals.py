@@ -73,7 +73,7 @@ NORM_BACK = ("zero_layernorm_backward", "dy lddy x ldx w mean rstd res ldr dx ld
     (dict(dx=None, dw=None, db=None), E_INVAL), (dict(dy=None), E_INVAL), (dict(x=None), E_INVAL), (dict(mean=None), E_INVAL), (dict(rstd=None), E_INVAL), (dict(T=-1), E_INVAL),
     (dict(D=0), E_INVAL), (dict(lddy=63), E_INVAL), (dict(ldx=63), E_INVAL), (dict(ldr=63), E_INVAL), (dict(lddx=63), E_INVAL), (dict(type=2), E_INVAL), (dict(ws=None), E_INVAL),
     (dict(n=100), E_INVAL), (dict(ws=WS + 8), E_ALIGN), (dict(dy=A + 1), E_ALIGN), (dict(dx=G + 1), E_ALIGN), (dict(mean=D + 2), E_ALIGN), (dict(dw=H + 1), E_ALIGN),
-    (dict(dx=B), E_OVERLAP), (dict(dx=A + 2), E_OVERLAP), (dict(dx=A, D=9000, lddx=9000, lddy=9000, ldx=9000, ldr=9000), E_OVERLAP), (dict(dw=A), E_OVERLAP),
+    (dict(dx=B), E_OVERLAP), (dict(dx=A + 2), E_OVERLAP), (dict(dx=A, D=17000, lddx=17000, lddy=17000, ldx=17000, ldr=17000, n=1 << 23), E_OVERLAP), (dict(dw=A), E_OVERLAP),
     (dict(db=H + 64), E_OVERLAP), (dict(dw=G), E_OVERLAP), (dict(dw=C), E_OVERLAP), (dict(db=D), E_OVERLAP), (dict(ws=A), E_OVERLAP), (dict(ws=G - 256), E_OVERLAP)])
 def test_layernorm_backward(zlib, kw, code):
     assert call(zlib, *NORM_BACK, kw) == code

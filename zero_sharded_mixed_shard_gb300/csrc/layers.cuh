@@ -261,7 +261,7 @@ inline int widest_access(const void* p, int64_t ld) { return aligned16(p, ld) ? 
 inline int allow_smem(const void* fn, int bytes)
 {
     static std::mutex mu;
-    static struct { int dev; const void* fn; } known[64];
+    static struct { int dev; const void* fn; } known[128];
     static int n_known = 0;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -271,7 +271,7 @@ inline int allow_smem(const void* fn, int bytes)
         if (known[k].dev == dev && known[k].fn == fn) return ZERO_OK;
     e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return record(e);
-    if (n_known < 64) known[n_known++] = {dev, fn};
+    if (n_known < 128) known[n_known++] = {dev, fn};
     return ZERO_OK;
 }
 

@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kWideThreads) zero_layernorm_wide_kernel(const
 // MB) 46 us with the sums' launch, 5850 GB/s (rows read where they are used,
 // the CTA's barrier twice per four rows: 81 us); off 16 bytes 71 us.
 constexpr int kGradThreads = 512;
-template <int VPT> constexpr int kGradAhead = VPT == 1 ? 6 : 4;
+template <int VPT> constexpr int kGradAhead = VPT == 1 ? 6 : VPT == 2 ? 4 : 2;
 template <int VEC, int GROUP, int VPT> using GradRows = Rows<VEC, GROUP, VPT, 3, kGradAhead<VPT>, kGradThreads>;
 constexpr int kGradSums = 2 * kGradThreads * 8 * 4; // bytes of the groups' sums, for each vector of a thread
 
@@ -417,16 +417,21 @@ __global__ void __launch_bounds__(kGradThreads, 1) zero_layernorm_grad_kernel(co
         rows.read();
         ahead(s == 0 ? S - 1 : s - 1, r + (S - 1) * step); // into the slot that the last row has left
         rows.wait();
+        // the row's vectors; more than two of a thread are read again after the joins, its registers hold the columns' sums
+        constexpr bool kHeld = VPT < 3;
         uint4 px[VPT], pd[VPT];
-#pragma unroll
-        for (int k = 0; k < VPT; ++k) {
+        auto get = [&](int k) {
             px[k] = rows.get(s, 0, k, x + r * a.ldx, D);
             pd[k] = rows.get(s, 1, k, dy + r * a.lddy, D);
-        }
+        };
+        if (kHeld)
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) get(k);
         float2 sum_g = both(0.0f), sum_gh = both(0.0f);
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             float2 vx[4], vd[4], vw[4];
+            if (!kHeld) get(k);
             widen<BF16>(px[k], vx);
             widen<BF16>(pd[k], vd);
             widen<BF16>(w[k], vw);
@@ -451,6 +456,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) zero_layernorm_grad_kernel(co
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 float2 vx[4], vd[4], vw[4], o[4];
+                if (!kHeld) get(k);
                 widen<BF16>(px[k], vx);
                 widen<BF16>(pd[k], vd);
                 widen<BF16>(w[k], vw);
@@ -495,7 +501,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) zero_layernorm_grad_kernel(co
     }
 }
 
-// Rows of more than 8192 elements: dx with a CTA per row that reads it twice
+// Rows of more than 16384 elements: dx with a CTA per row that reads it twice
 // (the second time from L2), the sums of dw and db by stripes of columns.
 template <int BF16, int VEC>
 __global__ void __launch_bounds__(kWideThreads) zero_layernorm_wide_grad_kernel(const __grid_constant__ NormBackArgs a)
@@ -658,8 +664,7 @@ NormPick pick_norm(int64_t D, int bf16, int vec)
     return vec ? pick_norm<0, 1>(D) : pick_norm<0, 0>(D);
 }
 
-constexpr int64_t kForwardWide = 16384; // rows above it take the wide forward kernel
-constexpr int64_t kNormWide = 8192;     // rows above it the wide gradient kernels
+constexpr int64_t kNormWide = 16384; // rows above it take the wide kernels
 
 struct NormBackPick {
     NormBackKernel fn;
@@ -679,7 +684,9 @@ template <int BF16, int VEC> NormBackPick pick_back(int64_t D)
     if (D <= 1024) return back_pick<BF16, VEC, 128, 1>();
     if (D <= 2048) return back_pick<BF16, VEC, 128, 2>();
     if (D <= 4096) return back_pick<BF16, VEC, 256, 2>();
-    return back_pick<BF16, VEC, 512, 2>();
+    if (D <= 8192) return back_pick<BF16, VEC, 512, 2>();
+    if (D <= 12288) return back_pick<BF16, VEC, 512, 3>();
+    return back_pick<BF16, VEC, 512, 4>();
 }
 
 NormBackPick pick_back(int64_t D, int bf16, int vec)
@@ -736,7 +743,7 @@ extern "C" int zero_layernorm_forward(const void* x, int64_t ldx, const void* we
     NormArgs a{};
     a.x = x, a.w = weight, a.b = bias, a.y = y, a.mean = mean, a.rstd = rstd, a.ldx = ldx, a.ldy = ldy, a.T = T;
     a.D = static_cast<int>(D), a.eps = eps, a.inv_d = 1.0f / static_cast<float>(D);
-    if (D > kForwardWide) {
+    if (D > kNormWide) {
         NormKernel fn;
         if (bf16) fn = vec ? zero_layernorm_wide_kernel<1, 1> : zero_layernorm_wide_kernel<1, 0>;
         else fn = vec ? zero_layernorm_wide_kernel<0, 1> : zero_layernorm_wide_kernel<0, 0>;
