@@ -76,12 +76,14 @@ __global__ void __launch_bounds__(256) zero_gated_prep_kernel(const __grid_const
         if constexpr (ACT == ZERO_ACT_RELU) *dg = gv > 0.0f ? d * uv : 0.0f;
         else *dg = d * uv * slope<ACT>(gv);
     };
-    if (a.vec && col + 8 <= a.N) {
+    const bool whole = a.vec && col + 8 <= a.N; // else by granules; zeros past the last feature
+    if (col < a.half) {
 #pragma unroll 2
         for (long long r = r0 + line; r < r1; r += 8) {
-            const uint4 d4 = *reinterpret_cast<const uint4*>(dh + r * a.lddh + col);
-            const uint4 g4 = *reinterpret_cast<const uint4*>(g + r * a.ldg + col);
-            const uint4 u4 = *reinterpret_cast<const uint4*>(u + r * a.ldu + col);
+            const uint16_t *pd = dh + r * a.lddh, *pg = g + r * a.ldg, *pu = u + r * a.ldu;
+            const uint4 d4 = whole ? *reinterpret_cast<const uint4*>(pd + col) : load_any(pd, col, a.N);
+            const uint4 g4 = whole ? *reinterpret_cast<const uint4*>(pg + col) : load_any(pg, col, a.N);
+            const uint4 u4 = whole ? *reinterpret_cast<const uint4*>(pu + col) : load_any(pu, col, a.N);
             const uint32_t dw[4] = {d4.x, d4.y, d4.z, d4.w}, gw[4] = {g4.x, g4.y, g4.z, g4.w}, uw[4] = {u4.x, u4.y, u4.z, u4.w};
             uint32_t og[4], ou[4];
 #pragma unroll
@@ -98,23 +100,6 @@ __global__ void __launch_bounds__(256) zero_gated_prep_kernel(const __grid_const
             if (dz) {
                 *reinterpret_cast<uint4*>(dz + r * (2ll * a.half) + col) = make_uint4(og[0], og[1], og[2], og[3]);
                 *reinterpret_cast<uint4*>(dz + r * (2ll * a.half) + a.half + col) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
-            }
-        }
-    } else {
-        for (long long r = r0 + line; r < r1; r += 8) {
-            float dg[8], du[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                dg[j] = du[j] = 0.0f;
-                if (col + j < a.N)
-                    through(load16(dh, r * a.lddh + col + j, BF16), load16(g, r * a.ldg + col + j, BF16), load16(u, r * a.ldu + col + j, BF16),
-                            &dg[j], &du[j]);
-                sg[j] += dg[j];
-                su[j] += du[j];
-            }
-            if (dz && col < a.half) {
-                *reinterpret_cast<uint4*>(dz + r * (2ll * a.half) + col) = pack8(dg, BF16);
-                *reinterpret_cast<uint4*>(dz + r * (2ll * a.half) + a.half + col) = pack8(du, BF16);
             }
         }
     }

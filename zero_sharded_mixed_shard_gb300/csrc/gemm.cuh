@@ -1415,7 +1415,8 @@ struct Copy {
 };
 
 // 8 elements a thread, two bytes at a time (four-byte reads where rows allow
-// them were no faster: the copies' time is latency).
+// them were no faster, nor whole granules shifted: the copies' time is latency,
+// and of large ones their writes').
 __device__ __forceinline__ void copy_rows(const Copy& c, int cta)
 {
     const unsigned int vecs = (c.cols + 7) / 8;
