@@ -18,7 +18,7 @@
 // stored last, after the CTA's barrier, from logits read before the second
 // pass: logits and gradient may be one matrix.
 // Bound by HBM and, nearly, by issue and exponentials: 8192 rows of 44629 bf16
-// logits with 64 of a teacher's at temperature 2 (1.47 GB) 278 us, 5270 GB/s;
+// logits with 64 of a teacher's at temperature 2 (1.47 GB) 274 us, 5350 GB/s;
 // without a teacher 258 us.  (Each block's barrier for the teacher's sums, scalar
 // arithmetic and two exponentials an element 466 us.)
 #include "layers.cuh"
@@ -115,12 +115,14 @@ constexpr int kFewTeachers = 256;  // up to these the teacher's warp merges its 
 // VEC: a row of the gradient starts as far from a boundary of 16 bytes as its
 // row of logits.
 template <int BF16, int VEC, int SUMS, int kLossThreads>
-__global__ void __launch_bounds__(kLossThreads, kLossThreads == 128 ? 10 : 4) zero_distill_kernel(const __grid_constant__ LossArgs a)
+__global__ void __launch_bounds__(kLossThreads, kLossThreads == 64 ? 20 : kLossThreads == 128 ? 10 : 4) zero_distill_kernel(const __grid_constant__ LossArgs a)
 {
     constexpr int kLossWarps = kLossThreads / 32;
     __shared__ Tops tops[kLossWarps];
-    __shared__ float p_of[kMostTeacher], s_of[kMostTeacher], v_of[kMostTeacher];
-    __shared__ __align__(16) int j_of[kMostTeacher];
+    // the teacher's entries: probabilities, logits at their indices, the gradient's values, the indices
+    extern __shared__ float entries[];
+    float *p_of = entries, *s_of = p_of + a.K, *v_of = s_of + a.K;
+    int* j_of = reinterpret_cast<int*>(v_of + a.K);
     __shared__ int soft_flag;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long row = blockIdx.x;
@@ -346,13 +348,15 @@ template <int BF16, int VEC, int THREADS> LossKernel pick_loss(int sums)
     }
 }
 
-// Rows below this take 128 threads, ten rows an SM: a row's time is then the
-// latency of its steps (18280 rows of 5000 with 64 teacher's logits 129 us, 256
-// threads 280; without a teacher 74, 150).  Rows above it 256, four an SM, so
-// that L2 holds all of them for the second pass (8192 rows of 44629 with 64:
-// 280 us, 128 threads 390, 512 threads 380; the row in shared memory instead,
-// two CTAs an SM, 375).
+// Short rows take few threads and many rows an SM: a row's time is then the
+// latency of its steps (16384 rows of 1000 logits, 64 of a teacher's: 64 threads
+// 58 us, 128 87; of 4000 without a teacher 55, 68, with 20 of a teacher's 102, 84:
+// its warp leaves only one for the row; 9133 rows of 10007 with 64: 128 threads
+// 88, 256 159).  Long ones 256, four an SM, so that L2 holds all of them for the
+// second pass (8192 rows of 44629 with 64: 274 us, 128 threads 390, 512 380; the
+// row in shared memory instead, two CTAs an SM, 375).
 constexpr int64_t kShortRows = 16384;
+int64_t shortest_rows(int64_t K) { return K > 0 ? 2560 : 6144; }
 
 // A matrix for share(), which counts in 16 bits.
 struct Extent {
@@ -406,10 +410,9 @@ extern "C" int zero_distill_loss(const void* logits, int64_t ldl, const int32_t*
     const bool vec = !dlogits || ((addr(logits) - addr(dlogits)) % 16 == 0 && (ldl - lddl) % 8 == 0);
     const int bf16 = type == ZERO_TYPE_BF16;
     LossKernel fn;
-    const bool few = V < kShortRows;
-    if (few && vec) fn = bf16 ? pick_loss<1, 1, 128>(sums) : pick_loss<0, 1, 128>(sums);
-    else if (few) fn = bf16 ? pick_loss<1, 0, 128>(sums) : pick_loss<0, 0, 128>(sums);
-    else if (vec) fn = bf16 ? pick_loss<1, 1, 256>(sums) : pick_loss<0, 1, 256>(sums);
-    else fn = bf16 ? pick_loss<1, 0, 256>(sums) : pick_loss<0, 0, 256>(sums);
-    return launch_after(fn, a, T, few ? 128 : 256, 0, 1, static_cast<cudaStream_t>(cuda_stream));
+    const int threads = V < shortest_rows(K) ? 64 : V < kShortRows ? 128 : 256;
+    if (threads == 64) fn = bf16 ? (vec ? pick_loss<1, 1, 64>(sums) : pick_loss<1, 0, 64>(sums)) : (vec ? pick_loss<0, 1, 64>(sums) : pick_loss<0, 0, 64>(sums));
+    else if (threads == 128) fn = bf16 ? (vec ? pick_loss<1, 1, 128>(sums) : pick_loss<1, 0, 128>(sums)) : (vec ? pick_loss<0, 1, 128>(sums) : pick_loss<0, 0, 128>(sums));
+    else fn = bf16 ? (vec ? pick_loss<1, 1, 256>(sums) : pick_loss<1, 0, 256>(sums)) : (vec ? pick_loss<0, 1, 256>(sums) : pick_loss<0, 0, 256>(sums));
+    return launch_after(fn, a, T, threads, static_cast<int>(K) * 16, 1, static_cast<cudaStream_t>(cuda_stream));
 }
