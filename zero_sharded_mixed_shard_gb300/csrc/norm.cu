@@ -10,7 +10,9 @@
 // statistics and its use, and written once, while the rows to come are on their
 // way to shared memory.  A group of threads shares a row (eight lanes for
 // narrow ones, a CTA for wide ones), each with vectors of 8 elements; the variance is that of the centred values, not a difference of
-// large sums.  In the backward pass a thread keeps its columns' sums of dw and
+// large sums, and the centred values' own mean (what rounding left of it) is
+// taken out of them: a mean far above the row's spread costs no digits, and a
+// constant row's y is the bias.  In the backward pass a thread keeps its columns' sums of dw and
 // db over all rows of its group; the groups' sums go to the workspace and a
 // second launch adds them in a fixed order, so that a call repeats its bits.
 #include "layers.cuh"
@@ -27,6 +29,7 @@ struct NormArgs {
     long long ldx, ldy, T;
     int D;
     float eps, inv_d;
+    float share, whole, inv_whole; // 2^-k, D 2^-k (a half to 1), and one over it
 };
 
 struct NormBackArgs {
@@ -180,13 +183,33 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float (*part)[THREADS /
     }
 }
 
+// Values whose squares leave fp32's range are scaled by 2^-96.
+constexpr float kSmall = 1.262177448353619e-29f, kLarge = 7.922816251426434e28f;
+
+// The variance, from the mean square and the mean of values about the mean
+// (NaN goes on).
+__device__ __forceinline__ float centred(float square, float left)
+{
+    const float v = fmaf(-left, left, square);
+    return v < 0.0f ? 0.0f : v;
+}
+
+// x / y from y's rounded reciprocal and the remainder: exact where the
+// quotient has a float (a constant row's mean).
+__device__ __forceinline__ float quotient(float x, float y, float reciprocal)
+{
+    const float q = x * reciprocal;
+    return fmaf(fmaf(-q, y, x), reciprocal, q);
+}
+
 // Forward: a CTA that stays on every SM, as many groups as fit in it, a row per
 // group at a time.  A thread has four vectors of a row where it is wide enough:
 // fewer threads have less to join.  Its weights and biases stay in its
-// registers.  16384 rows of 2048 bf16 elements (134 MB) 23 us, 5700 GB/s (two
+// registers.  16384 rows of 2048 bf16 elements (134 MB) 24 us, 5600 GB/s (two
 // vectors a thread, two CTAs an SM, weights in shared memory 35 us: twice the
-// joins; a CTA of 256 threads per row that does not stay 40); off 16 bytes 49 us,
-// bound by shifting the granules.
+// joins; a CTA of 256 threads per row that does not stay 40); off 16 bytes 50 us,
+// bound by shifting the granules.  The centred values' mean, joined with their
+// squares, costs 0.3 of the 24, a division in place of the reciprocal 0.6 more.
 constexpr int kNormThreads = 512;
 template <int VPT> constexpr int kForwardAhead = VPT == 4 ? 5 : 8;
 template <int VEC, int GROUP, int VPT> using ForwardRows = Rows<VEC, GROUP, VPT, 1, kForwardAhead<VPT>, kNormThreads>;
@@ -196,7 +219,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) zero_layernorm_kernel(const _
 {
     extern __shared__ __align__(16) unsigned char raw[];
     constexpr int kGroups = kNormThreads / GROUP, S = kForwardAhead<VPT>;
-    __shared__ float part[2][kNormThreads / 32][1];
+    __shared__ float part[2][kNormThreads / 32][1], part2[2][kNormThreads / 32][2];
     const int self = threadIdx.x % GROUP, group = threadIdx.x / GROUP;
     let_successor_start();
     wait_for_predecessor();
@@ -229,17 +252,17 @@ __global__ void __launch_bounds__(kNormThreads, 1) zero_layernorm_kernel(const _
         ahead(s == 0 ? S - 1 : s - 1, r + (S - 1) * step); // into the slot that the last row has left
         rows.wait();
         float2 v[VPT][4];
-        // the mean as a sum of x / D: no partial sum is above the largest value
+        // the mean as a sum of x 2^-k, exact, with 2^k the power of two from D on: no partial sum is above the largest value
         float2 total = both(0.0f);
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             widen<BF16>(rows.get(s, 0, k, from, D), v[k]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) total = fma2(v[k][j], both(a.inv_d), total);
+            for (int j = 0; j < 4; ++j) total = fma2(v[k][j], both(a.share), total);
         }
         float sum[1] = {total.x + total.y};
         group_sum<GROUP, 1, kNormThreads>(sum, part, group, &turn);
-        const float mean = sum[0];
+        const float mean = quotient(sum[0], a.whole, a.inv_whole);
         // half of the centred values: a difference of two values of bf16's range may pass fp32's; 0 past the row's end
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
@@ -251,30 +274,36 @@ __global__ void __launch_bounds__(kNormThreads, 1) zero_layernorm_kernel(const _
                 if (VEC ? there <= 0 : there <= 2 * j + 1) v[k][j].y = 0.0f;
             }
         }
-        auto squares = [&](float scale) {
-            float2 all = both(0.0f);
+        // the centred values' mean (what the mean's rounding left) and their variance
+        auto moments = [&](float scale, float* left, float* variance) {
+            float2 all = both(0.0f), one = both(0.0f);
 #pragma unroll
             for (int k = 0; k < VPT; ++k)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float2 d = mul2(v[k][j], both(scale));
+                    one = add2(one, d);
                     all = fma2(d, d, all);
                 }
-            float q[1] = {all.x + all.y};
-            group_sum<GROUP, 1, kNormThreads>(q, part, group, &turn);
-            return q[0];
+            float q[2] = {one.x + one.y, all.x + all.y};
+            group_sum<GROUP, 2, kNormThreads>(q, part2, group, &turn);
+            *left = q[0] * a.inv_d;
+            *variance = centred(q[1] * a.inv_d, *left);
         };
-        const float q = squares(1.0f) * a.inv_d;
+        float left, q;
+        moments(1.0f, &left, &q);
         float rstd = __frsqrt_rn(fmaf(4.0f, q, a.eps));
         // squares of values above 2^63 leave fp32's range: taken again with the values scaled down (by the whole warp where
         // groups share one: the sum's shuffles are the warp's)
         const int over = !(q < 2e37f);
         if (BF16 && (GROUP < 32 ? __any_sync(0xffffffffu, over) : over)) {
-            const float small = squares(1.262177448353619e-29f) * a.inv_d; // 2^-96; eps does not count beside them
-            if (over) rstd = __frsqrt_rn(4.0f * small) * 1.262177448353619e-29f;
+            float small_left, small;
+            moments(kSmall, &small_left, &small); // eps does not count beside them
+            if (over) rstd = __frsqrt_rn(4.0f * small) * kSmall, left = small_left * kLarge;
         }
+        const float twice = 2.0f * rstd, back = -left * twice;
         if (self == 0 && D) {
-            if (a.mean) a.mean[r] = mean;
+            if (a.mean) a.mean[r] = fmaf(2.0f, left, mean);
             if (a.rstd) a.rstd[r] = rstd;
         }
 #pragma unroll
@@ -284,7 +313,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) zero_layernorm_kernel(const _
             widen<BF16>(weight[k], g);
             widen<BF16>(bias[k], h);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[k][j] = fma2(mul2(v[k][j], both(2.0f * rstd)), g[j], h[j]);
+            for (int j = 0; j < 4; ++j) v[k][j] = fma2(fma2(v[k][j], both(twice), both(back)), g[j], h[j]);
             store_row<VEC, GROUP>(y + r * a.ldy, c, self, D, narrow<BF16>(v[k]));
         }
         if (++s == S) s = 0;
@@ -298,7 +327,7 @@ constexpr int kWideThreads = 1024;
 template <int BF16, int VEC>
 __global__ void __launch_bounds__(kWideThreads) zero_layernorm_wide_kernel(const __grid_constant__ NormArgs a)
 {
-    __shared__ float part[2][kWideThreads / 32][1];
+    __shared__ float part[2][kWideThreads / 32][1], part2[2][kWideThreads / 32][2];
     const int self = threadIdx.x;
     const long long r = blockIdx.x;
     let_successor_start();
@@ -315,12 +344,12 @@ __global__ void __launch_bounds__(kWideThreads) zero_layernorm_wide_kernel(const
         float v[8];
         widen<BF16>(load_row<VEC>(x, column<kWideThreads>(k, self), a.D), v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum[0] = fmaf(v[j], a.inv_d, sum[0]);
+        for (int j = 0; j < 8; ++j) sum[0] = fmaf(v[j], a.share, sum[0]);
     }
     group_sum<kWideThreads, 1, kWideThreads>(sum, part, 0, &turn);
-    const float mean = sum[0], half_mean = -0.5f * mean;
-    auto squares = [&](float scale) {
-        float q[1] = {0.0f};
+    const float mean = sum[0] / a.whole, half_mean = -0.5f * mean;
+    auto moments = [&](float scale, float* left, float* variance) {
+        float q[2] = {0.0f, 0.0f};
 #pragma unroll 2
         for (int k = 0; k < steps; ++k) {
             float v[8];
@@ -329,23 +358,29 @@ __global__ void __launch_bounds__(kWideThreads) zero_layernorm_wide_kernel(const
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float d = fmaf(v[j], 0.5f, half_mean) * scale;
-                if (c + j < a.D) q[0] = fmaf(d, d, q[0]);
+                if (c + j < a.D) {
+                    q[0] += d;
+                    q[1] = fmaf(d, d, q[1]);
+                }
             }
         }
-        group_sum<kWideThreads, 1, kWideThreads>(q, part, 0, &turn);
-        return q[0];
+        group_sum<kWideThreads, 2, kWideThreads>(q, part2, 0, &turn);
+        *left = q[0] * a.inv_d;
+        *variance = centred(q[1] * a.inv_d, *left);
     };
-    const float q = squares(1.0f) * a.inv_d;
+    float left, q;
+    moments(1.0f, &left, &q);
     float rstd = __frsqrt_rn(fmaf(4.0f, q, a.eps));
     if (BF16 && !(q < 2e37f)) { // the same in every thread
-        const float small = squares(1.262177448353619e-29f) * a.inv_d;
-        rstd = __frsqrt_rn(4.0f * small) * 1.262177448353619e-29f;
+        float small_left, small;
+        moments(kSmall, &small_left, &small);
+        rstd = __frsqrt_rn(4.0f * small) * kSmall, left = small_left * kLarge;
     }
     if (self == 0) {
-        if (a.mean) a.mean[r] = mean;
+        if (a.mean) a.mean[r] = fmaf(2.0f, left, mean);
         if (a.rstd) a.rstd[r] = rstd;
     }
-    const float twice = 2.0f * rstd;
+    const float twice = 2.0f * rstd, back = -left * twice;
     for (int k = 0; k < steps; ++k) {
         const int c = column<kWideThreads>(k, self);
         float v[8], g[8], h[8];
@@ -354,7 +389,7 @@ __global__ void __launch_bounds__(kWideThreads) zero_layernorm_wide_kernel(const
         if (b) widen<BF16>(load_row<VEC>(b, c, a.D), h);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            v[j] = fmaf(v[j], 0.5f, half_mean) * twice;
+            v[j] = fmaf(fmaf(v[j], 0.5f, half_mean), twice, back);
             if (w) v[j] *= g[j];
             if (b) v[j] += h[j];
         }
@@ -743,6 +778,9 @@ extern "C" int zero_layernorm_forward(const void* x, int64_t ldx, const void* we
     NormArgs a{};
     a.x = x, a.w = weight, a.b = bias, a.y = y, a.mean = mean, a.rstd = rstd, a.ldx = ldx, a.ldy = ldy, a.T = T;
     a.D = static_cast<int>(D), a.eps = eps, a.inv_d = 1.0f / static_cast<float>(D);
+    a.share = 1.0f;
+    for (int64_t power = 1; power < D; power *= 2) a.share *= 0.5f;
+    a.whole = static_cast<float>(D) * a.share, a.inv_whole = 1.0f / a.whole;
     if (D > kNormWide) {
         NormKernel fn;
         if (bf16) fn = vec ? zero_layernorm_wide_kernel<1, 1> : zero_layernorm_wide_kernel<1, 0>;
