@@ -183,8 +183,8 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float (*part)[THREADS /
     }
 }
 
-// Values whose squares leave fp32's range are scaled by 2^-96.
-constexpr float kSmall = 1.262177448353619e-29f, kLarge = 7.922816251426434e28f;
+// Values whose squares leave fp32's range (or do with eps) are scaled by 2^-96.
+constexpr float kSmall = 1.262177448353619e-29f, kLarge = 7.922816251426434e28f, kMost = 3.402823466e38f;
 
 // The variance, from the mean square and the mean of values about the mean
 // (NaN goes on).
@@ -292,14 +292,15 @@ __global__ void __launch_bounds__(kNormThreads, 1) zero_layernorm_kernel(const _
         };
         float left, q;
         moments(1.0f, &left, &q);
-        float rstd = __frsqrt_rn(fmaf(4.0f, q, a.eps));
+        const float spread = fmaf(4.0f, q, a.eps);
+        float rstd = __frsqrt_rn(spread);
         // squares of values above 2^63 leave fp32's range: taken again with the values scaled down (by the whole warp where
         // groups share one: the sum's shuffles are the warp's)
-        const int over = !(q < 2e37f);
+        const int over = !(spread <= kMost);
         if (BF16 && (GROUP < 32 ? __any_sync(0xffffffffu, over) : over)) {
             float small_left, small;
-            moments(kSmall, &small_left, &small); // eps does not count beside them
-            if (over) rstd = __frsqrt_rn(4.0f * small) * kSmall, left = small_left * kLarge;
+            moments(kSmall, &small_left, &small);
+            if (over) rstd = __frsqrt_rn(fmaf(4.0f, small, a.eps * kSmall * kSmall)) * kSmall, left = small_left * kLarge;
         }
         const float twice = 2.0f * rstd, back = -left * twice;
         if (self == 0 && D) {
@@ -370,11 +371,12 @@ __global__ void __launch_bounds__(kWideThreads) zero_layernorm_wide_kernel(const
     };
     float left, q;
     moments(1.0f, &left, &q);
-    float rstd = __frsqrt_rn(fmaf(4.0f, q, a.eps));
-    if (BF16 && !(q < 2e37f)) { // the same in every thread
+    const float spread = fmaf(4.0f, q, a.eps);
+    float rstd = __frsqrt_rn(spread);
+    if (BF16 && !(spread <= kMost)) { // the same in every thread
         float small_left, small;
         moments(kSmall, &small_left, &small);
-        rstd = __frsqrt_rn(4.0f * small) * kSmall, left = small_left * kLarge;
+        rstd = __frsqrt_rn(fmaf(4.0f, small, a.eps * kSmall * kSmall)) * kSmall, left = small_left * kLarge;
     }
     if (self == 0) {
         if (a.mean) a.mean[r] = fmaf(2.0f, left, mean);
