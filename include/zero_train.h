@@ -281,8 +281,10 @@ int zero_embed_forward(const int32_t* ids, const void* table, int64_t ldt, void*
                        int64_t T, int64_t D, int64_t V, float scale, int32_t type,
                        void* cuda_stream);
 
-/* Bytes of workspace of zero_embed_backward: T * (D / 4 + 16) and less for many
- * tokens, up to 2 T * (D + 18) for few.  Host only.  Errors: ZERO_EINVAL. */
+/* Bytes of workspace of zero_embed_backward, never above
+ * 2 (T + 3) (D + 23) + 17408 (the parts of rows that are added up last, for few
+ * tokens; for many about an eighth of that).  Host only.  Errors:
+ * ZERO_EINVAL. */
 int zero_embed_workspace(int64_t T, int64_t D, int64_t V, int64_t* bytes);
 
 /* The table's gradient, dtable[v] = scale * sum of dy[t] over the tokens with
