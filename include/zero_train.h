@@ -367,7 +367,14 @@ int zero_layernorm_backward(const void* dy, int64_t lddy, const void* x, int64_t
  * [T][ldk] of teacher_type (ZERO_TYPE_FP16, _BF16 or _FP32).  weights: fp32
  * [T] or NULL (ones).  A row with weight 0 or without terms gets loss 0 and a
  * gradient of zeros, whatever its logits hold.  Logits of minus infinity
- * (masked) have probability 0.
+ * (masked) have probability 0: a row whose target, or a teacher's entry with a
+ * probability, is masked has an infinite loss (its gradient is finite), and one
+ * with a term whose logits are all masked has neither a loss nor a gradient:
+ * both are NaN, as they are of a row that holds NaN or plus infinity.  Give such
+ * rows weight 0.
+ * The second term is z^2 times a difference of fp32 logarithms, off by about
+ * z^2 2^-19: where the teacher's entries are nearly all of V and z is in the
+ * hundreds, that is not small beside the term (its gradient is not concerned).
  * loss: fp32 [T].  dlogits [T][lddl], of `type` like the logits, or NULL (not
  * computed); it may be logits itself (same pointer and stride).  Sums are in
  * fp32, the gradient is rounded once; the same call gives the same bits.  T
