@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(256) zero_gated_prep_kernel(const __grid_const
     auto through = [](float d, float gv, float uv, float* dg, float* du) {
         *du = d * activate<ACT>(gv);
         if constexpr (ACT == ZERO_ACT_RELU) *dg = gv > 0.0f ? d * uv : 0.0f;
-        else *dg = d * uv * slope<ACT>(gv);
+        else *dg = d * (uv * slope<ACT>(gv)); // d u alone may leave the range that the slope brings it back to
     };
     const bool whole = a.vec && col + 8 <= a.N; // else by granules; zeros past the last feature
     if (col < a.half) {
