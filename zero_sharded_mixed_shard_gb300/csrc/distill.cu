@@ -18,9 +18,9 @@
 // stored last, after the CTA's barrier, from logits read before the second
 // pass: logits and gradient may be one matrix.
 // Bound by HBM and, nearly, by issue and exponentials: 8192 rows of 44629 bf16
-// logits with 64 of a teacher's at temperature 2 (1.47 GB) 274 us, 5350 GB/s;
-// without a teacher 258 us.  (Each block's barrier for the teacher's sums, scalar
-// arithmetic and two exponentials an element 466 us.)
+// logits with 64 of a teacher's at temperature 2 (1.47 GB) 275 us, 5330 GB/s;
+// without a teacher 260 us, the loss alone 146 and 131.  (Each block's barrier for
+// the teacher's sums, scalar arithmetic and two exponentials an element 466 us.)
 #include "layers.cuh"
 
 namespace {
@@ -93,7 +93,9 @@ template <int BF16> __device__ __forceinline__ uint32_t max16(uint32_t a, uint32
 // The exponentials of two logits below the largest: `hard` 2^(l d), `soft`
 // 2^(lz d).  SUMS 0: one serves both (in `hard`).  1: two of them.  2 and 4: the
 // temperature is that, and e^d is a power of e^(d / z): half of the
-// exponentials.
+// exponentials (8192 rows of 44629 with 64 of a teacher's at temperature 2 or 4
+// 280 to 283 us, with two of them 293, as at temperatures 1.5 and 3; 9133 of 10007
+// 86 to 90, 94; 16384 of 1000 60, 62).
 template <int SUMS> __device__ __forceinline__ void exponentials(float2 d, float l, float lz, float2* hard, float2* soft)
 {
     if constexpr (SUMS == 0) {
@@ -265,7 +267,9 @@ __global__ void __launch_bounds__(kLossThreads, kLossThreads == 64 ? 20 : kLossT
         return mul2(make_float2(f_hard + f_soft, f_hard + f_soft), e);
     };
     auto slope1 = [&](float v) { return slope(make_float2(v, v)).x; };
-    // the gradient's value at an entry: an index that occurs twice has the same, whole value both times
+    // the gradient's value at an entry: an index that occurs twice has the same, whole value both times.  Each entry
+    // looks at all K: nothing beside a row for tens of them, but K^2 steps (16384 rows of 2000: K = 16 57 us, 64 63,
+    // 256 334, 1024 3610)
     auto merged = [&](int k) {
         const int j = j_of[k];
         float p = 0.0f;
@@ -353,8 +357,11 @@ template <int BF16, int VEC, int THREADS> LossKernel pick_loss(int sums)
 // 58 us, 128 87; of 4000 without a teacher 55, 68, with 20 of a teacher's 102, 84:
 // its warp leaves only one for the row; 9133 rows of 10007 with 64: 128 threads
 // 88, 256 159).  Long ones 256, four an SM, so that L2 holds all of them for the
-// second pass (8192 rows of 44629 with 64: 274 us, 128 threads 390, 512 380; the
-// row in shared memory instead, two CTAs an SM, 375).
+// second pass (8192 rows of 44629 with 64: 275 us, 128 threads 390, 512 380; the
+// row in shared memory instead, two CTAs an SM, 375).  A row is one CTA's however
+// few there are: 1 to 64 rows of 10007 7 us, of 44629 10, of 150000 23 to 34; 509
+// of them 9, 24 and 79.  (At 48 registers ten of the forms with 64 or 128 threads
+// spill 4 to 8 bytes.)
 constexpr int64_t kShortRows = 16384;
 int64_t shortest_rows(int64_t K) { return K > 0 ? 2560 : 6144; }
 

@@ -19,8 +19,10 @@
 // in fp32 and are added in order by a last launch.  However often an id occurs,
 // no warp has more than a chunk of rows to read.
 // 16384 tokens, a table of 44629 x 2048 (250 MB, 183 of them written) 60 us: sort
-// and cleared rows 12, sums and the other rows without a token 38, joins 10.
-// Writing alone is slower than copying here: a plain fill of the table takes 51.
+// and cleared rows 12, sums and the other rows without a token 38 (210 MB, 5500
+// GB/s), joins 10.  The sort and the joins are latency with HBM nearly idle: a
+// fill of the table alone takes 31 (6000 GB/s, by vectors or by bulk copies from
+// cleared shared memory alike).
 #include "layers.cuh"
 
 namespace {
@@ -412,6 +414,9 @@ template <int VEC> __device__ __forceinline__ void clear_rows(const RunArgs& a, 
     }
 }
 
+// CTAs an SM: about as many as the rows in flight leave registers for (aligned
+// rows that are written spill 24 bytes at three, unaligned ones that are added to
+// 108 at four).
 template <int BF16, int VEC, int ADD> __global__ void __launch_bounds__(256, VEC ? (ADD ? 2 : 3) : 4) zero_embed_grad_kernel(const __grid_constant__ RunArgs a)
 {
     constexpr int kAhead = VEC ? 8 : 4; // rows in flight (two granules each off 16 bytes)
@@ -601,8 +606,12 @@ GradPlan plan_grad(int64_t T, int64_t D, int64_t V, void* workspace)
     p.passes = (bits + kDigitBits - 1) / kDigitBits;
     p.pitch = up(D + 7, 8); // granules of a row that starts anywhere
     p.stripes = (p.pitch + kStripe - 1) / kStripe;
-    // short chunks where there are few: a chunk's rows follow on each other; longer ones once there are warps
-    // enough: fewer runs are cut
+    // short chunks where there are few: a chunk's rows follow on each other (up to 16 warps an SM: 2432 chunks and
+    // stripes on 152); longer ones once there are warps enough, so that fewer runs are cut (8192 of them from 32 tokens
+    // a chunk on).  Chunks of 4, 8, 16, 32, 64, 128 and 256 tokens, us, with the gradient added to bf16 rows (fp16 for
+    // 331 columns): 1009 tokens x 331 17, 20, 27, 40, 68, 124, 223 (the rule takes 4); 2048 x 2048 21, 16, 18, 21, 29,
+    // 46, 78 (8); 16384 x 2048 106, 71, 56, 47, 46, 58, 94 (32); 200000 x 1024 885, 506, 321, 233, 190, 173, 189 (96:
+    // 178); 1e6 x 64 3066, 1556, 880, 520, 347, 269, 219 (96: 294)
     p.chunk = 4;
     while (p.chunk < 32 && T * p.stripes > 2432 * p.chunk) p.chunk *= 2;
     if (p.chunk == 32) p.chunk = static_cast<int>(std::min<int64_t>(256, std::max<int64_t>(32, T * p.stripes / 8192 / 32 * 32)));
@@ -616,7 +625,11 @@ GradPlan plan_grad(int64_t T, int64_t D, int64_t V, void* workspace)
     return p;
 }
 
-constexpr int64_t kClearBytes = 40 << 20; // of the table's gradient that is cleared during a sort by one cluster
+// Of the table's gradient, cleared during a sort by one cluster, and the CTAs that
+// do it (with the sort's eight 18 clusters, one CTA an SM).  44629 x 2048 with 1024,
+// 16384 and 65536 tokens: nothing cleared ahead 45, 66 and 132 us; 20 MB 42, 64,
+// 132; 40 MB 43, 62, 132; 80 MB 48, 66, 130.  64 CTAs 46, 62, 132; 144 as 136.
+constexpr int64_t kClearBytes = 40 << 20;
 constexpr int kClearCtas = 136;
 
 using ClusterSort = void (*)(ClusterSortArgs);

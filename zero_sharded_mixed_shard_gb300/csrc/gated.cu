@@ -18,10 +18,12 @@
 // All three products go into one launch where they take the same kernel.
 //
 // Bound by the tensor cores: x [8192, 2048], 8192 features, SiLU, bf16, g and u
-// kept: forward 292 us (1880 TFLOP/s; 350 back to back at the card's power
+// kept: forward 292 us (1880 TFLOP/s; 345 to 353 back to back at the card's power
 // limit), the backward pass's products 605 us (1820 TFLOP/s, tensor pipe 97 %
-// busy; in all 745, back to back 782).  With few tokens by the reads of the
-// weights: 4 tokens 14 us (67 MB).
+// busy; in all 723 to 750, back to back 780 to 805).  With few tokens by the reads
+// of the weights: 4 tokens 14 us (67 MB); backward, where the weights' gradients
+// are written too (134 MB, 20 us at a copy's rate), 44: dg and du, dx and both dW
+// are three launches, one after the other.
 #include "gemm.cuh"
 
 namespace {

@@ -403,7 +403,9 @@ __global__ void __launch_bounds__(kWideThreads) zero_layernorm_wide_kernel(const
 // a row per group at a time.  A group joins its two sums of a row by one
 // barrier of its own.  16384 rows of 2048 bf16 elements with the residual (269
 // MB) 46 us with the sums' launch, 5850 GB/s (rows read where they are used,
-// the CTA's barrier twice per four rows: 81 us); off 16 bytes 71 us.
+// the CTA's barrier twice per four rows: 81 us); off 16 bytes 71 us.  Above 12288
+// columns the columns' sums fill the registers: 40 to 264 bytes spilled, one row
+// ahead (2048 x 16384 69 us, off 16 bytes 113).
 constexpr int kGradThreads = 512;
 template <int VPT> constexpr int kGradAhead = VPT == 1 ? 6 : VPT == 2 ? 4 : 2;
 template <int VEC, int GROUP, int VPT> using GradRows = Rows<VEC, GROUP, VPT, 3, kGradAhead<VPT>, kGradThreads>;
